@@ -19,6 +19,8 @@ __all__ = ["fwd", "bwd", "fwd_workspace_size", "bwd_workspace_size", "device_sta
            "record_kernel_events", "launch_count", "workspace", "bwd_noalloc",
            "noalloc_device_status",
            "fwd_splitkv", "QKShape",
+           "append_paged", "fwd_paged", "fwd_prefix", "PagedShape", "paged_shape",
+           "paged_workspace_size", "prefix_workspace_size",
            "MASK_NONE", "MASK_CAUSAL", "MASK_WINDOW", "MASK_BITMASK"]
 
 MASK_NONE, MASK_CAUSAL, MASK_WINDOW, MASK_BITMASK = 0, 1, 2, 3
@@ -48,6 +50,15 @@ class QKShape(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int), ("heads", ctypes.c_int), ("nq", ctypes.c_int),
                 ("nk", ctypes.c_int), ("d", ctypes.c_int), ("v", ctypes.c_int),
                 ("dtype", ctypes.c_int)]
+
+
+class PagedShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("tokens", ctypes.c_int), ("heads", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("d", ctypes.c_int), ("v", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong),
+                ("v_stride", ctypes.c_longlong)]
 
 
 class Shape(ctypes.Structure):
@@ -111,6 +122,18 @@ def load_library():
     lib.exattn_splitkv_workspace_size.restype = sz
     lib.attn_fwd_splitkv.argtypes = [qp, vp, vp, vp, cf, ci, ci, vp, ci, vp, vp, vp, sz, vp]
     lib.attn_fwd_splitkv.restype = ci
+    pp = ctypes.POINTER(PagedShape)
+    lib.exattn_paged_workspace_size.argtypes = [pp]
+    lib.exattn_paged_workspace_size.restype = sz
+    lib.exattn_prefix_workspace_size.argtypes = [pp]
+    lib.exattn_prefix_workspace_size.restype = sz
+    lib.attn_append_paged.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, vp, vp, vp, vp,
+                                      sz, vp]
+    lib.attn_append_paged.restype = ci
+    lib.attn_fwd_paged.argtypes = [pp, vp, vp, vp, vp, vp, vp, cf, ci, ci, vp, vp, vp, sz, vp]
+    lib.attn_fwd_paged.restype = ci
+    lib.attn_fwd_prefix.argtypes = [pp, vp, vp, vp, vp, ci, vp, vp, vp, cf, ci, vp, vp, vp, sz, vp]
+    lib.attn_fwd_prefix.restype = ci
     lib.exattn_last_error.argtypes = []
     lib.exattn_last_error.restype = ctypes.c_char_p
     lib.exattn_host_step_workspace_size.argtypes = [sp, ci]
@@ -362,6 +385,197 @@ def fwd_splitkv(q, k, v, scale, mask="none", window=0, bitmask=None, num_splits=
     return y, L
 
 
+def _token_stride(name, t, heads, width):
+    """Elements from one token of t [tokens, heads, width] to the next; each
+    token's heads must be dense (rows of a projection's output are)."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != width:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [tokens, {heads}, {width}]")
+    step, hs, ws = t.stride()
+    if (ws != 1 and width > 1) or (hs != width and heads > 1):
+        raise ValueError(f"{name}'s heads must be dense within a token")
+    if t.shape[0] == 1:  # the stride of a single token is not used
+        return heads * width
+    if step < heads * width:
+        raise ValueError(f"{name}'s tokens overlap")
+    return step
+
+
+def paged_shape(q, k_pages, v_pages, page_table) -> PagedShape:
+    """The PagedShape of q [tokens, heads, d] (or a k [tokens, kv_heads, d]) over
+    k_pages [num_pages, kv_heads, page_size, d], v_pages [num_pages, kv_heads, page_size, v]
+    and page_table [batch, max_pages], for the workspace queries."""
+    if q.dim() != 3 or k_pages.dim() != 4 or v_pages.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("expected q [tokens, heads, d], pages [num_pages, kv_heads, page_size, "
+                         "width] and page_table [batch, max_pages]")
+    if q.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {q.dtype}")
+    pages, kv, size, d = k_pages.shape
+    batch, most = page_table.shape
+    return PagedShape(batch, q.shape[0], q.shape[1], kv, d, v_pages.shape[3], _DTYPES[q.dtype],
+                      size, pages, most, 0, 0, 0)
+
+
+def paged_workspace_size(shape: PagedShape) -> int:
+    return load_library().exattn_paged_workspace_size(ctypes.byref(shape))
+
+
+def prefix_workspace_size(shape: PagedShape) -> int:
+    return load_library().exattn_prefix_workspace_size(ctypes.byref(shape))
+
+
+def _check_paged(q, k_pages, v_pages, page_table, seq_lens, q_starts, ws):
+    """The cache and its tables, which the library takes as bare pointers.  Raises
+    ValueError before anything reaches the library; returns the PagedShape."""
+    shape = paged_shape(q, k_pages, v_pages, page_table)
+    dev = q.device
+    _check((k_pages, v_pages), q.dtype, dev)
+    if k_pages.shape[:3] != v_pages.shape[:3]:
+        raise ValueError(f"v_pages has shape {tuple(v_pages.shape)}, k_pages "
+                         f"{tuple(k_pages.shape)}: they differ before the width")
+    for name, t, n in (("page_table", page_table, None), ("seq_lens", seq_lens, shape.batch),
+                       ("q_starts", q_starts, shape.batch + 1)):
+        if t is None:
+            continue
+        if t.dtype != torch.int32 or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{name} must be contiguous int32 on {dev}")
+        if n is not None and tuple(t.shape) != (n,):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({n},)")
+    if q_starts is None and shape.batch and shape.tokens % shape.batch:
+        raise ValueError(f"{shape.tokens} tokens do not divide among {shape.batch} sequences: "
+                         "give q_starts")
+    if ws is not None and (ws.device != dev or not ws.is_contiguous()):
+        raise ValueError(f"the workspace must be a contiguous tensor on {dev}")
+    return shape
+
+
+def _int32(name, x) -> int:
+    """x as the int that the library takes (ctypes would drop its high bits)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} = {x} does not fit 32 bits")
+    return x
+
+
+def _paged_outputs(q, vw, y, L):
+    want = (q.shape[0], q.shape[1], vw)
+    if y is None:
+        y = torch.empty(want, dtype=q.dtype, device=q.device)
+    elif tuple(y.shape) != want or y.dtype != q.dtype or y.device != q.device or not y.is_contiguous():
+        raise ValueError(f"y must be a contiguous {q.dtype} tensor of shape {want} on {q.device}")
+    if L is None:
+        L = torch.empty(want[:2], dtype=torch.float32, device=q.device)
+    elif (tuple(L.shape) != want[:2] or L.dtype != torch.float32 or L.device != q.device
+          or not L.is_contiguous()):
+        raise ValueError(f"L must be a contiguous float32 tensor of shape {want[:2]} on {q.device}")
+    return y, L
+
+
+def _device_call(device, stream, call):
+    """``call(stream pointer)`` with ``device`` current; ``stream`` None: its current stream."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    if device.index is None or device.index == torch.cuda.current_device():
+        return call(s.cuda_stream)
+    with torch.cuda.device(device):
+        return call(s.cuda_stream)
+
+
+def append_paged(k, v, k_pages, v_pages, page_table, seq_lens, q_starts=None, q=None, q_out=None,
+                 inv_freq=None, interleaved=False, pos_offset=0, ws=None, stream=None):
+    """attn_append_paged: the new tokens' k [tokens, kv_heads, d] and v [tokens, kv_heads, v] go
+    into the pages of their sequences, k rotated by position with ``inv_freq`` (float32
+    [pairs]; None: not rotated).  ``q`` [tokens, heads, d] is rotated beside them and
+    returned (``q_out`` may be given, and may be ``q``).  seq_lens [batch] counts each sequence's
+    tokens with the new ones; q_starts [batch + 1] gives each its range of tokens (None: equally
+    many each).  k, v and q may be columns of one projection's output."""
+    lib = load_library()
+    pos_offset = _int32("pos_offset", pos_offset)
+    lead = k if q is None else q
+    shape = _check_paged(lead, k_pages, v_pages, page_table, seq_lens, q_starts, ws)
+    for name, t in (("k", k), ("v", v), ("q_out", q_out)):
+        if t is not None and (t.dtype != lead.dtype or t.device != lead.device):
+            raise ValueError(f"{name} must be {lead.dtype} on {lead.device}")
+    shape.k_stride = _token_stride("k", k, shape.kv_heads, shape.d)
+    shape.v_stride = _token_stride("v", v, shape.kv_heads, shape.v)
+    if k.shape[0] != shape.tokens or v.shape[0] != shape.tokens:
+        raise ValueError(f"q, k and v must have as many tokens: {shape.tokens}, {k.shape[0]}, "
+                         f"{v.shape[0]}")
+    if q is not None:
+        shape.q_stride = _token_stride("q", q, shape.heads, shape.d)
+        if q_out is None:
+            q_out = torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)
+        elif q_out.shape != q.shape or not q_out.is_contiguous():
+            raise ValueError(f"q_out must be contiguous of shape {tuple(q.shape)}")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    pairs = 0
+    if inv_freq is not None:
+        if (inv_freq.dim() != 1 or inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous()
+                or inv_freq.device != lead.device):
+            raise ValueError(f"inv_freq must be contiguous float32 [pairs] on {lead.device}")
+        pairs = inv_freq.numel()
+    if ws is None:
+        ws = workspace(256, lead.device)
+    st = _device_call(lead.device, stream, lambda s: lib.attn_append_paged(
+        shape, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        page_table.data_ptr(), seq_lens.data_ptr(), None if q_starts is None else q_starts.data_ptr(),
+        inv_freq.data_ptr() if pairs else None, pairs, int(bool(interleaved)), pos_offset,
+        None if q is None else q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+        ws.data_ptr(), _nbytes(ws), s))
+    if st != 0:
+        raise ExattnError(st, "attn_append_paged")
+    return q_out
+
+
+def fwd_paged(q, k_pages, v_pages, page_table, seq_lens, scale, mask="none", window=0, q_starts=None,
+              y=None, L=None, ws=None, stream=None):
+    """attn_fwd_paged -> (Y [tokens, heads, v], L [tokens, heads]): q [tokens, heads, d] over the
+    cached keys of each token's sequence (see append_paged for the tables)."""
+    lib = load_library()
+    shape = _check_paged(q, k_pages, v_pages, page_table, seq_lens, q_starts, ws)
+    shape.q_stride = _token_stride("q", q, shape.heads, shape.d)
+    y, L = _paged_outputs(q, shape.v, y, L)
+    if ws is None:
+        ws = workspace(lib.exattn_paged_workspace_size(shape), q.device)
+    window = _int32("window", window)
+    st = _device_call(q.device, stream, lambda s: lib.attn_fwd_paged(
+        shape, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+        seq_lens.data_ptr(), None if q_starts is None else q_starts.data_ptr(), float(scale),
+        _mask_kind(mask), window, y.data_ptr(), L.data_ptr(), ws.data_ptr(), _nbytes(ws), s))
+    if st != 0:
+        raise ExattnError(st, "attn_fwd_paged")
+    return y, L
+
+
+def fwd_prefix(q, k_pages, v_pages, prefix_table, prefix_len, page_table, seq_lens, scale,
+               mask="none", q_starts=None, y=None, L=None, ws=None, stream=None):
+    """attn_fwd_prefix -> (Y, L): fwd_paged for sequences that all begin with the
+    ``prefix_len`` keys of the pages ``prefix_table`` (int32 [pages]), which are read once for all of
+    them; page_table and seq_lens describe each sequence's own keys behind the prefix."""
+    lib = load_library()
+    shape = _check_paged(q, k_pages, v_pages, page_table, seq_lens, q_starts, ws)
+    shape.q_stride = _token_stride("q", q, shape.heads, shape.d)
+    prefix_len = _int32("prefix_len", prefix_len)
+    if (prefix_table.dtype != torch.int32 or prefix_table.dim() != 1
+            or not prefix_table.is_contiguous() or prefix_table.device != q.device):
+        raise ValueError(f"prefix_table must be contiguous int32 [pages] on {q.device}")
+    if prefix_table.numel() * shape.page_size < prefix_len:
+        raise ValueError(f"prefix_table holds {prefix_table.numel()} pages of {shape.page_size}, "
+                         f"the prefix has {prefix_len} keys")
+    y, L = _paged_outputs(q, shape.v, y, L)
+    if ws is None:
+        ws = workspace(lib.exattn_prefix_workspace_size(shape), q.device)
+    st = _device_call(q.device, stream, lambda s: lib.attn_fwd_prefix(
+        shape, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), prefix_table.data_ptr(),
+        prefix_len, page_table.data_ptr(), seq_lens.data_ptr(),
+        None if q_starts is None else q_starts.data_ptr(), float(scale), _mask_kind(mask),
+        y.data_ptr(), L.data_ptr(), ws.data_ptr(), _nbytes(ws), s))
+    if st != 0:
+        raise ExattnError(st, "attn_fwd_prefix")
+    return y, L
+
+
 def bwd_noalloc(q, k, v, y, dy, L, scale, mask="none", window=0, bitmask=None, dq=None,
                 dk=None, dv=None, stream=None, check_status=False):
     """Reverse pass through attn_bwd_noalloc: no workspace is passed or allocated;
@@ -397,6 +611,7 @@ def noalloc_device_status(stream=None) -> int:
 
 KERNEL_FWD, KERNEL_DELTA, KERNEL_BWD, KERNEL_DQ_CONVERT, KERNEL_BWD_Q = 0, 1, 2, 3, 4
 KERNEL_SPLIT_PARTIAL, KERNEL_SPLIT_MERGE, KERNEL_SPLIT32 = 5, 6, 7
+KERNEL_APPEND, KERNEL_PAGED, KERNEL_PAGED_MERGE = 8, 9, 10
 
 
 def step_host(q, k, v, dy, scale, mask="none", window=0, bitmask=None, out=None, ws=None,

@@ -757,6 +757,7 @@ int exattn_device_status(const void* workspace, void* cuda_stream) {
   if (cudaMemcpy(&word, workspace, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess)
     return EXATTN_CUDA_ERROR;
   if (word & 2u) return EXATTN_TIMEOUT;
+  if (word & 4u) return EXATTN_BAD_PAGE;
   if (word & 1u) return EXATTN_EMPTY_ROW;
   return EXATTN_OK;
 }
@@ -771,6 +772,7 @@ const char* exattn_status_string(int status) {
     case EXATTN_EMPTY_ROW: return "an allowed-key set was empty";
     case EXATTN_CUDA_ERROR: return "CUDA error";
     case EXATTN_TIMEOUT: return "a bounded device wait timed out";
+    case EXATTN_BAD_PAGE: return "a sequence's tokens or keys have no place in the paged cache";
     default: return "unknown status";
   }
 }

@@ -16,6 +16,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Bits of the device status word (first word of every workspace).
 constexpr unsigned kStatusEmptyRow = 1u;
 constexpr unsigned kStatusTimeout = 2u;
+constexpr unsigned kStatusBadPage = 4u;
 
 __device__ __forceinline__ void raise_status(unsigned* status, unsigned bit) {
   atomicOr(status, bit);

@@ -74,7 +74,10 @@ enum KernelRole {
   kKernSplitPartial = 5,
   kKernSplitMerge = 6,
   kKernSplit32 = 7,
-  kKernRoles = 8
+  kKernAppend = 8,
+  kKernPaged = 9,
+  kKernPagedMerge = 10,
+  kKernRoles = 11
 };
 void before_launch(int role, cudaStream_t s);
 // Remember the last failing step of this host thread (exattn_last_error).

@@ -1,0 +1,368 @@
+// Paged attention without tensor cores, for every width and type the library
+// takes, and the merge of the row tiles that several CTAs share.
+//
+// paged_simt_kernel: kW warps share a segment's keys.  A group of G lanes
+// covers one key row in 16-byte pieces (CPL a lane), so a warp-wide load reads
+// 32 / G rows; scores are partial dot products summed inside the group, and
+// each group keeps the running maximum, sum and output of NQ rows in registers
+// (the running-max recurrence of "txf-modern-flash-attention", Hints, in the
+// exp2 domain).  Groups, then warps, are joined with the star rule.  Keys and
+// values are read straight into registers, so nothing outside a segment's keys
+// is ever read or multiplied: what stale rows of a page hold does not matter.
+#include "paged.cuh"
+
+namespace exattn {
+namespace {
+
+constexpr int kW = 4;
+constexpr int kUnit = 64;  // keys of a unit of work
+
+__device__ __forceinline__ float pexp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <typename T> struct Row16;
+template <> struct Row16<float> {
+  static constexpr int E = 4;
+  __device__ static void unpack(const uint4& r, float (&f)[4]) {
+    f[0] = __uint_as_float(r.x);
+    f[1] = __uint_as_float(r.y);
+    f[2] = __uint_as_float(r.z);
+    f[3] = __uint_as_float(r.w);
+  }
+};
+template <> struct Row16<__nv_bfloat16> {
+  static constexpr int E = 8;
+  __device__ static void unpack(const uint4& r, float (&f)[8]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
+
+__device__ __forceinline__ uint4 ldg_once16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
+template <typename T, int G, int CPL, int NQ>
+__global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) {
+  constexpr int E = Row16<T>::E;
+  constexpr int KPW = 32 / G;
+  constexpr int U = (NQ == 1 ? 8 : 4) / CPL;  // key steps in flight
+  constexpr int STEP = KPW * U;
+  constexpr int W = CPL * E;
+  __shared__ long long pre[kPagedMaxBatch + 1], scan[kW];
+  __shared__ float red_m[kW][NQ], red_l[kW][NQ];
+  __shared__ __align__(16) float red_z[kW][NQ][256];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane / G, gl = lane % G;
+  const int d = a.d, v = a.v;
+  const int kch = d / E, vch = v / E;
+  const T* Q = static_cast<const T*>(a.Q);
+  const T* Kp = static_cast<const T*>(a.Kp);
+  const T* Vp = static_cast<const T*>(a.Vp);
+  unsigned bits = 0;
+  if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  PagedWalk w;
+  bool more = paged_begin<NQ, kUnit, 32 * kW>(a, pre, scan, w, bits);
+  while (more) {
+    int j0, j1;
+    const int n = paged_segment<kUnit>(w, j0, j1);
+    const int r0 = w.rt * NQ, rows = w.t.rows;
+    const int* trow = a.table + static_cast<size_t>(w.b) * a.max_pages;
+
+    // Rows of Q with scale * log2(e) folded in, and the keys that each allows.
+    float qf[NQ][W];
+    int lo[NQ], hi[NQ];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const int r = r0 + (q < rows ? q : 0), i = r / a.G;
+      paged_row_span(a, w.s, i, lo[q], hi[q]);
+      if (q < rows && lo[q] >= hi[q] && w.rem == 0 && !a.initL) bits |= kStatusEmptyRow;
+      const T* qr = Q + (w.s.s0 + i) * a.q_stride + (w.h * a.G + r - i * a.G) * d;
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) {
+        const int pc = gl + c * G;
+        float f[E];
+        if (pc < kch) {
+          Row16<T>::unpack(*reinterpret_cast<const uint4*>(qr + pc * E), f);
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e) f[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) qf[q][c * E + e] = f[e] * a.sl2;
+      }
+    }
+    float m[NQ], l[NQ], z[NQ][W];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      m[q] = -INFINITY;
+      l[q] = 0.f;
+#pragma unroll
+      for (int e = 0; e < W; ++e) z[q][e] = 0.f;
+    }
+
+    for (int jb = j0 + warp * STEP; jb < j1; jb += kW * STEP) {
+      uint4 kr[U][CPL], vr[U][CPL];
+      bool have[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int key = jb + u * KPW + g;
+        long long row = -1;
+        if (key < j1) {
+          row = paged_key_row(a, trow, w.h, key);
+          if (row < 0) bits |= kStatusBadPage;
+        }
+        have[u] = row >= 0;
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+          const int pc = gl + c * G;
+          kr[u][c] = have[u] && pc < kch ? ldg_once16(Kp + row * d + pc * E) : make_uint4(0u, 0u, 0u, 0u);
+          vr[u][c] = have[u] && pc < vch ? ldg_once16(Vp + row * v + pc * E) : make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        if (q >= rows) break;
+        float s[U];
+        bool ok[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float acc0 = 0.f, acc1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < CPL; ++c) {
+            float f[E];
+            Row16<T>::unpack(kr[u][c], f);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+              acc0 = fmaf(qf[q][c * E + e], f[e], acc0);
+              acc1 = fmaf(qf[q][c * E + e + 1], f[e + 1], acc1);
+            }
+          }
+          float part = acc0 + acc1;
+#pragma unroll
+          for (int o = G / 2; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
+          const int key = jb + u * KPW + g;
+          ok[u] = have[u] && key >= lo[q] && key < hi[q];
+          s[u] = ok[u] ? part : -INFINITY;
+        }
+        float mx = m[q];
+#pragma unroll
+        for (int u = 0; u < U; ++u) mx = fmaxf(mx, s[u]);
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        const float alpha = pexp2(m[q] - ref);
+        float psum = 0.f;
+#pragma unroll
+        for (int e = 0; e < W; ++e) z[q][e] *= alpha;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float p = pexp2(s[u] - ref);
+          psum += p;
+          if (ok[u]) {  // a key that this row does not allow leaves no trace, whatever its value
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+              float f[E];
+              Row16<T>::unpack(vr[u][c], f);
+#pragma unroll
+              for (int e = 0; e < E; ++e) z[q][c * E + e] = fmaf(p, f[e], z[q][c * E + e]);
+            }
+          }
+        }
+        l[q] = l[q] * alpha + psum;
+        m[q] = mx;
+      }
+    }
+
+    // Groups of the warp, then warps.
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      float M = m[q];
+#pragma unroll
+      for (int o = G; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+      const float f = M == -INFINITY ? 0.f : pexp2(m[q] - M);
+      float lq = l[q] * f;
+#pragma unroll
+      for (int o = G; o < 32; o <<= 1) lq += __shfl_xor_sync(0xFFFFFFFFu, lq, o);
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        float ze = z[q][e] * f;
+#pragma unroll
+        for (int o = G; o < 32; o <<= 1) ze += __shfl_xor_sync(0xFFFFFFFFu, ze, o);
+        z[q][e] = ze;
+      }
+      if (q < rows && lane < G) {
+        if (lane == 0) {
+          red_m[warp][q] = M;
+          red_l[warp][q] = lq;
+        }
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+          const int pc = gl + c * G;
+          if (pc < vch)
+#pragma unroll
+            for (int e = 0; e < E; ++e) red_z[warp][q][pc * E + e] = z[q][c * E + e];
+        }
+      }
+    }
+    const int slot = paged_slot(a, w, n);
+    __syncthreads();
+    for (int idx = threadIdx.x; idx < rows * v; idx += 32 * kW) {
+      const int q = idx / v, col = idx - q * v;
+      float M = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kW; ++k) M = fmaxf(M, red_m[k][q]);
+      float zc = 0.f, lq = 0.f;
+      if (M != -INFINITY) {
+#pragma unroll
+        for (int k = 0; k < kW; ++k) {
+          const float f = pexp2(red_m[k][q] - M);
+          zc = fmaf(f, red_z[k][q][col], zc);
+          lq = fmaf(f, red_l[k][q], lq);
+        }
+      }
+      if (slot < 0) {
+        const size_t row = paged_out_row(a, w.s, w.h, r0 + q);
+        const PagedScale f = paged_finish(a, row, M, lq);
+        paged_store(a, row, col, paged_join(a, f, row, col, zc));
+        if (col == 0) a.L[row] = f.L;
+      } else {
+        const size_t row = static_cast<size_t>(slot) * NQ + q;
+        a.pz[row * v + col] = zc;
+        if (col == 0) {
+          a.pm[row] = M;
+          a.pl[row] = lq;
+        }
+      }
+    }
+    more = paged_next<NQ, kUnit>(a, w, n);
+    __syncthreads();  // the joined rows are read before the next segment's
+  }
+  const unsigned all = (__syncthreads_or(bits & kStatusEmptyRow) ? kStatusEmptyRow : 0u) |
+                       (__syncthreads_or(bits & kStatusBadPage) ? kStatusBadPage : 0u);
+  if (threadIdx.x == 0) a.flags[blockIdx.x] = all;
+}
+
+// Row r of the tile that CTA c of the attention launch starts and others end:
+// the star merge of its pieces.  One CTA of four warps a row; the warps share
+// the pieces.  CTA (0, 0) also joins the status bits of every CTA.
+constexpr int kMergeW = 4;
+
+template <int RT>
+__global__ void __launch_bounds__(32 * kMergeW) paged_merge_kernel(const PagedArgs a) {
+  __shared__ float red_l[kMergeW], red_m[kMergeW];
+  __shared__ __align__(16) float red_z[kMergeW][256];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (a.status && blockIdx.x == 0 && blockIdx.y == 0) {
+    unsigned bits = 0;
+    for (int k = threadIdx.x; k < a.n_flags; k += 32 * kMergeW) bits |= a.flags0[k];
+    const unsigned all = (__syncthreads_or(bits & kStatusEmptyRow) ? kStatusEmptyRow : 0u) |
+                         (__syncthreads_or(bits & kStatusBadPage) ? kStatusBadPage : 0u) |
+                         (__syncthreads_or(bits & kStatusTimeout) ? kStatusTimeout : 0u);
+    if (threadIdx.x == 0) *a.status = all;
+  }
+  const int c = blockIdx.x, q = blockIdx.y;
+  const int4 t = a.desc[c];
+  if (t.w == 0) return;
+  const PagedSeq s = paged_seq(a, t.x);
+  const int r = t.z * RT + q;
+  if (r >= s.nq * a.G) return;
+  const int v = a.v;
+  // Piece 0 is slot 2c + 1, piece k > 0 slot 2 (c + k).
+  auto at = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * RT + q; };
+  float M = -INFINITY;
+  for (int k = threadIdx.x; k < t.w; k += 32 * kMergeW) M = fmaxf(M, a.pm[at(k)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  if (lane == 0) red_m[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kMergeW; ++k) M = fmaxf(M, red_m[k]);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float l = 0.f;
+  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
+  for (int k = warp; k < t.w; k += kMergeW) {
+    const size_t row = at(k);
+    const float f = pexp2(a.pm[row] - ref);
+    l = fmaf(f, a.pl[row], l);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int col = 4 * lane + 128 * x;
+      if (col >= v) break;
+      const float4 z = *reinterpret_cast<const float4*>(a.pz + row * v + col);
+      acc[x].x = fmaf(f, z.x, acc[x].x);
+      acc[x].y = fmaf(f, z.y, acc[x].y);
+      acc[x].z = fmaf(f, z.z, acc[x].z);
+      acc[x].w = fmaf(f, z.w, acc[x].w);
+    }
+  }
+  if (lane == 0) red_l[warp] = l;
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    if (4 * lane + 128 * x < v) *reinterpret_cast<float4*>(&red_z[warp][4 * lane + 128 * x]) = acc[x];
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int k = 0; k < kMergeW; ++k) l += red_l[k];
+  const size_t row = paged_out_row(a, s, t.y, r);
+  const PagedScale f = paged_finish(a, row, M, l);
+  for (int col = threadIdx.x; col < v; col += 32 * kMergeW) {
+    float z = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMergeW; ++k) z += red_z[k][col];
+    paged_store(a, row, col, paged_join(a, f, row, col, z));
+  }
+  if (threadIdx.x == 0) a.L[row] = f.L;
+}
+
+template <typename T, int G, int CPL>
+cudaError_t simt_launch(const PagedArgs& a, bool one_row, cudaStream_t s) {
+  before_launch(kKernPaged, s);
+  if (one_row) paged_simt_kernel<T, G, CPL, 1><<<a.ctas, 32 * kW, 0, s>>>(a);
+  else paged_simt_kernel<T, G, CPL, 4><<<a.ctas, 32 * kW, 0, s>>>(a);
+  after_launch(kKernPaged, s);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+PagedKernel paged_simt_kernel(const PagedArgs& a, bool one_row) {
+  (void)a;
+  return {one_row ? 1 : 4, 4 * 152, 256};
+}
+
+cudaError_t launch_paged_simt(const PagedArgs& a, bool one_row, cudaStream_t s) {
+  const int bytes = (a.d > a.v ? a.d : a.v) * (a.dtype == kF32 ? 4 : 2);
+  if (a.dtype == kF32) {
+    if (bytes <= 128) return simt_launch<float, 8, 1>(a, one_row, s);
+    if (bytes <= 256) return simt_launch<float, 16, 1>(a, one_row, s);
+    if (bytes <= 512) return simt_launch<float, 32, 1>(a, one_row, s);
+    return simt_launch<float, 32, 2>(a, one_row, s);
+  }
+  if (bytes <= 128) return simt_launch<__nv_bfloat16, 8, 1>(a, one_row, s);
+  if (bytes <= 256) return simt_launch<__nv_bfloat16, 16, 1>(a, one_row, s);
+  return simt_launch<__nv_bfloat16, 32, 1>(a, one_row, s);
+}
+
+cudaError_t launch_paged_merge(const PagedArgs& a, int rt, cudaStream_t s) {
+  before_launch(kKernPagedMerge, s);
+  const dim3 grid(a.ctas, rt);
+  if (rt == 1) paged_merge_kernel<1><<<grid, 32 * kMergeW, 0, s>>>(a);
+  else if (rt == 4) paged_merge_kernel<4><<<grid, 32 * kMergeW, 0, s>>>(a);
+  else return cudaErrorInvalidValue;
+  after_launch(kKernPagedMerge, s);
+  return cudaGetLastError();
+}
+
+}  // namespace exattn

@@ -1,0 +1,324 @@
+// Attention over a paged key/value cache: the problem, the way its work is
+// shared out over the CTAs of one launch, and the two ways a row leaves it.
+//
+// Sequence b owns the packed tokens s0 .. s0 + nq - 1 and len cached keys, of
+// which its tokens are the last nq; token i sits at position len - nq + i.  The
+// group = heads / kv_heads query heads of one key head read the same keys, so
+// the rows of (b, key head h) are the nq * group pairs (i, g), row = i * group + g.
+//
+// Work.  A row tile is kRT consecutive rows of one (b, h); its keys, from the
+// first that any of its rows allows to the last, are cut at multiples of
+// kUnitKeys into units.  All units of the launch stand in one line, ordered by
+// (b, h, row tile, key), and CTA c takes units [c W, (c + 1) W), W = ceil(total
+// / CTAs): every CTA reads the same number of keys, however unequal the lengths
+// are and without the host knowing them (they are read on the device, so a
+// captured launch follows them).  A CTA's run of units is a list of segments,
+// one for each row tile that it touches.  A segment that holds all of its row
+// tile's units writes Y and L; any other writes its summary (m, l, z) of
+// "Exact tiled softmax attention with block-recomputed vector-Jacobian
+// products", Forward procedure, to a slot of the workspace: slot 2c + 1 when
+// it starts the row tile, slot 2c when it continues one (a CTA has at most one
+// of each), and paged_merge_kernel joins the slots with the star rule.
+#pragma once
+
+#include <math.h>
+
+#include "common.cuh"
+
+namespace exattn {
+
+constexpr int kPagedMaxBatch = 1024;  // prefix sums of the units stay in shared memory
+
+struct PagedArgs {
+  const void* Q;
+  const void* Kp;
+  const void* Vp;
+  const int* table;   // [B][max_pages]
+  const int* lens;    // [B], or null: fixed_len for every sequence
+  const int* starts;  // [B + 1], or null: T / B tokens for every sequence
+  int fixed_len;
+  int B, T, Hk, G, d, v, dtype;
+  int lps;  // log2(page_size)
+  int num_pages, max_pages;
+  int mask_kind, window;
+  float sl2;  // scale * log2(e)
+  long long q_stride;  // elements between tokens of Q
+  void* Y;             // [T][Hk * G][v] of dtype, or null: Yf
+  float* Yf;           // the same in fp32
+  float* L;            // [T][Hk * G], natural log
+  // The rows' summary over keys already attended to (a shared prefix): Y and L
+  // of those keys alone; null: none.
+  const float* initY;
+  const float* initL;
+  // Workspace.
+  unsigned* status;  // written by the merge kernel; null: left for a later launch
+  unsigned* flags;   // [n_flags] status bits, one word for each CTA of each launch
+  int n_flags;       // words that the merge kernel joins (from flags0)
+  const unsigned* flags0;
+  int4* desc;  // [ctas] of CTA c: (b, h, row tile, parts) of the tile it starts and others end
+  float* pm;   // [2 ctas][RT] exp2 domain
+  float* pl;   // [2 ctas][RT]
+  float* pz;   // [2 ctas][RT][v]
+  int ctas;
+};
+
+struct PagedSeq {
+  int s0, nq, len;
+  bool bad;  // the caller's numbers do not fit (they are clamped)
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int b) {
+  PagedSeq s;
+  s.bad = false;
+  if (a.starts) {
+    const int x = __ldg(a.starts + b), y = __ldg(a.starts + b + 1);
+    s.s0 = min(max(x, 0), a.T);
+    const int s1 = min(max(y, s.s0), a.T);
+    s.nq = s1 - s.s0;
+    s.bad = x != s.s0 || y != s1;
+  } else {
+    s.nq = a.T / a.B;
+    s.s0 = b * s.nq;
+  }
+  const int n = a.lens ? __ldg(a.lens + b) : a.fixed_len;
+  s.len = min(max(n, 0), a.max_pages << a.lps);
+  s.bad |= s.len != n;
+  return s;
+}
+
+// Keys [lo, hi) that row token i allows (an empty range is lo >= hi).
+__device__ __forceinline__ void paged_row_span(const PagedArgs& a, const PagedSeq& s, int i, int& lo,
+                                               int& hi) {
+  lo = 0;
+  hi = s.len;
+  const int pos = s.len - s.nq + i;
+  if (a.mask_kind != kMaskNone) hi = min(hi, pos + 1);
+  if (a.mask_kind == kMaskWindow) lo = max(0, pos + 1 - a.window);
+}
+
+// A row tile's rows and keys: units [kt0, kt0 + cnt), keys [lo, hi).
+struct PagedTile {
+  int rows, i0, i1;  // rows in the tile, first and last token
+  int lo, hi, kt0, cnt;
+};
+
+template <int RT, int UK>
+__device__ __forceinline__ PagedTile paged_tile(const PagedArgs& a, const PagedSeq& s, int rt) {
+  PagedTile t;
+  const int r0 = rt * RT, all = s.nq * a.G;
+  t.rows = min(RT, all - r0);
+  t.i0 = r0 / a.G;
+  t.i1 = (r0 + t.rows - 1) / a.G;
+  int x;
+  paged_row_span(a, s, t.i0, t.lo, x);
+  paged_row_span(a, s, t.i1, x, t.hi);
+  if (t.hi <= t.lo) t.hi = t.lo = 0;
+  t.kt0 = t.lo / UK;
+  t.cnt = max(1, (t.hi + UK - 1) / UK - t.kt0);  // a tile without keys still writes its rows
+  return t;
+}
+
+// The CTA's place in the line of units.  `pre` (shared, kPagedMaxBatch + 1
+// words) receives the number of units before each sequence.
+struct PagedWalk {
+  long long u, end, total, w;  // next unit, the CTA's end, all units, units for each CTA
+  int b, h, rt, rem;           // of unit u: sequence, key head, row tile, unit in the tile
+  PagedSeq s;
+  PagedTile t;
+  int tiles;  // row tiles of (b, h)
+};
+
+template <int RT, int UK>
+__device__ __forceinline__ long long paged_units(const PagedArgs& a, const PagedSeq& s) {
+  const int tiles = (s.nq * a.G + RT - 1) / RT;
+  long long u = 0;
+  for (int rt = 0; rt < tiles; ++rt) u += paged_tile<RT, UK>(a, s, rt).cnt;
+  return u * a.Hk;
+}
+
+// All threads; returns false when the CTA has no unit.  Status bits that the
+// caller's numbers raise go to `bits` (of CTA 0).
+template <int RT, int UK, int NT>
+__device__ __forceinline__ bool paged_begin(const PagedArgs& a, long long* pre, long long* scan,
+                                            PagedWalk& w, unsigned& bits) {
+  const int tid = threadIdx.x;
+  const int per = (a.B + NT - 1) / NT;
+  long long mine = 0;
+  bool bad = false;
+  for (int k = 0; k < per; ++k) {
+    const int b = tid * per + k;
+    if (b >= a.B) break;
+    const PagedSeq s = paged_seq(a, b);
+    bad |= s.bad;
+    pre[b + 1] = mine += paged_units<RT, UK>(a, s);
+  }
+  // Exclusive sum of `mine` over the threads.
+  const int lane = tid & 31, warp = tid >> 5;
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) scan[warp] = inc;
+  const int any_bad = __syncthreads_or(bad);
+  if (any_bad && blockIdx.x == 0) bits |= kStatusBadPage;
+  long long before = inc - mine;
+  for (int k = 0; k < warp; ++k) before += scan[k];
+  for (int k = 0; k < per; ++k) {
+    const int b = tid * per + k;
+    if (b >= a.B) break;
+    pre[b + 1] += before;
+  }
+  if (tid == 0) pre[0] = 0;
+  __syncthreads();
+  w.total = pre[a.B];
+  w.w = (w.total + a.ctas - 1) / a.ctas;
+  w.u = min(w.total, w.w * blockIdx.x);
+  w.end = min(w.total, w.u + w.w);
+  if (w.u >= w.end) return false;
+  int b0 = 0, b1 = a.B;  // pre[b0] <= u < pre[b1]
+  while (b1 - b0 > 1) {
+    const int mid = (b0 + b1) >> 1;
+    if (pre[mid] <= w.u) b0 = mid;
+    else b1 = mid;
+  }
+  w.b = b0;
+  w.s = paged_seq(a, w.b);
+  w.tiles = (w.s.nq * a.G + RT - 1) / RT;
+  const long long per_head = (pre[b0 + 1] - pre[b0]) / a.Hk;
+  const long long local = w.u - pre[b0];
+  w.h = static_cast<int>(local / per_head);
+  long long rem = local - w.h * per_head;
+  w.rt = 0;
+  w.t = paged_tile<RT, UK>(a, w.s, 0);
+  while (rem >= w.t.cnt) {
+    rem -= w.t.cnt;
+    w.t = paged_tile<RT, UK>(a, w.s, ++w.rt);
+  }
+  w.rem = static_cast<int>(rem);
+  return true;
+}
+
+// Past the segment of `n` units that starts at w.u; false at the CTA's end.
+template <int RT, int UK>
+__device__ __forceinline__ bool paged_next(const PagedArgs& a, PagedWalk& w, int n) {
+  w.u += n;
+  if (w.u >= w.end) return false;
+  w.rem = 0;
+  if (++w.rt == w.tiles) {
+    w.rt = 0;
+    if (++w.h == a.Hk) {
+      w.h = 0;
+      do {  // a sequence without tokens has no units
+        ++w.b;
+        w.s = paged_seq(a, w.b);
+      } while (w.s.nq == 0);
+      w.tiles = (w.s.nq * a.G + RT - 1) / RT;
+    }
+  }
+  w.t = paged_tile<RT, UK>(a, w.s, w.rt);
+  return true;
+}
+
+// Units of the segment that starts at w.u, and the keys they stand for.
+template <int UK>
+__device__ __forceinline__ int paged_segment(const PagedWalk& w, int& j0, int& j1) {
+  const int n = static_cast<int>(min(static_cast<long long>(w.t.cnt - w.rem), w.end - w.u));
+  const int kt = w.t.kt0 + w.rem;
+  j0 = max(w.t.lo, kt * UK);
+  j1 = min(w.t.hi, (kt + n) * UK);
+  return n;
+}
+
+// Where the summary of the CTA's present segment goes: its slot, or -1 when the
+// segment holds the whole row tile.  Thread 0 describes a tile that starts here
+// and ends in a later CTA; parts: the CTAs that hold a piece of it.
+__device__ __forceinline__ int paged_slot(const PagedArgs& a, const PagedWalk& w, int n) {
+  const int c = blockIdx.x;
+  if (w.rem > 0) return 2 * c;
+  if (n == w.t.cnt) return -1;
+  if (threadIdx.x == 0) {
+    const long long last = w.u + w.t.cnt - 1;
+    a.desc[c] = make_int4(w.b, w.h, w.rt, static_cast<int>(last / w.w) - c + 1);
+  }
+  return 2 * c + 1;
+}
+
+// Row r (of the tile's first row r0) as an index into [T][heads].
+__device__ __forceinline__ size_t paged_out_row(const PagedArgs& a, const PagedSeq& s, int h, int r) {
+  const int i = r / a.G;
+  return static_cast<size_t>(s.s0 + i) * (a.Hk * a.G) + h * a.G + (r - i * a.G);
+}
+
+// The two factors of a finished row (m in the exp2 domain, l): Y = z * fz +
+// initY * fi, and L is stored.  Empty rows give zeros and -inf.
+struct PagedScale {
+  float fz, fi, L;
+};
+__device__ __forceinline__ PagedScale paged_finish(const PagedArgs& a, size_t row, float m, float l) {
+  PagedScale f{0.f, 0.f, -INFINITY};
+  const float Li = a.initL ? a.initL[row] : -INFINITY;
+  const bool own = l > 0.f || l != l;  // a NaN score stays one
+  if (!own && Li == -INFINITY) return f;
+  const float mi = Li * kLog2e;  // the prefix's summary: m = mi, l = 1
+  const float M = own ? fmaxf(m, mi) : mi;
+  const float cz = own ? exp2f(m - M) : 0.f;
+  const float ci = Li == -INFINITY ? 0.f : exp2f(mi - M);
+  const float total = (own ? l * cz : 0.f) + ci;
+  f.fz = cz / total;
+  f.fi = ci / total;
+  f.L = (M + log2f(total)) * kLn2;
+  return f;
+}
+
+// One element of a finished row from its unnormalised sum z.
+__device__ __forceinline__ float paged_join(const PagedArgs& a, const PagedScale& f, size_t row, int col,
+                                            float z) {
+  float y = z * f.fz;
+  if (a.initY) y = fmaf(a.initY[row * a.v + col], f.fi, y);
+  return y;
+}
+
+__device__ __forceinline__ void paged_store(const PagedArgs& a, size_t row, int col, float y) {
+  const size_t at = row * a.v + col;
+  if (a.Yf) a.Yf[at] = y;
+  else if (a.dtype == kF32) static_cast<float*>(a.Y)[at] = y;
+  else static_cast<__nv_bfloat16*>(a.Y)[at] = __float2bfloat16_rn(y);
+}
+
+// The row of page table entries of sequence b, and the row of a key in the
+// pool (pages [num_pages][Hk][page_size][width]); -1 for a page outside it.
+__device__ __forceinline__ long long paged_key_row(const PagedArgs& a, const int* trow, int h, int key) {
+  const int page = __ldg(trow + (key >> a.lps));
+  if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages)) return -1;
+  return ((static_cast<long long>(page) * a.Hk + h) << a.lps) + (key & ((1 << a.lps) - 1));
+}
+
+// Host side.
+struct PagedKernel {
+  int rt, ctas, vw;  // rows of a tile, CTAs of the launch
+};
+cudaError_t launch_paged_simt(const PagedArgs& a, bool one_row, cudaStream_t s);
+PagedKernel paged_simt_kernel(const PagedArgs& a, bool one_row);
+cudaError_t launch_paged_merge(const PagedArgs& a, int rt, cudaStream_t s);
+
+struct AppendArgs {
+  const void* q;  // may be null
+  const void* k;
+  const void* v;
+  const int* starts;
+  const int* table;
+  const int* lens;
+  const float* inv_freq;
+  int pairs, interleaved, pos_offset;
+  int B, T, H, Hk, d, vw, dtype, lps, num_pages, max_pages;
+  long long qs, ks, vs;
+  void* q_out;
+  void* kp;
+  void* vp;
+  unsigned* status;
+};
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
+
+}  // namespace exattn

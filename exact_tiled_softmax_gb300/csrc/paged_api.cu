@@ -1,0 +1,298 @@
+// The C ABI of the paged-cache operators (include/exattn.h): argument checks,
+// workspace layout and kernel dispatch.  No memory is allocated here.
+#include <stdint.h>
+
+#include "../../include/exattn.h"
+#include "paged.cuh"
+
+namespace exattn {
+int append_max_pairs();
+extern thread_local char g_last_error[256];
+}  // namespace exattn
+
+namespace {
+
+using namespace exattn;
+
+constexpr int kMaxWidth = 256;
+constexpr int kMaxTokens = 1 << 20;
+constexpr int kMaxKeys = 1 << 30;
+constexpr int kMaxPageSize = 1024;
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+int log2_of(int x) {
+  int k = 0;
+  while ((1 << k) < x) ++k;
+  return k;
+}
+
+int check_paged(const exattn_paged_shape* s) {
+  if (!s) return EXATTN_INVALID_ARG;
+  if (s->batch < 1 || s->tokens < 1 || s->heads < 1 || s->kv_heads < 1 || s->d < 1 || s->v < 1 ||
+      s->page_size < 1 || s->num_pages < 1 || s->max_pages < 1)
+    return EXATTN_INVALID_ARG;
+  if (s->dtype != EXATTN_F32 && s->dtype != EXATTN_BF16) return EXATTN_INVALID_ARG;
+  if (s->heads % s->kv_heads != 0) return EXATTN_INVALID_ARG;
+  const int per16 = s->dtype == EXATTN_BF16 ? 8 : 4;
+  const long long qw = (long long)s->heads * s->d, kw = (long long)s->kv_heads * s->d,
+                  vw = (long long)s->kv_heads * s->v;
+  if ((s->q_stride != 0 && s->q_stride < qw) || (s->k_stride != 0 && s->k_stride < kw) ||
+      (s->v_stride != 0 && s->v_stride < vw))
+    return EXATTN_INVALID_ARG;
+  if (s->d > kMaxWidth || s->v > kMaxWidth || s->d % per16 != 0 || s->v % per16 != 0)
+    return EXATTN_UNSUPPORTED;
+  if (s->q_stride % per16 != 0 || s->k_stride % per16 != 0 || s->v_stride % per16 != 0)
+    return EXATTN_MISALIGNED;
+  if (s->page_size > kMaxPageSize || (s->page_size & (s->page_size - 1)) != 0) return EXATTN_UNSUPPORTED;
+  if (s->batch > kPagedMaxBatch || s->tokens > kMaxTokens || s->heads > 65535 ||
+      (long long)s->tokens * s->heads > INT32_MAX ||
+      (long long)s->max_pages * s->page_size > kMaxKeys)
+    return EXATTN_UNSUPPORTED;
+  return EXATTN_OK;
+}
+
+// The kernel of a call, from the shape and the process-wide path alone.
+struct Choice {
+  bool one_row;
+  PagedKernel k;
+};
+
+Choice choose(const PagedArgs& a) {
+  Choice c;
+  c.one_row = !a.starts && a.T == a.B && a.G == 1;
+  c.k = paged_simt_kernel(a, c.one_row);
+  return c;
+}
+
+// Workspace of one attention launch and its merge: flags | tile descriptions |
+// m | l | z of the slots.
+size_t pass_bytes(const PagedKernel& k, int v) {
+  const size_t rows = 2 * (size_t)k.ctas * k.rt;
+  return align256(sizeof(int4) * (size_t)k.ctas) + 2 * align256(sizeof(float) * rows) +
+         align256(sizeof(float) * rows * v);
+}
+constexpr size_t kFlagBytes = 8192;  // status bits of the CTAs of two passes (at most 2048)
+
+// The most that any kernel choice of this shape needs (the path may change
+// between the query and the call, and q_starts is not part of the shape).
+size_t most_bytes(const exattn_paged_shape* s) {
+  PagedArgs a{};
+  a.v = s->v;
+  size_t most = 0;
+  for (const bool one : {true, false}) {
+    const size_t x = pass_bytes(paged_simt_kernel(a, one), s->v);
+    most = x > most ? x : most;
+  }
+  return most;
+}
+
+char* place_pass(PagedArgs& a, const PagedKernel& k, char* ws) {
+  const size_t rows = 2 * (size_t)k.ctas * k.rt;
+  a.ctas = k.ctas;
+  a.desc = reinterpret_cast<int4*>(ws);
+  ws += align256(sizeof(int4) * (size_t)k.ctas);
+  a.pm = reinterpret_cast<float*>(ws);
+  ws += align256(sizeof(float) * rows);
+  a.pl = reinterpret_cast<float*>(ws);
+  ws += align256(sizeof(float) * rows);
+  a.pz = reinterpret_cast<float*>(ws);
+  return ws + align256(sizeof(float) * rows * a.v);
+}
+
+PagedArgs make_args(const exattn_paged_shape* s, const void* Q, const void* Kp, const void* Vp,
+                    const int* table, const int* lens, const int* starts, float scale, int mask_kind,
+                    int window, void* Y, float* L) {
+  PagedArgs a{};
+  a.Q = Q;
+  a.Kp = Kp;
+  a.Vp = Vp;
+  a.table = table;
+  a.lens = lens;
+  a.starts = starts;
+  a.B = s->batch;
+  a.T = s->tokens;
+  a.Hk = s->kv_heads;
+  a.G = s->heads / s->kv_heads;
+  a.d = s->d;
+  a.v = s->v;
+  a.dtype = s->dtype;
+  a.lps = log2_of(s->page_size);
+  a.num_pages = s->num_pages;
+  a.max_pages = s->max_pages;
+  a.mask_kind = mask_kind;
+  a.window = mask_kind == EXATTN_MASK_WINDOW ? (window < kMaxKeys ? window : kMaxKeys) : 0;
+  a.sl2 = scale * kLog2e;
+  a.q_stride = s->q_stride ? s->q_stride : (long long)s->heads * s->d;
+  a.Y = Y;
+  a.L = L;
+  return a;
+}
+
+int cuda_result(cudaError_t e, const char* where) {
+  if (e == cudaSuccess) return EXATTN_OK;
+  record_error(where, static_cast<int>(e), cudaGetErrorString(e));
+  return EXATTN_CUDA_ERROR;
+}
+
+cudaError_t run_pass(const PagedArgs& a, const Choice& c, cudaStream_t s) {
+  cudaError_t e = launch_paged_simt(a, c.one_row, s);
+  return e != cudaSuccess ? e : launch_paged_merge(a, c.k.rt, s);
+}
+
+int check_call(const exattn_paged_shape* shape, const void* Q, const void* Kp, const void* Vp,
+               const int* table, const int* lens, const int* starts, int mask_kind, int window,
+               const void* Y, const void* L, const void* workspace) {
+  if (mask_kind < EXATTN_MASK_NONE || mask_kind > EXATTN_MASK_BITMASK) return EXATTN_INVALID_ARG;
+  if (mask_kind == EXATTN_MASK_BITMASK) return EXATTN_UNSUPPORTED;
+  if (mask_kind == EXATTN_MASK_WINDOW && window < 1) return EXATTN_INVALID_ARG;
+  if (!Q || !Kp || !Vp || !table || !lens || !Y || !L || !workspace) return EXATTN_INVALID_ARG;
+  if (!starts && shape->tokens % shape->batch != 0) return EXATTN_INVALID_ARG;
+  if (!aligned(Q, 16) || !aligned(Kp, 16) || !aligned(Vp, 16) || !aligned(Y, 16) || !aligned(L, 16) ||
+      !aligned(table, 4) || !aligned(lens, 4) || !aligned(starts, 4) || !aligned(workspace, 256))
+    return EXATTN_MISALIGNED;
+  return EXATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t exattn_paged_workspace_size(const exattn_paged_shape* shape) {
+  if (check_paged(shape) != EXATTN_OK) return 0;
+  return kStatusBytes + kFlagBytes + most_bytes(shape);
+}
+
+size_t exattn_prefix_workspace_size(const exattn_paged_shape* shape) {
+  if (check_paged(shape) != EXATTN_OK) return 0;
+  const size_t rows = (size_t)shape->tokens * shape->heads;
+  return kStatusBytes + kFlagBytes + most_bytes(shape) + align256(sizeof(float) * rows) +
+         align256(sizeof(float) * rows * shape->v);
+}
+
+int attn_append_paged(const exattn_paged_shape* shape, const void* q, const void* k, const void* v,
+                      const int* page_table, const int* seq_lens, const int* q_starts,
+                      const float* inv_freq, int rot_pairs, int interleaved, int pos_offset,
+                      void* q_out, void* k_pages, void* v_pages, void* workspace,
+                      size_t workspace_bytes, void* cuda_stream) {
+  const int st = check_paged(shape);
+  if (st != EXATTN_OK) return st;
+  if (!k || !v || !page_table || !seq_lens || !k_pages || !v_pages || !workspace || (q && !q_out) ||
+      (rot_pairs > 0 && !inv_freq) || rot_pairs < 0 || 2 * (long long)rot_pairs > shape->d ||
+      pos_offset < 0)
+    return EXATTN_INVALID_ARG;
+  if (!q_starts && shape->tokens % shape->batch != 0) return EXATTN_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+      !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(page_table, 4) ||
+      !aligned(seq_lens, 4) || !aligned(q_starts, 4) || !aligned(inv_freq, 4) || !aligned(workspace, 256))
+    return EXATTN_MISALIGNED;
+  if (workspace_bytes < kStatusBytes) return EXATTN_WORKSPACE_TOO_SMALL;
+  g_last_error[0] = 0;
+  AppendArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.starts = q_starts;
+  a.table = page_table;
+  a.lens = seq_lens;
+  a.inv_freq = inv_freq;
+  a.pairs = rot_pairs;
+  a.interleaved = interleaved != 0;
+  a.pos_offset = pos_offset;
+  a.B = shape->batch;
+  a.T = shape->tokens;
+  a.H = shape->heads;
+  a.Hk = shape->kv_heads;
+  a.d = shape->d;
+  a.vw = shape->v;
+  a.dtype = shape->dtype;
+  a.lps = log2_of(shape->page_size);
+  a.num_pages = shape->num_pages;
+  a.max_pages = shape->max_pages;
+  a.qs = shape->q_stride ? shape->q_stride : (long long)shape->heads * shape->d;
+  a.ks = shape->k_stride ? shape->k_stride : (long long)shape->kv_heads * shape->d;
+  a.vs = shape->v_stride ? shape->v_stride : (long long)shape->kv_heads * shape->v;
+  a.q_out = q_out;
+  a.kp = k_pages;
+  a.vp = v_pages;
+  a.status = static_cast<unsigned*>(workspace);
+  return cuda_result(launch_append(a, static_cast<cudaStream_t>(cuda_stream)),
+                     "attn_append_paged: launch");
+}
+
+int attn_fwd_paged(const exattn_paged_shape* shape, const void* Q, const void* k_pages,
+                   const void* v_pages, const int* page_table, const int* seq_lens,
+                   const int* q_starts, float scale, int mask_kind, int window, void* Y, float* L,
+                   void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  int st = check_paged(shape);
+  if (st != EXATTN_OK) return st;
+  st = check_call(shape, Q, k_pages, v_pages, page_table, seq_lens, q_starts, mask_kind, window, Y, L,
+                  workspace);
+  if (st != EXATTN_OK) return st;
+  if (workspace_bytes < exattn_paged_workspace_size(shape)) return EXATTN_WORKSPACE_TOO_SMALL;
+  g_last_error[0] = 0;
+  char* ws = static_cast<char*>(workspace);
+  PagedArgs a = make_args(shape, Q, k_pages, v_pages, page_table, seq_lens, q_starts, scale, mask_kind,
+                          window, Y, L);
+  const Choice c = choose(a);
+  a.status = static_cast<unsigned*>(workspace);
+  a.flags = reinterpret_cast<unsigned*>(ws + kStatusBytes);
+  a.flags0 = a.flags;
+  a.n_flags = c.k.ctas;
+  place_pass(a, c.k, ws + kStatusBytes + kFlagBytes);
+  return cuda_result(run_pass(a, c, static_cast<cudaStream_t>(cuda_stream)), "attn_fwd_paged: launch");
+}
+
+int attn_fwd_prefix(const exattn_paged_shape* shape, const void* Q, const void* k_pages,
+                    const void* v_pages, const int* prefix_table, int prefix_len,
+                    const int* page_table, const int* seq_lens, const int* q_starts, float scale,
+                    int mask_kind, void* Y, float* L, void* workspace, size_t workspace_bytes,
+                    void* cuda_stream) {
+  int st = check_paged(shape);
+  if (st != EXATTN_OK) return st;
+  if (mask_kind == EXATTN_MASK_WINDOW) return EXATTN_UNSUPPORTED;
+  st = check_call(shape, Q, k_pages, v_pages, page_table, seq_lens, q_starts, mask_kind, 0, Y, L,
+                  workspace);
+  if (st != EXATTN_OK) return st;
+  if (prefix_len < 0 || (prefix_len > 0 && !prefix_table)) return EXATTN_INVALID_ARG;
+  if (prefix_len > kMaxKeys - kMaxPageSize) return EXATTN_UNSUPPORTED;
+  if (!aligned(prefix_table, 4)) return EXATTN_MISALIGNED;
+  if (workspace_bytes < exattn_prefix_workspace_size(shape)) return EXATTN_WORKSPACE_TOO_SMALL;
+  if (prefix_len == 0)
+    return attn_fwd_paged(shape, Q, k_pages, v_pages, page_table, seq_lens, q_starts, scale, mask_kind,
+                          0, Y, L, workspace, workspace_bytes, cuda_stream);
+  g_last_error[0] = 0;
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  char* ws = static_cast<char*>(workspace);
+  unsigned* flags = reinterpret_cast<unsigned*>(ws + kStatusBytes);
+  const size_t rows = (size_t)shape->tokens * shape->heads;
+  char* own = ws + kStatusBytes + kFlagBytes;  // the two passes follow one another: one area
+  char* init = own + most_bytes(shape);
+  // All tokens over the prefix, as one sequence without a mask.
+  PagedArgs p = make_args(shape, Q, k_pages, v_pages, prefix_table, nullptr, nullptr, scale,
+                          EXATTN_MASK_NONE, 0, nullptr, reinterpret_cast<float*>(init));
+  p.B = 1;
+  p.fixed_len = prefix_len;
+  p.max_pages = (prefix_len + shape->page_size - 1) / shape->page_size;
+  p.Yf = reinterpret_cast<float*>(init + align256(sizeof(float) * rows));
+  const Choice cp = choose(p);
+  p.flags = flags;
+  place_pass(p, cp.k, own);
+  int r = cuda_result(run_pass(p, cp, s), "attn_fwd_prefix: prefix launch");
+  if (r != EXATTN_OK) return r;
+  // Each sequence's own keys, joined with the prefix's rows.
+  PagedArgs a = make_args(shape, Q, k_pages, v_pages, page_table, seq_lens, q_starts, scale, mask_kind,
+                          0, Y, L);
+  const Choice c = choose(a);
+  a.initY = p.Yf;
+  a.initL = p.L;
+  a.status = static_cast<unsigned*>(workspace);
+  a.flags = flags + cp.k.ctas;
+  a.flags0 = flags;
+  a.n_flags = cp.k.ctas + c.k.ctas;
+  place_pass(a, c.k, own);
+  return cuda_result(run_pass(a, c, s), "attn_fwd_prefix: launch");
+}
+
+}  // extern "C"

@@ -70,7 +70,7 @@ enum exattn_mask_kind {
 };
 
 /* Return codes.  Host-side checks return 1-4 and 6 before queuing any work;
- * 5 and 7 are device-side conditions reported through the status word. */
+ * 5, 7 and 8 are device-side conditions reported through the status word. */
 enum exattn_status {
   EXATTN_OK = 0,
   EXATTN_INVALID_ARG = 1,        /* null pointer, non-positive size, bad mask kind/window */
@@ -79,7 +79,9 @@ enum exattn_status {
   EXATTN_WORKSPACE_TOO_SMALL = 4,
   EXATTN_EMPTY_ROW = 5,          /* some A_i was empty (status word) */
   EXATTN_CUDA_ERROR = 6,         /* a CUDA call or launch failed */
-  EXATTN_TIMEOUT = 7             /* a bounded wait inside a kernel gave up (status word) */
+  EXATTN_TIMEOUT = 7,            /* a bounded wait inside a kernel gave up (status word) */
+  EXATTN_BAD_PAGE = 8            /* paged cache: a length, a token range or a page entry does
+                                    not fit (status word) */
 };
 
 /* Problem shape.  batch, heads, n, d, v >= 1; dtype is an exattn_dtype. */
@@ -330,9 +332,105 @@ int attn_step_host(const exattn_shape* shape, const void* Q, const void* K, cons
                    void* Y, float* L, void* dQ, void* dK, void* dV, void* workspace,
                    size_t workspace_bytes, void* cuda_stream);
 
+/* ---------------------------------------------------------------------------
+ * A paged key/value cache: append, attention over it, attention behind a shared
+ * prefix.  None of the three has a counterpart in the pages that define the
+ * method; each row's attention is theirs, over keys that stand in pages.
+ *
+ * Pages.  k_pages is [num_pages][kv_heads][page_size][d], v_pages
+ * [num_pages][kv_heads][page_size][v], dense, of `dtype`.  Key j of sequence b is
+ * row j % page_size of page page_table[b * max_pages + j / page_size].  page_size
+ * is a power of two, at most 1024.  page_table (int32 [batch][max_pages]) and
+ * seq_lens (int32 [batch]) are device arrays that the kernels read, so a captured
+ * launch follows their contents.  Entries behind a sequence's last page, and
+ * with a window those before its first allowed key, are not read; a page may
+ * belong to several sequences.
+ *
+ * Tokens are packed: Q [tokens][heads][d], k [tokens][kv_heads][d],
+ * v [tokens][kv_heads][v].  q_stride, k_stride and v_stride are the elements from
+ * one token to the next (0: dense; a multiple of 16 bytes), for columns of one
+ * projection's output; Y [tokens][heads][v], L float32 [tokens][heads] and q_out
+ * [tokens][heads][d] are dense.  Sequence b owns tokens q_starts[b] ..
+ * q_starts[b + 1] - 1 (int32 device array [batch + 1]), possibly none; q_starts NULL
+ * means tokens / batch tokens each (tokens a multiple of batch).  Tokens that no
+ * sequence owns (a padded batch) are neither read into a result nor written: their
+ * rows of Y, L and q_out stay as they were.  seq_lens[b] counts the sequence's
+ * cached keys with its tokens, which are the last: token i of nq is at position
+ * seq_lens[b] - nq + i.  heads is a multiple of kv_heads; query head h reads key
+ * head h / (heads / kv_heads).
+ *
+ * Limits: batch <= 1024, tokens <= 2^20, max_pages * page_size <= 2^30, d, v <=
+ * 256 and rows of whole 16-byte pieces.  Masks: NONE, CAUSAL (keys up to the
+ * token's position) and WINDOW (the `window` keys that end there); a bitmask is
+ * EXATTN_UNSUPPORTED.
+ *
+ * Status word.  EXATTN_EMPTY_ROW: some row allows no key (Y = 0, L = -inf).
+ * EXATTN_BAD_PAGE: q_starts does not ascend inside [0, tokens], a seq_lens is
+ * outside [0, max_pages * page_size] (both are clamped), or an entry that was
+ * needed is outside [0, num_pages): its keys are left out, its tokens not
+ * written.  Nothing outside the caller's arrays is read or written.
+ * Ownership, streams and errors as for attn_fwd.
+ * ------------------------------------------------------------------------- */
+typedef struct exattn_paged_shape {
+  int batch;
+  int tokens;
+  int heads;
+  int kv_heads;
+  int d;
+  int v;
+  int dtype;
+  int page_size;
+  int num_pages;
+  int max_pages;
+  long long q_stride;
+  long long k_stride;
+  long long v_stride;
+} exattn_paged_shape;
+
+/* Workspace bytes: attn_append_paged and attn_fwd_paged take the first,
+ * attn_fwd_prefix the second; 0 if the shape is invalid. */
+size_t exattn_paged_workspace_size(const exattn_paged_shape* shape);
+size_t exattn_prefix_workspace_size(const exattn_paged_shape* shape);
+
+/* Writes every owned token's key and value to its position's page row, and
+ * rotates keys, and queries if q is not NULL (into q_out, which may be q itself
+ * when q is dense), by position: pair f of a row turns by
+ * (position + pos_offset) * inv_freq[f] radians, x' = x cos - y sin, y' = y cos +
+ * x sin, the angle reduced in 64 bits.  inv_freq is a float32 device array of rot_pairs
+ * values, 2 rot_pairs <= d (0: no rotation).  Pairs are columns (f, f + rot_pairs), or
+ * (2f, 2f + 1) if `interleaved`; columns from 2 rot_pairs on pass unchanged.
+ * pos_offset >= 0 counts tokens before the cache's first (a shared prefix).  No two
+ * tokens of a call may have the same place.  A token whose position is negative
+ * (seq_lens below its token count) or has no page is not written
+ * (EXATTN_BAD_PAGE); its query is rotated all the same. */
+int attn_append_paged(const exattn_paged_shape* shape, const void* q, const void* k, const void* v,
+                      const int* page_table, const int* seq_lens, const int* q_starts,
+                      const float* inv_freq, int rot_pairs, int interleaved, int pos_offset,
+                      void* q_out, void* k_pages, void* v_pages, void* workspace,
+                      size_t workspace_bytes, void* cuda_stream);
+
+/* Attention of every owned token over its sequence's cached keys. */
+int attn_fwd_paged(const exattn_paged_shape* shape, const void* Q, const void* k_pages,
+                   const void* v_pages, const int* page_table, const int* seq_lens,
+                   const int* q_starts, float scale, int mask_kind, int window, void* Y, float* L,
+                   void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* The same where every sequence begins with one common prefix of prefix_len keys
+ * (a host value), key j in row j % page_size of page prefix_table[j / page_size]
+ * (int32 device array of at least ceil(prefix_len / page_size) entries).  The prefix's keys
+ * are read once for all tokens, which all allow every one of them; page_table and
+ * seq_lens describe each sequence's own keys behind it, under mask_kind NONE or
+ * CAUSAL (WINDOW is EXATTN_UNSUPPORTED).  prefix_len 0 is attn_fwd_paged.  Rotated
+ * keys behind the prefix are appended with pos_offset = prefix_len. */
+int attn_fwd_prefix(const exattn_paged_shape* shape, const void* Q, const void* k_pages,
+                    const void* v_pages, const int* prefix_table, int prefix_len,
+                    const int* page_table, const int* seq_lens, const int* q_starts, float scale,
+                    int mask_kind, void* Y, float* L, void* workspace, size_t workspace_bytes,
+                    void* cuda_stream);
+
 /* Waits for `cuda_stream`, then reads the status word of `workspace` (the
  * workspace of the last call queued on it).  Returns EXATTN_OK,
- * EXATTN_EMPTY_ROW, EXATTN_TIMEOUT or EXATTN_CUDA_ERROR. */
+ * EXATTN_EMPTY_ROW, EXATTN_TIMEOUT, EXATTN_BAD_PAGE or EXATTN_CUDA_ERROR. */
 int exattn_device_status(const void* workspace, void* cuda_stream);
 
 /* Profiling aid.  Kernels of the library, by role. */
@@ -348,7 +446,10 @@ enum exattn_kernel {
   EXATTN_KERNEL_SPLIT_PARTIAL = 5, /* per-chunk summaries of attn_fwd_splitkv */
   EXATTN_KERNEL_SPLIT_MERGE = 6,   /* the merge kernel of attn_fwd_splitkv (shapes
                                      whose chunks do not merge themselves) */
-  EXATTN_KERNEL_SPLIT32 = 7        /* the tf32 hi / lo split of K and V (fp32 forward) */
+  EXATTN_KERNEL_SPLIT32 = 7,       /* the tf32 hi / lo split of K and V (fp32 forward) */
+  EXATTN_KERNEL_APPEND = 8,        /* attn_append_paged */
+  EXATTN_KERNEL_PAGED = 9,         /* the attention kernel of attn_fwd_paged */
+  EXATTN_KERNEL_PAGED_MERGE = 10   /* its merge of the rows that CTAs share */
 };
 
 /* One-shot: on the next launch of kernel `which` (an exattn_kernel), record

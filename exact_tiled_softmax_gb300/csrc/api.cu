@@ -134,6 +134,8 @@ void after_launch(int role, cudaStream_t s) {
   if (ev) cudaEventRecord(static_cast<cudaEvent_t>(ev), s);
 }
 
+int current_path() { return g_path.load(); }
+
 }  // namespace exattn
 
 extern "C" {

@@ -248,9 +248,7 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
     more = paged_next<NQ, kUnit>(a, w, n);
     __syncthreads();  // the joined rows are read before the next segment's
   }
-  const unsigned all = (__syncthreads_or(bits & kStatusEmptyRow) ? kStatusEmptyRow : 0u) |
-                       (__syncthreads_or(bits & kStatusBadPage) ? kStatusBadPage : 0u);
-  if (threadIdx.x == 0) a.flags[blockIdx.x] = all;
+  paged_end(a, bits);
 }
 
 // Row r of the tile that CTA c of the attention launch starts and others end:
@@ -337,10 +335,7 @@ cudaError_t simt_launch(const PagedArgs& a, bool one_row, cudaStream_t s) {
 
 }  // namespace
 
-PagedKernel paged_simt_kernel(const PagedArgs& a, bool one_row) {
-  (void)a;
-  return {one_row ? 1 : 4, 4 * 152, 256};
-}
+PagedKernel paged_simt_kernel(bool one_row) { return {one_row ? 1 : 4, 4 * 152}; }
 
 cudaError_t launch_paged_simt(const PagedArgs& a, bool one_row, cudaStream_t s) {
   const int bytes = (a.d > a.v ? a.d : a.v) * (a.dtype == kF32 ? 4 : 2);
@@ -360,6 +355,7 @@ cudaError_t launch_paged_merge(const PagedArgs& a, int rt, cudaStream_t s) {
   const dim3 grid(a.ctas, rt);
   if (rt == 1) paged_merge_kernel<1><<<grid, 32 * kMergeW, 0, s>>>(a);
   else if (rt == 4) paged_merge_kernel<4><<<grid, 32 * kMergeW, 0, s>>>(a);
+  else if (rt == 16) paged_merge_kernel<16><<<grid, 32 * kMergeW, 0, s>>>(a);
   else return cudaErrorInvalidValue;
   after_launch(kKernPagedMerge, s);
   return cudaGetLastError();

@@ -287,6 +287,38 @@ __device__ __forceinline__ void paged_store(const PagedArgs& a, size_t row, int 
   else static_cast<__nv_bfloat16*>(a.Y)[at] = __float2bfloat16_rn(y);
 }
 
+__device__ __forceinline__ float4 paged_join4(const PagedArgs& a, const PagedScale& f, size_t row, int col,
+                                              const float4& z) {
+  float4 y = make_float4(z.x * f.fz, z.y * f.fz, z.z * f.fz, z.w * f.fz);
+  if (a.initY) {
+    const float4 i = *reinterpret_cast<const float4*>(a.initY + row * a.v + col);
+    y = make_float4(fmaf(i.x, f.fi, y.x), fmaf(i.y, f.fi, y.y), fmaf(i.z, f.fi, y.z), fmaf(i.w, f.fi, y.w));
+  }
+  return y;
+}
+__device__ __forceinline__ void paged_store4(const PagedArgs& a, size_t row, int col, const float4& y) {
+  const size_t at = row * a.v + col;
+  if (a.Yf) {
+    *reinterpret_cast<float4*>(a.Yf + at) = y;
+  } else if (a.dtype == kF32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(a.Y) + at) = y;
+  } else {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(y.x, y.y), q = __floats2bfloat162_rn(y.z, y.w);
+    uint2 raw;
+    raw.x = *reinterpret_cast<const uint32_t*>(&p);
+    raw.y = *reinterpret_cast<const uint32_t*>(&q);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.Y) + at) = raw;
+  }
+}
+
+// The CTA's status bits, at its end.
+__device__ __forceinline__ void paged_end(const PagedArgs& a, unsigned bits) {
+  unsigned all = 0;
+  for (const unsigned bit : {kStatusEmptyRow, kStatusBadPage, kStatusTimeout})
+    if (__syncthreads_or(bits & bit)) all |= bit;
+  if (threadIdx.x == 0) a.flags[blockIdx.x] = all;
+}
+
 // The row of page table entries of sequence b, and the row of a key in the
 // pool (pages [num_pages][Hk][page_size][width]); -1 for a page outside it.
 __device__ __forceinline__ long long paged_key_row(const PagedArgs& a, const int* trow, int h, int key) {
@@ -297,10 +329,13 @@ __device__ __forceinline__ long long paged_key_row(const PagedArgs& a, const int
 
 // Host side.
 struct PagedKernel {
-  int rt, ctas, vw;  // rows of a tile, CTAs of the launch
+  int rt, ctas;  // rows of a tile, CTAs of the launch
 };
+PagedKernel paged_simt_kernel(bool one_row);
 cudaError_t launch_paged_simt(const PagedArgs& a, bool one_row, cudaStream_t s);
-PagedKernel paged_simt_kernel(const PagedArgs& a, bool one_row);
+bool paged_mma_shape(int dtype, int d, int v);
+PagedKernel paged_mma_kernel();
+cudaError_t launch_paged_mma(const PagedArgs& a, cudaStream_t s);
 cudaError_t launch_paged_merge(const PagedArgs& a, int rt, cudaStream_t s);
 
 struct AppendArgs {

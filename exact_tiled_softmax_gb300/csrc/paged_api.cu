@@ -8,6 +8,7 @@
 namespace exattn {
 int append_max_pairs();
 extern thread_local char g_last_error[256];
+int current_path();
 }  // namespace exattn
 
 namespace {
@@ -53,16 +54,23 @@ int check_paged(const exattn_paged_shape* s) {
   return EXATTN_OK;
 }
 
-// The kernel of a call, from the shape and the process-wide path alone.
+// The kernel of a call.
+enum Kind { kSimtOne, kSimt, kMma };
+
+PagedKernel kernel_of(Kind k) {
+  return k == kMma ? paged_mma_kernel() : paged_simt_kernel(k == kSimtOne);
+}
+
 struct Choice {
-  bool one_row;
+  Kind kind;
   PagedKernel k;
 };
 
 Choice choose(const PagedArgs& a) {
   Choice c;
-  c.one_row = !a.starts && a.T == a.B && a.G == 1;
-  c.k = paged_simt_kernel(a, c.one_row);
+  if (current_path() != EXATTN_PATH_SIMT && paged_mma_shape(a.dtype, a.d, a.v)) c.kind = kMma;
+  else c.kind = !a.starts && a.T == a.B && a.G == 1 ? kSimtOne : kSimt;
+  c.k = kernel_of(c.kind);
   return c;
 }
 
@@ -75,14 +83,13 @@ size_t pass_bytes(const PagedKernel& k, int v) {
 }
 constexpr size_t kFlagBytes = 8192;  // status bits of the CTAs of two passes (at most 2048)
 
-// The most that any kernel choice of this shape needs (the path may change
-// between the query and the call, and q_starts is not part of the shape).
+// The most that any kernel of this shape needs (the path may change between the
+// query and the call, and q_starts is not part of the shape).
 size_t most_bytes(const exattn_paged_shape* s) {
-  PagedArgs a{};
-  a.v = s->v;
   size_t most = 0;
-  for (const bool one : {true, false}) {
-    const size_t x = pass_bytes(paged_simt_kernel(a, one), s->v);
+  for (const Kind k : {kSimtOne, kSimt, kMma}) {
+    if (k == kMma && !paged_mma_shape(s->dtype, s->d, s->v)) continue;
+    const size_t x = pass_bytes(kernel_of(k), s->v);
     most = x > most ? x : most;
   }
   return most;
@@ -137,7 +144,8 @@ int cuda_result(cudaError_t e, const char* where) {
 }
 
 cudaError_t run_pass(const PagedArgs& a, const Choice& c, cudaStream_t s) {
-  cudaError_t e = launch_paged_simt(a, c.one_row, s);
+  const cudaError_t e =
+      c.kind == kMma ? launch_paged_mma(a, s) : launch_paged_simt(a, c.kind == kSimtOne, s);
   return e != cudaSuccess ? e : launch_paged_merge(a, c.k.rt, s);
 }
 

@@ -251,12 +251,13 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
   paged_end(a, bits);
 }
 
-// Row r of the tile that CTA c of the attention launch starts and others end:
-// the star merge of its pieces.  One CTA of four warps a row; the warps share
-// the pieces.  CTA (0, 0) also joins the status bits of every CTA.
+// The rows of the tile that CTA c = blockIdx.x of the attention launch starts and
+// others end: the star merge of their pieces.  kWPR warps share the pieces of a row
+// (4 for the small tiles, whose rows may be spread over every CTA; 1 for the tiles
+// of 256 rows).  CTA (0, 0) also joins the status bits of every CTA.
 constexpr int kMergeW = 4;
 
-template <int RT>
+template <int RT, int kWPR>
 __global__ void __launch_bounds__(32 * kMergeW) paged_merge_kernel(const PagedArgs a) {
   __shared__ float red_l[kMergeW], red_m[kMergeW];
   __shared__ __align__(16) float red_z[kMergeW][256];
@@ -264,33 +265,36 @@ __global__ void __launch_bounds__(32 * kMergeW) paged_merge_kernel(const PagedAr
   if (a.status && blockIdx.x == 0 && blockIdx.y == 0) {
     unsigned bits = 0;
     for (int k = threadIdx.x; k < a.n_flags; k += 32 * kMergeW) bits |= a.flags0[k];
-    const unsigned all = (__syncthreads_or(bits & kStatusEmptyRow) ? kStatusEmptyRow : 0u) |
-                         (__syncthreads_or(bits & kStatusBadPage) ? kStatusBadPage : 0u) |
-                         (__syncthreads_or(bits & kStatusTimeout) ? kStatusTimeout : 0u);
+    unsigned all = 0;
+    for (const unsigned bit : {kStatusEmptyRow, kStatusBadPage, kStatusTimeout})
+      if (__syncthreads_or(bits & bit)) all |= bit;
     if (threadIdx.x == 0) *a.status = all;
   }
-  const int c = blockIdx.x, q = blockIdx.y;
+  const int c = blockIdx.x;
+  const int q = blockIdx.y * (kMergeW / kWPR) + warp / kWPR, part = warp % kWPR;
   const int4 t = a.desc[c];
   if (t.w == 0) return;
   const PagedSeq s = paged_seq(a, t.x);
   const int r = t.z * RT + q;
-  if (r >= s.nq * a.G) return;
+  if (r >= s.nq * a.G) return;  // all warps of a row together
   const int v = a.v;
   // Piece 0 is slot 2c + 1, piece k > 0 slot 2 (c + k).
   auto at = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * RT + q; };
   float M = -INFINITY;
-  for (int k = threadIdx.x; k < t.w; k += 32 * kMergeW) M = fmaxf(M, a.pm[at(k)]);
+  for (int k = part * 32 + lane; k < t.w; k += 32 * kWPR) M = fmaxf(M, a.pm[at(k)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-  if (lane == 0) red_m[warp] = M;
-  __syncthreads();
+  if constexpr (kWPR > 1) {
+    if (lane == 0) red_m[warp] = M;
+    __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kMergeW; ++k) M = fmaxf(M, red_m[k]);
+    for (int k = 0; k < kWPR; ++k) M = fmaxf(M, red_m[k]);
+  }
   const float ref = M == -INFINITY ? 0.f : M;
   float l = 0.f;
   float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll 4
-  for (int k = warp; k < t.w; k += kMergeW) {
+  for (int k = part; k < t.w; k += kWPR) {
     const size_t row = at(k);
     const float f = pexp2(a.pm[row] - ref);
     l = fmaf(f, a.pl[row], l);
@@ -305,23 +309,33 @@ __global__ void __launch_bounds__(32 * kMergeW) paged_merge_kernel(const PagedAr
       acc[x].w = fmaf(f, z.w, acc[x].w);
     }
   }
-  if (lane == 0) red_l[warp] = l;
+  if constexpr (kWPR > 1) {
+    if (lane == 0) red_l[warp] = l;
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
-    if (4 * lane + 128 * x < v) *reinterpret_cast<float4*>(&red_z[warp][4 * lane + 128 * x]) = acc[x];
-  __syncthreads();
-  l = 0.f;
+    for (int x = 0; x < 2; ++x)
+      if (4 * lane + 128 * x < v) *reinterpret_cast<float4*>(&red_z[warp][4 * lane + 128 * x]) = acc[x];
+    __syncthreads();
+    if (part != 0) return;
+    l = 0.f;
 #pragma unroll
-  for (int k = 0; k < kMergeW; ++k) l += red_l[k];
+    for (int k = 0; k < kWPR; ++k) l += red_l[k];
+  }
   const size_t row = paged_out_row(a, s, t.y, r);
   const PagedScale f = paged_finish(a, row, M, l);
-  for (int col = threadIdx.x; col < v; col += 32 * kMergeW) {
-    float z = 0.f;
 #pragma unroll
-    for (int k = 0; k < kMergeW; ++k) z += red_z[k][col];
-    paged_store(a, row, col, paged_join(a, f, row, col, z));
+  for (int x = 0; x < 2; ++x) {
+    const int col = 4 * lane + 128 * x;
+    if (col >= v) break;
+    if constexpr (kWPR > 1) {
+#pragma unroll
+      for (int k = 1; k < kWPR; ++k) {
+        const float4 z = *reinterpret_cast<const float4*>(&red_z[k][col]);
+        acc[x] = make_float4(acc[x].x + z.x, acc[x].y + z.y, acc[x].z + z.z, acc[x].w + z.w);
+      }
+    }
+    paged_store4(a, row, col, paged_join4(a, f, row, col, acc[x]));
   }
-  if (threadIdx.x == 0) a.L[row] = f.L;
+  if (lane == 0) a.L[row] = f.L;
 }
 
 template <typename T, int G, int CPL>
@@ -352,11 +366,11 @@ cudaError_t launch_paged_simt(const PagedArgs& a, bool one_row, cudaStream_t s) 
 
 cudaError_t launch_paged_merge(const PagedArgs& a, int rt, cudaStream_t s) {
   before_launch(kKernPagedMerge, s);
-  const dim3 grid(a.ctas, rt);
-  if (rt == 1) paged_merge_kernel<1><<<grid, 32 * kMergeW, 0, s>>>(a);
-  else if (rt == 4) paged_merge_kernel<4><<<grid, 32 * kMergeW, 0, s>>>(a);
-  else if (rt == 16) paged_merge_kernel<16><<<grid, 32 * kMergeW, 0, s>>>(a);
-  else return cudaErrorInvalidValue;
+  constexpr int nt = 32 * kMergeW;
+  if (rt == 1) paged_merge_kernel<1, 4><<<dim3(a.ctas, 1), nt, 0, s>>>(a);
+  else if (rt == 4) paged_merge_kernel<4, 4><<<dim3(a.ctas, 4), nt, 0, s>>>(a);
+  else if (rt == 16) paged_merge_kernel<16, 4><<<dim3(a.ctas, 16), nt, 0, s>>>(a);
+  else paged_merge_kernel<256, 1><<<dim3(a.ctas, 256 / kMergeW), nt, 0, s>>>(a);
   after_launch(kKernPagedMerge, s);
   return cudaGetLastError();
 }

@@ -336,6 +336,9 @@ cudaError_t launch_paged_simt(const PagedArgs& a, bool one_row, cudaStream_t s);
 bool paged_mma_shape(int dtype, int d, int v);
 PagedKernel paged_mma_kernel();
 cudaError_t launch_paged_mma(const PagedArgs& a, cudaStream_t s);
+bool paged_tc_supported(const PagedArgs& a);
+PagedKernel paged_tc_kernel_of();
+cudaError_t launch_paged_tc(const PagedArgs& a, cudaStream_t s);
 cudaError_t launch_paged_merge(const PagedArgs& a, int rt, cudaStream_t s);
 
 struct AppendArgs {

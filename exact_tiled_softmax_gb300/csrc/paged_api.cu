@@ -55,10 +55,10 @@ int check_paged(const exattn_paged_shape* s) {
 }
 
 // The kernel of a call.
-enum Kind { kSimtOne, kSimt, kMma };
+enum Kind { kSimtOne, kSimt, kMma, kTc };
 
 PagedKernel kernel_of(Kind k) {
-  return k == kMma ? paged_mma_kernel() : paged_simt_kernel(k == kSimtOne);
+  return k == kTc ? paged_tc_kernel_of() : k == kMma ? paged_mma_kernel() : paged_simt_kernel(k == kSimtOne);
 }
 
 struct Choice {
@@ -66,9 +66,14 @@ struct Choice {
   PagedKernel k;
 };
 
+// Rows of a key head on average: all that the host knows of them.
+long long rows_of(const PagedArgs& a) { return (long long)(a.T + a.B - 1) / a.B * a.G; }
+constexpr int kTcRows = 64;
+
 Choice choose(const PagedArgs& a) {
   Choice c;
-  if (current_path() != EXATTN_PATH_SIMT && paged_mma_shape(a.dtype, a.d, a.v)) c.kind = kMma;
+  if (current_path() != EXATTN_PATH_SIMT && paged_mma_shape(a.dtype, a.d, a.v))
+    c.kind = rows_of(a) > kTcRows && paged_tc_supported(a) ? kTc : kMma;
   else c.kind = !a.starts && a.T == a.B && a.G == 1 ? kSimtOne : kSimt;
   c.k = kernel_of(c.kind);
   return c;
@@ -87,8 +92,10 @@ constexpr size_t kFlagBytes = 8192;  // status bits of the CTAs of two passes (a
 // query and the call, and q_starts is not part of the shape).
 size_t most_bytes(const exattn_paged_shape* s) {
   size_t most = 0;
-  for (const Kind k : {kSimtOne, kSimt, kMma}) {
-    if (k == kMma && !paged_mma_shape(s->dtype, s->d, s->v)) continue;
+  for (const Kind k : {kSimtOne, kSimt, kMma, kTc}) {
+    if ((k == kMma || k == kTc) && !paged_mma_shape(s->dtype, s->d, s->v)) continue;
+    // A prefix's pass takes all tokens as one sequence's.
+    if (k == kTc && (long long)s->tokens * (s->heads / s->kv_heads) <= kTcRows) continue;
     const size_t x = pass_bytes(kernel_of(k), s->v);
     most = x > most ? x : most;
   }
@@ -145,7 +152,8 @@ int cuda_result(cudaError_t e, const char* where) {
 
 cudaError_t run_pass(const PagedArgs& a, const Choice& c, cudaStream_t s) {
   const cudaError_t e =
-      c.kind == kMma ? launch_paged_mma(a, s) : launch_paged_simt(a, c.kind == kSimtOne, s);
+      c.kind == kTc ? launch_paged_tc(a, s)
+                    : c.kind == kMma ? launch_paged_mma(a, s) : launch_paged_simt(a, c.kind == kSimtOne, s);
   return e != cudaSuccess ? e : launch_paged_merge(a, c.k.rt, s);
 }
 

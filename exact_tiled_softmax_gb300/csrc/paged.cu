@@ -16,6 +16,7 @@ namespace {
 
 constexpr int kW = 4;
 constexpr int kUnit = 64;  // keys of a unit of work
+constexpr int kCtas = 4 * 152;
 
 __device__ __forceinline__ float pexp2(float x) {
   float y;
@@ -72,9 +73,14 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
   const T* Kp = static_cast<const T*>(a.Kp);
   const T* Vp = static_cast<const T*>(a.Vp);
   unsigned bits = 0;
-  if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  __shared__ unsigned joined;
+  if (threadIdx.x == 0) {
+    a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    joined = 0;
+  }
   PagedWalk w;
-  bool more = paged_begin<NQ, kUnit, 32 * kW>(a, pre, scan, w, bits);
+  paged_scan<NQ, kUnit, 32 * kW>(a, pre, scan, bits);
+  bool more = paged_begin<NQ, kUnit>(a, pre, blockIdx.x, w);
   while (more) {
     int j0, j1;
     const int n = paged_segment<kUnit>(w, j0, j1);
@@ -86,7 +92,7 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
     int lo[NQ], hi[NQ];
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      const int r = r0 + (q < rows ? q : 0), i = r / a.G;
+      const int r = r0 + (q < rows ? q : 0), i = div_by(r, a.by_group);
       paged_row_span(a, w.s, i, lo[q], hi[q]);
       if (q < rows && lo[q] >= hi[q] && w.rem == 0 && !a.initL) bits |= kStatusEmptyRow;
       const T* qr = Q + (w.s.s0 + i) * a.q_stride + (w.h * a.G + r - i * a.G) * d;
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
         }
       }
     }
-    const int slot = paged_slot(a, w, n);
+    const int slot = paged_slot(a, w, n, blockIdx.x, threadIdx.x == 0);
     __syncthreads();
     for (int idx = threadIdx.x; idx < rows * v; idx += 32 * kW) {
       const int q = idx / v, col = idx - q * v;
@@ -248,108 +254,182 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
     more = paged_next<NQ, kUnit>(a, w, n);
     __syncthreads();  // the joined rows are read before the next segment's
   }
-  paged_end(a, bits);
+  paged_end(a, bits, &joined);
 }
 
-// The rows of the tile that CTA c = blockIdx.x of the attention launch starts and
-// others end: the star merge of their pieces.  kWPR warps share the pieces of a row
-// (4 for the small tiles, whose rows may be spread over every CTA; 1 for the tiles
-// of 256 rows).  CTA (0, 0) also joins the status bits of every CTA.
-constexpr int kMergeW = 4;
+// The star merge of the row tiles that a worker starts and others end.  kSpread:
+// CTA (x, y) takes row y of the tiles of workers 32 x .. 32 x + 31, all of its warps
+// sharing a row's pieces; else rows 16 y .. 16 y + 15 of the tiles of workers 4 x ..
+// 4 x + 3, a warp a row.  (Measured with a CTA for every worker and row: 2 us a
+// thousand CTAs, most of them without a tile.)  CTA (0, 0) also joins the status bits
+// of every CTA of the attention launches.
+constexpr int kMergeW = 16;
 
-template <int RT, int kWPR>
-__global__ void __launch_bounds__(32 * kMergeW) paged_merge_kernel(const PagedArgs a) {
-  __shared__ float red_l[kMergeW], red_m[kMergeW];
-  __shared__ __align__(16) float red_z[kMergeW][256];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (a.status && blockIdx.x == 0 && blockIdx.y == 0) {
-    unsigned bits = 0;
-    for (int k = threadIdx.x; k < a.n_flags; k += 32 * kMergeW) bits |= a.flags0[k];
-    unsigned all = 0;
-    for (const unsigned bit : {kStatusEmptyRow, kStatusBadPage, kStatusTimeout})
-      if (__syncthreads_or(bits & bit)) all |= bit;
-    if (threadIdx.x == 0) *a.status = all;
-  }
-  const int c = blockIdx.x;
-  const int q = blockIdx.y * (kMergeW / kWPR) + warp / kWPR, part = warp % kWPR;
-  const int4 t = a.desc[c];
-  if (t.w == 0) return;
-  const PagedSeq s = paged_seq(a, t.x);
-  const int r = t.z * RT + q;
-  if (r >= s.nq * a.G) return;  // all warps of a row together
-  const int v = a.v;
+// What a warp gathers of one row: pieces part, part + step, ... of `parts`.
+struct Gathered {
+  float l;
+  float4 z[2];
+};
+__device__ __forceinline__ Gathered gather_row(const PagedArgs& a, int c, int rt, int q, int parts, int part,
+                                               int step, float& M) {
+  const int lane = threadIdx.x & 31, v = a.v;
   // Piece 0 is slot 2c + 1, piece k > 0 slot 2 (c + k).
-  auto at = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * RT + q; };
-  float M = -INFINITY;
-  for (int k = part * 32 + lane; k < t.w; k += 32 * kWPR) M = fmaxf(M, a.pm[at(k)]);
+  auto at = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * rt + q; };
+  M = -INFINITY;
+#pragma unroll 1
+  for (int k = lane; k < parts; k += 32) M = fmaxf(M, a.pm[at(k)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-  if constexpr (kWPR > 1) {
-    if (lane == 0) red_m[warp] = M;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kWPR; ++k) M = fmaxf(M, red_m[k]);
-  }
   const float ref = M == -INFINITY ? 0.f : M;
-  float l = 0.f;
-  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  Gathered s{0.f, {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)}};
 #pragma unroll 4
-  for (int k = part; k < t.w; k += kWPR) {
+  for (int k = part; k < parts; k += step) {
     const size_t row = at(k);
     const float f = pexp2(a.pm[row] - ref);
-    l = fmaf(f, a.pl[row], l);
+    s.l = fmaf(f, a.pl[row], s.l);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int col = 4 * lane + 128 * x;
       if (col >= v) break;
       const float4 z = *reinterpret_cast<const float4*>(a.pz + row * v + col);
-      acc[x].x = fmaf(f, z.x, acc[x].x);
-      acc[x].y = fmaf(f, z.y, acc[x].y);
-      acc[x].z = fmaf(f, z.z, acc[x].z);
-      acc[x].w = fmaf(f, z.w, acc[x].w);
+      s.z[x].x = fmaf(f, z.x, s.z[x].x);
+      s.z[x].y = fmaf(f, z.y, s.z[x].y);
+      s.z[x].z = fmaf(f, z.z, s.z[x].z);
+      s.z[x].w = fmaf(f, z.w, s.z[x].w);
     }
   }
-  if constexpr (kWPR > 1) {
-    if (lane == 0) red_l[warp] = l;
+  return s;
+}
+
+// The warp's row out.
+__device__ __forceinline__ void finish_row(const PagedArgs& a, size_t row, float M, const Gathered& s) {
+  const int lane = threadIdx.x & 31;
+  const PagedScale f = paged_finish(a, row, M, s.l);
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-      if (4 * lane + 128 * x < v) *reinterpret_cast<float4*>(&red_z[warp][4 * lane + 128 * x]) = acc[x];
+  for (int x = 0; x < 2; ++x) {
+    const int col = 4 * lane + 128 * x;
+    if (col < a.v) paged_store4(a, row, col, paged_join4(a, f, row, col, s.z[x]));
+  }
+  if (lane == 0) a.L[row] = f.L;
+}
+
+template <bool kSpread>
+__global__ void __launch_bounds__(32 * kMergeW) paged_merge_kernel(const PagedArgs a, int rt) {
+  __shared__ float red_l[kMergeW];
+  __shared__ __align__(16) float4 red_z[kSpread ? kMergeW : 1][64];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (a.status && blockIdx.x == 0 && blockIdx.y == 0) {
+    __shared__ unsigned joined;
+    if (threadIdx.x == 0) joined = 0;
     __syncthreads();
-    if (part != 0) return;
-    l = 0.f;
+    unsigned bits = 0;
+    for (int k = threadIdx.x; k < a.n_flags; k += 32 * kMergeW) bits |= a.flags0[k];
+    if (bits) atomicOr(&joined, bits);
+    __syncthreads();
+    if (threadIdx.x == 0) *a.status = joined;
+  }
+  constexpr int kPer = kSpread ? 32 : 4;
+  const int c0 = blockIdx.x * kPer;
+  int4 mine = make_int4(0, 0, 0, 0);
+  if (lane < kPer && c0 + lane < a.workers) mine = a.desc[c0 + lane];
+  for (unsigned todo = __ballot_sync(0xFFFFFFFFu, mine.w > 0); todo; todo &= todo - 1) {
+    const int who = __ffs(todo) - 1, c = c0 + who;
+    const int b = __shfl_sync(0xFFFFFFFFu, mine.x, who), h = __shfl_sync(0xFFFFFFFFu, mine.y, who),
+              tile = __shfl_sync(0xFFFFFFFFu, mine.z, who), parts = __shfl_sync(0xFFFFFFFFu, mine.w, who);
+    const PagedSeq s = paged_seq(a, b);
+    const int q = kSpread ? blockIdx.y : 16 * blockIdx.y + warp;
+    const int r = tile * rt + q;
+    if (q >= rt || r >= s.nq * a.G) continue;  // kSpread: all warps alike
+    const size_t row = paged_out_row(a, s, h, r);
+    float M;
+    Gathered x = gather_row(a, c, rt, q, parts, kSpread ? warp : 0, kSpread ? kMergeW : 1, M);
+    if constexpr (kSpread) {
+      if (lane == 0) red_l[warp] = x.l;
+      red_z[warp][lane] = x.z[0];
+      red_z[warp][32 + lane] = x.z[1];
+      __syncthreads();
+      if (warp == 0) {
+        for (int k = 1; k < min(kMergeW, parts); ++k) {
+          x.l += red_l[k];
 #pragma unroll
-    for (int k = 0; k < kWPR; ++k) l += red_l[k];
+          for (int y = 0; y < 2; ++y) {
+            const float4 z = red_z[k][32 * y + lane];
+            x.z[y] = make_float4(x.z[y].x + z.x, x.z[y].y + z.y, x.z[y].z + z.z, x.z[y].w + z.w);
+          }
+        }
+        finish_row(a, row, M, x);
+      }
+      __syncthreads();
+    } else {
+      finish_row(a, row, M, x);
+    }
+  }
+}
+
+// The same for tiles of 256 rows, whose summaries stand column by column ([v / 4][256]
+// pieces of four): CTA (c, y) takes columns 16 y .. 16 y + 15 of worker c's tile, a
+// thread a row, so that loads are whole lines.
+constexpr int kTall = 256;
+
+__global__ void __launch_bounds__(kTall) paged_merge_tall_kernel(const PagedArgs a) {
+  if (a.status && blockIdx.x == 0 && blockIdx.y == 0) {
+    __shared__ unsigned joined;
+    if (threadIdx.x == 0) joined = 0;
+    __syncthreads();
+    unsigned bits = 0;
+    for (int k = threadIdx.x; k < a.n_flags; k += kTall) bits |= a.flags0[k];
+    if (bits) atomicOr(&joined, bits);
+    __syncthreads();
+    if (threadIdx.x == 0) *a.status = joined;
+  }
+  const int c = blockIdx.x, q = threadIdx.x, n4 = a.v / 4, first = 4 * blockIdx.y;
+  const int4 t = a.desc[c];
+  if (t.w == 0) return;
+  const PagedSeq s = paged_seq(a, t.x);
+  const int r = t.z * kTall + q;
+  if (r >= s.nq * a.G) return;
+  auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)); };
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int k = 0; k < t.w; ++k) M = fmaxf(M, a.pm[slot(k) * kTall + q]);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float l = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4* z = reinterpret_cast<const float4*>(a.pz);
+#pragma unroll 2
+  for (int k = 0; k < t.w; ++k) {
+    const float f = pexp2(a.pm[slot(k) * kTall + q] - ref);
+    l = fmaf(f, a.pl[slot(k) * kTall + q], l);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (first + x >= n4) break;
+      const float4 p = z[(slot(k) * n4 + first + x) * kTall + q];
+      acc[x] = make_float4(fmaf(f, p.x, acc[x].x), fmaf(f, p.y, acc[x].y), fmaf(f, p.z, acc[x].z),
+                           fmaf(f, p.w, acc[x].w));
+    }
   }
   const size_t row = paged_out_row(a, s, t.y, r);
   const PagedScale f = paged_finish(a, row, M, l);
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int col = 4 * lane + 128 * x;
-    if (col >= v) break;
-    if constexpr (kWPR > 1) {
-#pragma unroll
-      for (int k = 1; k < kWPR; ++k) {
-        const float4 z = *reinterpret_cast<const float4*>(&red_z[k][col]);
-        acc[x] = make_float4(acc[x].x + z.x, acc[x].y + z.y, acc[x].z + z.z, acc[x].w + z.w);
-      }
-    }
-    paged_store4(a, row, col, paged_join4(a, f, row, col, acc[x]));
-  }
-  if (lane == 0) a.L[row] = f.L;
+  for (int x = 0; x < 4; ++x)
+    if (first + x < n4) paged_store4(a, row, 4 * (first + x), paged_join4(a, f, row, 4 * (first + x), acc[x]));
+  if (first == 0) a.L[row] = f.L;
 }
 
 template <typename T, int G, int CPL>
 cudaError_t simt_launch(const PagedArgs& a, bool one_row, cudaStream_t s) {
   before_launch(kKernPaged, s);
-  if (one_row) paged_simt_kernel<T, G, CPL, 1><<<a.ctas, 32 * kW, 0, s>>>(a);
-  else paged_simt_kernel<T, G, CPL, 4><<<a.ctas, 32 * kW, 0, s>>>(a);
+  if (one_row) paged_simt_kernel<T, G, CPL, 1><<<kCtas, 32 * kW, 0, s>>>(a);
+  else paged_simt_kernel<T, G, CPL, 4><<<kCtas, 32 * kW, 0, s>>>(a);
   after_launch(kKernPaged, s);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-PagedKernel paged_simt_kernel(bool one_row) { return {one_row ? 1 : 4, 4 * 152}; }
+PagedKernel paged_simt_kernel(bool one_row) { return {one_row ? 1 : 4, kCtas, kCtas, 1}; }
 
 cudaError_t launch_paged_simt(const PagedArgs& a, bool one_row, cudaStream_t s) {
   const int bytes = (a.d > a.v ? a.d : a.v) * (a.dtype == kF32 ? 4 : 2);
@@ -364,13 +444,20 @@ cudaError_t launch_paged_simt(const PagedArgs& a, bool one_row, cudaStream_t s) 
   return simt_launch<__nv_bfloat16, 32, 1>(a, one_row, s);
 }
 
+// Rows that a tile can have (q_starts hides how many tokens a sequence has).  Small
+// tiles that may be spread over more than 16 workers give a row to all of a CTA's
+// warps: a warp alone takes one piece of 512 bytes after the other.
 cudaError_t launch_paged_merge(const PagedArgs& a, int rt, cudaStream_t s) {
+  const long long all = static_cast<long long>(a.starts ? a.T : a.each) * a.G;
+  const unsigned rows = static_cast<unsigned>(all < rt ? all : rt);
+  const bool spread = a.workers > 16 * a.B * a.Hk;
   before_launch(kKernPagedMerge, s);
-  constexpr int nt = 32 * kMergeW;
-  if (rt == 1) paged_merge_kernel<1, 4><<<dim3(a.ctas, 1), nt, 0, s>>>(a);
-  else if (rt == 4) paged_merge_kernel<4, 4><<<dim3(a.ctas, 4), nt, 0, s>>>(a);
-  else if (rt == 16) paged_merge_kernel<16, 4><<<dim3(a.ctas, 16), nt, 0, s>>>(a);
-  else paged_merge_kernel<256, 1><<<dim3(a.ctas, 256 / kMergeW), nt, 0, s>>>(a);
+  if (rt == kTall)
+    paged_merge_tall_kernel<<<dim3(a.workers, (a.v + 15) / 16), kTall, 0, s>>>(a);
+  else if (spread)
+    paged_merge_kernel<true><<<dim3((a.workers + 31) / 32, rows), 32 * kMergeW, 0, s>>>(a, rt);
+  else
+    paged_merge_kernel<false><<<dim3((a.workers + 3) / 4, (rows + 15) / 16), 32 * kMergeW, 0, s>>>(a, rt);
   after_launch(kKernPagedMerge, s);
   return cudaGetLastError();
 }

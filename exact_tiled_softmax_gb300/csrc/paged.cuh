@@ -1,5 +1,5 @@
 // Attention over a paged key/value cache: the problem, the way its work is
-// shared out over the CTAs of one launch, and the two ways a row leaves it.
+// shared out over the workers of one launch, and the two ways a row leaves it.
 //
 // Sequence b owns the packed tokens s0 .. s0 + nq - 1 and len cached keys, of
 // which its tokens are the last nq; token i sits at position len - nq + i.  The
@@ -9,16 +9,17 @@
 // Work.  A row tile is kRT consecutive rows of one (b, h); its keys, from the
 // first that any of its rows allows to the last, are cut at multiples of
 // kUnitKeys into units.  All units of the launch stand in one line, ordered by
-// (b, h, row tile, key), and CTA c takes units [c W, (c + 1) W), W = ceil(total
-// / CTAs): every CTA reads the same number of keys, however unequal the lengths
-// are and without the host knowing them (they are read on the device, so a
-// captured launch follows them).  A CTA's run of units is a list of segments,
-// one for each row tile that it touches.  A segment that holds all of its row
-// tile's units writes Y and L; any other writes its summary (m, l, z) of
-// "Exact tiled softmax attention with block-recomputed vector-Jacobian
-// products", Forward procedure, to a slot of the workspace: slot 2c + 1 when
-// it starts the row tile, slot 2c when it continues one (a CTA has at most one
-// of each), and paged_merge_kernel joins the slots with the star rule.
+// (b, h, row tile, key), and worker c (a warp or a CTA, as the kernel has it) takes
+// units [c W, (c + 1) W), W = ceil(total / workers): every worker reads the same
+// number of keys, however unequal the lengths are and without the host knowing
+// them (they are read on the device, so a captured launch follows them).  A
+// worker's run of units is a list of segments, one for each row tile that it
+// touches.  A segment that holds all of its row tile's units writes Y and L; any
+// other writes its summary (m, l, z) of "Exact tiled softmax attention with
+// block-recomputed vector-Jacobian products", Forward procedure, to a slot of the
+// workspace: slot 2c + 1 when it starts the row tile, slot 2c when it continues
+// one (a worker has at most one of each), and paged_merge_kernel joins the slots
+// with the star rule.
 #pragma once
 
 #include <math.h>
@@ -29,6 +30,23 @@ namespace exattn {
 
 constexpr int kPagedMaxBatch = 1024;  // prefix sums of the units stay in shared memory
 
+// Division by a number that is fixed for a launch (n < 2^31): a high product, an
+// addition and a shift (Granlund and Montgomery, "Division by invariant integers
+// using multiplication", PLDI 1994, figure 4.1).
+struct FastDiv {
+  unsigned mul, shift;
+  int d;
+};
+inline FastDiv fast_div(int d) {
+  FastDiv f{0, 0, d};
+  while ((1ll << f.shift) < d) ++f.shift;
+  f.mul = static_cast<unsigned>(((1ull << 32) * ((1ull << f.shift) - d)) / d + 1);
+  return f;
+}
+__device__ __forceinline__ int div_by(int n, const FastDiv& f) {
+  return static_cast<int>((__umulhi(static_cast<unsigned>(n), f.mul) + static_cast<unsigned>(n)) >> f.shift);
+}
+
 struct PagedArgs {
   const void* Q;
   const void* Kp;
@@ -38,6 +56,8 @@ struct PagedArgs {
   const int* starts;  // [B + 1], or null: T / B tokens for every sequence
   int fixed_len;
   int B, T, Hk, G, d, v, dtype;
+  FastDiv by_group;  // G
+  int each;          // T / B
   int lps;  // log2(page_size)
   int num_pages, max_pages;
   int mask_kind, window;
@@ -55,11 +75,12 @@ struct PagedArgs {
   unsigned* flags;   // [n_flags] status bits, one word for each CTA of each launch
   int n_flags;       // words that the merge kernel joins (from flags0)
   const unsigned* flags0;
-  int4* desc;  // [ctas] of CTA c: (b, h, row tile, parts) of the tile it starts and others end
-  float* pm;   // [2 ctas][RT] exp2 domain
-  float* pl;   // [2 ctas][RT]
-  float* pz;   // [2 ctas][RT][v]
-  int ctas;
+  int4* desc;  // [workers] of worker c: (b, h, row tile, parts) of the tile it starts and others end
+  float* pm;   // [2 workers][RT] exp2 domain
+  float* pl;   // [2 workers][RT]
+  float* pz;   // [2 workers][RT][v]
+  int workers;
+  int least;  // units that a worker takes at least
 };
 
 struct PagedSeq {
@@ -77,7 +98,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int b) {
     s.nq = s1 - s.s0;
     s.bad = x != s.s0 || y != s1;
   } else {
-    s.nq = a.T / a.B;
+    s.nq = a.each;
     s.s0 = b * s.nq;
   }
   const int n = a.lens ? __ldg(a.lens + b) : a.fixed_len;
@@ -107,21 +128,26 @@ __device__ __forceinline__ PagedTile paged_tile(const PagedArgs& a, const PagedS
   PagedTile t;
   const int r0 = rt * RT, all = s.nq * a.G;
   t.rows = min(RT, all - r0);
-  t.i0 = r0 / a.G;
-  t.i1 = (r0 + t.rows - 1) / a.G;
+  t.i0 = div_by(r0, a.by_group);
+  t.i1 = div_by(r0 + t.rows - 1, a.by_group);
   int x;
   paged_row_span(a, s, t.i0, t.lo, x);
   paged_row_span(a, s, t.i1, x, t.hi);
   if (t.hi <= t.lo) t.hi = t.lo = 0;
-  t.kt0 = t.lo / UK;
-  t.cnt = max(1, (t.hi + UK - 1) / UK - t.kt0);  // a tile without keys still writes its rows
+  t.kt0 = static_cast<unsigned>(t.lo) / UK;
+  t.cnt = max(1, static_cast<int>((static_cast<unsigned>(t.hi) + UK - 1) / UK) - t.kt0);  // a tile without keys still writes its rows
   return t;
 }
 
-// The CTA's place in the line of units.  `pre` (shared, kPagedMaxBatch + 1
-// words) receives the number of units before each sequence.
+// n / d for n >= 0, d > 0: in 32 bits wherever they fit.
+__device__ __forceinline__ long long paged_div(long long n, long long d) {
+  if (((n | d) >> 32) == 0) return static_cast<unsigned>(n) / static_cast<unsigned>(d);
+  return static_cast<long long>(static_cast<unsigned long long>(n) / static_cast<unsigned long long>(d));
+}
+
+// A worker's place in the line of units.
 struct PagedWalk {
-  long long u, end, total, w;  // next unit, the CTA's end, all units, units for each CTA
+  long long u, end, w;  // next unit, the worker's end, units for each worker
   int b, h, rt, rem;           // of unit u: sequence, key head, row tile, unit in the tile
   PagedSeq s;
   PagedTile t;
@@ -132,19 +158,22 @@ template <int RT, int UK>
 __device__ __forceinline__ long long paged_units(const PagedArgs& a, const PagedSeq& s) {
   const int tiles = (s.nq * a.G + RT - 1) / RT;
   long long u = 0;
+#pragma unroll 1
   for (int rt = 0; rt < tiles; ++rt) u += paged_tile<RT, UK>(a, s, rt).cnt;
   return u * a.Hk;
 }
 
-// All threads; returns false when the CTA has no unit.  Status bits that the
-// caller's numbers raise go to `bits` (of CTA 0).
+// All threads of a CTA: `pre` (shared, kPagedMaxBatch + 1 words) receives the number
+// of units before each sequence.  Status bits that the caller's numbers raise go to
+// `bits` (of CTA 0).
 template <int RT, int UK, int NT>
-__device__ __forceinline__ bool paged_begin(const PagedArgs& a, long long* pre, long long* scan,
-                                            PagedWalk& w, unsigned& bits) {
+__device__ __forceinline__ void paged_scan(const PagedArgs& a, long long* pre, long long* scan,
+                                           unsigned& bits) {
   const int tid = threadIdx.x;
   const int per = (a.B + NT - 1) / NT;
   long long mine = 0;
   bool bad = false;
+#pragma unroll 1
   for (int k = 0; k < per; ++k) {
     const int b = tid * per + k;
     if (b >= a.B) break;
@@ -164,7 +193,9 @@ __device__ __forceinline__ bool paged_begin(const PagedArgs& a, long long* pre, 
   const int any_bad = __syncthreads_or(bad);
   if (any_bad && blockIdx.x == 0) bits |= kStatusBadPage;
   long long before = inc - mine;
+#pragma unroll 1
   for (int k = 0; k < warp; ++k) before += scan[k];
+#pragma unroll 1
   for (int k = 0; k < per; ++k) {
     const int b = tid * per + k;
     if (b >= a.B) break;
@@ -172,12 +203,18 @@ __device__ __forceinline__ bool paged_begin(const PagedArgs& a, long long* pre, 
   }
   if (tid == 0) pre[0] = 0;
   __syncthreads();
-  w.total = pre[a.B];
-  w.w = (w.total + a.ctas - 1) / a.ctas;
-  w.u = min(w.total, w.w * blockIdx.x);
-  w.end = min(w.total, w.u + w.w);
+}
+
+// Worker `c` at its first unit; false when it has none.
+template <int RT, int UK>
+__device__ __forceinline__ bool paged_begin(const PagedArgs& a, const long long* pre, int c, PagedWalk& w) {
+  const long long total = pre[a.B];
+  w.w = max(static_cast<long long>(a.least), paged_div(total + a.workers - 1, a.workers));
+  w.u = min(total, w.w * c);
+  w.end = min(total, w.u + w.w);
   if (w.u >= w.end) return false;
   int b0 = 0, b1 = a.B;  // pre[b0] <= u < pre[b1]
+#pragma unroll 1
   while (b1 - b0 > 1) {
     const int mid = (b0 + b1) >> 1;
     if (pre[mid] <= w.u) b0 = mid;
@@ -186,12 +223,13 @@ __device__ __forceinline__ bool paged_begin(const PagedArgs& a, long long* pre, 
   w.b = b0;
   w.s = paged_seq(a, w.b);
   w.tiles = (w.s.nq * a.G + RT - 1) / RT;
-  const long long per_head = (pre[b0 + 1] - pre[b0]) / a.Hk;
+  const long long per_head = paged_div(pre[b0 + 1] - pre[b0], a.Hk);
   const long long local = w.u - pre[b0];
-  w.h = static_cast<int>(local / per_head);
+  w.h = static_cast<int>(paged_div(local, per_head));
   long long rem = local - w.h * per_head;
   w.rt = 0;
   w.t = paged_tile<RT, UK>(a, w.s, 0);
+#pragma unroll 1
   while (rem >= w.t.cnt) {
     rem -= w.t.cnt;
     w.t = paged_tile<RT, UK>(a, w.s, ++w.rt);
@@ -200,7 +238,7 @@ __device__ __forceinline__ bool paged_begin(const PagedArgs& a, long long* pre, 
   return true;
 }
 
-// Past the segment of `n` units that starts at w.u; false at the CTA's end.
+// Past the segment of `n` units that starts at w.u; false at the worker's end.
 template <int RT, int UK>
 __device__ __forceinline__ bool paged_next(const PagedArgs& a, PagedWalk& w, int n) {
   w.u += n;
@@ -210,6 +248,7 @@ __device__ __forceinline__ bool paged_next(const PagedArgs& a, PagedWalk& w, int
     w.rt = 0;
     if (++w.h == a.Hk) {
       w.h = 0;
+#pragma unroll 1
       do {  // a sequence without tokens has no units
         ++w.b;
         w.s = paged_seq(a, w.b);
@@ -231,23 +270,22 @@ __device__ __forceinline__ int paged_segment(const PagedWalk& w, int& j0, int& j
   return n;
 }
 
-// Where the summary of the CTA's present segment goes: its slot, or -1 when the
-// segment holds the whole row tile.  Thread 0 describes a tile that starts here
-// and ends in a later CTA; parts: the CTAs that hold a piece of it.
-__device__ __forceinline__ int paged_slot(const PagedArgs& a, const PagedWalk& w, int n) {
-  const int c = blockIdx.x;
+// Where the summary of worker c's present segment goes: its slot, or -1 when the
+// segment holds the whole row tile.  The thread `one` describes a tile that starts
+// here and ends with a later worker; parts: the workers that hold a piece of it.
+__device__ __forceinline__ int paged_slot(const PagedArgs& a, const PagedWalk& w, int n, int c, bool one) {
   if (w.rem > 0) return 2 * c;
   if (n == w.t.cnt) return -1;
-  if (threadIdx.x == 0) {
+  if (one) {
     const long long last = w.u + w.t.cnt - 1;
-    a.desc[c] = make_int4(w.b, w.h, w.rt, static_cast<int>(last / w.w) - c + 1);
+    a.desc[c] = make_int4(w.b, w.h, w.rt, static_cast<int>(paged_div(last, w.w)) - c + 1);
   }
   return 2 * c + 1;
 }
 
 // Row r (of the tile's first row r0) as an index into [T][heads].
 __device__ __forceinline__ size_t paged_out_row(const PagedArgs& a, const PagedSeq& s, int h, int r) {
-  const int i = r / a.G;
+  const int i = div_by(r, a.by_group);
   return static_cast<size_t>(s.s0 + i) * (a.Hk * a.G) + h * a.G + (r - i * a.G);
 }
 
@@ -311,12 +349,12 @@ __device__ __forceinline__ void paged_store4(const PagedArgs& a, size_t row, int
   }
 }
 
-// The CTA's status bits, at its end.
-__device__ __forceinline__ void paged_end(const PagedArgs& a, unsigned bits) {
-  unsigned all = 0;
-  for (const unsigned bit : {kStatusEmptyRow, kStatusBadPage, kStatusTimeout})
-    if (__syncthreads_or(bits & bit)) all |= bit;
-  if (threadIdx.x == 0) a.flags[blockIdx.x] = all;
+// The CTA's status bits, at its end (`joined`: a word in shared memory, zero since an
+// earlier barrier).
+__device__ __forceinline__ void paged_end(const PagedArgs& a, unsigned bits, unsigned* joined) {
+  if (bits) atomicOr(joined, bits);
+  __syncthreads();
+  if (threadIdx.x == 0) a.flags[blockIdx.x] = *joined;
 }
 
 // The row of page table entries of sequence b, and the row of a key in the
@@ -327,13 +365,14 @@ __device__ __forceinline__ long long paged_key_row(const PagedArgs& a, const int
   return ((static_cast<long long>(page) * a.Hk + h) << a.lps) + (key & ((1 << a.lps) - 1));
 }
 
-// Host side.
+// Host side: rows of a tile, CTAs and workers of the launch, units that a worker
+// takes at least.
 struct PagedKernel {
-  int rt, ctas;  // rows of a tile, CTAs of the launch
+  int rt, ctas, workers, least;
 };
 PagedKernel paged_simt_kernel(bool one_row);
 cudaError_t launch_paged_simt(const PagedArgs& a, bool one_row, cudaStream_t s);
-bool paged_mma_shape(int dtype, int d, int v);
+bool paged_mma_shape(int d, int v);
 PagedKernel paged_mma_kernel();
 cudaError_t launch_paged_mma(const PagedArgs& a, cudaStream_t s);
 bool paged_tc_supported(const PagedArgs& a);

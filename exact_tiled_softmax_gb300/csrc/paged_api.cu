@@ -72,7 +72,7 @@ constexpr int kTcRows = 64;
 
 Choice choose(const PagedArgs& a) {
   Choice c;
-  if (current_path() != EXATTN_PATH_SIMT && paged_mma_shape(a.dtype, a.d, a.v))
+  if (current_path() != EXATTN_PATH_SIMT && paged_mma_shape(a.d, a.v))
     c.kind = rows_of(a) > kTcRows && paged_tc_supported(a) ? kTc : kMma;
   else c.kind = !a.starts && a.T == a.B && a.G == 1 ? kSimtOne : kSimt;
   c.k = kernel_of(c.kind);
@@ -82,8 +82,8 @@ Choice choose(const PagedArgs& a) {
 // Workspace of one attention launch and its merge: flags | tile descriptions |
 // m | l | z of the slots.
 size_t pass_bytes(const PagedKernel& k, int v) {
-  const size_t rows = 2 * (size_t)k.ctas * k.rt;
-  return align256(sizeof(int4) * (size_t)k.ctas) + 2 * align256(sizeof(float) * rows) +
+  const size_t rows = 2 * (size_t)k.workers * k.rt;
+  return align256(sizeof(int4) * (size_t)k.workers) + 2 * align256(sizeof(float) * rows) +
          align256(sizeof(float) * rows * v);
 }
 constexpr size_t kFlagBytes = 8192;  // status bits of the CTAs of two passes (at most 2048)
@@ -93,9 +93,9 @@ constexpr size_t kFlagBytes = 8192;  // status bits of the CTAs of two passes (a
 size_t most_bytes(const exattn_paged_shape* s) {
   size_t most = 0;
   for (const Kind k : {kSimtOne, kSimt, kMma, kTc}) {
-    if ((k == kMma || k == kTc) && !paged_mma_shape(s->dtype, s->d, s->v)) continue;
+    if ((k == kMma || k == kTc) && !paged_mma_shape(s->d, s->v)) continue;
     // A prefix's pass takes all tokens as one sequence's.
-    if (k == kTc && (long long)s->tokens * (s->heads / s->kv_heads) <= kTcRows) continue;
+    if (k == kTc && (s->dtype != EXATTN_BF16 || (long long)s->tokens * (s->heads / s->kv_heads) <= kTcRows)) continue;
     const size_t x = pass_bytes(kernel_of(k), s->v);
     most = x > most ? x : most;
   }
@@ -103,10 +103,11 @@ size_t most_bytes(const exattn_paged_shape* s) {
 }
 
 char* place_pass(PagedArgs& a, const PagedKernel& k, char* ws) {
-  const size_t rows = 2 * (size_t)k.ctas * k.rt;
-  a.ctas = k.ctas;
+  const size_t rows = 2 * (size_t)k.workers * k.rt;
+  a.workers = k.workers;
+  a.least = k.least;
   a.desc = reinterpret_cast<int4*>(ws);
-  ws += align256(sizeof(int4) * (size_t)k.ctas);
+  ws += align256(sizeof(int4) * (size_t)k.workers);
   a.pm = reinterpret_cast<float*>(ws);
   ws += align256(sizeof(float) * rows);
   a.pl = reinterpret_cast<float*>(ws);
@@ -129,6 +130,8 @@ PagedArgs make_args(const exattn_paged_shape* s, const void* Q, const void* Kp, 
   a.T = s->tokens;
   a.Hk = s->kv_heads;
   a.G = s->heads / s->kv_heads;
+  a.by_group = fast_div(a.G);
+  a.each = a.T / a.B;
   a.d = s->d;
   a.v = s->v;
   a.dtype = s->dtype;
@@ -289,6 +292,7 @@ int attn_fwd_prefix(const exattn_paged_shape* shape, const void* Q, const void* 
   PagedArgs p = make_args(shape, Q, k_pages, v_pages, prefix_table, nullptr, nullptr, scale,
                           EXATTN_MASK_NONE, 0, nullptr, reinterpret_cast<float*>(init));
   p.B = 1;
+  p.each = p.T;
   p.fixed_len = prefix_len;
   p.max_pages = (prefix_len + shape->page_size - 1) / shape->page_size;
   p.Yf = reinterpret_cast<float*>(init + align256(sizeof(float) * rows));

@@ -3,9 +3,9 @@
 // the tensor cores and the exponentials.
 //
 // A row tile is 256 rows, two 128-row halves A and B that share every key block
-// of 128.  Roles as in the dense forward (12 warps): warps 0-3 and 4-7 the softmax
-// of A and B, one thread a row; warp 8 the loads, warp 9 the products, warps 10-11
-// the rows of Q.  Per key block t the MMA warp issues S_A(t), PV_B(t-1), S_B(t),
+// of 128.  Roles (12 warps): warps 0-3 and 4-7 the softmax of A and B, one thread a
+// row; warp 8 the loads, warp 9 the products, warps 10-11 the rows of Q.  Warp 11
+// also walks the CTA's segments and hands each to the others through a ring of two.  Per key block t the MMA warp issues S_A(t), PV_B(t-1), S_B(t),
 // PV_A(t), so each half's softmax overlaps two products of the other.  TMEM: S_A
 // [0,128), S_B [128,256), O_A, O_B behind; P (bf16) overwrites half of S and is the
 // TMEM operand of P.V.  The reference point of the exponentials moves only when a
@@ -38,10 +38,12 @@ using namespace tc;
 constexpr int kHalf = 128;
 constexpr int kRows = 2 * kHalf;
 constexpr int kUnit = 128;
+constexpr int kCtas = 152;
 constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 208;
 constexpr int kProducerRegs = 88;
 constexpr int kWarpTMA = 8, kWarpMMA = 9, kWarpQ = 10;
+constexpr int kTakers = 11;  // warps that read a segment from the ring
 constexpr int kQThreads = 64;
 constexpr float kRescale = 8.f;
 constexpr uint32_t kTmemCols = 512;
@@ -50,6 +52,11 @@ struct TcParams {
   CUtensorMap tk, tv;  // the pools as [num_pages * Hk * page_size][width], boxes 64 x box_rows
   PagedArgs a;
   int box_rows;
+};
+
+// A segment, as warp 11 hands it out; n == 0: no more.
+struct TcSegment {
+  int n, kb0, j0, j1, rows, r0, h, b, slot, first, s0, nq, len;
 };
 
 template <int D>
@@ -62,11 +69,12 @@ struct TcLayout {
   static constexpr int SLOT_OFF = 2 * QTILE;
   static constexpr int BAR_OFF = SLOT_OFF + NSLOT * SLOT;
   static constexpr int B_Q = 0, B_QFREE = 1, B_KVF = 2, B_KVE = B_KVF + NSLOT, B_S = B_KVE + NSLOT,
-                       B_P = B_S + 2, B_O = B_P + 2, B_OREAD = B_O + 2, B_DRAIN = B_OREAD + 2,
+                       B_P = B_S + 2, B_O = B_P + 2, B_OREAD = B_O + 2, B_SEGF = B_OREAD + 2, B_SEGE = B_SEGF + 2, B_DRAIN = B_SEGE + 2,
                        NBAR = B_DRAIN + 1;
   static constexpr int KEEP_OFF = BAR_OFF + (NBAR * 8 + 15) / 16 * 16;  // 4 words a slot
-  static constexpr int MISC_OFF = KEEP_OFF + NSLOT * 16;                // TMEM base, abort flag
-  static constexpr int TOTAL = MISC_OFF + 16;
+  static constexpr int MISC_OFF = KEEP_OFF + NSLOT * 16;                // TMEM base, abort flag, status bits
+  static constexpr int SEG_OFF = MISC_OFF + 16;
+  static constexpr int TOTAL = SEG_OFF + 2 * 64;
   static constexpr int ALLOC = TOTAL + 1024;
   static_assert(ALLOC + (kPagedMaxBatch + 1) * 8 + 256 <= 232448, "shared memory");
 };
@@ -123,9 +131,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       mbar_init(bar(Lay::B_P + X), kHalf);
       mbar_init(bar(Lay::B_O + X), 1);
       mbar_init(bar(Lay::B_OREAD + X), kHalf);
+      mbar_init(bar(Lay::B_SEGF + X), 1);
+      mbar_init(bar(Lay::B_SEGE + X), kTakers);
     }
     mbar_init(bar(Lay::B_DRAIN), 1);
-    misc[1] = 0;
+    misc[1] = misc[2] = 0;
     fence_mbar_init();
   }
   if (warp == kWarpMMA) {
@@ -133,15 +143,35 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     tmem_relinquish();
     tc_fence_before();
   }
-  __syncthreads();
+  unsigned bits = 0;
+  paged_scan<kRows, kUnit, kThreads>(a, pre, scan, bits);  // two barriers of the CTA
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  unsigned bits = 0;
-  PagedWalk w;
-  // Every role walks the CTA's segments by itself: the walk depends on device
-  // data that nothing changes during the launch.  `seg` counts segments, `blk`
-  // key blocks; K of block blk is fill 2 blk, V fill 2 blk + 1 of the ring.
-  bool more = paged_begin<kRows, kUnit, kThreads>(a, pre, scan, w, bits);
+  // Segment `seg` from the ring; false when there is none (or a wait gave up: ok).
+  volatile int* ring = reinterpret_cast<volatile int*>(smem + Lay::SEG_OFF);
+  auto take = [&](int seg, TcSegment& t, bool& ok) {
+    const int e = seg & 1;
+    if (!(ok = wait_all(bar(Lay::B_SEGF + e), (seg >> 1) & 1, abort_flag))) return false;
+    volatile int* r = ring + 16 * e;
+    t.n = r[0];
+    t.kb0 = r[1];
+    t.j0 = r[2];
+    t.j1 = r[3];
+    t.rows = r[4];
+    t.r0 = r[5];
+    t.h = r[6];
+    t.b = r[7];
+    t.slot = r[8];
+    t.first = r[9];
+    t.s0 = r[10];
+    t.nq = r[11];
+    t.len = r[12];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(Lay::B_SEGE + e));
+    return t.n > 0;
+  };
+  // Roles count segments (`seg`) and key blocks; K of block blk is fill 2 blk of the
+  // ring of tiles, V fill 2 blk + 1.
 
   if (warp >= 8) {
     regs_dec<kProducerRegs>();
@@ -154,26 +184,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       const int br = p.box_rows, nb = kUnit / br;
       bool ok = true;
       int fill = 0;
-      while (more && ok) {
-        int j0, j1;
-        const int n = paged_segment<kUnit>(w, j0, j1);
-        const int* trow = a.table + static_cast<size_t>(w.b) * a.max_pages;
-        const int kb0 = (w.t.kt0 + w.rem) * kUnit;
+      TcSegment t;
+      for (int seg = 0; take(seg, t, ok); ++seg) {
+        const int* trow = a.table + static_cast<size_t>(t.b) * a.max_pages;
         // Lane l: the pool row of box l of block u, or -1.
         auto find = [&](int u) {
           int row = -1;
-          const int key = kb0 + u * kUnit + lane * br;
-          if (u < n && lane < nb && key < j1 && key + br > j0) {
-            const long long at = paged_key_row(a, trow, w.h, key);
+          const int key = t.kb0 + u * kUnit + lane * br;
+          if (u < t.n && lane < nb && key < t.j1 && key + br > t.j0) {
+            const long long at = paged_key_row(a, trow, t.h, key);
             if (at < 0) bits |= kStatusBadPage;
             row = static_cast<int>(at);
           }
           return row;
         };
         int row = find(0);
-        for (int u = 0; u < n && ok; ++u) {
+        for (int u = 0; u < t.n && ok; ++u) {
           const int next = find(u + 1);
-          const int kb = kb0 + u * kUnit;
+          const int kb = t.kb0 + u * kUnit;
           const unsigned boxes = __ballot_sync(0xFFFFFFFFu, row >= 0);
           const uint32_t bytes = __popc(boxes) * br * 128 * Lay::CHUNKS;
 #pragma unroll
@@ -182,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             if (!(ok = wait_all(bar(Lay::B_KVE + slot), phase ^ 1, abort_flag))) break;
             ++fill;
             if (kv == 1 && lane < 4) {
-              uint32_t word = range_bits(j0 - kb - 32 * lane, j1 - 1 - kb - 32 * lane);
+              uint32_t word = range_bits(t.j0 - kb - 32 * lane, t.j1 - 1 - kb - 32 * lane);
               for (int b = 0; b < nb; ++b)
                 if (!((boxes >> b) & 1u)) word &= ~range_bits(b * br - 32 * lane, b * br + br - 1 - 32 * lane);
               keep[slot * 4 + lane] = word;
@@ -199,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
           }
           row = next;
         }
-        more = paged_next<kRows, kUnit>(a, w, n);
+        if (!ok) break;
       }
       if (!ok) {
         bits |= kStatusTimeout;
@@ -242,10 +270,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                    kk > 0 || !first ? 1u : 0u);
         }
       };
-      for (int seg = 0; more && ok; ++seg) {
-        int j0, j1;
-        const int n = paged_segment<kUnit>(w, j0, j1);
-        const bool two = w.t.rows > kHalf;
+      TcSegment t;
+      for (int seg = 0; take(seg, t, ok); ++seg) {
+        const int n = t.n;
+        const bool two = t.rows > kHalf;
         if (!(ok = wait_all(bar(Lay::B_Q), seg & 1, abort_flag))) break;
         tc_fence_after();
         int v_prev = -1;  // V slot whose P.V of half B is still to come
@@ -306,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
           commit(Lay::B_O + X);
         }
         __syncwarp();
-        more = paged_next<kRows, kUnit>(a, w, n);
+        if (!ok) break;
       }
       if (!ok) {
         bits |= kStatusTimeout;
@@ -316,34 +344,88 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       commit(Lay::B_DRAIN);
       mbar_wait_inflight(bar(Lay::B_DRAIN), 0);
     } else {
-      // The rows of Q, in the 128-byte swizzled layout of the products' operand.
+      // The rows of Q, in the 128-byte swizzled layout of the products' operand: warp
+      // 10 the even groups of 32 rows, warp 11 the odd ones.  A lane finds one row, the
+      // warp copies them together.
       const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(a.Q);
-      const int qt = threadIdx.x - kWarpQ * 32;
-      constexpr int CH = D / 8;
+      constexpr int CH = D / 8, kPass = 32 / CH;  // rows that a warp copies at once
       const int kch = a.d / 8;
       bool ok = true;
-      for (int seg = 0; more && ok; ++seg) {
-        int j0, j1;
-        const int n = paged_segment<kUnit>(w, j0, j1);
-        if (seg > 0 && !(ok = wait_all(bar(Lay::B_QFREE), (seg - 1) & 1, abort_flag))) break;
-        const int r0 = w.rt * kRows;
-        const int halves = w.t.rows > kHalf ? kRows : kHalf;
+      auto copy_q = [&](const TcSegment& t) {
+        const int groups = t.rows > kHalf ? kRows / 32 : kHalf / 32;
+#pragma unroll 1
+        for (int x = warp - kWarpQ; x < groups; x += 2) {
+          const int mine = x * 32 + lane, r = t.r0 + (mine < t.rows ? mine : 0);
+          const int i = div_by(r, a.by_group);
+          const long long src = reinterpret_cast<long long>(Q + (t.s0 + i) * a.q_stride +
+                                                            (t.h * a.G + r - i * a.G) * a.d);
+          const uint32_t half = sbase + Lay::Q_OFF + (x / (kHalf / 32)) * Lay::QTILE;
+          const int c = lane % CH;
+          const uint32_t piece = half + (c >> 3) * (kHalf * 128);
 #pragma unroll 4
-        for (int x = qt; x < halves * CH; x += kQThreads) {
-          const int r = x / CH, c = x % CH;
-          const int rr = r0 + (r < w.t.rows ? r : 0), i = rr / a.G;
-          const __nv_bfloat16* src = Q + (w.s.s0 + i) * a.q_stride + (w.h * a.G + rr - i * a.G) * a.d;
-          const uint32_t dst = sbase + Lay::Q_OFF + (r / kHalf) * Lay::QTILE + (c >> 3) * (kHalf * 128) +
-                               (r % kHalf) * 128 + (((c & 7) ^ (r & 7)) << 4);
-          const bool has = r < w.t.rows && c < kch;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                       "l"(src + (c < kch ? c * 8 : 0)), "r"(has ? 16 : 0)
-                       : "memory");
+          for (int y = 0; y < 32; y += kPass) {
+            const int rr = y + lane / CH, row = x * 32 + rr;  // of the tile
+            const char* from = reinterpret_cast<const char*>(__shfl_sync(0xFFFFFFFFu, src, rr));
+            const bool has = row < t.rows && c < kch;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             piece + (row % kHalf) * 128 + (((c & 7) ^ (row & 7)) << 4)),
+                         "l"(from + (c < kch ? c * 16 : 0)), "r"(has ? 16 : 0)
+                         : "memory");
+          }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async_smem();
         mbar_arrive(bar(Lay::B_Q));
-        more = paged_next<kRows, kUnit>(a, w, n);
+      };
+      TcSegment t;
+      if (warp == kWarpQ) {
+        for (int seg = 0; take(seg, t, ok); ++seg) {
+          if (seg > 0 && !(ok = wait_all(bar(Lay::B_QFREE), (seg - 1) & 1, abort_flag))) break;
+          copy_q(t);
+        }
+      } else {
+        PagedWalk w;
+        bool more = paged_begin<kRows, kUnit>(a, pre, blockIdx.x, w);
+        for (int seg = 0; ok; ++seg) {
+          const int e = seg & 1;
+          t.n = 0;
+          if (more) {
+            t.n = paged_segment<kUnit>(w, t.j0, t.j1);
+            t.kb0 = (w.t.kt0 + w.rem) * kUnit;
+            t.rows = w.t.rows;
+            t.r0 = w.rt * kRows;
+            t.h = w.h;
+            t.b = w.b;
+            t.slot = paged_slot(a, w, t.n, blockIdx.x, lane == 0);
+            t.first = w.rem == 0;
+            t.s0 = w.s.s0;
+            t.nq = w.s.nq;
+            t.len = w.s.len;
+          }
+          if (seg >= 2 && !(ok = wait_all(bar(Lay::B_SEGE + e), ((seg >> 1) - 1) & 1, abort_flag))) break;
+          if (lane == 0) {
+            volatile int* r = ring + 16 * e;
+            r[0] = t.n;
+            r[1] = t.kb0;
+            r[2] = t.j0;
+            r[3] = t.j1;
+            r[4] = t.rows;
+            r[5] = t.r0;
+            r[6] = t.h;
+            r[7] = t.b;
+            r[8] = t.slot;
+            r[9] = t.first;
+            r[10] = t.s0;
+            r[11] = t.nq;
+            r[12] = t.len;
+            mbar_arrive(bar(Lay::B_SEGF + e));
+          }
+          __syncwarp();
+          if (!more) break;
+          if (seg > 0 && !(ok = wait_all(bar(Lay::B_QFREE), (seg - 1) & 1, abort_flag))) break;
+          copy_q(t);
+          more = paged_next<kRows, kUnit>(a, w, t.n);
+        }
       }
       if (!ok) {
         bits |= kStatusTimeout;
@@ -361,22 +443,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     const float sl2 = a.sl2;
     bool ok = true;
     int blk = 0, cnt = 0;
-    for (int seg = 0; more && ok; ++seg) {
-      int j0, j1;
-      const int n = paged_segment<kUnit>(w, j0, j1);
-      const int r0 = w.rt * kRows, rows = w.t.rows;
+    TcSegment t;
+    for (int seg = 0; take(seg, t, ok); ++seg) {
+      const int n = t.n, r0 = t.r0, rows = t.rows, kb0 = t.kb0;
+      const PagedSeq sq{t.s0, t.nq, t.len, false};
       const bool on = X * kHalf < rows;  // this half has rows
       const bool valid = rl < rows;
       int lo, hi, all_lo = 0, all_hi = 0;
-      paged_row_span(a, w.s, (r0 + (valid ? rl : 0)) / a.G, lo, hi);
-      if (valid && lo >= hi && w.rem == 0 && !a.initL) bits |= kStatusEmptyRow;
+      paged_row_span(a, sq, div_by(r0 + (valid ? rl : 0), a.by_group), lo, hi);
+      if (valid && lo >= hi && t.first && !a.initL) bits |= kStatusEmptyRow;
       if (on) {
         int unused;
-        paged_row_span(a, w.s, (r0 + min(rows, X * kHalf + kHalf) - 1) / a.G, all_lo, unused);
-        paged_row_span(a, w.s, (r0 + X * kHalf) / a.G, unused, all_hi);
+        paged_row_span(a, sq, div_by(r0 + min(rows, X * kHalf + kHalf) - 1, a.by_group), all_lo, unused);
+        paged_row_span(a, sq, div_by(r0 + X * kHalf, a.by_group), unused, all_hi);
       }
       float m_ref = -INFINITY, l = 0.f;
-      const int kb0 = (w.t.kt0 + w.rem) * kUnit;
       for (int u = 0; u < n && on; ++u) {
         const int vf = 2 * (blk + u) + 1, vs = vf % NS;
         if (!(ok = wait_all(bar(Lay::B_KVF + vs), (vf / NS) & 1, abort_flag))) break;
@@ -456,44 +537,74 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       }
       if (!ok) break;
       blk += n;
-      int slot = paged_slot(a, w, n);
       if (!(ok = wait_all(bar(Lay::B_O + X), seg & 1, abort_flag))) break;
       tc_fence_after();
-      const size_t row = slot < 0 ? paged_out_row(a, w.s, w.h, r0 + (valid ? rl : 0))
-                                  : static_cast<size_t>(slot) * kRows + rl;
       const float m = l > 0.f || l != l ? m_ref : -INFINITY;
-      PagedScale f{1.f, 0.f, 0.f};
-      if (slot < 0 && valid) f = paged_finish(a, row, m, l);
+      if (t.slot >= 0) {
+        // The summary, columns outside rows: a warp's stores are whole lines.
+        float4* z = reinterpret_cast<float4*>(a.pz) + static_cast<size_t>(t.slot) * (a.v / 4) * kRows + rl;
 #pragma unroll
-      for (int ch = 0; ch < D / 32; ++ch) {
-        if (!on) break;
-        uint32_t o[32];
-        tmem_ld32(t_o + ch * 32, o);
-        tmem_ld_wait();
-        reg_fence(o);
+        for (int ch = 0; ch < D / 32; ++ch) {
+          if (!on || ch * 32 >= a.v) break;
+          uint32_t o[32];
+          tmem_ld32(t_o + ch * 32, o);
+          tmem_ld_wait();
+          reg_fence(o);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (valid && ch * 32 + 4 * e < a.v)
+              z[(ch * 8 + e) * kRows] =
+                  make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                              __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+        }
+        tc_fence_before();
+        mbar_arrive(bar(Lay::B_OREAD + X));
         if (valid) {
+          a.pm[static_cast<size_t>(t.slot) * kRows + rl] = m;
+          a.pl[static_cast<size_t>(t.slot) * kRows + rl] = l;
+        }
+      } else {
+        const size_t row = paged_out_row(a, sq, t.h, r0 + (valid ? rl : 0));
+        PagedScale f{0.f, 0.f, 0.f};
+        if (valid) {
+          f = paged_finish(a, row, m, l);
+          a.L[row] = f.L;
+        }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int col = ch * 32 + 4 * e;
-            if (col >= a.v) break;
-            const float4 z = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                         __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-            if (slot < 0) paged_store4(a, row, col, paged_join4(a, f, row, col, z));
-            else *reinterpret_cast<float4*>(a.pz + row * a.v + col) = z;
+        for (int ch = 0; ch < D / 32; ++ch) {
+          if (!on || ch * 32 >= a.v) break;
+          uint32_t o[32];
+          tmem_ld32(t_o + ch * 32, o);
+          tmem_ld_wait();
+          reg_fence(o);
+          if (!valid) continue;
+          if (!a.initY && !a.Yf) {
+            uint4* y = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.Y) + row * a.v + ch * 32);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // eight columns a store (v is a multiple of 8)
+              if (ch * 32 + 8 * e >= a.v) break;
+              uint32_t h[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                h[k] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * f.fz,
+                                   __uint_as_float(o[8 * e + 2 * k + 1]) * f.fz);
+              y[e] = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int col = ch * 32 + 4 * e;
+              if (col >= a.v) break;
+              paged_store4(a, row, col,
+                           paged_join4(a, f, row, col,
+                                       make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                   __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]))));
+            }
           }
         }
+        tc_fence_before();
+        mbar_arrive(bar(Lay::B_OREAD + X));
       }
-      tc_fence_before();
-      mbar_arrive(bar(Lay::B_OREAD + X));
-      if (valid) {
-        if (slot < 0) {
-          a.L[row] = f.L;
-        } else {
-          a.pm[row] = m;
-          a.pl[row] = l;
-        }
-      }
-      more = paged_next<kRows, kUnit>(a, w, n);
     }
     if (!ok) {
       bits |= kStatusTimeout;
@@ -502,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
   }
 
   tc_fence_before();
-  paged_end(a, bits);
+  paged_end(a, bits, reinterpret_cast<unsigned*>(misc + 2));
   if (warp == kWarpMMA) {
     tc_fence_after();
     __syncwarp();
@@ -537,7 +648,7 @@ cudaError_t tc_launch(const PagedArgs& a, cudaStream_t s) {
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcLayout<D>::ALLOC);
   if (e != cudaSuccess) return e;
   before_launch(kKernPaged, s);
-  kern<<<a.ctas, kThreads, TcLayout<D>::ALLOC, s>>>(p);
+  kern<<<kCtas, kThreads, TcLayout<D>::ALLOC, s>>>(p);
   after_launch(kKernPaged, s);
   return cudaGetLastError();
 }
@@ -547,10 +658,10 @@ cudaError_t tc_launch(const PagedArgs& a, cudaStream_t s) {
 // Pages of at least 8 rows (a swizzle atom), pool rows within TMA's 32-bit
 // coordinates, a scale whose sign keeps the maximum a maximum.
 bool paged_tc_supported(const PagedArgs& a) {
-  return paged_mma_shape(a.dtype, a.d, a.v) && a.lps >= 3 && a.sl2 > 0.f &&
+  return a.dtype == kBF16 && paged_mma_shape(a.d, a.v) && a.lps >= 3 && a.sl2 > 0.f &&
          ((static_cast<long long>(a.num_pages) * a.Hk) << a.lps) < (1ll << 31) && tmap_encoder() != nullptr;
 }
-PagedKernel paged_tc_kernel_of() { return {kRows, 152}; }
+PagedKernel paged_tc_kernel_of() { return {kRows, kCtas, kCtas, 1}; }
 
 cudaError_t launch_paged_tc(const PagedArgs& a, cudaStream_t s) {
   return a.d <= 64 && a.v <= 64 ? tc_launch<64>(a, s) : tc_launch<128>(a, s);

@@ -30,7 +30,10 @@ def path(ex, request):
 
 def _p_bits(path, dtype, tokens, batch, group):
     """Significant bits of p in P.V: the kernel for many rows to a key head rounds it to
-    bf16 (off by 2^-8 of p at most), the others keep 16 or more."""
+    bf16 (off by 2^-8 of p at most), the one for few keeps 2^-17 in bf16; in fp32 p is
+    whole or two tf32 parts (2^-21), which the sums' own terms cover."""
+    if dtype == "f32":
+        return 21
     many = -(-tokens // batch) * group > 64
     return 8 if path == "auto" and dtype == "bf16" and many else 16
 
@@ -168,7 +171,7 @@ def test_a_key_that_a_row_does_not_allow_leaves_no_trace_in_its_score(ex, path, 
         ref = oracle.attend(b.np(b.q[:1]), b.np(b.k_pages), b.np(b.v_pages), b.table, np.array([99]),
                             [0, 1], 0.125, "causal")
         y, L, _ = _attend(ex, b, "causal", 0, 0.125)
-        check_attention(dtype, y[:1], L[:1], ref, 64, 99)
+        check_attention(dtype, y[:1], L[:1], ref, 64, 99, _p_bits(path, dtype, 2, 1, 2))
 
 
 def test_equal_tokens_without_q_starts(ex, path):

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -134,6 +135,8 @@ def load_library():
     lib.attn_fwd_paged.restype = ci
     lib.attn_fwd_prefix.argtypes = [pp, vp, vp, vp, vp, ci, vp, vp, vp, cf, ci, vp, vp, vp, sz, vp]
     lib.attn_fwd_prefix.restype = ci
+    lib.exattn_paged_run.argtypes = [ci, ctypes.c_char_p]  # a packed exattn_paged_call
+    lib.exattn_paged_run.restype = ci
     lib.exattn_last_error.argtypes = []
     lib.exattn_last_error.restype = ctypes.c_char_p
     lib.exattn_host_step_workspace_size.argtypes = [sp, ci]
@@ -456,29 +459,49 @@ def _int32(name, x) -> int:
     return x
 
 
-def _paged_outputs(q, vw, y, L):
+def _check_outputs(q, vw, y, L):
     want = (q.shape[0], q.shape[1], vw)
-    if y is None:
-        y = torch.empty(want, dtype=q.dtype, device=q.device)
-    elif tuple(y.shape) != want or y.dtype != q.dtype or y.device != q.device or not y.is_contiguous():
+    if y is not None and (tuple(y.shape) != want or y.dtype != q.dtype or y.device != q.device
+                          or not y.is_contiguous()):
         raise ValueError(f"y must be a contiguous {q.dtype} tensor of shape {want} on {q.device}")
-    if L is None:
-        L = torch.empty(want[:2], dtype=torch.float32, device=q.device)
-    elif (tuple(L.shape) != want[:2] or L.dtype != torch.float32 or L.device != q.device
-          or not L.is_contiguous()):
+    if L is not None and (tuple(L.shape) != want[:2] or L.dtype != torch.float32
+                          or L.device != q.device or not L.is_contiguous()):
         raise ValueError(f"L must be a contiguous float32 tensor of shape {want[:2]} on {q.device}")
-    return y, L
 
 
-def _device_call(device, stream, call):
-    """``call(stream pointer)`` with ``device`` current; ``stream`` None: its current stream."""
-    if device.type != "cuda":
+# A decode step's kernels take a few microseconds, so its checks are made once for each
+# combination of shapes, strides, types and devices: the key holds all that they look at,
+# the value is the fields of the PagedShape.
+_paged_known = {}
+_PAGED_CALL = struct.Struct("@10i3q15Qf5i")  # exattn_paged_call
+
+
+def _meta(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _remember(key, shape):
+    if len(_paged_known) >= 4096:
+        _paged_known.clear()
+    known = tuple(getattr(shape, name) for name, _ in PagedShape._fields_)
+    _paged_known[key] = known
+    return known
+
+
+def _paged_call(op, name, index, known, stream, fields):
+    """exattn_paged_run on the device ``index``; ``fields``: the call's from the workspace's
+    size on, before and behind the stream."""
+    if index < 0:
         raise ValueError("tensors must be on a CUDA device")
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if device.index is None or device.index == torch.cuda.current_device():
-        return call(s.cuda_stream)
-    with torch.cuda.device(device):
-        return call(s.cuda_stream)
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    call = _PAGED_CALL.pack(*known, *fields[0], s, *fields[1])
+    if index == torch.cuda.current_device():
+        st = _lib.exattn_paged_run(op, call)
+    else:
+        with torch.cuda.device(index):
+            st = _lib.exattn_paged_run(op, call)
+    if st != 0:
+        raise ExattnError(st, name)
 
 
 def append_paged(k, v, k_pages, v_pages, page_table, seq_lens, q_starts=None, q=None, q_out=None,
@@ -489,63 +512,88 @@ def append_paged(k, v, k_pages, v_pages, page_table, seq_lens, q_starts=None, q=
     returned (``q_out`` may be given, and may be ``q``).  seq_lens [batch] counts each sequence's
     tokens with the new ones; q_starts [batch + 1] gives each its range of tokens (None: equally
     many each).  k, v and q may be columns of one projection's output."""
-    lib = load_library()
+    load_library()
     pos_offset = _int32("pos_offset", pos_offset)
-    lead = k if q is None else q
-    shape = _check_paged(lead, k_pages, v_pages, page_table, seq_lens, q_starts, ws)
-    for name, t in (("k", k), ("v", v), ("q_out", q_out)):
-        if t is not None and (t.dtype != lead.dtype or t.device != lead.device):
-            raise ValueError(f"{name} must be {lead.dtype} on {lead.device}")
-    shape.k_stride = _token_stride("k", k, shape.kv_heads, shape.d)
-    shape.v_stride = _token_stride("v", v, shape.kv_heads, shape.v)
-    if k.shape[0] != shape.tokens or v.shape[0] != shape.tokens:
-        raise ValueError(f"q, k and v must have as many tokens: {shape.tokens}, {k.shape[0]}, "
-                         f"{v.shape[0]}")
-    if q is not None:
-        shape.q_stride = _token_stride("q", q, shape.heads, shape.d)
-        if q_out is None:
-            q_out = torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)
-        elif q_out.shape != q.shape or not q_out.is_contiguous():
-            raise ValueError(f"q_out must be contiguous of shape {tuple(q.shape)}")
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    pairs = 0
-    if inv_freq is not None:
-        if (inv_freq.dim() != 1 or inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous()
-                or inv_freq.device != lead.device):
+    key = (0, _meta(k), _meta(v), _meta(k_pages), _meta(v_pages), _meta(page_table), _meta(seq_lens),
+           _meta(q_starts), _meta(q), _meta(q_out), _meta(inv_freq), _meta(ws))
+    known = _paged_known.get(key)
+    if known is None:
+        lead = k if q is None else q
+        shape = _check_paged(lead, k_pages, v_pages, page_table, seq_lens, q_starts, ws)
+        for name, t in (("k", k), ("v", v), ("q_out", q_out)):
+            if t is not None and (t.dtype != lead.dtype or t.device != lead.device):
+                raise ValueError(f"{name} must be {lead.dtype} on {lead.device}")
+        shape.k_stride = _token_stride("k", k, shape.kv_heads, shape.d)
+        shape.v_stride = _token_stride("v", v, shape.kv_heads, shape.v)
+        if k.shape[0] != shape.tokens or v.shape[0] != shape.tokens:
+            raise ValueError(f"q, k and v must have as many tokens: {shape.tokens}, {k.shape[0]}, "
+                             f"{v.shape[0]}")
+        if q is not None:
+            shape.q_stride = _token_stride("q", q, shape.heads, shape.d)
+            if q_out is not None and (q_out.shape != q.shape or not q_out.is_contiguous()):
+                raise ValueError(f"q_out must be contiguous of shape {tuple(q.shape)}")
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        if inv_freq is not None and (
+                inv_freq.dim() != 1 or inv_freq.dtype != torch.float32
+                or not inv_freq.is_contiguous() or inv_freq.device != lead.device):
             raise ValueError(f"inv_freq must be contiguous float32 [pairs] on {lead.device}")
-        pairs = inv_freq.numel()
+        known = _remember(key, shape)
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if ws is None:
-        ws = workspace(256, lead.device)
-    st = _device_call(lead.device, stream, lambda s: lib.attn_append_paged(
-        shape, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
-        page_table.data_ptr(), seq_lens.data_ptr(), None if q_starts is None else q_starts.data_ptr(),
-        inv_freq.data_ptr() if pairs else None, pairs, int(bool(interleaved)), pos_offset,
-        None if q is None else q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-        ws.data_ptr(), _nbytes(ws), s))
-    if st != 0:
-        raise ExattnError(st, "attn_append_paged")
+        ws = workspace(256, k.device)
+    pairs = 0 if inv_freq is None else inv_freq.numel()
+    _paged_call(0, "attn_append_paged", k.get_device(), known, stream, (
+        (0 if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), k_pages.data_ptr(),
+         v_pages.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
+         0 if q_starts is None else q_starts.data_ptr(), 0, inv_freq.data_ptr() if pairs else 0,
+         0 if q is None else q_out.data_ptr(), 0, ws.data_ptr(), ws.nbytes),
+        (0.0, 0, 0, pos_offset, pairs, 1 if interleaved else 0)))
     return q_out
+
+
+def _attend_paged(op, name, q, k_pages, v_pages, prefix_table, prefix_len, page_table, seq_lens, scale,
+                  mask, window, q_starts, y, L, ws, stream):
+    load_library()
+    window = _int32("window", window)
+    prefix_len = _int32("prefix_len", prefix_len)
+    key = (op, _meta(q), _meta(k_pages), _meta(v_pages), _meta(page_table), _meta(seq_lens),
+           _meta(q_starts), _meta(prefix_table), _meta(y), _meta(L), _meta(ws))
+    known = _paged_known.get(key)
+    if known is None:
+        shape = _check_paged(q, k_pages, v_pages, page_table, seq_lens, q_starts, ws)
+        shape.q_stride = _token_stride("q", q, shape.heads, shape.d)
+        if op == 2 and (prefix_table.dtype != torch.int32 or prefix_table.dim() != 1
+                        or not prefix_table.is_contiguous() or prefix_table.device != q.device):
+            raise ValueError(f"prefix_table must be contiguous int32 [pages] on {q.device}")
+        _check_outputs(q, shape.v, y, L)
+        known = _remember(key, shape)
+    if op == 2 and prefix_table.numel() * k_pages.shape[2] < prefix_len:
+        raise ValueError(f"prefix_table holds {prefix_table.numel()} pages of {k_pages.shape[2]}, "
+                         f"the prefix has {prefix_len} keys")
+    if y is None:
+        y = torch.empty(q.shape[:2] + v_pages.shape[3:], dtype=q.dtype, device=q.device)
+    if L is None:
+        L = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    if ws is None:
+        shape = PagedShape(*known)
+        ws = workspace(prefix_workspace_size(shape) if op == 2 else paged_workspace_size(shape), q.device)
+    _paged_call(op, name, q.get_device(), known, stream, (
+        (q.data_ptr(), 0, 0, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+         seq_lens.data_ptr(), 0 if q_starts is None else q_starts.data_ptr(),
+         0 if prefix_table is None else prefix_table.data_ptr(), 0, y.data_ptr(), L.data_ptr(),
+         ws.data_ptr(), ws.nbytes),
+        (float(scale), _mask_kind(mask), window, prefix_len, 0, 0)))
+    return y, L
 
 
 def fwd_paged(q, k_pages, v_pages, page_table, seq_lens, scale, mask="none", window=0, q_starts=None,
               y=None, L=None, ws=None, stream=None):
     """attn_fwd_paged -> (Y [tokens, heads, v], L [tokens, heads]): q [tokens, heads, d] over the
     cached keys of each token's sequence (see append_paged for the tables)."""
-    lib = load_library()
-    shape = _check_paged(q, k_pages, v_pages, page_table, seq_lens, q_starts, ws)
-    shape.q_stride = _token_stride("q", q, shape.heads, shape.d)
-    y, L = _paged_outputs(q, shape.v, y, L)
-    if ws is None:
-        ws = workspace(lib.exattn_paged_workspace_size(shape), q.device)
-    window = _int32("window", window)
-    st = _device_call(q.device, stream, lambda s: lib.attn_fwd_paged(
-        shape, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-        seq_lens.data_ptr(), None if q_starts is None else q_starts.data_ptr(), float(scale),
-        _mask_kind(mask), window, y.data_ptr(), L.data_ptr(), ws.data_ptr(), _nbytes(ws), s))
-    if st != 0:
-        raise ExattnError(st, "attn_fwd_paged")
-    return y, L
+    return _attend_paged(1, "attn_fwd_paged", q, k_pages, v_pages, None, 0, page_table, seq_lens, scale,
+                         mask, window, q_starts, y, L, ws, stream)
 
 
 def fwd_prefix(q, k_pages, v_pages, prefix_table, prefix_len, page_table, seq_lens, scale,
@@ -553,27 +601,8 @@ def fwd_prefix(q, k_pages, v_pages, prefix_table, prefix_len, page_table, seq_le
     """attn_fwd_prefix -> (Y, L): fwd_paged for sequences that all begin with the
     ``prefix_len`` keys of the pages ``prefix_table`` (int32 [pages]), which are read once for all of
     them; page_table and seq_lens describe each sequence's own keys behind the prefix."""
-    lib = load_library()
-    shape = _check_paged(q, k_pages, v_pages, page_table, seq_lens, q_starts, ws)
-    shape.q_stride = _token_stride("q", q, shape.heads, shape.d)
-    prefix_len = _int32("prefix_len", prefix_len)
-    if (prefix_table.dtype != torch.int32 or prefix_table.dim() != 1
-            or not prefix_table.is_contiguous() or prefix_table.device != q.device):
-        raise ValueError(f"prefix_table must be contiguous int32 [pages] on {q.device}")
-    if prefix_table.numel() * shape.page_size < prefix_len:
-        raise ValueError(f"prefix_table holds {prefix_table.numel()} pages of {shape.page_size}, "
-                         f"the prefix has {prefix_len} keys")
-    y, L = _paged_outputs(q, shape.v, y, L)
-    if ws is None:
-        ws = workspace(lib.exattn_prefix_workspace_size(shape), q.device)
-    st = _device_call(q.device, stream, lambda s: lib.attn_fwd_prefix(
-        shape, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), prefix_table.data_ptr(),
-        prefix_len, page_table.data_ptr(), seq_lens.data_ptr(),
-        None if q_starts is None else q_starts.data_ptr(), float(scale), _mask_kind(mask),
-        y.data_ptr(), L.data_ptr(), ws.data_ptr(), _nbytes(ws), s))
-    if st != 0:
-        raise ExattnError(st, "attn_fwd_prefix")
-    return y, L
+    return _attend_paged(2, "attn_fwd_prefix", q, k_pages, v_pages, prefix_table, prefix_len, page_table,
+                         seq_lens, scale, mask, 0, q_starts, y, L, ws, stream)
 
 
 def bwd_noalloc(q, k, v, y, dy, L, scale, mask="none", window=0, bitmask=None, dq=None,

@@ -5,7 +5,11 @@
 // rotated row turns by (pos + pos_offset) * inv_freq[f]:
 //   x' = x cos - y sin,  y' = y cos + x sin,
 // pairs (f, f + pairs) or, interleaved, (2f, 2f + 1); other columns pass.
-// Bound by memory: every element is read once and written once.
+// Bound by memory: every element is read once and written once, in 16-byte accesses
+// where the rotated halves allow them.  A CTA takes the accesses of a few tokens as one
+// list.  A thread's source addresses need no table, so it loads first and works out
+// angles and places while the loads are under way.  One CTA more checks that every
+// token has a place and writes the status word.
 #include "paged.cuh"
 
 namespace exattn {
@@ -58,111 +62,12 @@ template <int N> struct Vec<__nv_bfloat16, N> {
   }
 };
 
-// W: elements of an access.  Interleaved pairs stay inside an access; the two
-// halves of the other form are W apart in units when W divides `pairs`.
-template <typename T, int W>
-__device__ __forceinline__ void rotate_row(const AppendArgs& a, const T* src, T* dst, int unit,
-                                           const float* cs, const float* sn) {
-  if (a.interleaved) {
-    float x[W];
-    Vec<T, W>::load(src + unit * W, x);
-    if constexpr (W > 1) {
-#pragma unroll
-      for (int e = 0; e < W; e += 2) {
-        const int f = (unit * W + e) >> 1;
-        if (f < a.pairs) {
-          const float c = cs[f], s = sn[f], x0 = x[e], x1 = x[e + 1];
-          x[e] = x0 * c - x1 * s;
-          x[e + 1] = x1 * c + x0 * s;
-        }
-      }
-    }
-    Vec<T, W>::store(dst + unit * W, x);
-    return;
-  }
-  const int half = a.pairs / W;
-  if (unit < half) {
-    float x[W], y[W], p[W], q[W];
-    Vec<T, W>::load(src + unit * W, x);
-    Vec<T, W>::load(src + a.pairs + unit * W, y);
-#pragma unroll
-    for (int e = 0; e < W; ++e) {
-      const float c = cs[unit * W + e], s = sn[unit * W + e];
-      p[e] = x[e] * c - y[e] * s;
-      q[e] = y[e] * c + x[e] * s;
-    }
-    Vec<T, W>::store(dst + unit * W, p);
-    Vec<T, W>::store(dst + a.pairs + unit * W, q);
-  } else {
-    float x[W];
-    const int col = (unit + half) * W;
-    Vec<T, W>::load(src + col, x);
-    Vec<T, W>::store(dst + col, x);
-  }
-}
-
-template <typename T, int W>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
-  __shared__ float cs[kMaxPairs], sn[kMaxPairs];
-  const int t = blockIdx.x;
-  const int b = owner(a, t);
-  if (b < 0) return;  // behind the last sequence
-  int s0, nq;
-  if (a.starts) {
-    s0 = __ldg(a.starts + b);
-    nq = __ldg(a.starts + b + 1) - s0;
-  } else {
-    nq = a.T / a.B;
-    s0 = b * nq;
-  }
-  const int pos = __ldg(a.lens + b) - nq + (t - s0);
-  for (int f = threadIdx.x; f < a.pairs; f += kAppendThreads) {
-    // Whole turns are dropped in 64 bits: far positions keep their angle.
-    constexpr double kInv2Pi = 0.15915494309189533577;
-    const double turns = (static_cast<double>(pos) + a.pos_offset) *
-                         (static_cast<double>(a.inv_freq[f]) * kInv2Pi);
-    sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &sn[f], &cs[f]);
-  }
-  // Where the token's key and value go; -1: nowhere.
-  long long slot = -1;
-  if (pos >= 0 && pos < a.max_pages << a.lps) {
-    const int page = __ldg(a.table + static_cast<size_t>(b) * a.max_pages + (pos >> a.lps));
-    if (static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages))
-      slot = (static_cast<long long>(page) * a.Hk << a.lps) + (pos & ((1 << a.lps) - 1));
-  }
-  __syncthreads();
-  const int units = (a.interleaved ? a.d : a.d - a.pairs) / W;  // of a row of q or k
-  if (a.q) {
-    const T* src = static_cast<const T*>(a.q) + t * a.qs;
-    T* dst = static_cast<T*>(a.q_out) + static_cast<size_t>(t) * a.H * a.d;
-    for (int x = threadIdx.x; x < a.H * units; x += kAppendThreads) {
-      const int h = x / units, u = x - h * units;
-      rotate_row<T, W>(a, src + h * a.d, dst + h * a.d, u, cs, sn);
-    }
-  }
-  if (slot < 0) return;
-  const T* ks = static_cast<const T*>(a.k) + t * a.ks;
-  T* kd = static_cast<T*>(a.kp) + slot * a.d;
-  for (int x = threadIdx.x; x < a.Hk * units; x += kAppendThreads) {
-    const int h = x / units, u = x - h * units;
-    rotate_row<T, W>(a, ks + h * a.d, kd + (static_cast<size_t>(h) << a.lps) * a.d, u, cs, sn);
-  }
-  constexpr int E = 16 / sizeof(T);
-  const int vch = a.vw / E;
-  const T* vs = static_cast<const T*>(a.v) + t * a.vs;
-  T* vd = static_cast<T*>(a.vp) + slot * a.vw;
-  for (int x = threadIdx.x; x < a.Hk * vch; x += kAppendThreads) {
-    const int h = x / vch, u = x - h * vch;
-    *reinterpret_cast<uint4*>(vd + (static_cast<size_t>(h) << a.lps) * a.vw + u * E) =
-        *reinterpret_cast<const uint4*>(vs + h * a.vw + u * E);
-  }
-}
-
-// Status: whether every new token has a place.  One CTA; a thread takes a
-// sequence at a time, a warp the pages of a long one.
-__global__ void __launch_bounds__(kAppendThreads) append_check_kernel(const AppendArgs a) {
+// Status: whether every new token has a place.  A thread takes a sequence at a time, a
+// warp the pages of a long one.
+__device__ void append_check(const AppendArgs& a) {
   bool bad = false;
   const int lane = threadIdx.x & 31;
+#pragma unroll 1
   for (int b0 = (threadIdx.x & ~31); b0 < a.B; b0 += kAppendThreads) {
     const int b = b0 + lane;
     int first = 0, last = -1;  // pages of the new tokens
@@ -179,31 +84,176 @@ __global__ void __launch_bounds__(kAppendThreads) append_check_kernel(const Appe
       if (nq > 0) {
         bad |= n < nq;
         first = max(0, min(n, cap) - nq) >> a.lps;
-        last = (min(n, cap) - 1) >> a.lps;  // below `first` when n <= 0
-        if (n <= 0) last = -1;
+        last = n > 0 ? (min(n, cap) - 1) >> a.lps : -1;
       }
     }
-    const bool many = last - first >= 4;
-    for (int p = first; !many && p <= last; ++p)
-      bad |= static_cast<unsigned>(__ldg(a.table + static_cast<size_t>(b) * a.max_pages + p)) >=
+    auto outside = [&](int of, int p) {
+      return static_cast<unsigned>(__ldg(a.table + static_cast<size_t>(of) * a.max_pages + p)) >=
              static_cast<unsigned>(a.num_pages);
+    };
+    const bool many = last - first >= 4;
+#pragma unroll 1
+    for (int p = first; !many && p <= last; ++p) bad |= outside(b, p);
+#pragma unroll 1
     for (unsigned todo = __ballot_sync(0xFFFFFFFFu, many); todo; todo &= todo - 1) {
       const int who = __ffs(todo) - 1;
       const int f = __shfl_sync(0xFFFFFFFFu, first, who), e = __shfl_sync(0xFFFFFFFFu, last, who);
-      for (int p = f + lane; p <= e; p += 32)
-        bad |= static_cast<unsigned>(__ldg(a.table + static_cast<size_t>(b0 + who) * a.max_pages + p)) >=
-               static_cast<unsigned>(a.num_pages);
+      for (int p = f + lane; p <= e; p += 32) bad |= outside(b0 + who, p);
     }
   }
   const int any = __syncthreads_or(bad);
   if (threadIdx.x == 0) *a.status = any ? kStatusBadPage : 0u;
 }
 
+constexpr int kMaxPer = 8;    // tokens of a CTA
+constexpr int kPerThread = 2;  // accesses of a thread whose loads overlap
+
+// W: elements of an access.  A rotated row is cut into units: interleaved, unit u is
+// access u; else units below pairs / W are the accesses u W and pairs + u W of the two
+// halves, those above one access of the columns that pass.
 template <typename T, int W>
-cudaError_t append_launch(const AppendArgs& a, cudaStream_t s) {
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a) {
+  if (blockIdx.x == gridDim.x - 1) {
+    append_check(a);
+    return;
+  }
+  __shared__ float cs[kMaxPer][kMaxPairs], sn[kMaxPer][kMaxPairs];
+  __shared__ long long slots[kMaxPer];  // the token's row of the pool (key head 0); -1: nowhere
+  __shared__ bool owned[kMaxPer];
+  constexpr int E = 16 / sizeof(T);
+  const int t0 = blockIdx.x * a.per, tokens = min(a.per, a.T - t0);
+  const int total = tokens * a.by_items.d, half = a.pairs / W;
+  bool placed = false;
+#pragma unroll 1
+  for (int base = 0; base < total; base += kPerThread * kAppendThreads) {
+    float x[kPerThread][W], y[kPerThread][W];
+    uint4 raw[kPerThread];
+    int tok[kPerThread], head[kPerThread], unit[kPerThread], kind[kPerThread];  // kind: 0 q, 1 k, 2 v, 3 none
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      const int idx = base + j * kAppendThreads + threadIdx.x;
+      kind[j] = 3;
+      if (idx >= total) continue;
+      tok[j] = div_by(idx, a.by_items);
+      int i = idx - tok[j] * a.by_items.d;
+      const int t = t0 + tok[j];
+      if (i < a.qk_items) {
+        kind[j] = i < a.q_items ? 0 : 1;
+        if (kind[j] == 1) i -= a.q_items;
+        head[j] = div_by(i, a.by_units);
+        unit[j] = i - head[j] * a.by_units.d;
+        const T* src = (kind[j] == 0 ? static_cast<const T*>(a.q) + t * a.qs : static_cast<const T*>(a.k) + t * a.ks) +
+                       head[j] * a.d;
+        if (a.interleaved) {
+          Vec<T, W>::load(src + unit[j] * W, x[j]);
+        } else if (unit[j] < half) {
+          Vec<T, W>::load(src + unit[j] * W, x[j]);
+          Vec<T, W>::load(src + a.pairs + unit[j] * W, y[j]);
+        } else {
+          Vec<T, W>::load(src + (unit[j] + half) * W, x[j]);
+        }
+      } else {
+        i -= a.qk_items;
+        kind[j] = 2;
+        head[j] = div_by(i, a.by_vch);
+        unit[j] = i - head[j] * a.by_vch.d;
+        raw[j] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + t * a.vs + head[j] * a.vw + unit[j] * E);
+      }
+    }
+    if (!placed) {
+      placed = true;
+#pragma unroll 1
+      for (int i = threadIdx.x; i < tokens * max(a.pairs, 1); i += kAppendThreads) {
+        const int k = i / max(a.pairs, 1), f = i - k * max(a.pairs, 1), t = t0 + k;
+        const int b = owner(a, t);
+        if (f == 0) owned[k] = b >= 0;
+        if (b < 0) continue;
+        int s0, nq;
+        if (a.starts) {
+          s0 = __ldg(a.starts + b);
+          nq = __ldg(a.starts + b + 1) - s0;
+        } else {
+          nq = a.T / a.B;
+          s0 = b * nq;
+        }
+        const int pos = __ldg(a.lens + b) - nq + (t - s0);
+        if (f == 0) {
+          long long slot = -1;
+          if (pos >= 0 && pos < a.max_pages << a.lps) {
+            const int page = __ldg(a.table + static_cast<size_t>(b) * a.max_pages + (pos >> a.lps));
+            if (static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages))
+              slot = (static_cast<long long>(page) * a.Hk << a.lps) + (pos & ((1 << a.lps) - 1));
+          }
+          slots[k] = slot;
+        }
+        if (f < a.pairs) {
+          // Whole turns are dropped in 64 bits: far positions keep their angle.
+          constexpr double kInv2Pi = 0.15915494309189533577;
+          const double turns = (static_cast<double>(pos) + a.pos_offset) *
+                               (static_cast<double>(a.inv_freq[f]) * kInv2Pi);
+          sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &sn[k][f], &cs[k][f]);
+        }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      if (kind[j] == 3 || !owned[tok[j]]) continue;
+      const long long slot = slots[tok[j]];
+      if (kind[j] == 2) {
+        if (slot >= 0)
+          *reinterpret_cast<uint4*>(static_cast<T*>(a.vp) +
+                                    (slot + (static_cast<long long>(head[j]) << a.lps)) * a.vw + unit[j] * E) = raw[j];
+        continue;
+      }
+      if (kind[j] == 1 && slot < 0) continue;
+      T* dst = kind[j] == 0 ? static_cast<T*>(a.q_out) + (static_cast<size_t>(t0 + tok[j]) * a.H + head[j]) * a.d
+                            : static_cast<T*>(a.kp) + (slot + (static_cast<long long>(head[j]) << a.lps)) * a.d;
+      const float *c = cs[tok[j]], *s = sn[tok[j]];
+      if (a.interleaved) {
+        if constexpr (W > 1) {
+#pragma unroll
+          for (int e = 0; e < W; e += 2) {
+            const int f = (unit[j] * W + e) >> 1;
+            if (f < a.pairs) {
+              const float x0 = x[j][e], x1 = x[j][e + 1];
+              x[j][e] = x0 * c[f] - x1 * s[f];
+              x[j][e + 1] = x1 * c[f] + x0 * s[f];
+            }
+          }
+        }
+        Vec<T, W>::store(dst + unit[j] * W, x[j]);
+      } else if (unit[j] < half) {
+        float p[W], q[W];
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const int f = unit[j] * W + e;
+          p[e] = x[j][e] * c[f] - y[j][e] * s[f];
+          q[e] = y[j][e] * c[f] + x[j][e] * s[f];
+        }
+        Vec<T, W>::store(dst + unit[j] * W, p);
+        Vec<T, W>::store(dst + a.pairs + unit[j] * W, q);
+      } else {
+        Vec<T, W>::store(dst + (unit[j] + half) * W, x[j]);
+      }
+    }
+  }
+}
+
+template <typename T, int W>
+cudaError_t append_launch(AppendArgs a, cudaStream_t s) {
+  const int units = (a.interleaved ? a.d : a.d - a.pairs) / W, vch = a.vw * static_cast<int>(sizeof(T)) / 16;
+  a.by_units = fast_div(units);
+  a.by_vch = fast_div(vch);
+  a.q_items = a.q ? a.H * units : 0;
+  a.qk_items = a.q_items + a.Hk * units;
+  a.by_items = fast_div(a.qk_items + a.Hk * vch);
+  // Tokens of a CTA: enough for two accesses a thread, unless that leaves SMs idle.
+  a.per = 1;
+  while (a.per < kMaxPer && a.per * a.by_items.d < kPerThread * kAppendThreads && a.T / (2 * a.per) >= 4 * 152)
+    a.per *= 2;
   before_launch(kKernAppend, s);
-  append_check_kernel<<<1, kAppendThreads, 0, s>>>(a);
-  append_kernel<T, W><<<a.T, kAppendThreads, 0, s>>>(a);
+  append_kernel<T, W><<<(a.T + a.per - 1) / a.per + 1, kAppendThreads, 0, s>>>(a);
   after_launch(kKernAppend, s);
   return cudaGetLastError();
 }

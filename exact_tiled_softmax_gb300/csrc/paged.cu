@@ -74,6 +74,8 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
   const T* Vp = static_cast<const T*>(a.Vp);
   unsigned bits = 0;
   __shared__ unsigned joined;
+  if (a.second) wait_for_previous();
+  let_next_start();
   if (threadIdx.x == 0) {
     a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     joined = 0;
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
         }
       }
     }
-    const int slot = paged_slot(a, w, n, blockIdx.x, threadIdx.x == 0);
+    const int slot = paged_slot<NQ>(a, w, n, blockIdx.x, threadIdx.x == 0);
     __syncthreads();
     for (int idx = threadIdx.x; idx < rows * v; idx += 32 * kW) {
       const int q = idx / v, col = idx - q * v;
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
         }
       }
       if (slot < 0) {
-        const size_t row = paged_out_row(a, w.s, w.h, r0 + q);
+        const size_t row = paged_out_row(a, w.s.s0, w.h, r0 + q);
         const PagedScale f = paged_finish(a, row, M, lq);
         paged_store(a, row, col, paged_join(a, f, row, col, zc));
         if (col == 0) a.L[row] = f.L;
@@ -257,172 +259,180 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
   paged_end(a, bits, &joined);
 }
 
-// The star merge of the row tiles that a worker starts and others end.  kSpread:
-// CTA (x, y) takes row y of the tiles of workers 32 x .. 32 x + 31, all of its warps
-// sharing a row's pieces; else rows 16 y .. 16 y + 15 of the tiles of workers 4 x ..
-// 4 x + 3, a warp a row.  (Measured with a CTA for every worker and row: 2 us a
-// thousand CTAs, most of them without a tile.)  CTA (0, 0) also joins the status bits
-// of every CTA of the attention launches.
-constexpr int kMergeW = 16;
-
-// What a warp gathers of one row: pieces part, part + step, ... of `parts`.
-struct Gathered {
-  float l;
-  float4 z[2];
-};
-__device__ __forceinline__ Gathered gather_row(const PagedArgs& a, int c, int rt, int q, int parts, int part,
-                                               int step, float& M) {
-  const int lane = threadIdx.x & 31, v = a.v;
-  // Piece 0 is slot 2c + 1, piece k > 0 slot 2 (c + k).
-  auto at = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * rt + q; };
-  M = -INFINITY;
+// The star merge of the row tiles that one worker starts and others end.  Piece 0 of
+// worker c's tile is in slot 2c + 1, piece k > 0 in slot 2 (c + k).  Each kernel is
+// launched early and waits for the attention kernel at its start; CTA (0, 0) also joins
+// the status bits of every CTA of the attention launches.
+//
+// A row's state while its pieces come in, four at a time so that their loads overlap.
+template <int N>
+struct Gather {
+  float m = -INFINITY, l = 0.f;
+  float4 z[N];
+  __device__ __forceinline__ Gather() {
+#pragma unroll
+    for (int x = 0; x < N; ++x) z[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  // Pieces first, first + step, ... below `parts`; row(k): piece k's index into pm and pl,
+  // at(k, x): its x-th four columns, or null.
+  template <typename R, typename F>
+  __device__ __forceinline__ void take(const PagedArgs& a, int first, int step, int parts, R row, F at) {
 #pragma unroll 1
-  for (int k = lane; k < parts; k += 32) M = fmaxf(M, a.pm[at(k)]);
+    for (int k0 = first; k0 < parts; k0 += 4 * step) {
+      float pm[4], pl[4];
+      float4 p[4][N];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-  const float ref = M == -INFINITY ? 0.f : M;
-  Gathered s{0.f, {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)}};
-#pragma unroll 4
-  for (int k = part; k < parts; k += step) {
-    const size_t row = at(k);
-    const float f = pexp2(a.pm[row] - ref);
-    s.l = fmaf(f, a.pl[row], s.l);
+      for (int j = 0; j < 4; ++j) {
+        const int k = k0 + j * step;
+        const bool on = k < parts;
+        pm[j] = on ? a.pm[row(k)] : -INFINITY;
+        pl[j] = on ? a.pl[row(k)] : 0.f;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int col = 4 * lane + 128 * x;
-      if (col >= v) break;
-      const float4 z = *reinterpret_cast<const float4*>(a.pz + row * v + col);
-      s.z[x].x = fmaf(f, z.x, s.z[x].x);
-      s.z[x].y = fmaf(f, z.y, s.z[x].y);
-      s.z[x].z = fmaf(f, z.z, s.z[x].z);
-      s.z[x].w = fmaf(f, z.w, s.z[x].w);
+        for (int x = 0; x < N; ++x) {
+          const float4* from = on ? at(k, x) : nullptr;
+          p[j][x] = from ? *from : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+      const float top = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), m);
+      const float ref = top == -INFINITY ? 0.f : top;
+      const float f0 = pexp2(m - ref);
+      m = top;
+      l *= f0;
+#pragma unroll
+      for (int x = 0; x < N; ++x) z[x] = make_float4(z[x].x * f0, z[x].y * f0, z[x].z * f0, z[x].w * f0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float f = pexp2(pm[j] - ref);
+        l = fmaf(f, pl[j], l);
+#pragma unroll
+        for (int x = 0; x < N; ++x)
+          z[x] = make_float4(fmaf(f, p[j][x].x, z[x].x), fmaf(f, p[j][x].y, z[x].y), fmaf(f, p[j][x].z, z[x].z),
+                             fmaf(f, p[j][x].w, z[x].w));
+      }
     }
   }
-  return s;
+};
+
+__device__ __forceinline__ void join_status(const PagedArgs& a) {
+  if (!a.status || blockIdx.x != 0 || blockIdx.y != 0) return;
+  __shared__ unsigned joined;
+  if (threadIdx.x == 0) joined = 0;
+  __syncthreads();
+  unsigned bits = 0;
+  for (int k = threadIdx.x; k < a.n_flags; k += blockDim.x) bits |= a.flags0[k];
+  if (bits) atomicOr(&joined, bits);
+  __syncthreads();
+  if (threadIdx.x == 0) *a.status = joined;
 }
 
-// The warp's row out.
-__device__ __forceinline__ void finish_row(const PagedArgs& a, size_t row, float M, const Gathered& s) {
-  const int lane = threadIdx.x & 31;
-  const PagedScale f = paged_finish(a, row, M, s.l);
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int col = 4 * lane + 128 * x;
-    if (col < a.v) paged_store4(a, row, col, paged_join4(a, f, row, col, s.z[x]));
-  }
-  if (lane == 0) a.L[row] = f.L;
-}
+// Tiles of up to 16 rows, summaries row by row ([rows][v]).  kSpread: CTA (x, y) takes
+// row y of the tiles of every gridDim.x-th worker from x on (at most 32), its warps
+// sharing a row's pieces; else a warp takes a row of each.  (A CTA for every worker and
+// row cost 2 us a thousand CTAs, most of them without a tile.)
+constexpr int kMergeW = 16;
 
 template <bool kSpread>
 __global__ void __launch_bounds__(32 * kMergeW) paged_merge_kernel(const PagedArgs a, int rt) {
-  __shared__ float red_l[kMergeW];
-  __shared__ __align__(16) float4 red_z[kSpread ? kMergeW : 1][64];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (a.status && blockIdx.x == 0 && blockIdx.y == 0) {
-    __shared__ unsigned joined;
-    if (threadIdx.x == 0) joined = 0;
-    __syncthreads();
-    unsigned bits = 0;
-    for (int k = threadIdx.x; k < a.n_flags; k += 32 * kMergeW) bits |= a.flags0[k];
-    if (bits) atomicOr(&joined, bits);
-    __syncthreads();
-    if (threadIdx.x == 0) *a.status = joined;
-  }
-  constexpr int kPer = kSpread ? 32 : 4;
-  const int c0 = blockIdx.x * kPer;
+  __shared__ float red_m[kMergeW], red_l[kMergeW];
+  __shared__ __align__(16) float red_z[kSpread ? kMergeW : 1][256];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, v = a.v;
+  let_next_start();
+  wait_for_previous();
+  // Workers far apart: in a small launch only the first ones have tiles.
+  const int cl = blockIdx.x + lane * gridDim.x;
   int4 mine = make_int4(0, 0, 0, 0);
-  if (lane < kPer && c0 + lane < a.workers) mine = a.desc[c0 + lane];
-  for (unsigned todo = __ballot_sync(0xFFFFFFFFu, mine.w > 0); todo; todo &= todo - 1) {
-    const int who = __ffs(todo) - 1, c = c0 + who;
-    const int b = __shfl_sync(0xFFFFFFFFu, mine.x, who), h = __shfl_sync(0xFFFFFFFFu, mine.y, who),
-              tile = __shfl_sync(0xFFFFFFFFu, mine.z, who), parts = __shfl_sync(0xFFFFFFFFu, mine.w, who);
-    const PagedSeq s = paged_seq(a, b);
-    const int q = kSpread ? blockIdx.y : 16 * blockIdx.y + warp;
-    const int r = tile * rt + q;
-    if (q >= rt || r >= s.nq * a.G) continue;  // kSpread: all warps alike
-    const size_t row = paged_out_row(a, s, h, r);
-    float M;
-    Gathered x = gather_row(a, c, rt, q, parts, kSpread ? warp : 0, kSpread ? kMergeW : 1, M);
+  if (cl < a.workers) mine = a.desc[cl];
+  for (unsigned todo = __ballot_sync(0xFFFFFFFFu, mine.w != 0); todo; todo &= todo - 1) {
+    const int who = __ffs(todo) - 1, c = blockIdx.x + who * gridDim.x;
+    const int q = kSpread ? blockIdx.y : warp;
+    const int r = __shfl_sync(0xFFFFFFFFu, mine.x, who) + q, all = __shfl_sync(0xFFFFFFFFu, mine.y, who),
+              s0 = __shfl_sync(0xFFFFFFFFu, mine.z, who), hp = __shfl_sync(0xFFFFFFFFu, mine.w, who);
+    const int parts = hp & 0xFFFF;
+    if (q >= rt || r >= all) continue;  // kSpread: all warps alike
+    const size_t row = paged_out_row(a, s0, static_cast<unsigned>(hp) >> 16, r);
+    Gather<2> x;
+    auto at = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * rt + q; };
+    x.take(a, kSpread ? warp : 0, kSpread ? kMergeW : 1, parts, at, [&](int k, int y) -> const float4* {
+      const int col = 4 * lane + 128 * y;
+      return col < v ? reinterpret_cast<const float4*>(a.pz + at(k) * v + col) : nullptr;
+    });
     if constexpr (kSpread) {
-      if (lane == 0) red_l[warp] = x.l;
-      red_z[warp][lane] = x.z[0];
-      red_z[warp][32 + lane] = x.z[1];
+      if (lane == 0) {
+        red_m[warp] = x.m;
+        red_l[warp] = x.l;
+      }
+      *reinterpret_cast<float4*>(&red_z[warp][4 * lane]) = x.z[0];
+      *reinterpret_cast<float4*>(&red_z[warp][4 * lane + 128]) = x.z[1];
       __syncthreads();
-      if (warp == 0) {
-        for (int k = 1; k < min(kMergeW, parts); ++k) {
-          x.l += red_l[k];
+      const int col = threadIdx.x;
+      if (col < v) {
+        float M = -INFINITY, l = 0.f, z = 0.f;
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float4 z = red_z[k][32 * y + lane];
-            x.z[y] = make_float4(x.z[y].x + z.x, x.z[y].y + z.y, x.z[y].z + z.z, x.z[y].w + z.w);
-          }
+        for (int k = 0; k < kMergeW; ++k) M = fmaxf(M, red_m[k]);
+        const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int k = 0; k < kMergeW; ++k) {
+          const float f = pexp2(red_m[k] - ref);
+          l = fmaf(f, red_l[k], l);
+          z = fmaf(f, red_z[k][col], z);
         }
-        finish_row(a, row, M, x);
+        const PagedScale f = paged_finish(a, row, M, l);
+        paged_store(a, row, col, paged_join(a, f, row, col, z));
+        if (col == 0) a.L[row] = f.L;
       }
       __syncthreads();
     } else {
-      finish_row(a, row, M, x);
+      const PagedScale f = paged_finish(a, row, x.m, x.l);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int col = 4 * lane + 128 * y;
+        if (col < v) paged_store4(a, row, col, paged_join4(a, f, row, col, x.z[y]));
+      }
+      if (lane == 0) a.L[row] = f.L;
     }
   }
+  join_status(a);
 }
 
-// The same for tiles of 256 rows, whose summaries stand column by column ([v / 4][256]
-// pieces of four): CTA (c, y) takes columns 16 y .. 16 y + 15 of worker c's tile, a
-// thread a row, so that loads are whole lines.
+// Tiles of 256 rows, summaries column by column ([v / 4][256] pieces of four): a thread a
+// row, so that loads are whole lines.  CTA (x, y) takes pieces N y .. of the tiles of
+// workers kPer x ..: N = 4, kPer = 1 where most workers start a tile that others end, else
+// N = 1 and kPer = 8.
 constexpr int kTall = 256;
 
+template <int N, int kPer>
 __global__ void __launch_bounds__(kTall) paged_merge_tall_kernel(const PagedArgs a) {
-  if (a.status && blockIdx.x == 0 && blockIdx.y == 0) {
-    __shared__ unsigned joined;
-    if (threadIdx.x == 0) joined = 0;
-    __syncthreads();
-    unsigned bits = 0;
-    for (int k = threadIdx.x; k < a.n_flags; k += kTall) bits |= a.flags0[k];
-    if (bits) atomicOr(&joined, bits);
-    __syncthreads();
-    if (threadIdx.x == 0) *a.status = joined;
-  }
-  const int c = blockIdx.x, q = threadIdx.x, n4 = a.v / 4, first = 4 * blockIdx.y;
-  const int4 t = a.desc[c];
-  if (t.w == 0) return;
-  const PagedSeq s = paged_seq(a, t.x);
-  const int r = t.z * kTall + q;
-  if (r >= s.nq * a.G) return;
-  auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)); };
-  float M = -INFINITY;
-#pragma unroll 4
-  for (int k = 0; k < t.w; ++k) M = fmaxf(M, a.pm[slot(k) * kTall + q]);
-  const float ref = M == -INFINITY ? 0.f : M;
-  float l = 0.f;
-  float4 acc[4];
-#pragma unroll
-  for (int x = 0; x < 4; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int q = threadIdx.x, n4 = a.v / 4, first = N * blockIdx.y;
   const float4* z = reinterpret_cast<const float4*>(a.pz);
-#pragma unroll 2
-  for (int k = 0; k < t.w; ++k) {
-    const float f = pexp2(a.pm[slot(k) * kTall + q] - ref);
-    l = fmaf(f, a.pl[slot(k) * kTall + q], l);
+  let_next_start();
+  wait_for_previous();
+#pragma unroll 1
+  for (int c = blockIdx.x * kPer; c < min(a.workers, (static_cast<int>(blockIdx.x) + 1) * kPer); ++c) {
+    const int4 t = a.desc[c];
+    const int r = t.x + q;
+    if (t.w == 0 || r >= t.y) continue;
+    const size_t row = paged_out_row(a, t.z, static_cast<unsigned>(t.w) >> 16, r);
+    Gather<N> x;
+    auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)); };
+    x.take(a, 0, 1, t.w & 0xFFFF, [&](int k) { return slot(k) * kTall + q; },
+           [&](int k, int y) -> const float4* {
+             return first + y < n4 ? z + (slot(k) * n4 + first + y) * kTall + q : nullptr;
+           });
+    const PagedScale f = paged_finish(a, row, x.m, x.l);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      if (first + x >= n4) break;
-      const float4 p = z[(slot(k) * n4 + first + x) * kTall + q];
-      acc[x] = make_float4(fmaf(f, p.x, acc[x].x), fmaf(f, p.y, acc[x].y), fmaf(f, p.z, acc[x].z),
-                           fmaf(f, p.w, acc[x].w));
-    }
+    for (int y = 0; y < N; ++y)
+      if (first + y < n4)
+        paged_store4(a, row, 4 * (first + y), paged_join4(a, f, row, 4 * (first + y), x.z[y]));
+    if (first == 0) a.L[row] = f.L;
   }
-  const size_t row = paged_out_row(a, s, t.y, r);
-  const PagedScale f = paged_finish(a, row, M, l);
-#pragma unroll
-  for (int x = 0; x < 4; ++x)
-    if (first + x < n4) paged_store4(a, row, 4 * (first + x), paged_join4(a, f, row, 4 * (first + x), acc[x]));
-  if (first == 0) a.L[row] = f.L;
+  join_status(a);
 }
 
 template <typename T, int G, int CPL>
 cudaError_t simt_launch(const PagedArgs& a, bool one_row, cudaStream_t s) {
   before_launch(kKernPaged, s);
-  if (one_row) paged_simt_kernel<T, G, CPL, 1><<<kCtas, 32 * kW, 0, s>>>(a);
-  else paged_simt_kernel<T, G, CPL, 4><<<kCtas, 32 * kW, 0, s>>>(a);
+  auto kern = one_row ? paged_simt_kernel<T, G, CPL, 1> : paged_simt_kernel<T, G, CPL, 4>;
+  kern<<<kCtas, 32 * kW, 0, s>>>(a);
   after_launch(kKernPaged, s);
   return cudaGetLastError();
 }
@@ -444,22 +454,26 @@ cudaError_t launch_paged_simt(const PagedArgs& a, bool one_row, cudaStream_t s) 
   return simt_launch<__nv_bfloat16, 32, 1>(a, one_row, s);
 }
 
-// Rows that a tile can have (q_starts hides how many tokens a sequence has).  Small
-// tiles that may be spread over more than 16 workers give a row to all of a CTA's
-// warps: a warp alone takes one piece of 512 bytes after the other.
+// Rows that a tile can have (q_starts hides how many tokens a sequence has).  Tiles that
+// may be spread over more than 16 workers give a row to all of a CTA's warps: a warp
+// alone takes four pieces of 512 bytes after four.
 cudaError_t launch_paged_merge(const PagedArgs& a, int rt, cudaStream_t s) {
   const long long all = static_cast<long long>(a.starts ? a.T : a.each) * a.G;
   const unsigned rows = static_cast<unsigned>(all < rt ? all : rt);
-  const bool spread = a.workers > 16 * a.B * a.Hk;
+  const unsigned n4 = a.v / 4, workers = a.workers;
+  const long long usual = (static_cast<long long>(a.T + a.B - 1) / a.B * a.G + rt - 1) / rt;
+  const long long tiles = usual * a.B * a.Hk;
+  const bool spread = workers > (rt == kTall ? 8 : 16) * tiles;
+  cudaError_t e;
   before_launch(kKernPagedMerge, s);
   if (rt == kTall)
-    paged_merge_tall_kernel<<<dim3(a.workers, (a.v + 15) / 16), kTall, 0, s>>>(a);
-  else if (spread)
-    paged_merge_kernel<true><<<dim3((a.workers + 31) / 32, rows), 32 * kMergeW, 0, s>>>(a, rt);
+    e = spread ? launch_early(paged_merge_tall_kernel<1, 8>, dim3((workers + 7) / 8, n4), kTall, 0, s, a)
+               : launch_early(paged_merge_tall_kernel<4, 1>, dim3(workers, (n4 + 3) / 4), kTall, 0, s, a);
   else
-    paged_merge_kernel<false><<<dim3((a.workers + 3) / 4, (rows + 15) / 16), 32 * kMergeW, 0, s>>>(a, rt);
+    e = spread ? launch_early(paged_merge_kernel<true>, dim3((workers + 31) / 32, rows), 32 * kMergeW, 0, s, a, rt)
+               : launch_early(paged_merge_kernel<false>, dim3((workers + 1) / 2), 32 * kMergeW, 0, s, a, rt);
   after_launch(kKernPagedMerge, s);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace exattn

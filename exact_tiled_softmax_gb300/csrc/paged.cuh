@@ -24,6 +24,8 @@
 
 #include <math.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace exattn {
@@ -75,12 +77,16 @@ struct PagedArgs {
   unsigned* flags;   // [n_flags] status bits, one word for each CTA of each launch
   int n_flags;       // words that the merge kernel joins (from flags0)
   const unsigned* flags0;
-  int4* desc;  // [workers] of worker c: (b, h, row tile, parts) of the tile it starts and others end
+  // [workers] Of worker c: the row tile that it starts and others end, as (first row of the
+  // tile among (b, h)'s, rows of (b, h), s0, h << 16 | workers that hold a piece); the last
+  // is 0 where there is none.
+  int4* desc;
   float* pm;   // [2 workers][RT] exp2 domain
   float* pl;   // [2 workers][RT]
   float* pz;   // [2 workers][RT][v]
   int workers;
-  int least;  // units that a worker takes at least
+  int least;    // units that a worker takes at least
+  bool second;  // behind another launch whose results (initY, initL) it joins
 };
 
 struct PagedSeq {
@@ -273,20 +279,29 @@ __device__ __forceinline__ int paged_segment(const PagedWalk& w, int& j0, int& j
 // Where the summary of worker c's present segment goes: its slot, or -1 when the
 // segment holds the whole row tile.  The thread `one` describes a tile that starts
 // here and ends with a later worker; parts: the workers that hold a piece of it.
+template <int RT>
 __device__ __forceinline__ int paged_slot(const PagedArgs& a, const PagedWalk& w, int n, int c, bool one) {
   if (w.rem > 0) return 2 * c;
   if (n == w.t.cnt) return -1;
   if (one) {
     const long long last = w.u + w.t.cnt - 1;
-    a.desc[c] = make_int4(w.b, w.h, w.rt, static_cast<int>(paged_div(last, w.w)) - c + 1);
+    a.desc[c] = make_int4(w.rt * RT, w.s.nq * a.G, w.s.s0,
+                          static_cast<int>((static_cast<unsigned>(w.h) << 16) |
+                                           (static_cast<unsigned>(paged_div(last, w.w)) - c + 1)));
   }
   return 2 * c + 1;
 }
 
+// Programmatic dependent launch: a kernel lets its successor's CTAs start as SMs
+// become free, and the successor waits, before it touches what its predecessors
+// write, until they are complete.  Both do nothing in an ordinary launch.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Row r (of the tile's first row r0) as an index into [T][heads].
-__device__ __forceinline__ size_t paged_out_row(const PagedArgs& a, const PagedSeq& s, int h, int r) {
+__device__ __forceinline__ size_t paged_out_row(const PagedArgs& a, int s0, int h, int r) {
   const int i = div_by(r, a.by_group);
-  return static_cast<size_t>(s.s0 + i) * (a.Hk * a.G) + h * a.G + (r - i * a.G);
+  return static_cast<size_t>(s0 + i) * (a.Hk * a.G) + h * a.G + (r - i * a.G);
 }
 
 // The two factors of a finished row (m in the exp2 domain, l): Y = z * fz +
@@ -365,6 +380,38 @@ __device__ __forceinline__ long long paged_key_row(const PagedArgs& a, const int
   return ((static_cast<long long>(page) * a.Hk + h) << a.lps) + (key & ((1 << a.lps) - 1));
 }
 
+// Allows a kernel its dynamic shared memory, once for each device.
+template <auto kernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<unsigned long long> done{0};  // a bit a device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load() & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit);
+  return e;
+}
+
+// A launch that may start before its predecessor in the stream is complete (the
+// kernel waits by itself).
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                         Args... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 // Host side: rows of a tile, CTAs and workers of the launch, units that a worker
 // takes at least.
 struct PagedKernel {
@@ -395,6 +442,10 @@ struct AppendArgs {
   void* kp;
   void* vp;
   unsigned* status;
+  // Set by the launcher: accesses of a row of q or k and of v, items of a token (accesses of
+  // its q, k and v), tokens of a CTA.
+  FastDiv by_units, by_vch, by_items;
+  int q_items, qk_items, per;
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
 

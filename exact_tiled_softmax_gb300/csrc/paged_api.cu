@@ -186,7 +186,7 @@ size_t exattn_paged_workspace_size(const exattn_paged_shape* shape) {
 size_t exattn_prefix_workspace_size(const exattn_paged_shape* shape) {
   if (check_paged(shape) != EXATTN_OK) return 0;
   const size_t rows = (size_t)shape->tokens * shape->heads;
-  return kStatusBytes + kFlagBytes + most_bytes(shape) + align256(sizeof(float) * rows) +
+  return kStatusBytes + kFlagBytes + 2 * most_bytes(shape) + align256(sizeof(float) * rows) +
          align256(sizeof(float) * rows * shape->v);
 }
 
@@ -286,8 +286,8 @@ int attn_fwd_prefix(const exattn_paged_shape* shape, const void* Q, const void* 
   char* ws = static_cast<char*>(workspace);
   unsigned* flags = reinterpret_cast<unsigned*>(ws + kStatusBytes);
   const size_t rows = (size_t)shape->tokens * shape->heads;
-  char* own = ws + kStatusBytes + kFlagBytes;  // the two passes follow one another: one area
-  char* init = own + most_bytes(shape);
+  char* own = ws + kStatusBytes + kFlagBytes;  // of the prefix's pass, then of the sequences' own
+  char* init = own + 2 * most_bytes(shape);
   // All tokens over the prefix, as one sequence without a mask.
   PagedArgs p = make_args(shape, Q, k_pages, v_pages, prefix_table, nullptr, nullptr, scale,
                           EXATTN_MASK_NONE, 0, nullptr, reinterpret_cast<float*>(init));
@@ -311,8 +311,28 @@ int attn_fwd_prefix(const exattn_paged_shape* shape, const void* Q, const void* 
   a.flags = flags + cp.k.ctas;
   a.flags0 = flags;
   a.n_flags = cp.k.ctas + c.k.ctas;
-  place_pass(a, c.k, own);
+  a.second = true;
+  place_pass(a, c.k, own + most_bytes(shape));
   return cuda_result(run_pass(a, c, s), "attn_fwd_prefix: launch");
+}
+
+int exattn_paged_run(int op, const exattn_paged_call* c) {
+  if (!c) return EXATTN_INVALID_ARG;
+  switch (op) {
+    case EXATTN_PAGED_APPEND:
+      return attn_append_paged(&c->shape, c->q, c->k, c->v, c->page_table, c->seq_lens, c->q_starts,
+                               c->inv_freq, c->rot_pairs, c->interleaved, c->prefix_len, c->y, c->k_pages,
+                               c->v_pages, c->workspace, c->workspace_bytes, c->cuda_stream);
+    case EXATTN_PAGED_FWD:
+      return attn_fwd_paged(&c->shape, c->q, c->k_pages, c->v_pages, c->page_table, c->seq_lens, c->q_starts,
+                            c->scale, c->mask_kind, c->window, c->y, c->L, c->workspace, c->workspace_bytes,
+                            c->cuda_stream);
+    case EXATTN_PAGED_PREFIX:
+      return attn_fwd_prefix(&c->shape, c->q, c->k_pages, c->v_pages, c->prefix_table, c->prefix_len,
+                             c->page_table, c->seq_lens, c->q_starts, c->scale, c->mask_kind, c->y, c->L,
+                             c->workspace, c->workspace_bytes, c->cuda_stream);
+    default: return EXATTN_INVALID_ARG;
+  }
 }
 
 }  // extern "C"

@@ -333,6 +333,7 @@ __global__ void __launch_bounds__(32 * kW, 2) paged_mma_kernel(const PagedArgs a
   uint8_t* own = sm + warp * Lay::kWarpBytes;
   const uint32_t kbase = smem_u32(own), vbase = kbase + S * Lay::kTileBytes;
   unsigned bits = 0;
+  let_next_start();
   if (lane == 0) a.desc[c] = make_int4(0, 0, 0, 0);
   if (threadIdx.x == 0) joined = 0;
   // Columns of K that the rows do not have stay zero: no copy writes them.
@@ -467,10 +468,11 @@ __global__ void __launch_bounds__(32 * kW, 2) paged_mma_kernel(const PagedArgs a
     if (--left > 0) continue;
 
     // The segment's rows.
+    if (a.second) wait_for_previous();
     const PagedWalk w = walks[warp][1];
     int j0, j1;
     const int n = paged_segment<KT>(w, j0, j1);
-    const int slot = paged_slot(a, w, n, c, lane == 0);
+    const int slot = paged_slot<kRows>(a, w, n, c, lane == 0);
     size_t to[2];
     bool on[2];
     PagedScale f[2];
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(32 * kW, 2) paged_mma_kernel(const PagedArgs a
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
       if (slot < 0) {
-        to[x] = paged_out_row(a, w.s, w.h, w.rt * kRows + (on[x] ? q : 0));
+        to[x] = paged_out_row(a, w.s.s0, w.h, w.rt * kRows + (on[x] ? q : 0));
         f[x] = paged_finish(a, to[x], st.m[x], l);
         if (on[x] && t == 0) a.L[to[x]] = f[x].L;
       } else {
@@ -516,6 +518,7 @@ __global__ void __launch_bounds__(32 * kW, 2) paged_mma_kernel(const PagedArgs a
     }
   }
   cp_wait<0>();
+  if (a.second) wait_for_previous();  // warps without units too: the next launch counts on it
   paged_end(a, bits, &joined);
 }
 
@@ -523,12 +526,14 @@ template <typename T, int D>
 cudaError_t mma_launch(const PagedArgs& a, cudaStream_t s) {
   auto kern = paged_mma_kernel<T, D>;
   constexpr int bytes = MmaLayout<T, D>::kBytes;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const cudaError_t e = allow_smem<paged_mma_kernel<T, D>>(bytes);
   if (e != cudaSuccess) return e;
   before_launch(kKernPaged, s);
-  kern<<<kCtas, 32 * kW, bytes, s>>>(a);
+  cudaError_t le = cudaSuccess;
+  if (a.second) le = launch_early(kern, dim3(kCtas), 32 * kW, bytes, s, a);
+  else kern<<<kCtas, 32 * kW, bytes, s>>>(a);
   after_launch(kKernPaged, s);
-  return cudaGetLastError();
+  return le != cudaSuccess ? le : cudaGetLastError();
 }
 
 }  // namespace

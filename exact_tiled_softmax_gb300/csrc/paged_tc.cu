@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
   const PagedArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  let_next_start();
   if (threadIdx.x == 0) {
     a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     mbar_init(bar(Lay::B_Q), kQThreads);
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             t.r0 = w.rt * kRows;
             t.h = w.h;
             t.b = w.b;
-            t.slot = paged_slot(a, w, t.n, blockIdx.x, lane == 0);
+            t.slot = paged_slot<kRows>(a, w, t.n, blockIdx.x, lane == 0);
             t.first = w.rem == 0;
             t.s0 = w.s.s0;
             t.nq = w.s.nq;
@@ -540,6 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       if (!(ok = wait_all(bar(Lay::B_O + X), seg & 1, abort_flag))) break;
       tc_fence_after();
       const float m = l > 0.f || l != l ? m_ref : -INFINITY;
+      if (a.second) wait_for_previous();
       if (t.slot >= 0) {
         // The summary, columns outside rows: a warp's stores are whole lines.
         float4* z = reinterpret_cast<float4*>(a.pz) + static_cast<size_t>(t.slot) * (a.v / 4) * kRows + rl;
@@ -564,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
           a.pl[static_cast<size_t>(t.slot) * kRows + rl] = l;
         }
       } else {
-        const size_t row = paged_out_row(a, sq, t.h, r0 + (valid ? rl : 0));
+        const size_t row = paged_out_row(a, sq.s0, t.h, r0 + (valid ? rl : 0));
         PagedScale f{0.f, 0.f, 0.f};
         if (valid) {
           f = paged_finish(a, row, m, l);
@@ -613,6 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
   }
 
   tc_fence_before();
+  if (a.second) wait_for_previous();
   paged_end(a, bits, reinterpret_cast<unsigned*>(misc + 2));
   if (warp == kWarpMMA) {
     tc_fence_after();
@@ -644,13 +647,14 @@ cudaError_t tc_launch(const PagedArgs& a, cudaStream_t s) {
   if (!pool_map(&p.tk, a.Kp, a, a.d, p.box_rows) || !pool_map(&p.tv, a.Vp, a, a.v, p.box_rows))
     return cudaErrorInvalidValue;
   auto kern = paged_tc_kernel<D>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcLayout<D>::ALLOC);
+  const cudaError_t e = allow_smem<paged_tc_kernel<D>>(TcLayout<D>::ALLOC);
   if (e != cudaSuccess) return e;
   before_launch(kKernPaged, s);
-  kern<<<kCtas, kThreads, TcLayout<D>::ALLOC, s>>>(p);
+  cudaError_t le = cudaSuccess;
+  if (a.second) le = launch_early(kern, dim3(kCtas), kThreads, TcLayout<D>::ALLOC, s, p);
+  else kern<<<kCtas, kThreads, TcLayout<D>::ALLOC, s>>>(p);
   after_launch(kKernPaged, s);
-  return cudaGetLastError();
+  return le != cudaSuccess ? le : cudaGetLastError();
 }
 
 }  // namespace

@@ -428,6 +428,38 @@ int attn_fwd_prefix(const exattn_paged_shape* shape, const void* Q, const void* 
                     int mask_kind, void* Y, float* L, void* workspace, size_t workspace_bytes,
                     void* cuda_stream);
 
+/* The three calls with their arguments in one structure, for a binding whose cost
+ * grows with the number of arguments (a decode step's kernels take a few
+ * microseconds).  Fields that an operation does not take are not read: k, v,
+ * inv_freq, rot_pairs and interleaved are attn_append_paged's, scale, mask_kind,
+ * window and L the attention's; y is Y or q_out, prefix_len also pos_offset. */
+typedef struct exattn_paged_call {
+  exattn_paged_shape shape;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* k_pages;
+  void* v_pages;
+  const int* page_table;
+  const int* seq_lens;
+  const int* q_starts;
+  const int* prefix_table;
+  const float* inv_freq;
+  void* y;
+  float* L;
+  void* workspace;
+  size_t workspace_bytes;
+  void* cuda_stream;
+  float scale;
+  int mask_kind;
+  int window;
+  int prefix_len;
+  int rot_pairs;
+  int interleaved;
+} exattn_paged_call;
+enum exattn_paged_op { EXATTN_PAGED_APPEND = 0, EXATTN_PAGED_FWD = 1, EXATTN_PAGED_PREFIX = 2 };
+int exattn_paged_run(int op, const exattn_paged_call* call);
+
 /* Waits for `cuda_stream`, then reads the status word of `workspace` (the
  * workspace of the last call queued on it).  Returns EXATTN_OK,
  * EXATTN_EMPTY_ROW, EXATTN_TIMEOUT, EXATTN_BAD_PAGE or EXATTN_CUDA_ERROR. */

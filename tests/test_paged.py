@@ -157,6 +157,29 @@ def test_arguments_that_the_library_refuses(lib):
     assert append(shape=uneven, st=None) == 1
 
 
+def test_packed_calls_reach_the_same_checks(lib):
+    """The binding's packed structure has the C layout: each operation's own refusals."""
+    import exact_tiled_softmax_gb300 as ex
+    p, big = 1 << 20, 1 << 40
+
+    def run(op, shape=GOOD, **edit):
+        f = dict(q=p, k=p, v=p, kp=p, vp=p, t=p, n=p, st=p, pt=p, inv=p, y=p, L=p, w=p, size=big, s=0,
+                 scale=1.0, mask=0, win=0, plen=5, pairs=4, inter=0)
+        f.update(edit)
+        return lib.exattn_paged_run(op, ex._PAGED_CALL.pack(*shape.values(), *f.values()))
+
+    assert ex._PAGED_CALL.size == 208
+    assert run(3) == 1 and lib.exattn_paged_run(1, None) == 1
+    for op in range(3):
+        assert run(op, {**GOOD, "page_size": 24}) == 2
+        assert run(op, kp=p + 8) == 3 and run(op, y=p + 8) == 3 and run(op, w=p + 128) == 3
+        assert run(op, size=8) == 4 and run(op, n=0) == 1 and run(op, st=p + 2) == 3
+    assert run(0, pairs=33) == 1 and run(0, plen=-1) == 1 and run(0, inv=p + 2) == 3 and run(0, v=0) == 1
+    for op in (1, 2):
+        assert run(op, L=0) == 1 and run(op, mask=3) == 2 and run(op, mask=-2) == 1
+    assert run(1, mask=2, win=0) == 1 and run(2, plen=-1) == 1 and run(2, pt=0) == 1
+
+
 def test_workspace_does_not_grow_with_the_cache(lib):
     import exact_tiled_softmax_gb300 as ex
     size = lambda **e: ex.paged_workspace_size(ex.PagedShape(**{**GOOD, **e}))  # noqa: E731

@@ -442,10 +442,10 @@ struct AppendArgs {
   void* kp;
   void* vp;
   unsigned* status;
-  // Set by the launcher: accesses of a row of q or k and of v, items of a token (accesses of
-  // its q, k and v), tokens of a CTA.
-  FastDiv by_units, by_vch, by_items;
-  int q_items, qk_items, per;
+  // Set by the launcher: units of a row of q or k, accesses of a row of v, warps that
+  // share a token; T / B.
+  FastDiv by_units, by_vch, by_shares;
+  int each;
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
 

@@ -9,7 +9,7 @@
 // where the rotated halves allow them.  A warp takes a token (or a share of its rows):
 // it finds the token's place and angles once for all heads.  What hides the latency is
 // warps, not loads of a lane: six CTAs to an SM with one row in flight a lane moved 37
-// thousand tokens of 40 heads of 128 bf16 columns at 5.92 TB/s (87% of the measured
+// thousand tokens of 40 heads of 128 bf16 columns at 5.94 TB/s (88% of the measured
 // copy), two rows at four CTAs 5.41, four rows at two CTAs 4.05.  One CTA more checks that every token has a
 // place and writes the status word.
 #include "paged.cuh"
@@ -147,8 +147,9 @@ __global__ void __launch_bounds__(kAppendThreads, 6) append_kernel(const __grid_
       const bool is_q = r < q_rows;
       const T* src = (is_q ? qsrc + r * a.d : ksrc + (r - q_rows) * a.d) + col;
       P x = *reinterpret_cast<const P*>(src), y;
+      if (two) y = *reinterpret_cast<const P*>(src + a.pairs);
+      if (!is_q && slot < 0) continue;
       if (two) {
-        y = *reinterpret_cast<const P*>(src + a.pairs);
         const Piece<float, W> c = *reinterpret_cast<const Piece<float, W>*>(&cs[warp][u * W]),
                               s = *reinterpret_cast<const Piece<float, W>*>(&sn[warp][u * W]);
 #pragma unroll
@@ -170,7 +171,6 @@ __global__ void __launch_bounds__(kAppendThreads, 6) append_kernel(const __grid_
           }
         }
       }
-      if (!is_q && slot < 0) continue;
       T* dst = (is_q ? qdst + r * a.d : kdst + (static_cast<long long>(r - q_rows) << a.lps) * a.d) + col;
       *reinterpret_cast<P*>(dst) = x;
       if (two) *reinterpret_cast<P*>(dst + a.pairs) = y;

@@ -457,6 +457,10 @@ cudaError_t launch_paged_simt(const PagedArgs& a, bool one_row, cudaStream_t s) 
 // Rows that a tile can have (q_starts hides how many tokens a sequence has).  Tiles that
 // may be spread over more than 16 workers give a row to all of a CTA's warps: a warp
 // alone takes four pieces of 512 bytes after four.
+// CTAs that take at most 32 workers each: a prime number, so that tiles that start at
+// every so manyth worker do not meet in one CTA.
+unsigned spread_ctas(unsigned workers) { return workers <= 41 * 32 ? 41 : (workers + 31) / 32; }
+
 cudaError_t launch_paged_merge(const PagedArgs& a, int rt, cudaStream_t s) {
   const long long all = static_cast<long long>(a.starts ? a.T : a.each) * a.G;
   const unsigned rows = static_cast<unsigned>(all < rt ? all : rt);
@@ -470,7 +474,7 @@ cudaError_t launch_paged_merge(const PagedArgs& a, int rt, cudaStream_t s) {
     e = spread ? launch_early(paged_merge_tall_kernel<1, 8>, dim3((workers + 7) / 8, n4), kTall, 0, s, a)
                : launch_early(paged_merge_tall_kernel<4, 1>, dim3(workers, (n4 + 3) / 4), kTall, 0, s, a);
   else
-    e = spread ? launch_early(paged_merge_kernel<true>, dim3((workers + 31) / 32, rows), 32 * kMergeW, 0, s, a, rt)
+    e = spread ? launch_early(paged_merge_kernel<true>, dim3(spread_ctas(workers), rows), 32 * kMergeW, 0, s, a, rt)
                : launch_early(paged_merge_kernel<false>, dim3((workers + 1) / 2), 32 * kMergeW, 0, s, a, rt);
   after_launch(kKernPagedMerge, s);
   return e;

@@ -58,7 +58,7 @@ struct PagedArgs {
   const int* starts;  // [B + 1], or null: T / B tokens for every sequence
   int fixed_len;
   int B, T, Hk, G, d, v, dtype;
-  FastDiv by_group;  // G
+  FastDiv by_group, by_heads, by_workers;  // G, Hk, workers
   int each;          // T / B
   int lps;  // log2(page_size)
   int num_pages, max_pages;
@@ -145,6 +145,10 @@ __device__ __forceinline__ PagedTile paged_tile(const PagedArgs& a, const PagedS
   return t;
 }
 
+// n / d for n >= 0: a fixed divisor's fast form wherever n fits 31 bits.
+__device__ __forceinline__ long long paged_div(long long n, const FastDiv& d) {
+  return (n >> 31) == 0 ? div_by(static_cast<int>(n), d) : static_cast<long long>(static_cast<unsigned long long>(n) / d.d);
+}
 // n / d for n >= 0, d > 0: in 32 bits wherever they fit.
 __device__ __forceinline__ long long paged_div(long long n, long long d) {
   if (((n | d) >> 32) == 0) return static_cast<unsigned>(n) / static_cast<unsigned>(d);
@@ -215,7 +219,7 @@ __device__ __forceinline__ void paged_scan(const PagedArgs& a, long long* pre, l
 template <int RT, int UK>
 __device__ __forceinline__ bool paged_begin(const PagedArgs& a, const long long* pre, int c, PagedWalk& w) {
   const long long total = pre[a.B];
-  w.w = max(static_cast<long long>(a.least), paged_div(total + a.workers - 1, a.workers));
+  w.w = max(static_cast<long long>(a.least), paged_div(total + a.workers - 1, a.by_workers));
   w.u = min(total, w.w * c);
   w.end = min(total, w.u + w.w);
   if (w.u >= w.end) return false;
@@ -229,7 +233,7 @@ __device__ __forceinline__ bool paged_begin(const PagedArgs& a, const long long*
   w.b = b0;
   w.s = paged_seq(a, w.b);
   w.tiles = (w.s.nq * a.G + RT - 1) / RT;
-  const long long per_head = paged_div(pre[b0 + 1] - pre[b0], a.Hk);
+  const long long per_head = paged_div(pre[b0 + 1] - pre[b0], a.by_heads);
   const long long local = w.u - pre[b0];
   w.h = static_cast<int>(paged_div(local, per_head));
   long long rem = local - w.h * per_head;
@@ -420,8 +424,8 @@ struct PagedKernel {
 PagedKernel paged_simt_kernel(bool one_row);
 cudaError_t launch_paged_simt(const PagedArgs& a, bool one_row, cudaStream_t s);
 bool paged_mma_shape(int d, int v);
-PagedKernel paged_mma_kernel();
-cudaError_t launch_paged_mma(const PagedArgs& a, cudaStream_t s);
+PagedKernel paged_mma_kernel_of(int dtype, int d, int v, int rows);  // rows: 8 or 16
+cudaError_t launch_paged_mma(const PagedArgs& a, int rows, cudaStream_t s);
 bool paged_tc_supported(const PagedArgs& a);
 PagedKernel paged_tc_kernel_of();
 cudaError_t launch_paged_tc(const PagedArgs& a, cudaStream_t s);

@@ -55,10 +55,15 @@ int check_paged(const exattn_paged_shape* s) {
 }
 
 // The kernel of a call.
-enum Kind { kSimtOne, kSimt, kMma, kTc };
+enum Kind { kSimtOne, kSimt, kMma8, kMma16, kTc };
 
-PagedKernel kernel_of(Kind k) {
-  return k == kTc ? paged_tc_kernel_of() : k == kMma ? paged_mma_kernel() : paged_simt_kernel(k == kSimtOne);
+PagedKernel kernel_of(Kind k, int dtype, int d, int v) {
+  switch (k) {
+    case kTc: return paged_tc_kernel_of();
+    case kMma8: return paged_mma_kernel_of(dtype, d, v, 8);
+    case kMma16: return paged_mma_kernel_of(dtype, d, v, 16);
+    default: return paged_simt_kernel(k == kSimtOne);
+  }
 }
 
 struct Choice {
@@ -73,9 +78,9 @@ constexpr int kTcRows = 64;
 Choice choose(const PagedArgs& a) {
   Choice c;
   if (current_path() != EXATTN_PATH_SIMT && paged_mma_shape(a.d, a.v))
-    c.kind = rows_of(a) > kTcRows && paged_tc_supported(a) ? kTc : kMma;
+    c.kind = rows_of(a) > kTcRows && paged_tc_supported(a) ? kTc : rows_of(a) > 8 ? kMma16 : kMma8;
   else c.kind = !a.starts && a.T == a.B && a.G == 1 ? kSimtOne : kSimt;
-  c.k = kernel_of(c.kind);
+  c.k = kernel_of(c.kind, a.dtype, a.d, a.v);
   return c;
 }
 
@@ -92,11 +97,11 @@ constexpr size_t kFlagBytes = 8192;  // status bits of the CTAs of two passes (a
 // query and the call, and q_starts is not part of the shape).
 size_t most_bytes(const exattn_paged_shape* s) {
   size_t most = 0;
-  for (const Kind k : {kSimtOne, kSimt, kMma, kTc}) {
-    if ((k == kMma || k == kTc) && !paged_mma_shape(s->d, s->v)) continue;
+  for (const Kind k : {kSimtOne, kSimt, kMma8, kMma16, kTc}) {
+    if (k >= kMma8 && !paged_mma_shape(s->d, s->v)) continue;
     // A prefix's pass takes all tokens as one sequence's.
     if (k == kTc && (s->dtype != EXATTN_BF16 || (long long)s->tokens * (s->heads / s->kv_heads) <= kTcRows)) continue;
-    const size_t x = pass_bytes(kernel_of(k), s->v);
+    const size_t x = pass_bytes(kernel_of(k, s->dtype, s->d, s->v), s->v);
     most = x > most ? x : most;
   }
   return most;
@@ -105,6 +110,7 @@ size_t most_bytes(const exattn_paged_shape* s) {
 char* place_pass(PagedArgs& a, const PagedKernel& k, char* ws) {
   const size_t rows = 2 * (size_t)k.workers * k.rt;
   a.workers = k.workers;
+  a.by_workers = fast_div(k.workers);
   a.least = k.least;
   a.desc = reinterpret_cast<int4*>(ws);
   ws += align256(sizeof(int4) * (size_t)k.workers);
@@ -131,6 +137,7 @@ PagedArgs make_args(const exattn_paged_shape* s, const void* Q, const void* Kp, 
   a.Hk = s->kv_heads;
   a.G = s->heads / s->kv_heads;
   a.by_group = fast_div(a.G);
+  a.by_heads = fast_div(a.Hk);
   a.each = a.T / a.B;
   a.d = s->d;
   a.v = s->v;
@@ -154,9 +161,9 @@ int cuda_result(cudaError_t e, const char* where) {
 }
 
 cudaError_t run_pass(const PagedArgs& a, const Choice& c, cudaStream_t s) {
-  const cudaError_t e =
-      c.kind == kTc ? launch_paged_tc(a, s)
-                    : c.kind == kMma ? launch_paged_mma(a, s) : launch_paged_simt(a, c.kind == kSimtOne, s);
+  const cudaError_t e = c.kind == kTc     ? launch_paged_tc(a, s)
+                        : c.kind >= kMma8 ? launch_paged_mma(a, c.k.rt, s)
+                                          : launch_paged_simt(a, c.kind == kSimtOne, s);
   return e != cudaSuccess ? e : launch_paged_merge(a, c.k.rt, s);
 }
 

@@ -1,15 +1,16 @@
 // Paged attention for few rows to a key head (a decode step, a few guessed
 // tokens), widths up to 128: bound by reading K and V once.
 //
-// A row tile is 16 rows, the rows of one tensor-core tile: the rows of a key head's
-// whole group share each key that is read.  A worker is a warp.  It streams the key
-// tiles of its units (16 keys in bf16, 8 in fp32: 8 KB of K and V at width 128)
-// through a ring of kStages tiles of its own in shared memory (asynchronous 16-byte
-// copies, row by row through the page table), and holds maximum, sum and output of
-// its rows in registers.  No barrier and no other warp is involved between a
-// segment's first copy and its last store.  The copies run ahead of the products by
-// kStages - 1 tiles, over the ends of segments too, so that short sequences stream as
-// long ones do; 8 warps to an SM keep 128 KB in flight.
+// A row tile is 8 or 16 rows, one or two tensor-core tiles in their N dimension: the
+// products are transposed, S^T = K Q^T and O^T = V^T P^T, so that keys and columns fill
+// the 16 of M whatever few rows there are, and a key head's whole group shares each key
+// that is read.  A worker is a warp.  It streams the 16-key tiles of its units through a
+// ring of kStages tiles of its own in shared memory (asynchronous 16-byte copies through
+// the page table), and holds maximum, sum and output of its rows in registers.  No
+// barrier and no other warp is involved between a segment's first copy and its last
+// store.  The copies run ahead of the products by kStages - 1 tiles, over the ends of
+// segments too, so that short sequences stream as long ones do; an SM keeps 128 KB in
+// flight.
 //
 // bf16: m16n8k16.  p enters P.V as the sum of two bf16 values, its rounding and what
 // the rounding left out (2^-17 of p remains): the products are free beside the
@@ -30,8 +31,7 @@ using tc::pack_bf16x2;
 using tc::smem_u32;
 using tc::tf32_hi;
 
-constexpr int kW = 4;
-constexpr int kRows = 16;
+constexpr int kTile = 16;  // keys of a tile, a unit of work
 constexpr int kCtas = 2 * 152;
 constexpr float kRescale = 8.f;
 
@@ -77,246 +77,370 @@ __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
   lo = __float_as_uint(x - h);
 }
 
-// A worker's rows over a segment: maximum (the reference point), sum over the
-// thread's keys, output.  Thread (g, t) = (lane / 4, lane % 4) holds rows g and g + 8.
-template <int D>
-struct RowState {
-  float m[2], l[2], o[D / 8][4];
-  __device__ __forceinline__ void clear() {
-    m[0] = m[1] = -INFINITY;
-    l[0] = l[1] = 0.f;
-#pragma unroll
-    for (int x = 0; x < D / 8; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
-  }
-  // The reference point of rows whose tile maximum is top[].
-  __device__ __forceinline__ void refer(const float (&top)[2]) {
-    const bool move = top[0] > m[0] + kRescale || top[1] > m[1] + kRescale;
-    if (!__any_sync(0xFFFFFFFFu, move)) return;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const float to = fmaxf(m[x], top[x]);
-      const float f = m[x] == -INFINITY ? 0.f : ex2(m[x] - to);
-      m[x] = to;
-      l[x] *= f;
-#pragma unroll
-      for (int y = 0; y < D / 8; ++y) {
-        o[y][2 * x] *= f;
-        o[y][2 * x + 1] *= f;
-      }
-    }
-  }
-};
-
-__device__ __forceinline__ float quad_max(float x) {
-  x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
-  return fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+// The 8x8 matrix of 16-bit values whose rows the warp's lanes hold in fours, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
-// The keys that a thread's two rows allow, and those that every row of the tile does.
-struct Spans {
-  int lo[2], hi[2], all_lo, all_hi;
+__device__ __forceinline__ float max_over_keys(float x) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+  return x;
+}
+
+// A worker's rows over a segment.  Thread (g, t) = (lane / 4, lane % 4) holds, of rows
+// 8 n + 2 t + x, the reference point m, the sum over its own keys l, and of the output
+// the columns of o[n] (see Step).
+template <int D, int NT>
+struct RowState {
+  float m[NT][2], l[NT][2], o[NT][D / 16][4];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int y = 0; y < D / 16; ++y) o[n][y][0] = o[n][y][1] = o[n][y][2] = o[n][y][3] = 0.f;
+    }
+  }
+  // sc[n][2 k + x]: row x's score of the thread's key k = 0, 1, masked.  Moves the
+  // reference points and leaves p in sc.
+  __device__ __forceinline__ void softmax(float (&sc)[NT][4]) {
+    float top[NT][2];
+    bool move = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        top[n][x] = max_over_keys(fmaxf(sc[n][x], sc[n][2 + x]));
+        move |= top[n][x] > m[n][x] + kRescale;
+      }
+    if (__any_sync(0xFFFFFFFFu, move)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float to = fmaxf(m[n][x], top[n][x]);
+          const float f = m[n][x] == -INFINITY ? 0.f : ex2(m[n][x] - to);
+          m[n][x] = to;
+          l[n][x] *= f;
+#pragma unroll
+          for (int y = 0; y < D / 16; ++y) {
+            o[n][y][x] *= f;
+            o[n][y][2 + x] *= f;
+          }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float ref = m[n][x] == -INFINITY ? 0.f : m[n][x];
+        sc[n][x] = ex2(sc[n][x] - ref);
+        sc[n][2 + x] = ex2(sc[n][2 + x] - ref);
+        l[n][x] += sc[n][x] + sc[n][2 + x];
+      }
+  }
 };
 
-// What the two types differ in: the tile, its place in shared memory, Q's
-// fragments, and one tile's products.
-template <typename T, int D> struct Step;
+// The keys that a thread's rows allow, and those that every row of the tile does.
+template <int NT>
+struct Spans {
+  int lo[NT][2], hi[NT][2], all_lo, all_hi;
+};
 
-template <int D>
-struct Step<__nv_bfloat16, D> {
-  static constexpr int kTile = 16, kCh = D / 8, kStages = D == 128 ? 3 : 6;
-  uint32_t qa[D / 16][4];
+// Scores into the exp2 domain, those that do not count to -inf.
+template <int NT>
+__device__ __forceinline__ void mask_scores(float (&sc)[NT][4], const Spans<NT>& sp, unsigned have, int key0,
+                                            float sl2) {
+  const int g = (threadIdx.x & 31) >> 2;
+  const bool whole = have == 0xFFFFu && key0 >= sp.all_lo && key0 + kTile <= sp.all_hi;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sc[n][e] *= sl2;
+      if (!whole) {
+        const int k = g + 8 * (e >> 1), x = e & 1;
+        if (!((have >> k) & 1u) || key0 + k < sp.lo[n][x] || key0 + k >= sp.hi[n][x]) sc[n][e] = -INFINITY;
+      }
+    }
+}
+
+// What the two types differ in: a tile's place in shared memory, Q's fragments, one
+// tile's products, and the columns that a thread's outputs stand for.
+template <typename T, int D, int NT> struct Step;
+
+// bf16.  o[n][y]: columns 16 y + g (rows x = 0, 1) and 16 y + g + 8.
+template <int D, int NT>
+struct Step<__nv_bfloat16, D, NT> {
+  static constexpr int kW = 4, kStages = D == 128 ? 3 : 6;
+  uint32_t qb[NT][D / 16][2];
   static __device__ __forceinline__ int kpiece(int r, int c) { return c ^ (r & 7); }
   static __device__ __forceinline__ int vpiece(int r, int c) { return c ^ (r & 7); }
-  __device__ __forceinline__ void load_q(const __nv_bfloat16* (&row)[2], const bool (&on)[2], int t, int d) {
+  // Row n of the tile's row 8 n + g.
+  __device__ __forceinline__ void load_q(int n, const __nv_bfloat16* row, bool on, int t, int d) {
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int c = ks * 16 + y * 8 + 2 * t;
-          qa[ks][x + 2 * y] = on[x] && c < d ? *reinterpret_cast<const uint32_t*>(row[x] + c) : 0u;
-        }
+      for (int y = 0; y < 2; ++y) {
+        const int c = ks * 16 + y * 8 + 2 * t;
+        qb[n][ks][y] = on && c < d ? *reinterpret_cast<const uint32_t*>(row + c) : 0u;
+      }
   }
-  __device__ __forceinline__ void tile(RowState<D>& st, uint32_t kt, uint32_t vt, unsigned have, int key0,
-                                       const Spans& sp, float sl2) {
-    const int lane = threadIdx.x & 31, t = lane & 3;
-    float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  __device__ __forceinline__ void tile(RowState<D, NT>& st, uint32_t kt, uint32_t vt, unsigned have, int key0,
+                                       const Spans<NT>& sp, float sl2) {
+    const int lane = threadIdx.x & 31, i = lane >> 3;
+    float sc[NT][4], sb[NT][4];  // two chains each
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[n][e] = sb[n][e] = 0.f;
     {
-      const int r = ((lane >> 4) << 3) + (lane & 7), c = (lane >> 3) & 1;
+      const int r = ((i & 1) << 3) + (lane & 7), c = i >> 1;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t b[4];
-        ldm4(b, kt + r * (D * 2) + (kpiece(r, 2 * ks + c) << 4));
-        mma16(sc[0], qa[ks], b[0], b[1]);
-        mma16(sc[1], qa[ks], b[2], b[3]);
+        uint32_t k[4];
+        ldm4(k, kt + r * (D * 2) + (kpiece(r, 2 * ks + c) << 4));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16(ks & 1 ? sb[n] : sc[n], k, qb[n][ks][0], qb[n][ks][1]);
       }
     }
-    const bool whole = have == 0xFFFFu && key0 >= sp.all_lo && key0 + kTile <= sp.all_hi;
 #pragma unroll
-    for (int y = 0; y < 2; ++y)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sc[y][e] *= sl2;
-        if (!whole) {
-          const int k = y * 8 + 2 * t + (e & 1), x = e >> 1;
-          if (!((have >> k) & 1u) || key0 + k < sp.lo[x] || key0 + k >= sp.hi[x]) sc[y][e] = -INFINITY;
-        }
-      }
-    float top[2];
+      for (int e = 0; e < 4; ++e) sc[n][e] += sb[n][e];
+    mask_scores<NT>(sc, sp, have, key0, sl2);
+    st.softmax(sc);
+    uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-      top[x] = quad_max(fmaxf(fmaxf(sc[0][2 * x], sc[0][2 * x + 1]), fmaxf(sc[1][2 * x], sc[1][2 * x + 1])));
-    st.refer(top);
-    uint32_t ph[4], pl[4];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const float ref = st.m[x] == -INFINITY ? 0.f : st.m[x];
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const float p0 = ex2(sc[y][2 * x] - ref), p1 = ex2(sc[y][2 * x + 1] - ref);
-        st.l[x] += p0 + p1;
+      for (int k = 0; k < 2; ++k) {
+        const float p0 = sc[n][2 * k], p1 = sc[n][2 * k + 1];
         const uint32_t h = pack_bf16x2(p0, p1);
-        ph[x + 2 * y] = h;
-        pl[x + 2 * y] = pack_bf16x2(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xFFFF0000u));
+        ph[n][k] = transpose8(h);
+        pl[n][k] = transpose8(pack_bf16x2(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xFFFF0000u)));
       }
-    }
-    const int r = (((lane >> 3) & 1) << 3) + (lane & 7), c = lane >> 4;
+    const int r = ((i >> 1) << 3) + (lane & 7), c = i & 1;
 #pragma unroll
     for (int y = 0; y < D / 16; ++y) {
-      uint32_t b[4];
-      ldm4t(b, vt + r * (D * 2) + (vpiece(r, 2 * y + c) << 4));
-      mma16(st.o[2 * y], ph, b[0], b[1]);
-      mma16(st.o[2 * y + 1], ph, b[2], b[3]);
-      mma16(st.o[2 * y], pl, b[0], b[1]);
-      mma16(st.o[2 * y + 1], pl, b[2], b[3]);
+      uint32_t v[4];
+      ldm4t(v, vt + r * (D * 2) + (vpiece(r, 2 * y + c) << 4));
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma16(st.o[n][y], v, ph[n][0], ph[n][1]);
+        mma16(st.o[n][y], v, pl[n][0], pl[n][1]);
+      }
     }
   }
-  // put(x, column, values): the thread's columns of its row x, two at a time.
-  template <typename F>
-  static __device__ __forceinline__ void out(const RowState<D>& st, int t, F put) {
+  // Row pair n of the summary to z0, z1 (null: no such row).
+  static __device__ __forceinline__ void put_summary(const RowState<D, NT>& st, int n, float* z0, float* z1, int v) {
+    const int g = (threadIdx.x & 31) >> 2;
+#pragma unroll
+    for (int y = 0; y < D / 16; ++y)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int col = 16 * y + 8 * h + g;
+        if (col >= v) continue;
+        if (z0) z0[col] = st.o[n][y][2 * h];
+        if (z1) z1[col] = st.o[n][y][2 * h + 1];
+      }
+  }
+  // Row pair n finished: rows to[0], to[1] of [T][heads], where on[].
+  static __device__ __forceinline__ void put_rows(const PagedArgs& a, const RowState<D, NT>& st, int n,
+                                                  const size_t (&to)[2], const bool (&on)[2],
+                                                  const PagedScale (&f)[2]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    // Every load of the joined rows before the first store: they may not pass one another.
+    float z[2][D / 8];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int y = 0; y < D / 8; ++y) put(x, y * 8 + 2 * t, make_float2(st.o[y][2 * x], st.o[y][2 * x + 1]));
+      for (int y = 0; y < D / 8; ++y) {
+        const int col = 8 * y + g;
+        z[x][y] = a.initY && on[x] && col < a.v ? a.initY[to[x] * a.v + col] * f[x].fi : 0.f;
+      }
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int y = 0; y < D / 8; ++y) z[x][y] = fmaf(st.o[n][y / 2][2 * (y & 1) + x], f[x].fz, z[x][y]);
+    if (a.Yf) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int y = 0; y < D / 8; ++y)
+          if (on[x] && 8 * y + g < a.v) a.Yf[to[x] * a.v + 8 * y + g] = z[x][y];
+      return;
+    }
+    // Lane (g, t) stores row g of the tile, two columns at a time, after a transposition.
+    const size_t r0 = __shfl_sync(0xFFFFFFFFu, to[0], g >> 1), r1 = __shfl_sync(0xFFFFFFFFu, to[1], g >> 1);
+    const int o0 = __shfl_sync(0xFFFFFFFFu, static_cast<int>(on[0]), g >> 1),
+              o1 = __shfl_sync(0xFFFFFFFFu, static_cast<int>(on[1]), g >> 1);
+    __nv_bfloat16* mine = static_cast<__nv_bfloat16*>(a.Y) + (g & 1 ? r1 : r0) * a.v;
+    const bool mine_on = g & 1 ? o1 : o0;
+#pragma unroll
+    for (int y = 0; y < D / 8; ++y) {
+      const uint32_t pair = transpose8(pack_bf16x2(z[0][y], z[1][y]));  // row g, columns 2 t and 2 t + 1 of eight
+      if (mine_on && 8 * y < a.v) *reinterpret_cast<uint32_t*>(mine + 8 * y + 2 * t) = pair;
+    }
   }
 };
 
-// fp32.  The products' inner index is permuted so that a thread's operands are
-// 16-byte pieces: of K, piece 4 s + t of key g gives steps 2 s and 2 s + 1 (columns
-// 16 s + 4 t + {0, 1} and {2, 3}); of V, piece 8 q + g of keys 2 t and 2 t + 1 gives
-// output tiles 4 q + {0..3}, whose column n stands for 32 q + 4 n + {0..3}.
-template <int D>
-struct Step<float, D> {
-  static constexpr int kTile = 8, kCh = D / 4, kStages = D == 128 ? 3 : 6;
-  float qa[D / 16][2][4];
+// fp32.  The products' inner index is permuted so that a thread's operands are 16-byte
+// pieces: of K, piece 4 s + t of keys g and g + 8 gives steps 2 s and 2 s + 1 (columns
+// 16 s + 4 t + {0, 1} and {2, 3}); of V, piece 8 q + g of keys t and t + 4 (then t + 8 and
+// t + 12) gives output tiles 2 q and 2 q + 1, so that o[n][2 q] and o[n][2 q + 1] are
+// columns 32 q + 4 g + {0, 1} and {2, 3}.
+template <int D, int NT>
+struct Step<float, D, NT> {
+  static constexpr int kW = D == 128 ? 2 : 4, kStages = 3;
+  float qb[NT][D / 16][4];
   static __device__ __forceinline__ int kpiece(int r, int c) { return c ^ ((r & 1) << 2); }
-  static __device__ __forceinline__ int vpiece(int r, int c) { return c ^ (r & 6); }
-  __device__ __forceinline__ void load_q(const float* (&row)[2], const bool (&on)[2], int t, int d) {
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int c = 16 * s + 4 * t;
-        const float4 q = on[x] && c < d ? *reinterpret_cast<const float4*>(row[x] + c)
-                                        : make_float4(0.f, 0.f, 0.f, 0.f);
-        qa[s][x][0] = q.x;
-        qa[s][x][1] = q.y;
-        qa[s][x][2] = q.z;
-        qa[s][x][3] = q.w;
-      }
-  }
-  __device__ __forceinline__ void tile(RowState<D>& st, uint32_t kt, uint32_t vt, unsigned have, int key0,
-                                       const Spans& sp, float sl2) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    float hh[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}, hl[4] = {0.f, 0.f, 0.f, 0.f},
-          lh[4] = {0.f, 0.f, 0.f, 0.f};  // four chains
+  static __device__ __forceinline__ int vpiece(int r, int c) { return c ^ ((r & 3) << 1); }
+  __device__ __forceinline__ void load_q(int n, const float* row, bool on, int t, int d) {
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
-      const uint4 raw = ld_shared_v4(kt + g * (D * 4) + (kpiece(g, 4 * s + t) << 4));
-      const float kf[4] = {__uint_as_float(raw.x), __uint_as_float(raw.y), __uint_as_float(raw.z),
-                           __uint_as_float(raw.w)};
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        uint32_t ah[4], al[4], bh[2], bl[2];
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          split(kf[2 * y + z], bh[z], bl[z]);
-#pragma unroll
-          for (int x = 0; x < 2; ++x) split(qa[s][x][2 * y + z], ah[x + 2 * z], al[x + 2 * z]);
-        }
-        mma8(hh[y], ah, bh[0], bh[1]);
-        mma8(hl, ah, bl[0], bl[1]);
-        mma8(lh, al, bh[0], bh[1]);
-      }
-    }
-    const bool whole = have == 0xFFu && key0 >= sp.all_lo && key0 + kTile <= sp.all_hi;
-    float sc[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      sc[e] = ((hl[e] + lh[e]) + (hh[0][e] + hh[1][e])) * sl2;
-      if (!whole) {
-        const int k = 2 * t + (e & 1), x = e >> 1;
-        if (!((have >> k) & 1u) || key0 + k < sp.lo[x] || key0 + k >= sp.hi[x]) sc[e] = -INFINITY;
-      }
-    }
-    const float top[2] = {quad_max(fmaxf(sc[0], sc[1])), quad_max(fmaxf(sc[2], sc[3]))};
-    st.refer(top);
-    uint32_t ph[4], pl[4];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const float ref = st.m[x] == -INFINITY ? 0.f : st.m[x];
-      const float p0 = ex2(sc[2 * x] - ref), p1 = ex2(sc[2 * x + 1] - ref);
-      st.l[x] += p0 + p1;
-      split(p0, ph[x], pl[x]);
-      split(p1, ph[x + 2], pl[x + 2]);
-    }
-#pragma unroll
-    for (int q = 0; q < D / 32; ++q) {
-      const uint4 r0 = ld_shared_v4(vt + (2 * t) * (D * 4) + (vpiece(2 * t, 8 * q + g) << 4));
-      const uint4 r1 = ld_shared_v4(vt + (2 * t + 1) * (D * 4) + (vpiece(2 * t + 1, 8 * q + g) << 4));
-      const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        uint32_t bh[2], bl[2];
-        split(__uint_as_float(w0[y]), bh[0], bl[0]);
-        split(__uint_as_float(w1[y]), bh[1], bl[1]);
-        mma8(st.o[4 * q + y], ph, bh[0], bh[1]);
-        mma8(st.o[4 * q + y], ph, bl[0], bl[1]);
-        mma8(st.o[4 * q + y], pl, bh[0], bh[1]);
-      }
+      const int c = 16 * s + 4 * t;
+      const float4 q = on && c < d ? *reinterpret_cast<const float4*>(row + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+      qb[n][s][0] = q.x;
+      qb[n][s][1] = q.y;
+      qb[n][s][2] = q.z;
+      qb[n][s][3] = q.w;
     }
   }
-  template <typename F>
-  static __device__ __forceinline__ void out(const RowState<D>& st, int t, F put) {
+  __device__ __forceinline__ void tile(RowState<D, NT>& st, uint32_t kt, uint32_t vt, unsigned have, int key0,
+                                       const Spans<NT>& sp, float sl2) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float hh[NT][4], hl[NT][4], lh[NT][4];  // three chains
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) hh[n][e] = hl[n][e] = lh[n][e] = 0.f;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      uint32_t kh[4][2], kl[4][2];  // [column of the piece][key g, g + 8]
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int r = g + 8 * z;
+        const uint4 raw = ld_shared_v4(kt + r * (D * 4) + (kpiece(r, 4 * s + t) << 4));
+        split(__uint_as_float(raw.x), kh[0][z], kl[0][z]);
+        split(__uint_as_float(raw.y), kh[1][z], kl[1][z]);
+        split(__uint_as_float(raw.z), kh[2][z], kl[2][z]);
+        split(__uint_as_float(raw.w), kh[3][z], kl[3][z]);
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const uint32_t ah[4] = {kh[2 * y][0], kh[2 * y][1], kh[2 * y + 1][0], kh[2 * y + 1][1]};
+        const uint32_t al[4] = {kl[2 * y][0], kl[2 * y][1], kl[2 * y + 1][0], kl[2 * y + 1][1]};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          uint32_t bh[2], bl[2];
+          split(qb[n][s][2 * y], bh[0], bl[0]);
+          split(qb[n][s][2 * y + 1], bh[1], bl[1]);
+          mma8(hh[n], ah, bh[0], bh[1]);
+          mma8(hl[n], ah, bl[0], bl[1]);
+          mma8(lh[n], al, bh[0], bh[1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) hh[n][e] += hl[n][e] + lh[n][e];
+    mask_scores<NT>(hh, sp, have, key0, sl2);
+    st.softmax(hh);
+    // p as B operands: row g, keys t and t + 4 of each half of the tile.
+    uint32_t ph[NT][4], pl[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int from = ((k & 1) * 4 + t) * 4 + (g >> 1);  // the thread of key t + 4 (k & 1), rows g, g ^ 1
+        const float a0 = __shfl_sync(0xFFFFFFFFu, hh[n][2 * (k >> 1)], from),
+                    a1 = __shfl_sync(0xFFFFFFFFu, hh[n][2 * (k >> 1) + 1], from);
+        split(g & 1 ? a1 : a0, ph[n][k], pl[n][k]);
+      }
+#pragma unroll
+    for (int q = 0; q < D / 32; ++q)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t vh[4][2], vl[4][2];  // [column of the piece][key t, t + 4]
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const int r = 8 * half + 4 * z + t;
+          const uint4 raw = ld_shared_v4(vt + r * (D * 4) + (vpiece(r, 8 * q + g) << 4));
+          split(__uint_as_float(raw.x), vh[0][z], vl[0][z]);
+          split(__uint_as_float(raw.y), vh[1][z], vl[1][z]);
+          split(__uint_as_float(raw.z), vh[2][z], vl[2][z]);
+          split(__uint_as_float(raw.w), vh[3][z], vl[3][z]);
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t ah[4] = {vh[2 * y][0], vh[2 * y + 1][0], vh[2 * y][1], vh[2 * y + 1][1]};
+          const uint32_t al[4] = {vl[2 * y][0], vl[2 * y + 1][0], vl[2 * y][1], vl[2 * y + 1][1]};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma8(st.o[n][2 * q + y], ah, ph[n][2 * half], ph[n][2 * half + 1]);
+            mma8(st.o[n][2 * q + y], al, ph[n][2 * half], ph[n][2 * half + 1]);
+            mma8(st.o[n][2 * q + y], ah, pl[n][2 * half], pl[n][2 * half + 1]);
+          }
+        }
+      }
+  }
+  static __device__ __forceinline__ float4 columns(const RowState<D, NT>& st, int n, int q, int x) {
+    return make_float4(st.o[n][2 * q][x], st.o[n][2 * q][2 + x], st.o[n][2 * q + 1][x], st.o[n][2 * q + 1][2 + x]);
+  }
+  static __device__ __forceinline__ void put_summary(const RowState<D, NT>& st, int n, float* z0, float* z1, int v) {
+    const int g = (threadIdx.x & 31) >> 2;
+#pragma unroll
+    for (int q = 0; q < D / 32; ++q) {
+      const int col = 32 * q + 4 * g;
+      if (col >= v) continue;
+      if (z0) *reinterpret_cast<float4*>(z0 + col) = columns(st, n, q, 0);
+      if (z1) *reinterpret_cast<float4*>(z1 + col) = columns(st, n, q, 1);
+    }
+  }
+  static __device__ __forceinline__ void put_rows(const PagedArgs& a, const RowState<D, NT>& st, int n,
+                                                  const size_t (&to)[2], const bool (&on)[2],
+                                                  const PagedScale (&f)[2]) {
+    const int g = (threadIdx.x & 31) >> 2;
+    float* Y = a.Yf ? a.Yf : static_cast<float*>(a.Y);
+    float4 z[2][D / 32];  // every load of the joined rows before the first store
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        const int col = 32 * q + 4 * g;
+        z[x][q] = on[x] && col < a.v ? paged_join4(a, f[x], to[x], col, columns(st, n, q, x))
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int q = 0; q < D / 32; ++q)
-#pragma unroll
-        for (int z = 0; z < 2; ++z)
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-            put(x, 32 * q + 8 * t + 4 * z + 2 * y,
-                make_float2(st.o[4 * q + 2 * y][2 * x + z], st.o[4 * q + 2 * y + 1][2 * x + z]));
+        if (on[x] && 32 * q + 4 * g < a.v) *reinterpret_cast<float4*>(Y + to[x] * a.v + 32 * q + 4 * g) = z[x][q];
   }
 };
 
-template <typename T, int D>
+template <typename T, int D, int NT>
 struct MmaLayout {
-  using St = Step<T, D>;
+  using St = Step<T, D, NT>;
   static constexpr int kRowBytes = D * static_cast<int>(sizeof(T));
-  static constexpr int kTileBytes = St::kTile * kRowBytes;  // of K or V
+  static constexpr int kTileBytes = kTile * kRowBytes;  // of K or V
   static constexpr int kWarpBytes = 2 * St::kStages * kTileBytes;
-  static constexpr int kBytes = kW * kWarpBytes;
+  static constexpr int kBytes = St::kW * kWarpBytes;
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * kW, 2) paged_mma_kernel(const PagedArgs a) {
-  using St = Step<T, D>;
-  using Lay = MmaLayout<T, D>;
-  constexpr int S = St::kStages, KT = St::kTile, CH = St::kCh, E = 16 / sizeof(T);
-  constexpr unsigned kAll = (1u << KT) - 1u;
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(const PagedArgs a) {
+  using St = Step<T, D, NT>;
+  using Lay = MmaLayout<T, D, NT>;
+  constexpr int S = St::kStages, kW = St::kW, kRows = 8 * NT, E = 16 / sizeof(T);
+  constexpr int CH = D / E;                 // pieces of a row
+  constexpr int kCopies = kTile * CH / 32;  // pieces of K or V that a lane copies of a tile
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ long long pre[kPagedMaxBatch + 1], scan[kW];
   __shared__ PagedWalk walks[kW][2];     // the present segment of the copies, of the products
@@ -340,11 +464,11 @@ __global__ void __launch_bounds__(32 * kW, 2) paged_mma_kernel(const PagedArgs a
   if (kch < CH)
     for (int x = lane; x < S * Lay::kTileBytes / 16; x += 32)
       *reinterpret_cast<uint4*>(own + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
-  paged_scan<kRows, KT, 32 * kW>(a, pre, scan, bits);
+  paged_scan<kRows, kTile, 32 * kW>(a, pre, scan, bits);
   int todo = 0;  // tiles of the worker
   {
     PagedWalk w;
-    if (paged_begin<kRows, KT>(a, pre, c, w)) {
+    if (paged_begin<kRows, kTile>(a, pre, c, w)) {
       todo = static_cast<int>(w.end - w.u);
       if (lane < 2) walks[warp][lane] = w;
     }
@@ -357,8 +481,7 @@ __global__ void __launch_bounds__(32 * kW, 2) paged_mma_kernel(const PagedArgs a
   int p_left = 0, p_key = 0, p_base = 0, p_j0 = 0, p_j1 = 0, p_h = 0;
   int pages = -1, pages_next = -1;
   const int* p_row = nullptr;
-  constexpr int kLogTile = KT == 16 ? 4 : 3;
-  const int lpk = min(a.lps, kLogTile), span = 32 << lpk;
+  const int lpk = min(a.lps, 4), span = 32 << lpk;
   auto entries = [&](int base) {
     const int key = base + (lane << lpk);
     int page = -1;
@@ -371,11 +494,22 @@ __global__ void __launch_bounds__(32 * kW, 2) paged_mma_kernel(const PagedArgs a
     }
     return page;
   };
+  // A lane's pieces: rows r1, r1 + kStep, ... of a tile, one column each.
+  constexpr int kStep = 32 / CH > 0 ? 32 / CH : 1;
+  const int r1 = lane / CH, pc = lane % CH;
+  uint32_t k_at[kStep < 8 ? 8 / kStep : 1], v_at[kStep < 8 ? 8 / kStep : 1];  // swizzles repeat every 8 rows
+  constexpr int kAts = sizeof(k_at) / 4;
+#pragma unroll
+  for (int x = 0; x < kAts; ++x) {
+    const int r = r1 + x * kStep;
+    k_at[x] = kbase + r * Lay::kRowBytes + (St::kpiece(r, pc) << 4);
+    v_at[x] = vbase + r * Lay::kRowBytes + (St::vpiece(r, pc) << 4);
+  }
   // The products' segment.
   int left = 0, key0 = 0;
-  Spans sp;
+  Spans<NT> sp;
   St step;
-  RowState<D> st;
+  RowState<D, NT> st;
 
   // One loop: step `it` copies tile it in and multiplies tile i = it - (S - 1).  Every
   // part of the code stands in one place, also while the ring fills: code that runs
@@ -390,14 +524,14 @@ __global__ void __launch_bounds__(32 * kW, 2) paged_mma_kernel(const PagedArgs a
       PagedWalk w = walks[warp][who];
       if (who == 0 ? it > 0 : i > 0) {
         int x, y;
-        paged_next<kRows, KT>(a, w, paged_segment<KT>(w, x, y));
+        paged_next<kRows, kTile>(a, w, paged_segment<kTile>(w, x, y));
         __syncwarp();
         if (lane == 0) walks[warp][who] = w;
         __syncwarp();
       }
       int j0, j1;
-      const int n = paged_segment<KT>(w, j0, j1);
-      const int key = (w.t.kt0 + w.rem) * KT;
+      const int n = paged_segment<kTile>(w, j0, j1);
+      const int key = (w.t.kt0 + w.rem) * kTile;
       if (who == 0) {
         p_left = n;
         p_base = p_key = key;
@@ -411,17 +545,21 @@ __global__ void __launch_bounds__(32 * kW, 2) paged_mma_kernel(const PagedArgs a
         left = n;
         key0 = key;
         const int r0 = w.rt * kRows;
-        const T* qr[2];
-        bool on[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int q = g + 8 * x, r = r0 + (q < w.t.rows ? q : 0), tok = div_by(r, a.by_group);
-          on[x] = q < w.t.rows;
-          paged_row_span(a, w.s, tok, sp.lo[x], sp.hi[x]);
-          if (on[x] && sp.lo[x] >= sp.hi[x] && w.rem == 0 && !a.initL) bits |= kStatusEmptyRow;
-          qr[x] = static_cast<const T*>(a.Q) + (w.s.s0 + tok) * a.q_stride + (w.h * a.G + r - tok * a.G) * d;
+        for (int y = 0; y < NT; ++y) {
+          // Row g of the tile for the operand, rows 2 t and 2 t + 1 for the statistics.
+          const int q = 8 * y + g, r = r0 + (q < w.t.rows ? q : 0), tok = div_by(r, a.by_group);
+          step.load_q(y,
+                      static_cast<const T*>(a.Q) + (w.s.s0 + tok) * a.q_stride + (w.h * a.G + r - tok * a.G) * d,
+                      q < w.t.rows, t, d);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int row = 8 * y + 2 * t + x;
+            const bool on = row < w.t.rows;
+            paged_row_span(a, w.s, div_by(r0 + (on ? row : 0), a.by_group), sp.lo[y][x], sp.hi[y][x]);
+            if (on && sp.lo[y][x] >= sp.hi[y][x] && w.rem == 0 && !a.initL) bits |= kStatusEmptyRow;
+          }
         }
-        step.load_q(qr, on, t, d);
         int unused;
         paged_row_span(a, w.s, w.t.i1, sp.all_lo, unused);
         paged_row_span(a, w.s, w.t.i0, unused, sp.all_hi);
@@ -435,27 +573,43 @@ __global__ void __launch_bounds__(32 * kW, 2) paged_mma_kernel(const PagedArgs a
         pages = pages_next;
         pages_next = entries(p_base + span);
       }
-      // Lane r: key r of the tile as a row of the pool, -1 for none.
-      const int key = p_key + lane % KT;
-      const int page = __shfl_sync(0xFFFFFFFFu, pages, (key - p_base) >> lpk);
-      const long long row = page < 0 || key < p_j0 || key >= p_j1
-                                ? -1
-                                : ((static_cast<long long>(page) * a.Hk + p_h) << a.lps) +
-                                      (key & ((1 << a.lps) - 1));
       const int s = it % S;
-      const unsigned have = __ballot_sync(0xFFFFFFFFu, row >= 0) & kAll;
-      if (lane == 0) tile_keys[warp][s] = have;
-      const uint32_t kd = kbase + s * Lay::kTileBytes, vd = vbase + s * Lay::kTileBytes;
+      const uint32_t slot = s * Lay::kTileBytes;
+      const int first = __shfl_sync(0xFFFFFFFFu, pages, (p_key - p_base) >> lpk);
+      unsigned have = 0xFFFFu;
+      if (lpk == 4 && first >= 0 && p_key >= p_j0 && p_key + kTile <= p_j1) {
+        // All sixteen keys, one page: rows behind one another.
+        const long long row = ((static_cast<long long>(first) * a.Hk + p_h) << a.lps) +
+                              (p_key & ((1 << a.lps) - 1)) + r1;
+        const T* kf = Kp + row * d + pc * E;
+        const T* vf = Vp + row * v + pc * E;
 #pragma unroll
-      for (int x = 0; x < KT * CH / 32; ++x) {
-        const int idx = x * 32 + lane, r = idx / CH, pc = idx % CH;
-        const long long at = __shfl_sync(0xFFFFFFFFu, row, r);
-        const long long from = at < 0 ? 0 : at;
-        const uint32_t off = r * Lay::kRowBytes;
-        if (pc < kch) cp16(kd + off + (St::kpiece(r, pc) << 4), Kp + from * d + pc * E, at < 0 ? 0 : 16);
-        if (pc < vch) cp16(vd + off + (St::vpiece(r, pc) << 4), Vp + from * v + pc * E, at < 0 ? 0 : 16);
+        for (int x = 0; x < kCopies; ++x) {
+          const uint32_t up = slot + (x / kAts) * kAts * kStep * Lay::kRowBytes;
+          if (pc < kch) cp16(k_at[x % kAts] + up, kf + x * kStep * d, 16);
+          if (pc < vch) cp16(v_at[x % kAts] + up, vf + x * kStep * v, 16);
+        }
+      } else {
+        // Lane r: key r of the tile as a row of the pool, -1 for none.
+        const int key = p_key + (lane & 15);
+        const int page = __shfl_sync(0xFFFFFFFFu, pages, (key - p_base) >> lpk);
+        const long long row = page < 0 || key < p_j0 || key >= p_j1
+                                  ? -1
+                                  : ((static_cast<long long>(page) * a.Hk + p_h) << a.lps) +
+                                        (key & ((1 << a.lps) - 1));
+        have = __ballot_sync(0xFFFFFFFFu, row >= 0) & 0xFFFFu;
+#pragma unroll 1
+        for (int x = 0; x < kCopies; ++x) {
+          const int r = r1 + x * kStep;
+          const long long at = __shfl_sync(0xFFFFFFFFu, row, r);
+          const long long from = at < 0 ? 0 : at;
+          const uint32_t off = slot + r * Lay::kRowBytes;
+          if (pc < kch) cp16(kbase + off + (St::kpiece(r, pc) << 4), Kp + from * d + pc * E, at < 0 ? 0 : 16);
+          if (pc < vch) cp16(vbase + off + (St::vpiece(r, pc) << 4), Vp + from * v + pc * E, at < 0 ? 0 : 16);
+        }
       }
-      p_key += KT;
+      if (lane == 0) tile_keys[warp][s] = have;
+      p_key += kTile;
       --p_left;
     }
     cp_commit();
@@ -464,57 +618,43 @@ __global__ void __launch_bounds__(32 * kW, 2) paged_mma_kernel(const PagedArgs a
     __syncwarp();  // tile i is in
     const int s = i % S;
     step.tile(st, kbase + s * Lay::kTileBytes, vbase + s * Lay::kTileBytes, tile_keys[warp][s], key0, sp, a.sl2);
-    key0 += KT;
+    key0 += kTile;
     if (--left > 0) continue;
 
     // The segment's rows.
     if (a.second) wait_for_previous();
     const PagedWalk w = walks[warp][1];
     int j0, j1;
-    const int n = paged_segment<KT>(w, j0, j1);
+    const int n = paged_segment<kTile>(w, j0, j1);
     const int slot = paged_slot<kRows>(a, w, n, c, lane == 0);
-    size_t to[2];
-    bool on[2];
-    PagedScale f[2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int q = g + 8 * x;
-      on[x] = q < w.t.rows;
-      float l = st.l[x];
-      l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
-      l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-      if (slot < 0) {
-        to[x] = paged_out_row(a, w.s.s0, w.h, w.rt * kRows + (on[x] ? q : 0));
-        f[x] = paged_finish(a, to[x], st.m[x], l);
-        if (on[x] && t == 0) a.L[to[x]] = f[x].L;
-      } else {
-        to[x] = static_cast<size_t>(slot) * kRows + q;
-        if (on[x] && t == 0) {
-          a.pm[to[x]] = st.m[x];
-          a.pl[to[x]] = l;
+    for (int y = 0; y < NT; ++y) {
+      size_t to[2];
+      bool on[2];
+      PagedScale f[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int q = 8 * y + 2 * t + x;
+        on[x] = q < w.t.rows;
+        float l = st.l[y][x];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        if (slot < 0) {
+          to[x] = paged_out_row(a, w.s.s0, w.h, w.rt * kRows + (on[x] ? q : 0));
+          f[x] = paged_finish(a, to[x], st.m[y][x], l);
+          if (on[x] && g == 0) a.L[to[x]] = f[x].L;
+        } else {
+          to[x] = static_cast<size_t>(slot) * kRows + q;
+          if (on[x] && g == 0) {
+            a.pm[to[x]] = st.m[y][x];
+            a.pl[to[x]] = l;
+          }
         }
       }
-    }
-    if (slot >= 0) {
-      St::out(st, t, [&](int x, int col, const float2& z) {
-        if (on[x] && col < v) *reinterpret_cast<float2*>(a.pz + to[x] * v + col) = z;
-      });
-    } else {
-      St::out(st, t, [&](int x, int col, const float2& z) {
-        if (!on[x] || col >= v) return;
-        const size_t at = to[x] * v + col;
-        float2 y = make_float2(z.x * f[x].fz, z.y * f[x].fz);
-        if (a.initY) {
-          const float2 p = *reinterpret_cast<const float2*>(a.initY + at);
-          y = make_float2(fmaf(p.x, f[x].fi, y.x), fmaf(p.y, f[x].fi, y.y));
-        }
-        if constexpr (sizeof(T) == 4) {
-          *reinterpret_cast<float2*>((a.Yf ? a.Yf : static_cast<float*>(a.Y)) + at) = y;
-        } else {
-          if (a.Yf) *reinterpret_cast<float2*>(a.Yf + at) = y;
-          else *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.Y) + at) = pack_bf16x2(y.x, y.y);
-        }
-      });
+      if (slot >= 0)
+        St::put_summary(st, y, on[0] ? a.pz + to[0] * v : nullptr, on[1] ? a.pz + to[1] * v : nullptr, v);
+      else
+        St::put_rows(a, st, y, to, on, f);
     }
   }
   cp_wait<0>();
@@ -522,29 +662,38 @@ __global__ void __launch_bounds__(32 * kW, 2) paged_mma_kernel(const PagedArgs a
   paged_end(a, bits, &joined);
 }
 
-template <typename T, int D>
+template <typename T, int D, int NT>
 cudaError_t mma_launch(const PagedArgs& a, cudaStream_t s) {
-  auto kern = paged_mma_kernel<T, D>;
-  constexpr int bytes = MmaLayout<T, D>::kBytes;
-  const cudaError_t e = allow_smem<paged_mma_kernel<T, D>>(bytes);
+  auto kern = paged_mma_kernel<T, D, NT>;
+  constexpr int bytes = MmaLayout<T, D, NT>::kBytes, threads = 32 * Step<T, D, NT>::kW;
+  const cudaError_t e = allow_smem<paged_mma_kernel<T, D, NT>>(bytes);
   if (e != cudaSuccess) return e;
-  before_launch(kKernPaged, s);
   cudaError_t le = cudaSuccess;
-  if (a.second) le = launch_early(kern, dim3(kCtas), 32 * kW, bytes, s, a);
-  else kern<<<kCtas, 32 * kW, bytes, s>>>(a);
+  before_launch(kKernPaged, s);
+  if (a.second) le = launch_early(kern, dim3(kCtas), threads, bytes, s, a);
+  else kern<<<kCtas, threads, bytes, s>>>(a);
   after_launch(kKernPaged, s);
   return le != cudaSuccess ? le : cudaGetLastError();
 }
 
+template <typename T, int D>
+cudaError_t mma_rows(const PagedArgs& a, int rows, cudaStream_t s) {
+  return rows == 8 ? mma_launch<T, D, 1>(a, s) : mma_launch<T, D, 2>(a, s);
+}
+
+bool narrow(int d, int v) { return d <= 64 && v <= 64; }
+
 }  // namespace
 
 bool paged_mma_shape(int d, int v) { return d <= 128 && v <= 128; }
-PagedKernel paged_mma_kernel() { return {kRows, kCtas, kCtas * kW, 4}; }
+PagedKernel paged_mma_kernel_of(int dtype, int d, int v, int rows) {
+  const int warps = dtype == kF32 && !narrow(d, v) ? Step<float, 128, 1>::kW : Step<float, 64, 1>::kW;
+  return {rows, kCtas, kCtas * warps, 4};
+}
 
-cudaError_t launch_paged_mma(const PagedArgs& a, cudaStream_t s) {
-  const bool narrow = a.d <= 64 && a.v <= 64;
-  if (a.dtype == kF32) return narrow ? mma_launch<float, 64>(a, s) : mma_launch<float, 128>(a, s);
-  return narrow ? mma_launch<__nv_bfloat16, 64>(a, s) : mma_launch<__nv_bfloat16, 128>(a, s);
+cudaError_t launch_paged_mma(const PagedArgs& a, int rows, cudaStream_t s) {
+  if (a.dtype == kF32) return narrow(a.d, a.v) ? mma_rows<float, 64>(a, rows, s) : mma_rows<float, 128>(a, rows, s);
+  return narrow(a.d, a.v) ? mma_rows<__nv_bfloat16, 64>(a, rows, s) : mma_rows<__nv_bfloat16, 128>(a, rows, s);
 }
 
 }  // namespace exattn

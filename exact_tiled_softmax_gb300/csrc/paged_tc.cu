@@ -593,15 +593,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
               y[e] = make_uint4(h[0], h[1], h[2], h[3]);
             }
           } else {
+            float4 y[8];  // every load of the joined rows before the first store
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const int col = ch * 32 + 4 * e;
-              if (col >= a.v) break;
-              paged_store4(a, row, col,
-                           paged_join4(a, f, row, col,
-                                       make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                                   __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]))));
+              y[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                 __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+              if (col < a.v) y[e] = paged_join4(a, f, row, col, y[e]);
             }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (ch * 32 + 4 * e < a.v) paged_store4(a, row, ch * 32 + 4 * e, y[e]);
           }
         }
         tc_fence_before();

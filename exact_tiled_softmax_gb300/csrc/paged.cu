@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
         }
       }
     }
-    const int slot = paged_slot<NQ>(a, w, n, blockIdx.x, threadIdx.x == 0);
+    const int slot = paged_slot<NQ>(a, pre, w, n, blockIdx.x, threadIdx.x == 0);
     __syncthreads();
     for (int idx = threadIdx.x; idx < rows * v; idx += 32 * kW) {
       const int q = idx / v, col = idx - q * v;
@@ -253,14 +253,14 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
         }
       }
     }
-    more = paged_next<NQ, kUnit>(a, w, n);
+    more = paged_next<NQ, kUnit>(a, w);
     __syncthreads();  // the joined rows are read before the next segment's
   }
   paged_end(a, bits, &joined);
 }
 
-// The star merge of the row tiles that one worker starts and others end.  Piece 0 of
-// worker c's tile is in slot 2c + 1, piece k > 0 in slot 2 (c + k).  Each kernel is
+// The star merge of the row tiles that one run starts and others end.  Piece 0 of run
+// c's tile is in slot 2c + 1, piece k > 0 in slot 2 (c + k).  Each kernel is
 // launched early and waits for the attention kernel at its start; CTA (0, 0) also joins
 // the status bits of every CTA of the attention launches.
 //
@@ -326,9 +326,9 @@ __device__ __forceinline__ void join_status(const PagedArgs& a) {
 }
 
 // Tiles of up to 16 rows, summaries row by row ([rows][v]).  kSpread: CTA (x, y) takes
-// row y of the tiles of every gridDim.x-th worker from x on (at most 32), its warps
-// sharing a row's pieces; else a warp takes a row of each.  (A CTA for every worker and
-// row cost 2 us a thousand CTAs, most of them without a tile.)
+// row y of the tiles of every gridDim.x-th run from x on (at most 32), its warps sharing a row's
+// pieces; else a warp takes a row of each.  (A CTA for every run and row cost 2 us a
+// thousand CTAs, most of them without a tile.)
 constexpr int kMergeW = 16;
 
 template <bool kSpread>
@@ -338,10 +338,10 @@ __global__ void __launch_bounds__(32 * kMergeW) paged_merge_kernel(const PagedAr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, v = a.v;
   let_next_start();
   wait_for_previous();
-  // Workers far apart: in a small launch only the first ones have tiles.
+  // Runs far apart: in a small launch only the first ones have tiles.
   const int cl = blockIdx.x + lane * gridDim.x;
   int4 mine = make_int4(0, 0, 0, 0);
-  if (cl < a.workers) mine = a.desc[cl];
+  if (cl < a.runs) mine = a.desc[cl];
   for (unsigned todo = __ballot_sync(0xFFFFFFFFu, mine.w != 0); todo; todo &= todo - 1) {
     const int who = __ffs(todo) - 1, c = blockIdx.x + who * gridDim.x;
     const int q = kSpread ? blockIdx.y : warp;
@@ -395,9 +395,9 @@ __global__ void __launch_bounds__(32 * kMergeW) paged_merge_kernel(const PagedAr
 }
 
 // Tiles of 256 rows, summaries column by column ([v / 4][256] pieces of four): a thread a
-// row, so that loads are whole lines.  CTA (x, y) takes pieces N y .. of the tiles of
-// workers kPer x ..: N = 4, kPer = 1 where most workers start a tile that others end, else
-// N = 1 and kPer = 8.
+// row, so that loads are whole lines.  CTA (x, y) takes pieces N y .. of the tiles of runs
+// kPer x ..: N = 4, kPer = 1 where most runs start a tile that others end, else N = 1 and
+// kPer = 8.
 constexpr int kTall = 256;
 
 template <int N, int kPer>
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kTall) paged_merge_tall_kernel(const PagedArgs
   let_next_start();
   wait_for_previous();
 #pragma unroll 1
-  for (int c = blockIdx.x * kPer; c < min(a.workers, (static_cast<int>(blockIdx.x) + 1) * kPer); ++c) {
+  for (int c = blockIdx.x * kPer; c < min(a.runs, (static_cast<int>(blockIdx.x) + 1) * kPer); ++c) {
     const int4 t = a.desc[c];
     const int r = t.x + q;
     if (t.w == 0 || r >= t.y) continue;
@@ -455,27 +455,24 @@ cudaError_t launch_paged_simt(const PagedArgs& a, bool one_row, cudaStream_t s) 
 }
 
 // Rows that a tile can have (q_starts hides how many tokens a sequence has).  Tiles that
-// may be spread over more than 16 workers give a row to all of a CTA's warps: a warp
-// alone takes four pieces of 512 bytes after four.
-// CTAs that take at most 32 workers each: a prime number, so that tiles that start at
-// every so manyth worker do not meet in one CTA.
-unsigned spread_ctas(unsigned workers) { return workers <= 41 * 32 ? 41 : (workers + 31) / 32; }
-
+// may be spread over more than 16 runs give a row to all of a CTA's warps: a warp alone
+// takes four pieces of 512 bytes after four.
 cudaError_t launch_paged_merge(const PagedArgs& a, int rt, cudaStream_t s) {
   const long long all = static_cast<long long>(a.starts ? a.T : a.each) * a.G;
   const unsigned rows = static_cast<unsigned>(all < rt ? all : rt);
-  const unsigned n4 = a.v / 4, workers = a.workers;
+  const unsigned n4 = a.v / 4, runs = a.runs;
   const long long usual = (static_cast<long long>(a.T + a.B - 1) / a.B * a.G + rt - 1) / rt;
   const long long tiles = usual * a.B * a.Hk;
-  const bool spread = workers > (rt == kTall ? 8 : 16) * tiles;
+  const bool spread = runs > (rt == kTall ? 8 : 16) * tiles;
   cudaError_t e;
   before_launch(kKernPagedMerge, s);
   if (rt == kTall)
-    e = spread ? launch_early(paged_merge_tall_kernel<1, 8>, dim3((workers + 7) / 8, n4), kTall, 0, s, a)
-               : launch_early(paged_merge_tall_kernel<4, 1>, dim3(workers, (n4 + 3) / 4), kTall, 0, s, a);
-  else
-    e = spread ? launch_early(paged_merge_kernel<true>, dim3(spread_ctas(workers), rows), 32 * kMergeW, 0, s, a, rt)
-               : launch_early(paged_merge_kernel<false>, dim3((workers + 1) / 2), 32 * kMergeW, 0, s, a, rt);
+    e = spread ? launch_early(paged_merge_tall_kernel<1, 8>, dim3((runs + 7) / 8, n4), kTall, 0, s, a)
+               : launch_early(paged_merge_tall_kernel<4, 1>, dim3(runs, (n4 + 3) / 4), kTall, 0, s, a);
+  else  // 41: a prime number, so that tiles that start at every so manyth run do not meet in one CTA
+    e = spread ? launch_early(paged_merge_kernel<true>, dim3(41, rows), 32 * kMergeW, 0, s, a, rt)
+               : launch_early(paged_merge_kernel<false>, dim3((runs + 1) / 2), 32 * kMergeW, 0, s,
+                              a, rt);
   after_launch(kKernPagedMerge, s);
   return e;
 }

@@ -9,17 +9,20 @@
 // Work.  A row tile is kRT consecutive rows of one (b, h); its keys, from the
 // first that any of its rows allows to the last, are cut at multiples of
 // kUnitKeys into units.  All units of the launch stand in one line, ordered by
-// (b, h, row tile, key), and worker c (a warp or a CTA, as the kernel has it) takes
-// units [c W, (c + 1) W), W = ceil(total / workers): every worker reads the same
-// number of keys, however unequal the lengths are and without the host knowing
-// them (they are read on the device, so a captured launch follows them).  A
-// worker's run of units is a list of segments, one for each row tile that it
-// touches.  A segment that holds all of its row tile's units writes Y and L; any
-// other writes its summary (m, l, z) of "Exact tiled softmax attention with
-// block-recomputed vector-Jacobian products", Forward procedure, to a slot of the
-// workspace: slot 2c + 1 when it starts the row tile, slot 2c when it continues
-// one (a worker has at most one of each), and paged_merge_kernel joins the slots
-// with the star rule.
+// (b, h, row tile, key), each row tile's rounded up to a multiple of `least`, and worker r
+// (a warp or a CTA, as the kernel has it) takes run r of W consecutive ones, W = total /
+// workers rounded up to such a multiple too: every worker reads the same number of keys,
+// however unequal the lengths are and without the host knowing them (they are read on
+// the device, so a captured launch follows them), and in a launch with few units none has
+// two tiles to end.  (A tail of short runs, taken from a counter by the workers that are done
+// first, changed nothing: 332 us for 2.1 GB either way, although the first worker is done
+// at 271 us; the memory is what is shared.)
+// A run is a list of segments, one for each row tile that it touches.  A segment that
+// holds all of its row tile's units writes Y and L; any other writes its summary
+// (m, l, z) of "Exact tiled softmax attention with block-recomputed vector-Jacobian
+// products", Forward procedure, to a slot of the workspace: slot 2 r + 1 when it starts
+// the row tile, slot 2 r when it continues one (run r has at most one of each), and a
+// merge kernel joins the slots with the star rule.
 #pragma once
 
 #include <math.h>
@@ -58,7 +61,7 @@ struct PagedArgs {
   const int* starts;  // [B + 1], or null: T / B tokens for every sequence
   int fixed_len;
   int B, T, Hk, G, d, v, dtype;
-  FastDiv by_group, by_heads, by_workers;  // G, Hk, workers
+  FastDiv by_group, by_heads;  // G, Hk
   int each;          // T / B
   int lps;  // log2(page_size)
   int num_pages, max_pages;
@@ -77,15 +80,16 @@ struct PagedArgs {
   unsigned* flags;   // [n_flags] status bits, one word for each CTA of each launch
   int n_flags;       // words that the merge kernel joins (from flags0)
   const unsigned* flags0;
-  // [workers] Of worker c: the row tile that it starts and others end, as (first row of the
-  // tile among (b, h)'s, rows of (b, h), s0, h << 16 | workers that hold a piece); the last
+  // [runs] Of run r: the row tile that it starts and others end, as (first row of the
+  // tile among (b, h)'s, rows of (b, h), s0, h << 16 | runs that hold a piece); the last
   // is 0 where there is none.
   int4* desc;
-  float* pm;   // [2 workers][RT] exp2 domain
-  float* pl;   // [2 workers][RT]
-  float* pz;   // [2 workers][RT][v]
-  int workers;
-  int least;    // units that a worker takes at least
+  float* pm;  // [2 runs][RT] exp2 domain
+  float* pl;  // [2 runs][RT]
+  float* pz;  // [2 runs][RT][v]
+  FastDiv by_runs;
+  int runs;   // and workers
+  int least;  // units that W and a row tile's are multiples of (a power of 2)
   bool second;  // behind another launch whose results (initY, initL) it joins
 };
 
@@ -155,10 +159,16 @@ __device__ __forceinline__ long long paged_div(long long n, long long d) {
   return static_cast<long long>(static_cast<unsigned long long>(n) / static_cast<unsigned long long>(d));
 }
 
-// A worker's place in the line of units.
+__device__ __forceinline__ long long round_up(long long x, int to) { return (x + to - 1) & -static_cast<long long>(to); }
+// Units of a run, W.
+__device__ __forceinline__ int run_units(const PagedArgs& a, long long total) {
+  return static_cast<int>(max(1ll * a.least, round_up(paged_div(total + a.runs - 1, a.by_runs), a.least)));
+}
+
+// A place in the line of units.
 struct PagedWalk {
-  long long u, end, w;  // next unit, the worker's end, units for each worker
-  int b, h, rt, rem;           // of unit u: sequence, key head, row tile, unit in the tile
+  long long u, end;   // next unit, the run's end
+  int b, h, rt, rem;  // of unit u: sequence, key head, row tile, unit in the tile
   PagedSeq s;
   PagedTile t;
   int tiles;  // row tiles of (b, h)
@@ -169,7 +179,7 @@ __device__ __forceinline__ long long paged_units(const PagedArgs& a, const Paged
   const int tiles = (s.nq * a.G + RT - 1) / RT;
   long long u = 0;
 #pragma unroll 1
-  for (int rt = 0; rt < tiles; ++rt) u += paged_tile<RT, UK>(a, s, rt).cnt;
+  for (int rt = 0; rt < tiles; ++rt) u += round_up(paged_tile<RT, UK>(a, s, rt).cnt, a.least);
   return u * a.Hk;
 }
 
@@ -215,13 +225,13 @@ __device__ __forceinline__ void paged_scan(const PagedArgs& a, long long* pre, l
   __syncthreads();
 }
 
-// Worker `c` at its first unit; false when it has none.
+// Run r's first unit; false when it has none.
 template <int RT, int UK>
-__device__ __forceinline__ bool paged_begin(const PagedArgs& a, const long long* pre, int c, PagedWalk& w) {
+__device__ __forceinline__ bool paged_begin(const PagedArgs& a, const long long* pre, int r, PagedWalk& w) {
   const long long total = pre[a.B];
-  w.w = max(static_cast<long long>(a.least), paged_div(total + a.workers - 1, a.by_workers));
-  w.u = min(total, w.w * c);
-  w.end = min(total, w.u + w.w);
+  const int n = run_units(a, total);
+  w.u = 1ll * n * r;
+  w.end = min(total, w.u + n);
   if (w.u >= w.end) return false;
   int b0 = 0, b1 = a.B;  // pre[b0] <= u < pre[b1]
 #pragma unroll 1
@@ -240,18 +250,18 @@ __device__ __forceinline__ bool paged_begin(const PagedArgs& a, const long long*
   w.rt = 0;
   w.t = paged_tile<RT, UK>(a, w.s, 0);
 #pragma unroll 1
-  while (rem >= w.t.cnt) {
-    rem -= w.t.cnt;
+  for (long long n; rem >= (n = round_up(w.t.cnt, a.least));) {
+    rem -= n;
     w.t = paged_tile<RT, UK>(a, w.s, ++w.rt);
   }
   w.rem = static_cast<int>(rem);
   return true;
 }
 
-// Past the segment of `n` units that starts at w.u; false at the worker's end.
+// Past the segment that starts at w.u; false at the run's end.
 template <int RT, int UK>
-__device__ __forceinline__ bool paged_next(const PagedArgs& a, PagedWalk& w, int n) {
-  w.u += n;
+__device__ __forceinline__ bool paged_next(const PagedArgs& a, PagedWalk& w) {
+  w.u += round_up(w.t.cnt, a.least) - w.rem;
   if (w.u >= w.end) return false;
   w.rem = 0;
   if (++w.rt == w.tiles) {
@@ -270,30 +280,32 @@ __device__ __forceinline__ bool paged_next(const PagedArgs& a, PagedWalk& w, int
   return true;
 }
 
-// Units of the segment that starts at w.u, and the keys they stand for.
+// Units of the segment that starts at w.u (0: only what the tile was rounded up by), and
+// the keys they stand for.
 template <int UK>
 __device__ __forceinline__ int paged_segment(const PagedWalk& w, int& j0, int& j1) {
-  const int n = static_cast<int>(min(static_cast<long long>(w.t.cnt - w.rem), w.end - w.u));
+  const int n = max(0, static_cast<int>(min(static_cast<long long>(w.t.cnt - w.rem), w.end - w.u)));
   const int kt = w.t.kt0 + w.rem;
   j0 = max(w.t.lo, kt * UK);
   j1 = min(w.t.hi, (kt + n) * UK);
   return n;
 }
 
-// Where the summary of worker c's present segment goes: its slot, or -1 when the
-// segment holds the whole row tile.  The thread `one` describes a tile that starts
-// here and ends with a later worker; parts: the workers that hold a piece of it.
+// Where the summary of run r's present segment of n units goes: its slot, or -1 when the
+// segment holds the whole row tile.  The thread `one` describes a tile that starts here
+// and ends in a later run.
 template <int RT>
-__device__ __forceinline__ int paged_slot(const PagedArgs& a, const PagedWalk& w, int n, int c, bool one) {
-  if (w.rem > 0) return 2 * c;
+__device__ __forceinline__ int paged_slot(const PagedArgs& a, const long long* pre, const PagedWalk& w, int n,
+                                          int r, bool one) {
+  if (w.rem > 0) return 2 * r;
   if (n == w.t.cnt) return -1;
   if (one) {
-    const long long last = w.u + w.t.cnt - 1;
-    a.desc[c] = make_int4(w.rt * RT, w.s.nq * a.G, w.s.s0,
+    const int last = static_cast<int>(paged_div(w.u + w.t.cnt - 1, static_cast<long long>(run_units(a, pre[a.B]))));
+    a.desc[r] = make_int4(w.rt * RT, w.s.nq * a.G, w.s.s0,
                           static_cast<int>((static_cast<unsigned>(w.h) << 16) |
-                                           (static_cast<unsigned>(paged_div(last, w.w)) - c + 1)));
+                                           static_cast<unsigned>(last - r + 1)));
   }
-  return 2 * c + 1;
+  return 2 * r + 1;
 }
 
 // Programmatic dependent launch: a kernel lets its successor's CTAs start as SMs
@@ -416,8 +428,7 @@ cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
-// Host side: rows of a tile, CTAs and workers of the launch, units that a worker
-// takes at least.
+// Host side: rows of a tile, CTAs and workers of the launch, the least multiple of units.
 struct PagedKernel {
   int rt, ctas, workers, least;
 };

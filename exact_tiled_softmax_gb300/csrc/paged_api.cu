@@ -84,8 +84,8 @@ Choice choose(const PagedArgs& a) {
   return c;
 }
 
-// Workspace of one attention launch and its merge: flags | tile descriptions |
-// m | l | z of the slots.
+// Workspace of one attention launch and its merge: tile descriptions | m | l | z of the
+// runs' slots.
 size_t pass_bytes(const PagedKernel& k, int v) {
   const size_t rows = 2 * (size_t)k.workers * k.rt;
   return align256(sizeof(int4) * (size_t)k.workers) + 2 * align256(sizeof(float) * rows) +
@@ -93,8 +93,8 @@ size_t pass_bytes(const PagedKernel& k, int v) {
 }
 constexpr size_t kFlagBytes = 8192;  // status bits of the CTAs of two passes (at most 2048)
 
-// The most that any kernel of this shape needs (the path may change between the
-// query and the call, and q_starts is not part of the shape).
+// The most that any kernel of this shape needs (the path may change between the query and
+// the call, and q_starts is not part of the shape).
 size_t most_bytes(const exattn_paged_shape* s) {
   size_t most = 0;
   for (const Kind k : {kSimtOne, kSimt, kMma8, kMma16, kTc}) {
@@ -107,19 +107,18 @@ size_t most_bytes(const exattn_paged_shape* s) {
   return most;
 }
 
-char* place_pass(PagedArgs& a, const PagedKernel& k, char* ws) {
-  const size_t rows = 2 * (size_t)k.workers * k.rt;
-  a.workers = k.workers;
-  a.by_workers = fast_div(k.workers);
+void place_pass(PagedArgs& a, const PagedKernel& k, char* at) {
+  a.runs = k.workers;
+  a.by_runs = fast_div(k.workers);
   a.least = k.least;
-  a.desc = reinterpret_cast<int4*>(ws);
-  ws += align256(sizeof(int4) * (size_t)k.workers);
-  a.pm = reinterpret_cast<float*>(ws);
-  ws += align256(sizeof(float) * rows);
-  a.pl = reinterpret_cast<float*>(ws);
-  ws += align256(sizeof(float) * rows);
-  a.pz = reinterpret_cast<float*>(ws);
-  return ws + align256(sizeof(float) * rows * a.v);
+  const size_t rows = 2 * (size_t)a.runs * k.rt;
+  a.desc = reinterpret_cast<int4*>(at);
+  at += align256(sizeof(int4) * (size_t)a.runs);
+  a.pm = reinterpret_cast<float*>(at);
+  at += align256(sizeof(float) * rows);
+  a.pl = reinterpret_cast<float*>(at);
+  at += align256(sizeof(float) * rows);
+  a.pz = reinterpret_cast<float*>(at);
 }
 
 PagedArgs make_args(const exattn_paged_shape* s, const void* Q, const void* Kp, const void* Vp,
@@ -306,8 +305,6 @@ int attn_fwd_prefix(const exattn_paged_shape* shape, const void* Q, const void* 
   const Choice cp = choose(p);
   p.flags = flags;
   place_pass(p, cp.k, own);
-  int r = cuda_result(run_pass(p, cp, s), "attn_fwd_prefix: prefix launch");
-  if (r != EXATTN_OK) return r;
   // Each sequence's own keys, joined with the prefix's rows.
   PagedArgs a = make_args(shape, Q, k_pages, v_pages, page_table, seq_lens, q_starts, scale, mask_kind,
                           0, Y, L);
@@ -320,6 +317,8 @@ int attn_fwd_prefix(const exattn_paged_shape* shape, const void* Q, const void* 
   a.n_flags = cp.k.ctas + c.k.ctas;
   a.second = true;
   place_pass(a, c.k, own + most_bytes(shape));
+  const int r = cuda_result(run_pass(p, cp, s), "attn_fwd_prefix: prefix launch");
+  if (r != EXATTN_OK) return r;
   return cuda_result(run_pass(a, c, s), "attn_fwd_prefix: launch");
 }
 

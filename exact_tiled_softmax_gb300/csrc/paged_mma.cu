@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   // Neighbouring workers on different SMs: a small launch spreads out.
-  const int c = warp * gridDim.x + blockIdx.x;
+  const int worker = warp * gridDim.x + blockIdx.x;
   const int d = a.d, v = a.v, kch = d / E, vch = v / E;
   const T* Kp = static_cast<const T*>(a.Kp);
   const T* Vp = static_cast<const T*>(a.Vp);
@@ -458,23 +458,13 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
   const uint32_t kbase = smem_u32(own), vbase = kbase + S * Lay::kTileBytes;
   unsigned bits = 0;
   let_next_start();
-  if (lane == 0) a.desc[c] = make_int4(0, 0, 0, 0);
+  if (lane == 0) a.desc[worker] = make_int4(0, 0, 0, 0);
   if (threadIdx.x == 0) joined = 0;
   // Columns of K that the rows do not have stay zero: no copy writes them.
   if (kch < CH)
     for (int x = lane; x < S * Lay::kTileBytes / 16; x += 32)
       *reinterpret_cast<uint4*>(own + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
   paged_scan<kRows, kTile, 32 * kW>(a, pre, scan, bits);
-  int todo = 0;  // tiles of the worker
-  {
-    PagedWalk w;
-    if (paged_begin<kRows, kTile>(a, pre, c, w)) {
-      todo = static_cast<int>(w.end - w.u);
-      if (lane < 2) walks[warp][lane] = w;
-    }
-  }
-  __syncwarp();
-
   // The copies' segment: tiles left, the next tile's first key, the keys that count.
   // Lane l holds the table entries of the keys from p_base + (l << lpk) on, and of as
   // many again behind those: one load for 512 keys, long before they are needed.
@@ -505,6 +495,9 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
     k_at[x] = kbase + r * Lay::kRowBytes + (St::kpiece(r, pc) << 4);
     v_at[x] = vbase + r * Lay::kRowBytes + (St::vpiece(r, pc) << 4);
   }
+  // Tiles copied so far, and whether more come.
+  int issued = 0;
+  bool more = true;
   // The products' segment.
   int left = 0, key0 = 0;
   Spans<NT> sp;
@@ -515,22 +508,26 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
   // part of the code stands in one place, also while the ring fills: code that runs
   // once costs its instruction fetches.
 #pragma unroll 1
-  for (int it = 0, i = 1 - S; i < todo; ++it, ++i) {
+  for (int it = 0, i = 1 - S; more || p_left > 0 || i < issued; ++it, ++i) {
     // Segments that start here: who = 0 the copies', 1 the products'.
 #pragma unroll 1
     for (int who = 0; who < 2; ++who) {
-      const bool starts = who == 0 ? p_left == 0 && it < todo : left == 0 && i >= 0;
+      const bool starts = who == 0 ? p_left == 0 && more : left == 0 && i >= 0 && i < issued;
       if (!starts) continue;
       PagedWalk w = walks[warp][who];
-      if (who == 0 ? it > 0 : i > 0) {
-        int x, y;
-        paged_next<kRows, kTile>(a, w, paged_segment<kTile>(w, x, y));
-        __syncwarp();
-        if (lane == 0) walks[warp][who] = w;
-        __syncwarp();
+      int n = 0, j0 = 0, j1 = 0;
+      bool on = (who == 0 ? it > 0 : i > 0) ? paged_next<kRows, kTile>(a, w)
+                                            : paged_begin<kRows, kTile>(a, pre, worker, w);
+      // A segment may hold only what its tile was rounded up by.
+#pragma unroll 1
+      while (on && (n = paged_segment<kTile>(w, j0, j1)) == 0) on = paged_next<kRows, kTile>(a, w);
+      if (!on) {  // the copies' end
+        more = false;
+        continue;
       }
-      int j0, j1;
-      const int n = paged_segment<kTile>(w, j0, j1);
+      __syncwarp();
+      if (lane == 0) walks[warp][who] = w;
+      __syncwarp();
       const int key = (w.t.kt0 + w.rem) * kTile;
       if (who == 0) {
         p_left = n;
@@ -567,13 +564,13 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
       }
     }
     __syncwarp();  // every lane is done with tile i - 1
-    if (it < todo) {
+    if (p_left > 0) {
       if (p_key - p_base >= span) {
         p_base += span;
         pages = pages_next;
         pages_next = entries(p_base + span);
       }
-      const int s = it % S;
+      const int s = issued++ % S;
       const uint32_t slot = s * Lay::kTileBytes;
       const int first = __shfl_sync(0xFFFFFFFFu, pages, (p_key - p_base) >> lpk);
       unsigned have = 0xFFFFu;
@@ -613,7 +610,7 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
       --p_left;
     }
     cp_commit();
-    if (i < 0) continue;
+    if (i < 0 || i >= issued) continue;
     cp_wait<S - 1>();
     __syncwarp();  // tile i is in
     const int s = i % S;
@@ -626,7 +623,7 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
     const PagedWalk w = walks[warp][1];
     int j0, j1;
     const int n = paged_segment<kTile>(w, j0, j1);
-    const int slot = paged_slot<kRows>(a, w, n, c, lane == 0);
+    const int slot = paged_slot<kRows>(a, pre, w, n, worker, lane == 0);
 #pragma unroll
     for (int y = 0; y < NT; ++y) {
       size_t to[2];

@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             t.r0 = w.rt * kRows;
             t.h = w.h;
             t.b = w.b;
-            t.slot = paged_slot<kRows>(a, w, t.n, blockIdx.x, lane == 0);
+            t.slot = paged_slot<kRows>(a, pre, w, t.n, blockIdx.x, lane == 0);
             t.first = w.rem == 0;
             t.s0 = w.s.s0;
             t.nq = w.s.nq;
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
           if (!more) break;
           if (seg > 0 && !(ok = wait_all(bar(Lay::B_QFREE), (seg - 1) & 1, abort_flag))) break;
           copy_q(t);
-          more = paged_next<kRows, kUnit>(a, w, t.n);
+          more = paged_next<kRows, kUnit>(a, w);
         }
       }
       if (!ok) {

@@ -466,7 +466,7 @@ def test_captured_launch_follows_lengths_and_tables(ex, path):
         with torch.cuda.graph(graph, stream=s):
             ex.append_paged(kn, vn, k, v, table, lens, ws=ws2)
             ex.fwd_paged(q, k, v, table, lens, 0.125, "causal", y=y, L=L, ws=ws)
-        graphs.append((graph, y, L, ws))
+        graphs.append((graph, y, L, ws, ws2))  # a graph's buffers live as long as it
     for step in range(3):
         lens.add_(1)
         kn.normal_()
@@ -474,9 +474,9 @@ def test_captured_launch_follows_lengths_and_tables(ex, path):
         graphs[1][0].replay()
         y, L = ex.fwd_paged(q, k, v, table, lens, 0.125, "causal")
         torch.cuda.synchronize()
-        for graph, yg, Lg, ws in graphs:
+        for graph, yg, Lg, ws, ws2 in graphs:
             assert torch.equal(y, yg) and torch.equal(L, Lg)
-            assert ex.device_status(ws) == 0
+            assert ex.device_status(ws) == 0 and ex.device_status(ws2) == 0
         ref = oracle.attend(b.np(b.q), k.double().cpu().numpy(), v.double().cpu().numpy(),
                             b.table, lens.cpu().numpy(), b.starts, 0.125, "causal")
         check_attention("bf16", y, L, ref, 64, 70)

@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
   constexpr int U = (NQ == 1 ? 8 : 4) / CPL;  // key steps in flight
   constexpr int STEP = KPW * U;
   constexpr int W = CPL * E;
-  __shared__ long long pre[kPagedMaxBatch + 1], scan[kW];
+  __shared__ long long pre[kPagedSums], scan[kW];
   __shared__ float red_m[kW][NQ], red_l[kW][NQ];
   __shared__ __align__(16) float red_z[kW][NQ][256];
 
@@ -74,7 +74,6 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
   const T* Vp = static_cast<const T*>(a.Vp);
   unsigned bits = 0;
   __shared__ unsigned joined;
-  if (a.second) wait_for_previous();
   let_next_start();
   if (threadIdx.x == 0) {
     a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -87,7 +86,7 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
     int j0, j1;
     const int n = paged_segment<kUnit>(w, j0, j1);
     const int r0 = w.rt * NQ, rows = w.t.rows;
-    const int* trow = a.table + static_cast<size_t>(w.b) * a.max_pages;
+    const int* trow = paged_table(a, w.b);
 
     // Rows of Q with scale * log2(e) folded in, and the keys that each allows.
     float qf[NQ][W];
@@ -96,7 +95,7 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
     for (int q = 0; q < NQ; ++q) {
       const int r = r0 + (q < rows ? q : 0), i = div_by(r, a.by_group);
       paged_row_span(a, w.s, i, lo[q], hi[q]);
-      if (q < rows && lo[q] >= hi[q] && w.rem == 0 && !a.initL) bits |= kStatusEmptyRow;
+      if (q < rows && lo[q] >= hi[q] && w.rem == 0 && !a.info) bits |= kStatusEmptyRow;
       const T* qr = Q + (w.s.s0 + i) * a.q_stride + (w.h * a.G + r - i * a.G) * d;
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
@@ -223,7 +222,8 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
         }
       }
     }
-    const int slot = paged_slot<NQ>(a, pre, w, n, blockIdx.x, threadIdx.x == 0);
+    const PagedPlace place = paged_place<NQ>(a, pre, w, n, blockIdx.x, threadIdx.x == 0);
+    const int slot = place.slot;
     __syncthreads();
     for (int idx = threadIdx.x; idx < rows * v; idx += 32 * kW) {
       const int q = idx / v, col = idx - q * v;
@@ -239,11 +239,12 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
           lq = fmaf(f, red_l[k][q], lq);
         }
       }
+      const size_t out = paged_out_row(a, w.s.s0, w.h, r0 + q, w.s.prefix);
+      if (a.info && col == 0 && place.parts >= 0) a.info[out] = make_int2(blockIdx.x, place.parts);
       if (slot < 0) {
-        const size_t row = paged_out_row(a, w.s.s0, w.h, r0 + q);
-        const PagedScale f = paged_finish(a, row, M, lq);
-        paged_store(a, row, col, paged_join(a, f, row, col, zc));
-        if (col == 0) a.L[row] = f.L;
+        const PagedScale f = paged_finish(M, lq);
+        paged_store(a, out, col, zc * f.fz);
+        if (col == 0) a.L[out] = f.L;
       } else {
         const size_t row = static_cast<size_t>(slot) * NQ + q;
         a.pz[row * v + col] = zc;
@@ -256,6 +257,7 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
     more = paged_next<NQ, kUnit>(a, w);
     __syncthreads();  // the joined rows are read before the next segment's
   }
+  if (a.second) wait_for_previous();
   paged_end(a, bits, &joined);
 }
 
@@ -275,8 +277,8 @@ struct Gather {
   }
   // Pieces first, first + step, ... below `parts`; row(k): piece k's index into pm and pl,
   // at(k, x): its x-th four columns, or null.
-  template <typename R, typename F>
-  __device__ __forceinline__ void take(const PagedArgs& a, int first, int step, int parts, R row, F at) {
+  template <typename A, typename R, typename F>
+  __device__ __forceinline__ void take(const A& a, int first, int step, int parts, R row, F at) {
 #pragma unroll 1
     for (int k0 = first; k0 < parts; k0 += 4 * step) {
       float pm[4], pl[4];
@@ -312,6 +314,10 @@ struct Gather {
     }
   }
 };
+
+__device__ __forceinline__ float4 scaled(const float4& z, float f) {
+  return make_float4(z.x * f, z.y * f, z.z * f, z.w * f);
+}
 
 __device__ __forceinline__ void join_status(const PagedArgs& a) {
   if (!a.status || blockIdx.x != 0 || blockIdx.y != 0) return;
@@ -349,7 +355,7 @@ __global__ void __launch_bounds__(32 * kMergeW) paged_merge_kernel(const PagedAr
               s0 = __shfl_sync(0xFFFFFFFFu, mine.z, who), hp = __shfl_sync(0xFFFFFFFFu, mine.w, who);
     const int parts = hp & 0xFFFF;
     if (q >= rt || r >= all) continue;  // kSpread: all warps alike
-    const size_t row = paged_out_row(a, s0, static_cast<unsigned>(hp) >> 16, r);
+    const size_t row = paged_out_row(a, s0, static_cast<unsigned>(hp) >> 16, r, false);
     Gather<2> x;
     auto at = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * rt + q; };
     x.take(a, kSpread ? warp : 0, kSpread ? kMergeW : 1, parts, at, [&](int k, int y) -> const float4* {
@@ -376,17 +382,17 @@ __global__ void __launch_bounds__(32 * kMergeW) paged_merge_kernel(const PagedAr
           l = fmaf(f, red_l[k], l);
           z = fmaf(f, red_z[k][col], z);
         }
-        const PagedScale f = paged_finish(a, row, M, l);
-        paged_store(a, row, col, paged_join(a, f, row, col, z));
+        const PagedScale f = paged_finish(M, l);
+        paged_store(a, row, col, z * f.fz);
         if (col == 0) a.L[row] = f.L;
       }
       __syncthreads();
     } else {
-      const PagedScale f = paged_finish(a, row, x.m, x.l);
+      const PagedScale f = paged_finish(x.m, x.l);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int col = 4 * lane + 128 * y;
-        if (col < v) paged_store4(a, row, col, paged_join4(a, f, row, col, x.z[y]));
+        if (col < v) paged_store4(a, row, col, scaled(x.z[y], f.fz));
       }
       if (lane == 0) a.L[row] = f.L;
     }
@@ -411,30 +417,153 @@ __global__ void __launch_bounds__(kTall) paged_merge_tall_kernel(const PagedArgs
     const int4 t = a.desc[c];
     const int r = t.x + q;
     if (t.w == 0 || r >= t.y) continue;
-    const size_t row = paged_out_row(a, t.z, static_cast<unsigned>(t.w) >> 16, r);
+    const size_t row = paged_out_row(a, t.z, static_cast<unsigned>(t.w) >> 16, r, false);
     Gather<N> x;
     auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)); };
     x.take(a, 0, 1, t.w & 0xFFFF, [&](int k) { return slot(k) * kTall + q; },
            [&](int k, int y) -> const float4* {
              return first + y < n4 ? z + (slot(k) * n4 + first + y) * kTall + q : nullptr;
            });
-    const PagedScale f = paged_finish(a, row, x.m, x.l);
+    const PagedScale f = paged_finish(x.m, x.l);
 #pragma unroll
     for (int y = 0; y < N; ++y)
       if (first + y < n4)
-        paged_store4(a, row, 4 * (first + y), paged_join4(a, f, row, 4 * (first + y), x.z[y]));
+        paged_store4(a, row, 4 * (first + y), scaled(x.z[y], f.fz));
     if (first == 0) a.L[row] = f.L;
   }
   join_status(a);
+}
+
+// A token's row over the shared prefix and over its own keys, joined.  A CTA a row of
+// [T][heads]; its warps share the pieces of both: a finished row is one piece (m = L
+// log2(e), l = 1), an unfinished one as many as runs hold some of it.
+constexpr int kJoinW = 4;
+
+struct JoinSide {
+  const float* pm;
+  const float* pl;
+  const float* pz;
+  int rt;
+};
+
+__global__ void __launch_bounds__(32 * kJoinW) paged_join_kernel(const PagedArgs a, const JoinSide own,
+                                                               const JoinSide prefix) {
+  __shared__ float red_m[kJoinW], red_l[kJoinW];
+  __shared__ __align__(16) float red_z[kJoinW][256];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, v = a.v, n4 = v / 4;
+  const int heads = a.Hk * a.G;
+  const size_t row = blockIdx.x, behind = static_cast<size_t>(a.T) * heads;
+  const int tok = blockIdx.x / heads, head = blockIdx.x - tok * heads;
+  wait_for_previous();
+  join_status(a);
+  // Rows of tokens that no sequence owns stay as they are.
+  int b = -1, s0 = 0;
+  if (a.starts) {
+    const int end = min(max(__ldg(a.starts + a.prefix_at), 0), a.T);
+    if (*a.sane && (tok < __ldg(a.starts) || tok >= end)) return;
+    // The owner, for the row's place in its tile (and, where q_starts is not sane, at all).
+    int b1 = a.prefix_at;
+    b = 0;
+    if (*a.sane) {
+      while (b1 - b > 1) {
+        const int mid = (b + b1) >> 1;
+        if (__ldg(a.starts + mid) <= tok) b = mid;
+        else b1 = mid;
+      }
+      s0 = __ldg(a.starts + b);
+    } else {
+      for (b = 0; b < b1; ++b) {
+        const PagedSeq s = paged_seq(a, b);
+        s0 = s.s0;
+        if (tok >= s0 && tok < s0 + s.nq) break;
+      }
+      if (b == b1) return;
+    }
+  } else {
+    s0 = tok / a.each * a.each;
+  }
+  const int h = div_by(head, a.by_group), g = head - h * a.G;
+  const int2 io = a.info[row], ip = a.info[row + behind];
+  const int q_own = ((tok - s0) * a.G + g) % own.rt, q_prefix = (tok * a.G + g) % prefix.rt;
+  float m = -INFINITY, l = 0.f;
+  float4 z[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    const JoinSide& of = side ? prefix : own;
+    const int2 at = side ? ip : io;
+    const int q = side ? q_prefix : q_own;
+    if (at.y == 0) {
+      if (warp != 0) continue;
+      const size_t from = row + (side ? behind : 0);
+      const float pm = a.L[from] * kLog2e;
+      const float4* p = reinterpret_cast<const float4*>(a.Yf + from * v);
+      const float top = fmaxf(m, pm), ref = top == -INFINITY ? 0.f : top;
+      const float f0 = pexp2(m - ref), f1 = pexp2(pm - ref);
+      m = top;
+      l = l * f0 + f1;
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        if (lane + 32 * y < n4) {
+          const float4 x = p[lane + 32 * y];
+          z[y] = make_float4(fmaf(x.x, f1, z[y].x * f0), fmaf(x.y, f1, z[y].y * f0), fmaf(x.z, f1, z[y].z * f0),
+                             fmaf(x.w, f1, z[y].w * f0));
+        }
+      continue;
+    }
+    Gather<2> x;
+    const int c = at.x;
+    auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)); };
+    const float4* pz = reinterpret_cast<const float4*>(of.pz);
+    x.take(of, warp, kJoinW, at.y, [&](int k) { return slot(k) * of.rt + q; },
+           [&](int k, int y) -> const float4* {
+             const int col = lane + 32 * y;
+             if (col >= n4) return nullptr;
+             return of.rt == kTall ? pz + (slot(k) * n4 + col) * kTall + q : pz + (slot(k) * of.rt + q) * n4 + col;
+           });
+    const float top = fmaxf(m, x.m), ref = top == -INFINITY ? 0.f : top;
+    const float f0 = pexp2(m - ref), f1 = pexp2(x.m - ref);
+    m = top;
+    l = l * f0 + x.l * f1;
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      z[y] = make_float4(fmaf(x.z[y].x, f1, z[y].x * f0), fmaf(x.z[y].y, f1, z[y].y * f0),
+                         fmaf(x.z[y].z, f1, z[y].z * f0), fmaf(x.z[y].w, f1, z[y].w * f0));
+  }
+  if (lane == 0) {
+    red_m[warp] = m;
+    red_l[warp] = l;
+  }
+  *reinterpret_cast<float4*>(&red_z[warp][4 * lane]) = z[0];
+  *reinterpret_cast<float4*>(&red_z[warp][4 * lane + 128]) = z[1];
+  __syncthreads();
+  float M = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < kJoinW; ++k) M = fmaxf(M, red_m[k]);
+  const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+  for (int k = 0; k < kJoinW; ++k) sum = fmaf(pexp2(red_m[k] - ref), red_l[k], sum);
+  const PagedScale f = paged_finish(M, sum);
+#pragma unroll 1
+  for (int col = threadIdx.x; col < v; col += 32 * kJoinW) {
+    float y = 0.f;
+#pragma unroll
+    for (int k = 0; k < kJoinW; ++k) y = fmaf(pexp2(red_m[k] - ref), red_z[k][col], y);
+    y *= f.fz;
+    if (a.dtype == kF32) static_cast<float*>(a.Y)[row * v + col] = y;
+    else static_cast<__nv_bfloat16*>(a.Y)[row * v + col] = __float2bfloat16_rn(y);
+  }
+  if (threadIdx.x == 0) a.Lout[row] = f.L;
 }
 
 template <typename T, int G, int CPL>
 cudaError_t simt_launch(const PagedArgs& a, bool one_row, cudaStream_t s) {
   before_launch(kKernPaged, s);
   auto kern = one_row ? paged_simt_kernel<T, G, CPL, 1> : paged_simt_kernel<T, G, CPL, 4>;
-  kern<<<kCtas, 32 * kW, 0, s>>>(a);
+  cudaError_t le = cudaSuccess;
+  if (a.second) le = launch_early(kern, dim3(kCtas), 32 * kW, 0, s, a);
+  else kern<<<kCtas, 32 * kW, 0, s>>>(a);
   after_launch(kKernPaged, s);
-  return cudaGetLastError();
+  return le != cudaSuccess ? le : cudaGetLastError();
 }
 
 }  // namespace
@@ -473,6 +602,16 @@ cudaError_t launch_paged_merge(const PagedArgs& a, int rt, cudaStream_t s) {
     e = spread ? launch_early(paged_merge_kernel<true>, dim3(41, rows), 32 * kMergeW, 0, s, a, rt)
                : launch_early(paged_merge_kernel<false>, dim3((runs + 1) / 2), 32 * kMergeW, 0, s,
                               a, rt);
+  after_launch(kKernPagedMerge, s);
+  return e;
+}
+
+cudaError_t launch_paged_join(const PagedArgs& own, int own_rt, const PagedArgs& prefix, int prefix_rt,
+                              cudaStream_t s) {
+  const JoinSide o{own.pm, own.pl, own.pz, own_rt}, p{prefix.pm, prefix.pl, prefix.pz, prefix_rt};
+  before_launch(kKernPagedMerge, s);
+  const cudaError_t e =
+      launch_early(paged_join_kernel, dim3(own.T * own.Hk * own.G), 32 * kJoinW, 0, s, own, o, p);
   after_launch(kKernPagedMerge, s);
   return e;
 }

@@ -23,6 +23,10 @@
 // products", Forward procedure, to a slot of the workspace: slot 2 r + 1 when it starts
 // the row tile, slot 2 r when it continues one (run r has at most one of each), and a
 // merge kernel joins the slots with the star rule.
+//
+// A shared prefix is one more sequence of the line: all T tokens over the prefix's keys,
+// without a mask.  Its rows and the sequences' own are two sets of results of the same
+// [T][heads], of which `info` says where each stands; paged_join_kernel joins them.
 #pragma once
 
 #include <math.h>
@@ -34,6 +38,7 @@
 namespace exattn {
 
 constexpr int kPagedMaxBatch = 1024;  // prefix sums of the units stay in shared memory
+constexpr int kPagedSums = kPagedMaxBatch + 2;
 
 // Division by a number that is fixed for a launch (n < 2^31): a high product, an
 // addition and a shift (Granlund and Montgomery, "Division by invariant integers
@@ -57,24 +62,27 @@ struct PagedArgs {
   const void* Kp;
   const void* Vp;
   const int* table;   // [B][max_pages]
-  const int* lens;    // [B], or null: fixed_len for every sequence
+  const int* prefix_table;
+  int prefix_at, prefix_len;  // sequence of the line that is the prefix (-1: none), its keys
+  const int* lens;    // [B]
   const int* starts;  // [B + 1], or null: T / B tokens for every sequence
-  int fixed_len;
-  int B, T, Hk, G, d, v, dtype;
+  int B, T, Hk, G, d, v, dtype;  // B: sequences of the line, the prefix among them
   FastDiv by_group, by_heads;  // G, Hk
-  int each;          // T / B
+  int each;                       // tokens of a sequence without starts
   int lps;  // log2(page_size)
   int num_pages, max_pages;
   int mask_kind, window;
   float sl2;  // scale * log2(e)
   long long q_stride;  // elements between tokens of Q
-  void* Y;             // [T][Hk * G][v] of dtype, or null: Yf
-  float* Yf;           // the same in fp32
+  void* Y;             // [T][Hk * G][v] of dtype
   float* L;            // [T][Hk * G], natural log
-  // The rows' summary over keys already attended to (a shared prefix): Y and L
-  // of those keys alone; null: none.
-  const float* initY;
-  const float* initL;
+  // With a shared prefix, instead of both: [2][T][Hk * G][v] and [2][T][Hk * G] in fp32, the
+  // sequences' own rows and the prefix's, and of each (first run, runs that hold a piece),
+  // the latter 0 where the row is finished.
+  float* Yf;
+  int2* info;
+  float* Lout;  // the call's L
+  int* sane;  // whether q_starts ascends and the lengths fit, for the join
   // Workspace.
   unsigned* status;  // written by the merge kernel; null: left for a later launch
   unsigned* flags;   // [n_flags] status bits, one word for each CTA of each launch
@@ -90,17 +98,25 @@ struct PagedArgs {
   FastDiv by_runs;
   int runs;   // and workers
   int least;  // units that W and a row tile's are multiples of (a power of 2)
-  bool second;  // behind another launch whose results (initY, initL) it joins
+  bool second;  // launched early behind another attention launch, independent of it
 };
 
 struct PagedSeq {
   int s0, nq, len;
-  bool bad;  // the caller's numbers do not fit (they are clamped)
+  bool prefix;  // all tokens over the shared prefix
+  bool bad;     // the caller's numbers do not fit (they are clamped)
 };
 
 __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int b) {
   PagedSeq s;
   s.bad = false;
+  s.prefix = b == a.prefix_at;
+  if (s.prefix) {
+    s.s0 = 0;
+    s.nq = a.T;
+    s.len = a.prefix_len;
+    return s;
+  }
   if (a.starts) {
     const int x = __ldg(a.starts + b), y = __ldg(a.starts + b + 1);
     s.s0 = min(max(x, 0), a.T);
@@ -111,7 +127,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int b) {
     s.nq = a.each;
     s.s0 = b * s.nq;
   }
-  const int n = a.lens ? __ldg(a.lens + b) : a.fixed_len;
+  const int n = __ldg(a.lens + b);
   s.len = min(max(n, 0), a.max_pages << a.lps);
   s.bad |= s.len != n;
   return s;
@@ -122,6 +138,7 @@ __device__ __forceinline__ void paged_row_span(const PagedArgs& a, const PagedSe
                                                int& hi) {
   lo = 0;
   hi = s.len;
+  if (s.prefix) return;
   const int pos = s.len - s.nq + i;
   if (a.mask_kind != kMaskNone) hi = min(hi, pos + 1);
   if (a.mask_kind == kMaskWindow) lo = max(0, pos + 1 - a.window);
@@ -183,7 +200,7 @@ __device__ __forceinline__ long long paged_units(const PagedArgs& a, const Paged
   return u * a.Hk;
 }
 
-// All threads of a CTA: `pre` (shared, kPagedMaxBatch + 1 words) receives the number
+// All threads of a CTA: `pre` (shared, kPagedSums words) receives the number
 // of units before each sequence.  Status bits that the caller's numbers raise go to
 // `bits` (of CTA 0).
 template <int RT, int UK, int NT>
@@ -211,7 +228,10 @@ __device__ __forceinline__ void paged_scan(const PagedArgs& a, long long* pre, l
   }
   if (lane == 31) scan[warp] = inc;
   const int any_bad = __syncthreads_or(bad);
-  if (any_bad && blockIdx.x == 0) bits |= kStatusBadPage;
+  if (blockIdx.x == 0) {
+    if (any_bad) bits |= kStatusBadPage;
+    if (a.info && tid == 0 && a.prefix_at != 0) *a.sane = !any_bad;
+  }
   long long before = inc - mine;
 #pragma unroll 1
   for (int k = 0; k < warp; ++k) before += scan[k];
@@ -291,21 +311,27 @@ __device__ __forceinline__ int paged_segment(const PagedWalk& w, int& j0, int& j
   return n;
 }
 
-// Where the summary of run r's present segment of n units goes: its slot, or -1 when the
-// segment holds the whole row tile.  The thread `one` describes a tile that starts here
-// and ends in a later run.
+// Where run r's present segment of n units goes: its slot, or -1 when the segment holds
+// the whole row tile; where the tile starts here, the runs that hold a piece of it (0: all
+// of it).  The thread `one` describes such a tile to the merge.
+struct PagedPlace {
+  int slot, parts;
+};
 template <int RT>
-__device__ __forceinline__ int paged_slot(const PagedArgs& a, const long long* pre, const PagedWalk& w, int n,
-                                          int r, bool one) {
-  if (w.rem > 0) return 2 * r;
-  if (n == w.t.cnt) return -1;
-  if (one) {
-    const int last = static_cast<int>(paged_div(w.u + w.t.cnt - 1, static_cast<long long>(run_units(a, pre[a.B]))));
+__device__ __forceinline__ PagedPlace paged_place(const PagedArgs& a, const long long* pre, const PagedWalk& w,
+                                                  int n, int r, bool one) {
+  if (w.rem > 0) return {2 * r, -1};
+  if (n == w.t.cnt) return {-1, 0};
+  const int last = static_cast<int>(paged_div(w.u + w.t.cnt - 1, static_cast<long long>(run_units(a, pre[a.B]))));
+  if (one)
     a.desc[r] = make_int4(w.rt * RT, w.s.nq * a.G, w.s.s0,
                           static_cast<int>((static_cast<unsigned>(w.h) << 16) |
                                            static_cast<unsigned>(last - r + 1)));
-  }
-  return 2 * r + 1;
+  return {2 * r + 1, last - r + 1};
+}
+
+__device__ __forceinline__ const int* paged_table(const PagedArgs& a, int b) {
+  return b == a.prefix_at ? a.prefix_table : a.table + static_cast<size_t>(b) * a.max_pages;
 }
 
 // Programmatic dependent launch: a kernel lets its successor's CTAs start as SMs
@@ -314,39 +340,19 @@ __device__ __forceinline__ int paged_slot(const PagedArgs& a, const long long* p
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Row r (of the tile's first row r0) as an index into [T][heads].
-__device__ __forceinline__ size_t paged_out_row(const PagedArgs& a, int s0, int h, int r) {
+// Row r of key head h as an index into [T][heads], the prefix's behind the sequences'.
+__device__ __forceinline__ size_t paged_out_row(const PagedArgs& a, int s0, int h, int r, bool prefix) {
   const int i = div_by(r, a.by_group);
-  return static_cast<size_t>(s0 + i) * (a.Hk * a.G) + h * a.G + (r - i * a.G);
+  return static_cast<size_t>(s0 + i + (prefix ? a.T : 0)) * (a.Hk * a.G) + h * a.G + (r - i * a.G);
 }
 
-// The two factors of a finished row (m in the exp2 domain, l): Y = z * fz +
-// initY * fi, and L is stored.  Empty rows give zeros and -inf.
+// A finished row (m in the exp2 domain, l): Y = z / l, and L.  Empty rows: 0 and -inf.
 struct PagedScale {
-  float fz, fi, L;
+  float fz, L;
 };
-__device__ __forceinline__ PagedScale paged_finish(const PagedArgs& a, size_t row, float m, float l) {
-  PagedScale f{0.f, 0.f, -INFINITY};
-  const float Li = a.initL ? a.initL[row] : -INFINITY;
-  const bool own = l > 0.f || l != l;  // a NaN score stays one
-  if (!own && Li == -INFINITY) return f;
-  const float mi = Li * kLog2e;  // the prefix's summary: m = mi, l = 1
-  const float M = own ? fmaxf(m, mi) : mi;
-  const float cz = own ? exp2f(m - M) : 0.f;
-  const float ci = Li == -INFINITY ? 0.f : exp2f(mi - M);
-  const float total = (own ? l * cz : 0.f) + ci;
-  f.fz = cz / total;
-  f.fi = ci / total;
-  f.L = (M + log2f(total)) * kLn2;
-  return f;
-}
-
-// One element of a finished row from its unnormalised sum z.
-__device__ __forceinline__ float paged_join(const PagedArgs& a, const PagedScale& f, size_t row, int col,
-                                            float z) {
-  float y = z * f.fz;
-  if (a.initY) y = fmaf(a.initY[row * a.v + col], f.fi, y);
-  return y;
+__device__ __forceinline__ PagedScale paged_finish(float m, float l) {
+  if (!(l > 0.f) && l == l) return {0.f, -INFINITY};  // a NaN score stays one
+  return {1.f / l, (m + log2f(l)) * kLn2};
 }
 
 __device__ __forceinline__ void paged_store(const PagedArgs& a, size_t row, int col, float y) {
@@ -355,21 +361,10 @@ __device__ __forceinline__ void paged_store(const PagedArgs& a, size_t row, int 
   else if (a.dtype == kF32) static_cast<float*>(a.Y)[at] = y;
   else static_cast<__nv_bfloat16*>(a.Y)[at] = __float2bfloat16_rn(y);
 }
-
-__device__ __forceinline__ float4 paged_join4(const PagedArgs& a, const PagedScale& f, size_t row, int col,
-                                              const float4& z) {
-  float4 y = make_float4(z.x * f.fz, z.y * f.fz, z.z * f.fz, z.w * f.fz);
-  if (a.initY) {
-    const float4 i = *reinterpret_cast<const float4*>(a.initY + row * a.v + col);
-    y = make_float4(fmaf(i.x, f.fi, y.x), fmaf(i.y, f.fi, y.y), fmaf(i.z, f.fi, y.z), fmaf(i.w, f.fi, y.w));
-  }
-  return y;
-}
+// Four columns into Y.
 __device__ __forceinline__ void paged_store4(const PagedArgs& a, size_t row, int col, const float4& y) {
   const size_t at = row * a.v + col;
-  if (a.Yf) {
-    *reinterpret_cast<float4*>(a.Yf + at) = y;
-  } else if (a.dtype == kF32) {
+  if (a.dtype == kF32) {
     *reinterpret_cast<float4*>(static_cast<float*>(a.Y) + at) = y;
   } else {
     const __nv_bfloat162 p = __floats2bfloat162_rn(y.x, y.y), q = __floats2bfloat162_rn(y.z, y.w);
@@ -441,6 +436,9 @@ bool paged_tc_supported(const PagedArgs& a);
 PagedKernel paged_tc_kernel_of();
 cudaError_t launch_paged_tc(const PagedArgs& a, cudaStream_t s);
 cudaError_t launch_paged_merge(const PagedArgs& a, int rt, cudaStream_t s);
+// own, prefix: the launches that hold the two sets (the same one, or two), with their tiles' rows.
+cudaError_t launch_paged_join(const PagedArgs& own, int own_rt, const PagedArgs& prefix, int prefix_rt,
+                              cudaStream_t s);
 
 struct AppendArgs {
   const void* q;  // may be null

@@ -107,6 +107,12 @@ size_t most_bytes(const exattn_paged_shape* s) {
   return most;
 }
 
+// With a shared prefix: both sets' rows and statistics, where each stands, a word.
+size_t join_bytes(size_t rows, int v) {
+  return align256(sizeof(float) * 2 * rows * v) + align256(sizeof(float) * 2 * rows) +
+         align256(sizeof(int2) * 2 * rows) + 256;
+}
+
 void place_pass(PagedArgs& a, const PagedKernel& k, char* at) {
   a.runs = k.workers;
   a.by_runs = fast_div(k.workers);
@@ -138,6 +144,7 @@ PagedArgs make_args(const exattn_paged_shape* s, const void* Q, const void* Kp, 
   a.by_group = fast_div(a.G);
   a.by_heads = fast_div(a.Hk);
   a.each = a.T / a.B;
+  a.prefix_at = -1;
   a.d = s->d;
   a.v = s->v;
   a.dtype = s->dtype;
@@ -159,11 +166,10 @@ int cuda_result(cudaError_t e, const char* where) {
   return EXATTN_CUDA_ERROR;
 }
 
-cudaError_t run_pass(const PagedArgs& a, const Choice& c, cudaStream_t s) {
-  const cudaError_t e = c.kind == kTc     ? launch_paged_tc(a, s)
-                        : c.kind >= kMma8 ? launch_paged_mma(a, c.k.rt, s)
-                                          : launch_paged_simt(a, c.kind == kSimtOne, s);
-  return e != cudaSuccess ? e : launch_paged_merge(a, c.k.rt, s);
+cudaError_t run_kernel(const PagedArgs& a, const Choice& c, cudaStream_t s) {
+  return c.kind == kTc     ? launch_paged_tc(a, s)
+         : c.kind >= kMma8 ? launch_paged_mma(a, c.k.rt, s)
+                           : launch_paged_simt(a, c.kind == kSimtOne, s);
 }
 
 int check_call(const exattn_paged_shape* shape, const void* Q, const void* Kp, const void* Vp,
@@ -192,8 +198,7 @@ size_t exattn_paged_workspace_size(const exattn_paged_shape* shape) {
 size_t exattn_prefix_workspace_size(const exattn_paged_shape* shape) {
   if (check_paged(shape) != EXATTN_OK) return 0;
   const size_t rows = (size_t)shape->tokens * shape->heads;
-  return kStatusBytes + kFlagBytes + 2 * most_bytes(shape) + align256(sizeof(float) * rows) +
-         align256(sizeof(float) * rows * shape->v);
+  return kStatusBytes + kFlagBytes + 2 * most_bytes(shape) + join_bytes(rows, shape->v);
 }
 
 int attn_append_paged(const exattn_paged_shape* shape, const void* q, const void* k, const void* v,
@@ -266,7 +271,10 @@ int attn_fwd_paged(const exattn_paged_shape* shape, const void* Q, const void* k
   a.flags0 = a.flags;
   a.n_flags = c.k.ctas;
   place_pass(a, c.k, ws + kStatusBytes + kFlagBytes);
-  return cuda_result(run_pass(a, c, static_cast<cudaStream_t>(cuda_stream)), "attn_fwd_paged: launch");
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  cudaError_t e = run_kernel(a, c, s);
+  if (e == cudaSuccess) e = launch_paged_merge(a, c.k.rt, s);
+  return cuda_result(e, "attn_fwd_paged: launch");
 }
 
 int attn_fwd_prefix(const exattn_paged_shape* shape, const void* Q, const void* k_pages,
@@ -290,36 +298,54 @@ int attn_fwd_prefix(const exattn_paged_shape* shape, const void* Q, const void* 
   g_last_error[0] = 0;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   char* ws = static_cast<char*>(workspace);
-  unsigned* flags = reinterpret_cast<unsigned*>(ws + kStatusBytes);
   const size_t rows = (size_t)shape->tokens * shape->heads;
-  char* own = ws + kStatusBytes + kFlagBytes;  // of the prefix's pass, then of the sequences' own
-  char* init = own + 2 * most_bytes(shape);
-  // All tokens over the prefix, as one sequence without a mask.
-  PagedArgs p = make_args(shape, Q, k_pages, v_pages, prefix_table, nullptr, nullptr, scale,
-                          EXATTN_MASK_NONE, 0, nullptr, reinterpret_cast<float*>(init));
+  char* area = ws + kStatusBytes + kFlagBytes;
+  char* sets = area + 2 * most_bytes(shape);
+  PagedArgs a = make_args(shape, Q, k_pages, v_pages, page_table, seq_lens, q_starts, scale, mask_kind, 0, Y, L);
+  a.Yf = reinterpret_cast<float*>(sets);
+  a.L = reinterpret_cast<float*>(sets + align256(sizeof(float) * 2 * rows * a.v));
+  a.info = reinterpret_cast<int2*>(reinterpret_cast<char*>(a.L) + align256(sizeof(float) * 2 * rows));
+  a.sane = reinterpret_cast<int*>(reinterpret_cast<char*>(a.info) + align256(sizeof(int2) * 2 * rows));
+  a.Lout = L;
+  a.prefix_table = prefix_table;
+  a.prefix_len = prefix_len;
+  a.flags = reinterpret_cast<unsigned*>(ws + kStatusBytes);
+  a.flags0 = a.flags;
+  // All tokens over the prefix are one sequence: of as many rows to a key head as the batch
+  // has, which may ask for another kernel than the sequences' own.
+  PagedArgs p = a;
   p.B = 1;
   p.each = p.T;
-  p.fixed_len = prefix_len;
-  p.max_pages = (prefix_len + shape->page_size - 1) / shape->page_size;
-  p.Yf = reinterpret_cast<float*>(init + align256(sizeof(float) * rows));
-  const Choice cp = choose(p);
-  p.flags = flags;
-  place_pass(p, cp.k, own);
-  // Each sequence's own keys, joined with the prefix's rows.
-  PagedArgs a = make_args(shape, Q, k_pages, v_pages, page_table, seq_lens, q_starts, scale, mask_kind,
-                          0, Y, L);
-  const Choice c = choose(a);
-  a.initY = p.Yf;
-  a.initL = p.L;
+  p.starts = nullptr;
+  p.prefix_at = 0;
+  Choice own = choose(a), of = choose(p);
+  const bool together = own.kind == of.kind || (own.kind <= kSimt) || (own.kind == kMma8 && of.kind == kMma16);
+  int launches_ctas = 0;
+  cudaError_t e;
+  if (together) {
+    // One launch over B + 1 sequences, with the larger tiles.
+    own = of;
+    ++a.B;
+    a.prefix_at = a.B - 1;
+    place_pass(a, own.k, area);
+    launches_ctas = own.k.ctas;
+    e = run_kernel(a, own, s);
+    p = a;
+  } else {
+    place_pass(p, of.k, area);
+    place_pass(a, own.k, area + most_bytes(shape));
+    a.flags = p.flags + of.k.ctas;
+    a.second = true;
+    launches_ctas = of.k.ctas + own.k.ctas;
+    e = run_kernel(p, of, s);
+    if (e == cudaSuccess) e = run_kernel(a, own, s);
+  }
+  if (e != cudaSuccess) return cuda_result(e, "attn_fwd_prefix: launch");
+  a.prefix_at = shape->batch;  // for the join: q_starts' last entry
+  a.Y = Y;
   a.status = static_cast<unsigned*>(workspace);
-  a.flags = flags + cp.k.ctas;
-  a.flags0 = flags;
-  a.n_flags = cp.k.ctas + c.k.ctas;
-  a.second = true;
-  place_pass(a, c.k, own + most_bytes(shape));
-  const int r = cuda_result(run_pass(p, cp, s), "attn_fwd_prefix: prefix launch");
-  if (r != EXATTN_OK) return r;
-  return cuda_result(run_pass(a, c, s), "attn_fwd_prefix: launch");
+  a.n_flags = launches_ctas;
+  return cuda_result(launch_paged_join(a, own.k.rt, p, of.k.rt, s), "attn_fwd_prefix: join launch");
 }
 
 int exattn_paged_run(int op, const exattn_paged_call* c) {

@@ -254,25 +254,13 @@ struct Step<__nv_bfloat16, D, NT> {
                                                   const size_t (&to)[2], const bool (&on)[2],
                                                   const PagedScale (&f)[2]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    // Every load of the joined rows before the first store: they may not pass one another.
-    float z[2][D / 8];
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int y = 0; y < D / 8; ++y) {
-        const int col = 8 * y + g;
-        z[x][y] = a.initY && on[x] && col < a.v ? a.initY[to[x] * a.v + col] * f[x].fi : 0.f;
-      }
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int y = 0; y < D / 8; ++y) z[x][y] = fmaf(st.o[n][y / 2][2 * (y & 1) + x], f[x].fz, z[x][y]);
     if (a.Yf) {
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int y = 0; y < D / 8; ++y)
-          if (on[x] && 8 * y + g < a.v) a.Yf[to[x] * a.v + 8 * y + g] = z[x][y];
+          if (on[x] && 8 * y + g < a.v)
+            a.Yf[to[x] * a.v + 8 * y + g] = st.o[n][y / 2][2 * (y & 1) + x] * f[x].fz;
       return;
     }
     // Lane (g, t) stores row g of the tile, two columns at a time, after a transposition.
@@ -283,7 +271,8 @@ struct Step<__nv_bfloat16, D, NT> {
     const bool mine_on = g & 1 ? o1 : o0;
 #pragma unroll
     for (int y = 0; y < D / 8; ++y) {
-      const uint32_t pair = transpose8(pack_bf16x2(z[0][y], z[1][y]));  // row g, columns 2 t and 2 t + 1 of eight
+      const float *o = &st.o[n][y / 2][2 * (y & 1)];
+      const uint32_t pair = transpose8(pack_bf16x2(o[0] * f[0].fz, o[1] * f[1].fz));  // row g, columns 2 t and 2 t + 1 of eight
       if (mine_on && 8 * y < a.v) *reinterpret_cast<uint32_t*>(mine + 8 * y + 2 * t) = pair;
     }
   }
@@ -408,20 +397,15 @@ struct Step<float, D, NT> {
                                                   const PagedScale (&f)[2]) {
     const int g = (threadIdx.x & 31) >> 2;
     float* Y = a.Yf ? a.Yf : static_cast<float*>(a.Y);
-    float4 z[2][D / 32];  // every load of the joined rows before the first store
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int q = 0; q < D / 32; ++q) {
-        const int col = 32 * q + 4 * g;
-        z[x][q] = on[x] && col < a.v ? paged_join4(a, f[x], to[x], col, columns(st, n, q, x))
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int q = 0; q < D / 32; ++q)
-        if (on[x] && 32 * q + 4 * g < a.v) *reinterpret_cast<float4*>(Y + to[x] * a.v + 32 * q + 4 * g) = z[x][q];
+        if (on[x] && 32 * q + 4 * g < a.v) {
+          const float4 z = columns(st, n, q, x);
+          *reinterpret_cast<float4*>(Y + to[x] * a.v + 32 * q + 4 * g) =
+              make_float4(z.x * f[x].fz, z.y * f[x].fz, z.z * f[x].fz, z.w * f[x].fz);
+        }
   }
 };
 
@@ -442,7 +426,7 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
   constexpr int CH = D / E;                 // pieces of a row
   constexpr int kCopies = kTile * CH / 32;  // pieces of K or V that a lane copies of a tile
   extern __shared__ __align__(128) uint8_t sm[];
-  __shared__ long long pre[kPagedMaxBatch + 1], scan[kW];
+  __shared__ long long pre[kPagedSums], scan[kW];
   __shared__ PagedWalk walks[kW][2];     // the present segment of the copies, of the products
   __shared__ unsigned tile_keys[kW][S];  // bit r: key r of the staged tile exists
   __shared__ unsigned joined;
@@ -535,7 +519,7 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
         p_j0 = j0;
         p_j1 = j1;
         p_h = w.h;
-        p_row = a.table + static_cast<size_t>(w.b) * a.max_pages;
+        p_row = paged_table(a, w.b);
         pages = entries(p_base);
         pages_next = entries(p_base + span);
       } else {
@@ -554,7 +538,7 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
             const int row = 8 * y + 2 * t + x;
             const bool on = row < w.t.rows;
             paged_row_span(a, w.s, div_by(r0 + (on ? row : 0), a.by_group), sp.lo[y][x], sp.hi[y][x]);
-            if (on && sp.lo[y][x] >= sp.hi[y][x] && w.rem == 0 && !a.initL) bits |= kStatusEmptyRow;
+            if (on && sp.lo[y][x] >= sp.hi[y][x] && w.rem == 0 && !a.info) bits |= kStatusEmptyRow;
           }
         }
         int unused;
@@ -619,11 +603,11 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
     if (--left > 0) continue;
 
     // The segment's rows.
-    if (a.second) wait_for_previous();
     const PagedWalk w = walks[warp][1];
     int j0, j1;
     const int n = paged_segment<kTile>(w, j0, j1);
-    const int slot = paged_slot<kRows>(a, pre, w, n, worker, lane == 0);
+    const PagedPlace place = paged_place<kRows>(a, pre, w, n, worker, lane == 0);
+    const int slot = place.slot;
 #pragma unroll
     for (int y = 0; y < NT; ++y) {
       size_t to[2];
@@ -636,9 +620,10 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
         float l = st.l[y][x];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        to[x] = paged_out_row(a, w.s.s0, w.h, w.rt * kRows + (on[x] ? q : 0), w.s.prefix);
+        if (a.info && place.parts >= 0 && on[x] && g == 0) a.info[to[x]] = make_int2(worker, place.parts);
         if (slot < 0) {
-          to[x] = paged_out_row(a, w.s.s0, w.h, w.rt * kRows + (on[x] ? q : 0));
-          f[x] = paged_finish(a, to[x], st.m[y][x], l);
+          f[x] = paged_finish(st.m[y][x], l);
           if (on[x] && g == 0) a.L[to[x]] = f[x].L;
         } else {
           to[x] = static_cast<size_t>(slot) * kRows + q;
@@ -655,7 +640,7 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
     }
   }
   cp_wait<0>();
-  if (a.second) wait_for_previous();  // warps without units too: the next launch counts on it
+  if (a.second) wait_for_previous();  // the next launch waits for this one alone
   paged_end(a, bits, &joined);
 }
 

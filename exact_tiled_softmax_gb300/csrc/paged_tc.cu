@@ -56,7 +56,7 @@ struct TcParams {
 
 // A segment, as warp 11 hands it out; n == 0: no more.
 struct TcSegment {
-  int n, kb0, j0, j1, rows, r0, h, b, slot, first, s0, nq, len;
+  int n, kb0, j0, j1, rows, r0, h, b, slot, parts, s0, nq, len;  // parts: see PagedPlace
 };
 
 template <int D>
@@ -76,7 +76,7 @@ struct TcLayout {
   static constexpr int SEG_OFF = MISC_OFF + 16;
   static constexpr int TOTAL = SEG_OFF + 2 * 64;
   static constexpr int ALLOC = TOTAL + 1024;
-  static_assert(ALLOC + (kPagedMaxBatch + 1) * 8 + 256 <= 232448, "shared memory");
+  static_assert(ALLOC + kPagedSums * 8 + 256 <= 232448, "shared memory");
 };
 
 __device__ __forceinline__ uint32_t range_bits(int a, int b) {  // bits [a, b] of a word
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
   using Lay = TcLayout<D>;
   constexpr int NS = Lay::NSLOT;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ long long pre[kPagedMaxBatch + 1], scan[kThreads / 32];
+  __shared__ long long pre[kPagedSums], scan[kThreads / 32];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     t.h = r[6];
     t.b = r[7];
     t.slot = r[8];
-    t.first = r[9];
+    t.parts = r[9];
     t.s0 = r[10];
     t.nq = r[11];
     t.len = r[12];
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       int fill = 0;
       TcSegment t;
       for (int seg = 0; take(seg, t, ok); ++seg) {
-        const int* trow = a.table + static_cast<size_t>(t.b) * a.max_pages;
+        const int* trow = paged_table(a, t.b);
         // Lane l: the pool row of box l of block u, or -1.
         auto find = [&](int u) {
           int row = -1;
@@ -397,8 +397,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             t.r0 = w.rt * kRows;
             t.h = w.h;
             t.b = w.b;
-            t.slot = paged_slot<kRows>(a, pre, w, t.n, blockIdx.x, lane == 0);
-            t.first = w.rem == 0;
+            const PagedPlace place = paged_place<kRows>(a, pre, w, t.n, blockIdx.x, lane == 0);
+            t.slot = place.slot;
+            t.parts = place.parts;
             t.s0 = w.s.s0;
             t.nq = w.s.nq;
             t.len = w.s.len;
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             r[6] = t.h;
             r[7] = t.b;
             r[8] = t.slot;
-            r[9] = t.first;
+            r[9] = t.parts;
             r[10] = t.s0;
             r[11] = t.nq;
             r[12] = t.len;
@@ -447,12 +448,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     TcSegment t;
     for (int seg = 0; take(seg, t, ok); ++seg) {
       const int n = t.n, r0 = t.r0, rows = t.rows, kb0 = t.kb0;
-      const PagedSeq sq{t.s0, t.nq, t.len, false};
+      const PagedSeq sq{t.s0, t.nq, t.len, t.b == a.prefix_at, false};
       const bool on = X * kHalf < rows;  // this half has rows
       const bool valid = rl < rows;
       int lo, hi, all_lo = 0, all_hi = 0;
       paged_row_span(a, sq, div_by(r0 + (valid ? rl : 0), a.by_group), lo, hi);
-      if (valid && lo >= hi && t.first && !a.initL) bits |= kStatusEmptyRow;
+      if (valid && lo >= hi && t.parts >= 0 && !a.info) bits |= kStatusEmptyRow;
       if (on) {
         int unused;
         paged_row_span(a, sq, div_by(r0 + min(rows, X * kHalf + kHalf) - 1, a.by_group), all_lo, unused);
@@ -541,7 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       if (!(ok = wait_all(bar(Lay::B_O + X), seg & 1, abort_flag))) break;
       tc_fence_after();
       const float m = l > 0.f || l != l ? m_ref : -INFINITY;
-      if (a.second) wait_for_previous();
+      const size_t row = paged_out_row(a, sq.s0, t.h, r0 + (valid ? rl : 0), sq.prefix);
+      if (a.info && t.parts >= 0 && valid) a.info[row] = make_int2(blockIdx.x, t.parts);
       if (t.slot >= 0) {
         // The summary, columns outside rows: a warp's stores are whole lines.
         float4* z = reinterpret_cast<float4*>(a.pz) + static_cast<size_t>(t.slot) * (a.v / 4) * kRows + rl;
@@ -566,10 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
           a.pl[static_cast<size_t>(t.slot) * kRows + rl] = l;
         }
       } else {
-        const size_t row = paged_out_row(a, sq.s0, t.h, r0 + (valid ? rl : 0));
-        PagedScale f{0.f, 0.f, 0.f};
+        PagedScale f{0.f, 0.f};
         if (valid) {
-          f = paged_finish(a, row, m, l);
+          f = paged_finish(m, l);
           a.L[row] = f.L;
         }
 #pragma unroll
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
           tmem_ld_wait();
           reg_fence(o);
           if (!valid) continue;
-          if (!a.initY && !a.Yf) {
+          if (!a.Yf) {
             uint4* y = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.Y) + row * a.v + ch * 32);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {  // eight columns a store (v is a multiple of 8)
@@ -593,17 +594,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
               y[e] = make_uint4(h[0], h[1], h[2], h[3]);
             }
           } else {
-            float4 y[8];  // every load of the joined rows before the first store
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int col = ch * 32 + 4 * e;
-              y[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                 __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-              if (col < a.v) y[e] = paged_join4(a, f, row, col, y[e]);
-            }
+            float4* y = reinterpret_cast<float4*>(a.Yf + row * a.v + ch * 32);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (ch * 32 + 4 * e < a.v) paged_store4(a, row, ch * 32 + 4 * e, y[e]);
+              if (ch * 32 + 4 * e < a.v)
+                y[e] = make_float4(__uint_as_float(o[4 * e]) * f.fz, __uint_as_float(o[4 * e + 1]) * f.fz,
+                                   __uint_as_float(o[4 * e + 2]) * f.fz, __uint_as_float(o[4 * e + 3]) * f.fz);
           }
         }
         tc_fence_before();

@@ -400,11 +400,15 @@ __global__ void __launch_bounds__(32 * kMergeW) paged_merge_kernel(const PagedAr
   join_status(a);
 }
 
-// Tiles of 256 rows, summaries column by column ([v / 4][256] pieces of four): a thread a
-// row, so that loads are whole lines.  CTA (x, y) takes pieces N y .. of the tiles of runs
-// kPer x ..: N = 4, kPer = 1 where most runs start a tile that others end, else N = 1 and
-// kPer = 8.
+// Tiles of 256 rows, summaries column by column ([v / 8][256] pieces of eight): a thread a
+// row, so that loads are whole lines.  CTA (x, y) takes four columns N y .. (in fours) of
+// the tiles of runs kPer x ..: N = 4, kPer = 1 where most runs start a tile that others end,
+// else N = 2 and kPer = 8.
 constexpr int kTall = 256;
+// Four columns, number c, of row q of slot s.
+__device__ __forceinline__ size_t tall_at(size_t s, int v, int c, int q) {
+  return ((s * (v / 8) + c / 2) * kTall + q) * 2 + (c & 1);
+}
 
 template <int N, int kPer>
 __global__ void __launch_bounds__(kTall) paged_merge_tall_kernel(const PagedArgs a) {
@@ -422,7 +426,7 @@ __global__ void __launch_bounds__(kTall) paged_merge_tall_kernel(const PagedArgs
     auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)); };
     x.take(a, 0, 1, t.w & 0xFFFF, [&](int k) { return slot(k) * kTall + q; },
            [&](int k, int y) -> const float4* {
-             return first + y < n4 ? z + (slot(k) * n4 + first + y) * kTall + q : nullptr;
+             return first + y < n4 ? z + tall_at(slot(k), a.v, first + y, q) : nullptr;
            });
     const PagedScale f = paged_finish(x.m, x.l);
 #pragma unroll
@@ -518,7 +522,7 @@ __global__ void __launch_bounds__(32 * kJoinW) paged_join_kernel(const PagedArgs
            [&](int k, int y) -> const float4* {
              const int col = lane + 32 * y;
              if (col >= n4) return nullptr;
-             return of.rt == kTall ? pz + (slot(k) * n4 + col) * kTall + q : pz + (slot(k) * of.rt + q) * n4 + col;
+             return of.rt == kTall ? pz + tall_at(slot(k), v, col, q) : pz + (slot(k) * of.rt + q) * n4 + col;
            });
     const float top = fmaxf(m, x.m), ref = top == -INFINITY ? 0.f : top;
     const float f0 = pexp2(m - ref), f1 = pexp2(x.m - ref);
@@ -596,7 +600,7 @@ cudaError_t launch_paged_merge(const PagedArgs& a, int rt, cudaStream_t s) {
   cudaError_t e;
   before_launch(kKernPagedMerge, s);
   if (rt == kTall)
-    e = spread ? launch_early(paged_merge_tall_kernel<1, 8>, dim3((runs + 7) / 8, n4), kTall, 0, s, a)
+    e = spread ? launch_early(paged_merge_tall_kernel<2, 8>, dim3((runs + 7) / 8, (n4 + 1) / 2), kTall, 0, s, a)
                : launch_early(paged_merge_tall_kernel<4, 1>, dim3(runs, (n4 + 3) / 4), kTall, 0, s, a);
   else  // 41: a prime number, so that tiles that start at every so manyth run do not meet in one CTA
     e = spread ? launch_early(paged_merge_kernel<true>, dim3(41, rows), 32 * kMergeW, 0, s, a, rt)

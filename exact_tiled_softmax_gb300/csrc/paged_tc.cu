@@ -545,8 +545,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       const size_t row = paged_out_row(a, sq.s0, t.h, r0 + (valid ? rl : 0), sq.prefix);
       if (a.info && t.parts >= 0 && valid) a.info[row] = make_int2(blockIdx.x, t.parts);
       if (t.slot >= 0) {
-        // The summary, columns outside rows: a warp's stores are whole lines.
-        float4* z = reinterpret_cast<float4*>(a.pz) + static_cast<size_t>(t.slot) * (a.v / 4) * kRows + rl;
+        // The summary, [v / 8][256] pieces of eight columns: a warp's stores are whole lines.
+        float* z = a.pz + (static_cast<size_t>(t.slot) * (a.v / 8) * kRows + rl) * 8;
 #pragma unroll
         for (int ch = 0; ch < D / 32; ++ch) {
           if (!on || ch * 32 >= a.v) break;
@@ -555,11 +555,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
           tmem_ld_wait();
           reg_fence(o);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (valid && ch * 32 + 4 * e < a.v)
-              z[(ch * 8 + e) * kRows] =
-                  make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                              __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+          for (int e = 0; e < 4; ++e)
+            if (valid && ch * 32 + 8 * e < a.v)
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                               z + static_cast<size_t>(ch * 4 + e) * kRows * 8),
+                           "r"(o[8 * e]), "r"(o[8 * e + 1]), "r"(o[8 * e + 2]), "r"(o[8 * e + 3]), "r"(o[8 * e + 4]),
+                           "r"(o[8 * e + 5]), "r"(o[8 * e + 6]), "r"(o[8 * e + 7])
+                           : "memory");
         }
         tc_fence_before();
         mbar_arrive(bar(Lay::B_OREAD + X));

@@ -337,10 +337,11 @@ __device__ __forceinline__ void join_status(const PagedArgs& a) {
 // thousand CTAs, most of them without a tile.)
 constexpr int kMergeW = 16;
 
-template <bool kSpread>
+// N: times 128 columns.
+template <bool kSpread, int N>
 __global__ void __launch_bounds__(32 * kMergeW) paged_merge_kernel(const PagedArgs a, int rt) {
   __shared__ float red_m[kMergeW], red_l[kMergeW];
-  __shared__ __align__(16) float red_z[kSpread ? kMergeW : 1][256];
+  __shared__ __align__(16) float red_z[kSpread ? kMergeW : 1][128 * N];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, v = a.v;
   let_next_start();
   wait_for_previous();
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(32 * kMergeW) paged_merge_kernel(const PagedAr
     const int parts = hp & 0xFFFF;
     if (q >= rt || r >= all) continue;  // kSpread: all warps alike
     const size_t row = paged_out_row(a, s0, static_cast<unsigned>(hp) >> 16, r, false);
-    Gather<2> x;
+    Gather<N> x;
     auto at = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * rt + q; };
     x.take(a, kSpread ? warp : 0, kSpread ? kMergeW : 1, parts, at, [&](int k, int y) -> const float4* {
       const int col = 4 * lane + 128 * y;
@@ -367,8 +368,8 @@ __global__ void __launch_bounds__(32 * kMergeW) paged_merge_kernel(const PagedAr
         red_m[warp] = x.m;
         red_l[warp] = x.l;
       }
-      *reinterpret_cast<float4*>(&red_z[warp][4 * lane]) = x.z[0];
-      *reinterpret_cast<float4*>(&red_z[warp][4 * lane + 128]) = x.z[1];
+#pragma unroll
+      for (int y = 0; y < N; ++y) *reinterpret_cast<float4*>(&red_z[warp][4 * lane + 128 * y]) = x.z[y];
       __syncthreads();
       const int col = threadIdx.x;
       if (col < v) {
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(32 * kMergeW) paged_merge_kernel(const PagedAr
     } else {
       const PagedScale f = paged_finish(x.m, x.l);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
+      for (int y = 0; y < N; ++y) {
         const int col = 4 * lane + 128 * y;
         if (col < v) paged_store4(a, row, col, scaled(x.z[y], f.fz));
       }
@@ -450,10 +451,11 @@ struct JoinSide {
   int rt;
 };
 
+template <int N>
 __global__ void __launch_bounds__(32 * kJoinW) paged_join_kernel(const PagedArgs a, const JoinSide own,
                                                                const JoinSide prefix) {
   __shared__ float red_m[kJoinW], red_l[kJoinW];
-  __shared__ __align__(16) float red_z[kJoinW][256];
+  __shared__ __align__(16) float red_z[kJoinW][128 * N];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, v = a.v, n4 = v / 4;
   const int heads = a.Hk * a.G;
   const size_t row = blockIdx.x, behind = static_cast<size_t>(a.T) * heads;
@@ -490,7 +492,9 @@ __global__ void __launch_bounds__(32 * kJoinW) paged_join_kernel(const PagedArgs
   const int2 io = a.info[row], ip = a.info[row + behind];
   const int q_own = ((tok - s0) * a.G + g) % own.rt, q_prefix = (tok * a.G + g) % prefix.rt;
   float m = -INFINITY, l = 0.f;
-  float4 z[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  float4 z[N];
+#pragma unroll
+  for (int y = 0; y < N; ++y) z[y] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
   for (int side = 0; side < 2; ++side) {
     const JoinSide& of = side ? prefix : own;
@@ -506,7 +510,7 @@ __global__ void __launch_bounds__(32 * kJoinW) paged_join_kernel(const PagedArgs
       m = top;
       l = l * f0 + f1;
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
+      for (int y = 0; y < N; ++y)
         if (lane + 32 * y < n4) {
           const float4 x = p[lane + 32 * y];
           z[y] = make_float4(fmaf(x.x, f1, z[y].x * f0), fmaf(x.y, f1, z[y].y * f0), fmaf(x.z, f1, z[y].z * f0),
@@ -514,7 +518,7 @@ __global__ void __launch_bounds__(32 * kJoinW) paged_join_kernel(const PagedArgs
         }
       continue;
     }
-    Gather<2> x;
+    Gather<N> x;
     const int c = at.x;
     auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)); };
     const float4* pz = reinterpret_cast<const float4*>(of.pz);
@@ -529,7 +533,7 @@ __global__ void __launch_bounds__(32 * kJoinW) paged_join_kernel(const PagedArgs
     m = top;
     l = l * f0 + x.l * f1;
 #pragma unroll
-    for (int y = 0; y < 2; ++y)
+    for (int y = 0; y < N; ++y)
       z[y] = make_float4(fmaf(x.z[y].x, f1, z[y].x * f0), fmaf(x.z[y].y, f1, z[y].y * f0),
                          fmaf(x.z[y].z, f1, z[y].z * f0), fmaf(x.z[y].w, f1, z[y].w * f0));
   }
@@ -537,8 +541,8 @@ __global__ void __launch_bounds__(32 * kJoinW) paged_join_kernel(const PagedArgs
     red_m[warp] = m;
     red_l[warp] = l;
   }
-  *reinterpret_cast<float4*>(&red_z[warp][4 * lane]) = z[0];
-  *reinterpret_cast<float4*>(&red_z[warp][4 * lane + 128]) = z[1];
+#pragma unroll
+  for (int y = 0; y < N; ++y) *reinterpret_cast<float4*>(&red_z[warp][4 * lane + 128 * y]) = z[y];
   __syncthreads();
   float M = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -603,9 +607,10 @@ cudaError_t launch_paged_merge(const PagedArgs& a, int rt, cudaStream_t s) {
     e = spread ? launch_early(paged_merge_tall_kernel<2, 8>, dim3((runs + 7) / 8, (n4 + 1) / 2), kTall, 0, s, a)
                : launch_early(paged_merge_tall_kernel<4, 1>, dim3(runs, (n4 + 3) / 4), kTall, 0, s, a);
   else  // 41: a prime number, so that tiles that start at every so manyth run do not meet in one CTA
-    e = spread ? launch_early(paged_merge_kernel<true>, dim3(41, rows), 32 * kMergeW, 0, s, a, rt)
-               : launch_early(paged_merge_kernel<false>, dim3((runs + 1) / 2), 32 * kMergeW, 0, s,
-                              a, rt);
+    e = spread ? launch_early(a.v <= 128 ? paged_merge_kernel<true, 1> : paged_merge_kernel<true, 2>, dim3(41, rows),
+                              32 * kMergeW, 0, s, a, rt)
+               : launch_early(a.v <= 128 ? paged_merge_kernel<false, 1> : paged_merge_kernel<false, 2>,
+                              dim3((runs + 1) / 2), 32 * kMergeW, 0, s, a, rt);
   after_launch(kKernPagedMerge, s);
   return e;
 }
@@ -615,7 +620,7 @@ cudaError_t launch_paged_join(const PagedArgs& own, int own_rt, const PagedArgs&
   const JoinSide o{own.pm, own.pl, own.pz, own_rt}, p{prefix.pm, prefix.pl, prefix.pz, prefix_rt};
   before_launch(kKernPagedMerge, s);
   const cudaError_t e =
-      launch_early(paged_join_kernel, dim3(own.T * own.Hk * own.G), 32 * kJoinW, 0, s, own, o, p);
+      launch_early(own.v <= 128 ? paged_join_kernel<1> : paged_join_kernel<2>, dim3(own.T * own.Hk * own.G), 32 * kJoinW, 0, s, own, o, p);
   after_launch(kKernPagedMerge, s);
   return e;
 }

@@ -73,7 +73,10 @@ struct Choice {
 
 // Rows of a key head on average: all that the host knows of them.
 long long rows_of(const PagedArgs& a) { return (long long)(a.T + a.B - 1) / a.B * a.G; }
-constexpr int kTcRows = 64;
+// From 17 rows on a second 16-row tile would read K and V again; the 256-row tiles read them
+// once.  32 sequences of 8192 keys, 8 key heads of 128 columns: 16 rows 183 us (186 on the
+// tall tiles), 24 rows 331 (190), 64 rows 644 (194); 4 of 4000: 16 rows 31 (31), 32 rows 42 (27).
+constexpr int kTcRows = 16;
 
 Choice choose(const PagedArgs& a) {
   Choice c;
@@ -319,7 +322,16 @@ int attn_fwd_prefix(const exattn_paged_shape* shape, const void* Q, const void* 
   p.starts = nullptr;
   p.prefix_at = 0;
   Choice own = choose(a), of = choose(p);
-  const bool together = own.kind == of.kind || (own.kind <= kSimt) || (own.kind == kMma8 && of.kind == kMma16);
+  if (own.kind != of.kind && of.kind == kTc && own.kind >= kMma8) {
+    // Tall tiles for the prefix alone mean a launch of their own, 6 us; 16-row tiles read the
+    // prefix again for each, at some 6.5 TB/s (of the L2 cache).
+    const double bytes = (double)prefix_len * a.Hk * (a.d + a.v) * 2, again = (double)((rows_of(p) + 15) / 16 - 1);
+    if (again * bytes < 40e6) {
+      of.kind = kMma16;
+      of.k = kernel_of(of.kind, a.dtype, a.d, a.v);
+    }
+  }
+  const bool together = own.kind == of.kind || own.kind <= kSimt || (own.kind == kMma8 && of.kind == kMma16);
   int launches_ctas = 0;
   cudaError_t e;
   if (together) {

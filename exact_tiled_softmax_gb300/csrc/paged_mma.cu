@@ -305,11 +305,11 @@ struct Step<float, D, NT> {
   __device__ __forceinline__ void tile(RowState<D, NT>& st, uint32_t kt, uint32_t vt, unsigned have, int key0,
                                        const Spans<NT>& sp, float sl2) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    float hh[NT][4], hl[NT][4], lh[NT][4];  // three chains
+    float hh[2][NT][4], hl[NT][4], lh[NT][4];  // four chains
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) hh[n][e] = hl[n][e] = lh[n][e] = 0.f;
+      for (int e = 0; e < 4; ++e) hh[0][n][e] = hh[1][n][e] = hl[n][e] = lh[n][e] = 0.f;
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
       uint32_t kh[4][2], kl[4][2];  // [column of the piece][key g, g + 8]
@@ -331,7 +331,7 @@ struct Step<float, D, NT> {
           uint32_t bh[2], bl[2];
           split(qb[n][s][2 * y], bh[0], bl[0]);
           split(qb[n][s][2 * y + 1], bh[1], bl[1]);
-          mma8(hh[n], ah, bh[0], bh[1]);
+          mma8(hh[y][n], ah, bh[0], bh[1]);
           mma8(hl[n], ah, bl[0], bl[1]);
           mma8(lh[n], al, bh[0], bh[1]);
         }
@@ -340,9 +340,10 @@ struct Step<float, D, NT> {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) hh[n][e] += hl[n][e] + lh[n][e];
-    mask_scores<NT>(hh, sp, have, key0, sl2);
-    st.softmax(hh);
+      for (int e = 0; e < 4; ++e) hh[0][n][e] = (hh[0][n][e] + hh[1][n][e]) + (hl[n][e] + lh[n][e]);
+    float(&sc)[NT][4] = hh[0];
+    mask_scores<NT>(sc, sp, have, key0, sl2);
+    st.softmax(sc);
     // p as B operands: row g, keys t and t + 4 of each half of the tile.
     uint32_t ph[NT][4], pl[NT][4];
 #pragma unroll
@@ -350,12 +351,19 @@ struct Step<float, D, NT> {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int from = ((k & 1) * 4 + t) * 4 + (g >> 1);  // the thread of key t + 4 (k & 1), rows g, g ^ 1
-        const float a0 = __shfl_sync(0xFFFFFFFFu, hh[n][2 * (k >> 1)], from),
-                    a1 = __shfl_sync(0xFFFFFFFFu, hh[n][2 * (k >> 1) + 1], from);
+        const float a0 = __shfl_sync(0xFFFFFFFFu, sc[n][2 * (k >> 1)], from),
+                    a1 = __shfl_sync(0xFFFFFFFFu, sc[n][2 * (k >> 1) + 1], from);
         split(g & 1 ? a1 : a0, ph[n][k], pl[n][k]);
       }
+    // A tile's products are summed by the tensor cores, which cut their sums instead of
+    // rounding them, and added to the output in rounded fp32.
 #pragma unroll
-    for (int q = 0; q < D / 32; ++q)
+    for (int q = 0; q < D / 32; ++q) {
+      float sum[2][NT][4];
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) sum[y][n][0] = sum[y][n][1] = sum[y][n][2] = sum[y][n][3] = 0.f;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t vh[4][2], vl[4][2];  // [column of the piece][key t, t + 4]
@@ -374,12 +382,19 @@ struct Step<float, D, NT> {
           const uint32_t al[4] = {vl[2 * y][0], vl[2 * y + 1][0], vl[2 * y][1], vl[2 * y + 1][1]};
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma8(st.o[n][2 * q + y], ah, ph[n][2 * half], ph[n][2 * half + 1]);
-            mma8(st.o[n][2 * q + y], al, ph[n][2 * half], ph[n][2 * half + 1]);
-            mma8(st.o[n][2 * q + y], ah, pl[n][2 * half], pl[n][2 * half + 1]);
+            mma8(sum[y][n], ah, ph[n][2 * half], ph[n][2 * half + 1]);
+            mma8(sum[y][n], al, ph[n][2 * half], ph[n][2 * half + 1]);
+            mma8(sum[y][n], ah, pl[n][2 * half], pl[n][2 * half + 1]);
           }
         }
       }
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) st.o[n][2 * q + y][e] += sum[y][n][e];
+    }
   }
   static __device__ __forceinline__ float4 columns(const RowState<D, NT>& st, int n, int q, int x) {
     return make_float4(st.o[n][2 * q][x], st.o[n][2 * q][2 + x], st.o[n][2 * q + 1][x], st.o[n][2 * q + 1][2 + x]);

@@ -34,7 +34,7 @@ def _p_bits(path, dtype, tokens, batch, group):
     whole or two tf32 parts (2^-21), which the sums' own terms cover."""
     if dtype == "f32":
         return 21
-    many = -(-tokens // batch) * group > 64
+    many = -(-tokens // batch) * group > 16
     return 8 if path == "auto" and dtype == "bf16" and many else 16
 
 

@@ -92,6 +92,8 @@ __device__ void append_check(const AppendArgs& a) {
 // halves, those above one access of the columns that pass.
 template <typename T, int W>
 __global__ void __launch_bounds__(kAppendThreads, 6) append_kernel(const __grid_constant__ AppendArgs a) {
+  wait_for_previous();
+  let_next_start();
   if (blockIdx.x == gridDim.x - 1) {
     append_check(a);
     return;
@@ -199,9 +201,9 @@ cudaError_t append_launch(AppendArgs a, cudaStream_t s) {
   a.by_shares = fast_div(shares);
   const unsigned ctas = (static_cast<unsigned>(a.T) * shares + kAppendWarps - 1) / kAppendWarps;
   before_launch(kKernAppend, s);
-  append_kernel<T, W><<<ctas + 1, kAppendThreads, 0, s>>>(a);
+  const cudaError_t e = launch_early(append_kernel<T, W>, dim3(ctas + 1), kAppendThreads, 0, s, a);
   after_launch(kKernAppend, s);
-  return cudaGetLastError();
+  return e;
 }
 
 template <typename T>

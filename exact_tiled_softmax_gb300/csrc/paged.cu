@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
   const T* Vp = static_cast<const T*>(a.Vp);
   unsigned bits = 0;
   __shared__ unsigned joined;
+  if (!a.second) wait_for_previous();
   let_next_start();
   if (threadIdx.x == 0) {
     a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -343,8 +344,8 @@ __global__ void __launch_bounds__(32 * kMergeW) paged_merge_kernel(const PagedAr
   __shared__ float red_m[kMergeW], red_l[kMergeW];
   __shared__ __align__(16) float red_z[kSpread ? kMergeW : 1][128 * N];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, v = a.v;
-  let_next_start();
   wait_for_previous();
+  let_next_start();
   // Runs far apart: in a small launch only the first ones have tiles.
   const int cl = blockIdx.x + lane * gridDim.x;
   int4 mine = make_int4(0, 0, 0, 0);
@@ -415,8 +416,8 @@ template <int N, int kPer>
 __global__ void __launch_bounds__(kTall) paged_merge_tall_kernel(const PagedArgs a) {
   const int q = threadIdx.x, n4 = a.v / 4, first = N * blockIdx.y;
   const float4* z = reinterpret_cast<const float4*>(a.pz);
-  let_next_start();
   wait_for_previous();
+  let_next_start();
 #pragma unroll 1
   for (int c = blockIdx.x * kPer; c < min(a.runs, (static_cast<int>(blockIdx.x) + 1) * kPer); ++c) {
     const int4 t = a.desc[c];
@@ -461,6 +462,7 @@ __global__ void __launch_bounds__(32 * kJoinW) paged_join_kernel(const PagedArgs
   const size_t row = blockIdx.x, behind = static_cast<size_t>(a.T) * heads;
   const int tok = blockIdx.x / heads, head = blockIdx.x - tok * heads;
   wait_for_previous();
+  let_next_start();
   join_status(a);
   // Rows of tokens that no sequence owns stay as they are.
   int b = -1, s0 = 0;
@@ -565,13 +567,11 @@ __global__ void __launch_bounds__(32 * kJoinW) paged_join_kernel(const PagedArgs
 
 template <typename T, int G, int CPL>
 cudaError_t simt_launch(const PagedArgs& a, bool one_row, cudaStream_t s) {
-  before_launch(kKernPaged, s);
   auto kern = one_row ? paged_simt_kernel<T, G, CPL, 1> : paged_simt_kernel<T, G, CPL, 4>;
-  cudaError_t le = cudaSuccess;
-  if (a.second) le = launch_early(kern, dim3(kCtas), 32 * kW, 0, s, a);
-  else kern<<<kCtas, 32 * kW, 0, s>>>(a);
+  before_launch(kKernPaged, s);
+  const cudaError_t e = launch_early(kern, dim3(kCtas), 32 * kW, 0, s, a);
   after_launch(kKernPaged, s);
-  return le != cudaSuccess ? le : cudaGetLastError();
+  return e;
 }
 
 }  // namespace

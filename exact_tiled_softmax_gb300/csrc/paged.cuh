@@ -334,9 +334,11 @@ __device__ __forceinline__ const int* paged_table(const PagedArgs& a, int b) {
   return b == a.prefix_at ? a.prefix_table : a.table + static_cast<size_t>(b) * a.max_pages;
 }
 
-// Programmatic dependent launch: a kernel lets its successor's CTAs start as SMs
-// become free, and the successor waits, before it touches what its predecessors
-// write, until they are complete.  Both do nothing in an ordinary launch.
+// Programmatic dependent launch.  Every kernel here is launched early: its CTAs may start
+// while its predecessor in the stream runs, and wait, before they touch global memory,
+// until that is complete; only then do they let their own successor start, so that a
+// kernel that has not waited itself (a.second) still finds all that came before the launch
+// in front of it.  Between calls this hides the launches, not the work.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -405,8 +407,7 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
-// A launch that may start before its predecessor in the stream is complete (the
-// kernel waits by itself).
+// A launch that may start before its predecessor in the stream is complete.
 template <typename... Params, typename... Args>
 cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s,
                          Args... args) {

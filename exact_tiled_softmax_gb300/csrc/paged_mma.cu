@@ -458,13 +458,14 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
   uint8_t* own = sm + warp * Lay::kWarpBytes;
   const uint32_t kbase = smem_u32(own), vbase = kbase + S * Lay::kTileBytes;
   unsigned bits = 0;
-  let_next_start();
-  if (lane == 0) a.desc[worker] = make_int4(0, 0, 0, 0);
   if (threadIdx.x == 0) joined = 0;
   // Columns of K that the rows do not have stay zero: no copy writes them.
   if (kch < CH)
     for (int x = lane; x < S * Lay::kTileBytes / 16; x += 32)
       *reinterpret_cast<uint4*>(own + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
+  if (!a.second) wait_for_previous();
+  let_next_start();
+  if (lane == 0) a.desc[worker] = make_int4(0, 0, 0, 0);
   paged_scan<kRows, kTile, 32 * kW>(a, pre, scan, bits);
   // The copies' segment: tiles left, the next tile's first key, the keys that count.
   // Lane l holds the table entries of the keys from p_base + (l << lpk) on, and of as
@@ -667,12 +668,10 @@ cudaError_t mma_launch(const PagedArgs& a, cudaStream_t s) {
   constexpr int bytes = MmaLayout<T, D, NT>::kBytes, threads = 32 * Step<T, D, NT>::kW;
   const cudaError_t e = allow_smem<paged_mma_kernel<T, D, NT>>(bytes);
   if (e != cudaSuccess) return e;
-  cudaError_t le = cudaSuccess;
   before_launch(kKernPaged, s);
-  if (a.second) le = launch_early(kern, dim3(kCtas), threads, bytes, s, a);
-  else kern<<<kCtas, threads, bytes, s>>>(a);
+  const cudaError_t le = launch_early(kern, dim3(kCtas), threads, bytes, s, a);
   after_launch(kKernPaged, s);
-  return le != cudaSuccess ? le : cudaGetLastError();
+  return le;
 }
 
 template <typename T, int D>

@@ -118,9 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
   const PagedArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  let_next_start();
   if (threadIdx.x == 0) {
-    a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     mbar_init(bar(Lay::B_Q), kQThreads);
     mbar_init(bar(Lay::B_QFREE), 1);
     for (int s = 0; s < NS; ++s) {
@@ -145,6 +143,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     tc_fence_before();
   }
   unsigned bits = 0;
+  if (!a.second) wait_for_previous();
+  let_next_start();
+  if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   paged_scan<kRows, kUnit, kThreads>(a, pre, scan, bits);  // two barriers of the CTA
   tc_fence_after();
   const uint32_t tmem = misc[0];
@@ -650,11 +651,9 @@ cudaError_t tc_launch(const PagedArgs& a, cudaStream_t s) {
   const cudaError_t e = allow_smem<paged_tc_kernel<D>>(TcLayout<D>::ALLOC);
   if (e != cudaSuccess) return e;
   before_launch(kKernPaged, s);
-  cudaError_t le = cudaSuccess;
-  if (a.second) le = launch_early(kern, dim3(kCtas), kThreads, TcLayout<D>::ALLOC, s, p);
-  else kern<<<kCtas, kThreads, TcLayout<D>::ALLOC, s>>>(p);
+  const cudaError_t le = launch_early(kern, dim3(kCtas), kThreads, TcLayout<D>::ALLOC, s, p);
   after_launch(kKernPaged, s);
-  return le != cudaSuccess ? le : cudaGetLastError();
+  return le;
 }
 
 }  // namespace

@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
         }
       }
     }
-    const PagedPlace place = paged_place<NQ>(a, pre, w, n, blockIdx.x, threadIdx.x == 0);
+    const PagedPlace place = paged_place<NQ>(a, pre[a.B], w, n, blockIdx.x, threadIdx.x == 0);
     const int slot = place.slot;
     __syncthreads();
     for (int idx = threadIdx.x; idx < rows * v; idx += 32 * kW) {

@@ -245,6 +245,22 @@ __device__ __forceinline__ void paged_scan(const PagedArgs& a, long long* pre, l
   __syncthreads();
 }
 
+// w at unit `local` of the `units` of its sequence.
+template <int RT, int UK>
+__device__ __forceinline__ void paged_enter(const PagedArgs& a, PagedWalk& w, long long units, long long local) {
+  w.tiles = (w.s.nq * a.G + RT - 1) / RT;
+  const long long per_head = paged_div(units, a.by_heads);
+  w.h = static_cast<int>(paged_div(local, per_head));
+  long long rem = local - w.h * per_head;
+  w.rt = 0;
+  w.t = paged_tile<RT, UK>(a, w.s, 0);
+  for (long long n; rem >= (n = round_up(w.t.cnt, a.least));) {
+    rem -= n;
+    w.t = paged_tile<RT, UK>(a, w.s, ++w.rt);
+  }
+  w.rem = static_cast<int>(rem);
+}
+
 // Run r's first unit; false when it has none.
 template <int RT, int UK>
 __device__ __forceinline__ bool paged_begin(const PagedArgs& a, const long long* pre, int r, PagedWalk& w) {
@@ -262,19 +278,46 @@ __device__ __forceinline__ bool paged_begin(const PagedArgs& a, const long long*
   }
   w.b = b0;
   w.s = paged_seq(a, w.b);
-  w.tiles = (w.s.nq * a.G + RT - 1) / RT;
-  const long long per_head = paged_div(pre[b0 + 1] - pre[b0], a.by_heads);
-  const long long local = w.u - pre[b0];
-  w.h = static_cast<int>(paged_div(local, per_head));
-  long long rem = local - w.h * per_head;
-  w.rt = 0;
-  w.t = paged_tile<RT, UK>(a, w.s, 0);
-#pragma unroll 1
-  for (long long n; rem >= (n = round_up(w.t.cnt, a.least));) {
-    rem -= n;
-    w.t = paged_tile<RT, UK>(a, w.s, ++w.rt);
+  paged_enter<RT, UK>(a, w, pre[b0 + 1] - pre[b0], w.u - pre[b0]);
+  return true;
+}
+
+// The same for a batch of at most 32 sequences, by one warp without the CTA's sums: lane b
+// looks at sequence b.  `total` receives the units of the line.
+template <int RT, int UK>
+__device__ __forceinline__ bool paged_begin_warp(const PagedArgs& a, int r, PagedWalk& w, long long& total,
+                                                 unsigned& bits) {
+  const int lane = threadIdx.x & 31;
+  PagedSeq s{0, 0, 0, false, false};
+  long long units = 0;
+  if (lane < a.B) {
+    s = paged_seq(a, lane);
+    units = paged_units<RT, UK>(a, s);
   }
-  w.rem = static_cast<int>(rem);
+  if (blockIdx.x == 0 && threadIdx.x < 32) {
+    const bool any_bad = __any_sync(0xFFFFFFFFu, s.bad);
+    if (any_bad) bits |= kStatusBadPage;
+    if (a.info && lane == 0 && a.prefix_at != 0) *a.sane = !any_bad;
+  }
+  long long upto = units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+  const int n = run_units(a, total);
+  w.u = 1ll * n * r;
+  w.end = min(total, w.u + n);
+  if (w.u >= w.end) return false;
+  w.b = __ffs(__ballot_sync(0xFFFFFFFFu, upto - units <= w.u && w.u < upto)) - 1;
+  w.s.s0 = __shfl_sync(0xFFFFFFFFu, s.s0, w.b);
+  w.s.nq = __shfl_sync(0xFFFFFFFFu, s.nq, w.b);
+  w.s.len = __shfl_sync(0xFFFFFFFFu, s.len, w.b);
+  w.s.prefix = w.b == a.prefix_at;
+  w.s.bad = false;
+  units = __shfl_sync(0xFFFFFFFFu, units, w.b);
+  paged_enter<RT, UK>(a, w, units, w.u - __shfl_sync(0xFFFFFFFFu, upto, w.b) + units);
   return true;
 }
 
@@ -318,11 +361,11 @@ struct PagedPlace {
   int slot, parts;
 };
 template <int RT>
-__device__ __forceinline__ PagedPlace paged_place(const PagedArgs& a, const long long* pre, const PagedWalk& w,
-                                                  int n, int r, bool one) {
+__device__ __forceinline__ PagedPlace paged_place(const PagedArgs& a, long long total, const PagedWalk& w, int n,
+                                                  int r, bool one) {
   if (w.rem > 0) return {2 * r, -1};
   if (n == w.t.cnt) return {-1, 0};
-  const int last = static_cast<int>(paged_div(w.u + w.t.cnt - 1, static_cast<long long>(run_units(a, pre[a.B]))));
+  const int last = static_cast<int>(paged_div(w.u + w.t.cnt - 1, static_cast<long long>(run_units(a, total))));
   if (one)
     a.desc[r] = make_int4(w.rt * RT, w.s.nq * a.G, w.s.s0,
                           static_cast<int>((static_cast<unsigned>(w.h) << 16) |

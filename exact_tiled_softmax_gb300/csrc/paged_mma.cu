@@ -463,10 +463,25 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
   if (kch < CH)
     for (int x = lane; x < S * Lay::kTileBytes / 16; x += 32)
       *reinterpret_cast<uint4*>(own + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();  // `joined` is zero
   if (!a.second) wait_for_previous();
   let_next_start();
   if (lane == 0) a.desc[worker] = make_int4(0, 0, 0, 0);
-  paged_scan<kRows, kTile, 32 * kW>(a, pre, scan, bits);
+  // The run's start, for both walks.
+  long long total;
+  bool more;  // more tiles to copy
+  {
+    PagedWalk w;
+    if (a.B <= 32) {
+      more = paged_begin_warp<kRows, kTile>(a, worker, w, total, bits);
+    } else {
+      paged_scan<kRows, kTile, 32 * kW>(a, pre, scan, bits);
+      total = pre[a.B];
+      more = paged_begin<kRows, kTile>(a, pre, worker, w);
+    }
+    if (more && lane < 2) walks[warp][lane] = w;
+    __syncwarp();
+  }
   // The copies' segment: tiles left, the next tile's first key, the keys that count.
   // Lane l holds the table entries of the keys from p_base + (l << lpk) on, and of as
   // many again behind those: one load for 512 keys, long before they are needed.
@@ -497,9 +512,7 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
     k_at[x] = kbase + r * Lay::kRowBytes + (St::kpiece(r, pc) << 4);
     v_at[x] = vbase + r * Lay::kRowBytes + (St::vpiece(r, pc) << 4);
   }
-  // Tiles copied so far, and whether more come.
-  int issued = 0;
-  bool more = true;
+  int issued = 0;  // tiles copied so far
   // The products' segment.
   int left = 0, key0 = 0;
   Spans<NT> sp;
@@ -518,8 +531,7 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
       if (!starts) continue;
       PagedWalk w = walks[warp][who];
       int n = 0, j0 = 0, j1 = 0;
-      bool on = (who == 0 ? it > 0 : i > 0) ? paged_next<kRows, kTile>(a, w)
-                                            : paged_begin<kRows, kTile>(a, pre, worker, w);
+      bool on = (who == 0 ? it == 0 : i == 0) || paged_next<kRows, kTile>(a, w);
       // A segment may hold only what its tile was rounded up by.
 #pragma unroll 1
       while (on && (n = paged_segment<kTile>(w, j0, j1)) == 0) on = paged_next<kRows, kTile>(a, w);
@@ -624,7 +636,7 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
     const PagedWalk w = walks[warp][1];
     int j0, j1;
     const int n = paged_segment<kTile>(w, j0, j1);
-    const PagedPlace place = paged_place<kRows>(a, pre, w, n, worker, lane == 0);
+    const PagedPlace place = paged_place<kRows>(a, total, w, n, worker, lane == 0);
     const int slot = place.slot;
 #pragma unroll
     for (int y = 0; y < NT; ++y) {

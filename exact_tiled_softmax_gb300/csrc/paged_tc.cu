@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             t.r0 = w.rt * kRows;
             t.h = w.h;
             t.b = w.b;
-            const PagedPlace place = paged_place<kRows>(a, pre, w, t.n, blockIdx.x, lane == 0);
+            const PagedPlace place = paged_place<kRows>(a, pre[a.B], w, t.n, blockIdx.x, lane == 0);
             t.slot = place.slot;
             t.parts = place.parts;
             t.s0 = w.s.s0;

@@ -178,8 +178,8 @@ __device__ __forceinline__ long long paged_div(long long n, long long d) {
 
 __device__ __forceinline__ long long round_up(long long x, int to) { return (x + to - 1) & -static_cast<long long>(to); }
 // Units of a run, W.
-__device__ __forceinline__ int run_units(const PagedArgs& a, long long total) {
-  return static_cast<int>(max(1ll * a.least, round_up(paged_div(total + a.runs - 1, a.by_runs), a.least)));
+__device__ __forceinline__ long long run_units(const PagedArgs& a, long long total) {
+  return max(1ll * a.least, round_up(paged_div(total + a.runs - 1, a.by_runs), a.least));
 }
 
 // A place in the line of units.
@@ -265,8 +265,8 @@ __device__ __forceinline__ void paged_enter(const PagedArgs& a, PagedWalk& w, lo
 template <int RT, int UK>
 __device__ __forceinline__ bool paged_begin(const PagedArgs& a, const long long* pre, int r, PagedWalk& w) {
   const long long total = pre[a.B];
-  const int n = run_units(a, total);
-  w.u = 1ll * n * r;
+  const long long n = run_units(a, total);
+  w.u = n * r;
   w.end = min(total, w.u + n);
   if (w.u >= w.end) return false;
   int b0 = 0, b1 = a.B;  // pre[b0] <= u < pre[b1]
@@ -306,8 +306,8 @@ __device__ __forceinline__ bool paged_begin_warp(const PagedArgs& a, int r, Page
     if (lane >= o) upto += x;
   }
   total = __shfl_sync(0xFFFFFFFFu, upto, 31);
-  const int n = run_units(a, total);
-  w.u = 1ll * n * r;
+  const long long n = run_units(a, total);
+  w.u = n * r;
   w.end = min(total, w.u + n);
   if (w.u >= w.end) return false;
   w.b = __ffs(__ballot_sync(0xFFFFFFFFu, upto - units <= w.u && w.u < upto)) - 1;
@@ -365,7 +365,7 @@ __device__ __forceinline__ PagedPlace paged_place(const PagedArgs& a, long long 
                                                   int r, bool one) {
   if (w.rem > 0) return {2 * r, -1};
   if (n == w.t.cnt) return {-1, 0};
-  const int last = static_cast<int>(paged_div(w.u + w.t.cnt - 1, static_cast<long long>(run_units(a, total))));
+  const int last = static_cast<int>(paged_div(w.u + w.t.cnt - 1, run_units(a, total)));
   if (one)
     a.desc[r] = make_int4(w.rt * RT, w.s.nq * a.G, w.s.s0,
                           static_cast<int>((static_cast<unsigned>(w.h) << 16) |

@@ -174,6 +174,81 @@ def test_a_key_that_a_row_does_not_allow_leaves_no_trace_in_its_score(ex, path, 
         check_attention(dtype, y[:1], L[:1], ref, 64, 99, _p_bits(path, dtype, 2, 1, 2))
 
 
+@pytest.mark.parametrize("dtype,nq,G", [("bf16", 1, 2), ("bf16", 3, 4), ("bf16", 40, 2), ("f32", 3, 2)])
+def test_keys_before_every_window_leave_no_trace(ex, path, dtype, nq, G):
+    """Keys and values that no token's window reaches hold NaN and infinities."""
+    n, w = 300, 70
+    b = Batch([n, 50], [nq, nq], 2 * G, 2, 64, 96, dtype, 32, seed=18)
+    first = n - nq + 1 - w
+    ref = oracle.attend(b.np(b.q), b.np(b.k_pages), b.np(b.v_pages), b.table, b.lens, b.starts, 0.1, "window", w)
+    for j in range(first):
+        for x in (b.k_pages, b.v_pages):
+            x[int(b.table[0, j // 32]), :, j % 32] = (float("nan"), float("inf"), -float("inf"))[j % 3]
+    y, L, status = _attend(ex, b, "window", w, 0.1)
+    assert status == 0
+    check_attention(dtype, y, L, ref, 64, w, _p_bits(path, dtype, b.T, 2, G))
+
+
+@pytest.mark.parametrize("d,v,page,nq,dtype", [(8, 8, 8, 40, "bf16"), (16, 128, 16, 40, "bf16"), (128, 8, 64, 300, "bf16"),
+                                               (64, 64, 4, 40, "bf16"), (4, 4, 2, 3, "f32"), (128, 128, 16, 60, "f32")])
+def test_narrow_rows_and_small_pages(ex, path, d, v, page, nq, dtype):
+    b = Batch([310, nq], [nq, nq], 4, 2, d, v, dtype, page, seed=d + v)
+    ref = oracle.attend(b.np(b.q), b.np(b.k_pages), b.np(b.v_pages), b.table, b.lens, b.starts, 0.2, "causal")
+    y, L, status = _attend(ex, b, "causal", 0, 0.2)
+    assert status == 0
+    check_attention(dtype, y, L, ref, d, 310, _p_bits(path, dtype, b.T, 2, 2))
+
+
+@pytest.mark.parametrize("prefix", [0, 37])
+@pytest.mark.parametrize("dtype,nq", [("bf16", 1), ("f32", 2), ("bf16", 30)])
+def test_large_batches(ex, path, dtype, nq, prefix):
+    """The largest batch, most sequences short, some without tokens or keys."""
+    B = 1024 if nq < 30 else 60
+    rng = np.random.default_rng(B)
+    nqs = [0 if x == 0 else int(rng.integers(1, nq + 1)) for x in rng.integers(0, 5, B)]
+    lens = [int(rng.integers(0, 40)) + q for q in nqs]
+    b = Batch(lens, nqs, 2, 1, 64, 64, dtype, 16, seed=B, prefix=prefix)
+    ref = oracle.attend(b.np(b.q), b.np(b.k_pages), b.np(b.v_pages), b.table, b.lens, b.starts, 0.1, "causal",
+                        prefix=(b.prefix_table, prefix) if prefix else None)
+    if prefix:
+        q, k, v, table, ln, starts, pt = b.dev("q", "k_pages", "v_pages", "table", "lens", "starts", "prefix_table")
+        y, L = ex.fwd_prefix(q, k, v, pt, prefix, table, ln, 0.1, "causal", q_starts=starts)
+    else:
+        y, L, status = _attend(ex, b, "causal", 0, 0.1)
+        assert status == 0
+    check_attention(dtype, y, L, ref, 64, 80 + prefix, _p_bits(path, dtype, b.T, 1 if prefix else B, 2),
+                    extra=2.0 ** -20)
+
+
+def test_tokens_in_front_of_the_first_sequence(ex, path):
+    """q_starts may begin behind some tokens, and descend by mistake: rows that no sequence
+    owns stay as they were in both operators; nothing outside the tokens is touched."""
+    b = Batch([60, 40, 33], [2, 3, 2], 4, 2, 64, 64, "bf16", 16, seed=4, prefix=50)
+    for starts, status in (([1, 3, 4, 6], 0), ([1, 4, 2, 6], 8), ([5, 3, 9, -2], 8)):
+        own = np.full(b.T, -1)
+        s = np.array(starts, dtype=np.int32)
+        lo = [min(max(int(x), 0), b.T) for x in s[:-1]]
+        hi = [min(max(int(y), x), b.T) for x, y in zip(lo, s[1:])]
+        for i, (x, y) in enumerate(zip(lo, hi)):
+            own[x:y] = i
+        b.starts = s
+        y, L, st = _attend(ex, b, "causal", 0, 0.125)
+        assert st == status
+        assert (y[torch.from_numpy(own < 0).cuda()] == 7).all()
+        q, k, v, table, lens, qs, pt = b.dev("q", "k_pages", "v_pages", "table", "lens", "starts", "prefix_table")
+        y2 = torch.full_like(q, 7.0)
+        L2 = torch.full((b.T, 4), 7.0, device="cuda")
+        ws = ex.workspace(ex.prefix_workspace_size(ex.paged_shape(q, k, v, table)), "cuda")
+        ws.fill_(0xFF)
+        ex.fwd_prefix(q, k, v, pt, 50, table, lens, 0.125, "causal", q_starts=qs, y=y2, L=L2, ws=ws)
+        assert ex.device_status(ws) == status
+        assert (y2[torch.from_numpy(own < 0).cuda()] == 7).all() and (L2[torch.from_numpy(own < 0).cuda()] == 7).all()
+        if status == 0:
+            ref = oracle.attend(b.np(b.q), b.np(b.k_pages), b.np(b.v_pages), b.table, b.lens, list(map(int, s)),
+                                0.125, "causal", prefix=(b.prefix_table, 50))
+            check_attention("bf16", y2, L2, ref, 64, 110, _p_bits(path, "bf16", b.T, 1, 2), extra=2.0 ** -20)
+
+
 def test_equal_tokens_without_q_starts(ex, path):
     b = Batch([70, 33, 128], [2, 2, 2], 4, 2, 128, 128, "bf16", 16, seed=21)
     q, k, v, table, lens, starts = b.dev("q", "k_pages", "v_pages", "table", "lens", "starts")

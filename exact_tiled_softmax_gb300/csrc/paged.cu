@@ -440,10 +440,15 @@ __global__ void __launch_bounds__(kTall) paged_merge_tall_kernel(const PagedArgs
   join_status(a);
 }
 
-// A token's row over the shared prefix and over its own keys, joined.  A CTA a row of
-// [T][heads]; its warps share the pieces of both: a finished row is one piece (m = L
-// log2(e), l = 1), an unfinished one as many as runs hold some of it.
-constexpr int kJoinW = 4;
+// A token's row over the shared prefix and over its own keys, joined: a finished row is
+// one piece (m = L log2(e), l = 1), an unfinished one as many as runs hold some of it.
+// kWarps warps share a row's pieces: four where the prefix's tiles may each be spread over
+// more than 16 runs (a CTA a row), else one (a CTA eight rows).  One warp's loads are four
+// pieces at a time: with 4 warps in place of 1, 28 to 64 runs a tile took 33.5 us in place of
+// 38.4 and 16.2 of 20.8 (whole calls, about 16,000 and 50,000 prefix keys); below 16 runs a
+// tile, 59.2 us with one and 60.9 with four (64 sequences behind 16384 keys).
+constexpr int kJoinRows = 8;
+constexpr int kJoinSpread = 16;
 
 struct JoinSide {
   const float* pm;
@@ -452,27 +457,30 @@ struct JoinSide {
   int rt;
 };
 
-template <int N>
-__global__ void __launch_bounds__(32 * kJoinW) paged_join_kernel(const PagedArgs a, const JoinSide own,
-                                                               const JoinSide prefix) {
-  __shared__ float red_m[kJoinW], red_l[kJoinW];
-  __shared__ __align__(16) float red_z[kJoinW][128 * N];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, v = a.v, n4 = v / 4;
+template <int N, int kWarps>
+__global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 32 * kJoinRows)
+    paged_join_kernel(const PagedArgs a, const JoinSide own, const JoinSide prefix) {
+  __shared__ float red_m[kWarps], red_l[kWarps];
+  __shared__ __align__(16) float red_z[kWarps][128 * N];
+  const int lane = threadIdx.x & 31, v = a.v, n4 = v / 4;
+  const int warp = kWarps > 1 ? threadIdx.x >> 5 : 0;
   const int heads = a.Hk * a.G;
-  const size_t row = blockIdx.x, behind = static_cast<size_t>(a.T) * heads;
-  const int tok = blockIdx.x / heads, head = blockIdx.x - tok * heads;
+  const int index = kWarps > 1 ? blockIdx.x : blockIdx.x * kJoinRows + (threadIdx.x >> 5);
+  const size_t row = index, behind = static_cast<size_t>(a.T) * heads;
+  const int tok = index / heads, head = index - tok * heads;
   wait_for_previous();
   let_next_start();
   join_status(a);
+  if (tok >= a.T) return;
   // Rows of tokens that no sequence owns stay as they are.
-  int b = -1, s0 = 0;
+  int s0 = 0;
   if (a.starts) {
     const int end = min(max(__ldg(a.starts + a.prefix_at), 0), a.T);
-    if (*a.sane && (tok < __ldg(a.starts) || tok >= end)) return;
     // The owner, for the row's place in its tile (and, where q_starts is not sane, at all).
-    int b1 = a.prefix_at;
-    b = 0;
+    int b = 0, b1 = a.prefix_at;
     if (*a.sane) {
+      if (tok < __ldg(a.starts) || tok >= end) return;
+#pragma unroll 1
       while (b1 - b > 1) {
         const int mid = (b + b1) >> 1;
         if (__ldg(a.starts + mid) <= tok) b = mid;
@@ -480,7 +488,8 @@ __global__ void __launch_bounds__(32 * kJoinW) paged_join_kernel(const PagedArgs
       }
       s0 = __ldg(a.starts + b);
     } else {
-      for (b = 0; b < b1; ++b) {
+#pragma unroll 1
+      for (; b < b1; ++b) {
         const PagedSeq s = paged_seq(a, b);
         s0 = s.s0;
         if (tok >= s0 && tok < s0 + s.nq) break;
@@ -490,9 +499,7 @@ __global__ void __launch_bounds__(32 * kJoinW) paged_join_kernel(const PagedArgs
   } else {
     s0 = tok / a.each * a.each;
   }
-  const int h = div_by(head, a.by_group), g = head - h * a.G;
-  const int2 io = a.info[row], ip = a.info[row + behind];
-  const int q_own = ((tok - s0) * a.G + g) % own.rt, q_prefix = (tok * a.G + g) % prefix.rt;
+  const int g = head - div_by(head, a.by_group) * a.G;
   float m = -INFINITY, l = 0.f;
   float4 z[N];
 #pragma unroll
@@ -500,36 +507,28 @@ __global__ void __launch_bounds__(32 * kJoinW) paged_join_kernel(const PagedArgs
 #pragma unroll 1
   for (int side = 0; side < 2; ++side) {
     const JoinSide& of = side ? prefix : own;
-    const int2 at = side ? ip : io;
-    const int q = side ? q_prefix : q_own;
+    const size_t from = row + (side ? behind : 0);
+    const int2 at = a.info[from];
+    Gather<N> x;
     if (at.y == 0) {
       if (warp != 0) continue;
-      const size_t from = row + (side ? behind : 0);
-      const float pm = a.L[from] * kLog2e;
       const float4* p = reinterpret_cast<const float4*>(a.Yf + from * v);
-      const float top = fmaxf(m, pm), ref = top == -INFINITY ? 0.f : top;
-      const float f0 = pexp2(m - ref), f1 = pexp2(pm - ref);
-      m = top;
-      l = l * f0 + f1;
+      x.m = a.L[from] * kLog2e;
+      x.l = x.m == -INFINITY ? 0.f : 1.f;
 #pragma unroll
       for (int y = 0; y < N; ++y)
-        if (lane + 32 * y < n4) {
-          const float4 x = p[lane + 32 * y];
-          z[y] = make_float4(fmaf(x.x, f1, z[y].x * f0), fmaf(x.y, f1, z[y].y * f0), fmaf(x.z, f1, z[y].z * f0),
-                             fmaf(x.w, f1, z[y].w * f0));
-        }
-      continue;
+        if (lane + 32 * y < n4) x.z[y] = p[lane + 32 * y];
+    } else {
+      const int c = at.x, q = ((side ? tok : tok - s0) * a.G + g) % of.rt;
+      auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)); };
+      const float4* pz = reinterpret_cast<const float4*>(of.pz);
+      x.take(of, warp, kWarps, at.y, [&](int k) { return slot(k) * of.rt + q; },
+             [&](int k, int y) -> const float4* {
+               const int col = lane + 32 * y;
+               if (col >= n4) return nullptr;
+               return of.rt == kTall ? pz + tall_at(slot(k), v, col, q) : pz + (slot(k) * of.rt + q) * n4 + col;
+             });
     }
-    Gather<N> x;
-    const int c = at.x;
-    auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)); };
-    const float4* pz = reinterpret_cast<const float4*>(of.pz);
-    x.take(of, warp, kJoinW, at.y, [&](int k) { return slot(k) * of.rt + q; },
-           [&](int k, int y) -> const float4* {
-             const int col = lane + 32 * y;
-             if (col >= n4) return nullptr;
-             return of.rt == kTall ? pz + tall_at(slot(k), v, col, q) : pz + (slot(k) * of.rt + q) * n4 + col;
-           });
     const float top = fmaxf(m, x.m), ref = top == -INFINITY ? 0.f : top;
     const float f0 = pexp2(m - ref), f1 = pexp2(x.m - ref);
     m = top;
@@ -539,30 +538,38 @@ __global__ void __launch_bounds__(32 * kJoinW) paged_join_kernel(const PagedArgs
       z[y] = make_float4(fmaf(x.z[y].x, f1, z[y].x * f0), fmaf(x.z[y].y, f1, z[y].y * f0),
                          fmaf(x.z[y].z, f1, z[y].z * f0), fmaf(x.z[y].w, f1, z[y].w * f0));
   }
-  if (lane == 0) {
-    red_m[warp] = m;
-    red_l[warp] = l;
-  }
+  if constexpr (kWarps == 1) {
+    const PagedScale f = paged_finish(m, l);
 #pragma unroll
-  for (int y = 0; y < N; ++y) *reinterpret_cast<float4*>(&red_z[warp][4 * lane + 128 * y]) = z[y];
-  __syncthreads();
-  float M = -INFINITY, sum = 0.f;
+    for (int y = 0; y < N; ++y)
+      if (lane + 32 * y < n4) paged_store4(a, row, 4 * (lane + 32 * y), scaled(z[y], f.fz));
+    if (lane == 0) a.Lout[row] = f.L;
+  } else {
+    if (lane == 0) {
+      red_m[warp] = m;
+      red_l[warp] = l;
+    }
 #pragma unroll
-  for (int k = 0; k < kJoinW; ++k) M = fmaxf(M, red_m[k]);
-  const float ref = M == -INFINITY ? 0.f : M;
+    for (int y = 0; y < N; ++y) *reinterpret_cast<float4*>(&red_z[warp][4 * lane + 128 * y]) = z[y];
+    __syncthreads();
+    float M = -INFINITY, sum = 0.f;
 #pragma unroll
-  for (int k = 0; k < kJoinW; ++k) sum = fmaf(pexp2(red_m[k] - ref), red_l[k], sum);
-  const PagedScale f = paged_finish(M, sum);
+    for (int k = 0; k < kWarps; ++k) M = fmaxf(M, red_m[k]);
+    const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) sum = fmaf(pexp2(red_m[k] - ref), red_l[k], sum);
+    const PagedScale f = paged_finish(M, sum);
 #pragma unroll 1
-  for (int col = threadIdx.x; col < v; col += 32 * kJoinW) {
-    float y = 0.f;
+    for (int col = threadIdx.x; col < v; col += 32 * kWarps) {
+      float y = 0.f;
 #pragma unroll
-    for (int k = 0; k < kJoinW; ++k) y = fmaf(pexp2(red_m[k] - ref), red_z[k][col], y);
-    y *= f.fz;
-    if (a.dtype == kF32) static_cast<float*>(a.Y)[row * v + col] = y;
-    else static_cast<__nv_bfloat16*>(a.Y)[row * v + col] = __float2bfloat16_rn(y);
+      for (int k = 0; k < kWarps; ++k) y = fmaf(pexp2(red_m[k] - ref), red_z[k][col], y);
+      y *= f.fz;
+      if (a.dtype == kF32) static_cast<float*>(a.Y)[row * v + col] = y;
+      else static_cast<__nv_bfloat16*>(a.Y)[row * v + col] = __float2bfloat16_rn(y);
+    }
+    if (threadIdx.x == 0) a.Lout[row] = f.L;
   }
-  if (threadIdx.x == 0) a.Lout[row] = f.L;
 }
 
 template <typename T, int G, int CPL>
@@ -619,8 +626,14 @@ cudaError_t launch_paged_join(const PagedArgs& own, int own_rt, const PagedArgs&
                               cudaStream_t s) {
   const JoinSide o{own.pm, own.pl, own.pz, own_rt}, p{prefix.pm, prefix.pl, prefix.pz, prefix_rt};
   before_launch(kKernPagedMerge, s);
+  const int rows = own.T * own.Hk * own.G;
+  const long long tiles = (static_cast<long long>(own.T) * own.G + prefix_rt - 1) / prefix_rt * own.Hk;
+  const bool spread = prefix.runs > kJoinSpread * tiles;
+  const dim3 grid(spread ? rows : (rows + kJoinRows - 1) / kJoinRows);
+  const int threads = 32 * (spread ? 4 : kJoinRows);
   const cudaError_t e =
-      launch_early(own.v <= 128 ? paged_join_kernel<1> : paged_join_kernel<2>, dim3(own.T * own.Hk * own.G), 32 * kJoinW, 0, s, own, o, p);
+      own.v <= 128 ? launch_early(spread ? paged_join_kernel<1, 4> : paged_join_kernel<1, 1>, grid, threads, 0, s, own, o, p)
+                   : launch_early(spread ? paged_join_kernel<2, 4> : paged_join_kernel<2, 1>, grid, threads, 0, s, own, o, p);
   after_launch(kKernPagedMerge, s);
   return e;
 }

@@ -220,6 +220,27 @@ def test_large_batches(ex, path, dtype, nq, prefix):
                     extra=2.0 ** -20)
 
 
+@pytest.mark.parametrize("prefix", [0, 100])
+@pytest.mark.parametrize("B", [31, 32, 33, 64, 127, 128, 129])
+def test_batches_around_a_warps_share(ex, path, B, prefix):
+    """A run's start is found lane by lane in small batches, the prefix among the sequences."""
+    rng = np.random.default_rng(B)
+    nqs = [int(rng.integers(0, 3)) for _ in range(B)]
+    nqs[0] = nqs[-1] = 0 if B % 2 else 2
+    lens = [int(rng.integers(0, 300)) + q for q in nqs]
+    b = Batch(lens, nqs, 4, 2, 64, 64, "bf16", 16, seed=B, prefix=prefix)
+    ref = oracle.attend(b.np(b.q), b.np(b.k_pages), b.np(b.v_pages), b.table, b.lens, b.starts, 0.1, "causal",
+                        prefix=(b.prefix_table, prefix) if prefix else None)
+    if prefix:
+        q, k, v, table, ln, starts, pt = b.dev("q", "k_pages", "v_pages", "table", "lens", "starts", "prefix_table")
+        y, L = ex.fwd_prefix(q, k, v, pt, prefix, table, ln, 0.1, "causal", q_starts=starts)
+    else:
+        y, L, status = _attend(ex, b, "causal", 0, 0.1)
+        assert status == 0
+    check_attention("bf16", y, L, ref, 64, 302 + prefix, _p_bits(path, "bf16", b.T, 1 if prefix else B, 2),
+                    extra=2.0 ** -20)
+
+
 def test_tokens_in_front_of_the_first_sequence(ex, path):
     """q_starts may begin behind some tokens, and descend by mistake: rows that no sequence
     owns stay as they were in both operators; nothing outside the tokens is touched."""

@@ -488,6 +488,14 @@ def _remember(key, shape):
     return known
 
 
+def _on(stream, make, *args, **kwargs):
+    """A tensor from ``make``, of the stream that the call's kernels run on (None: the current)."""
+    if stream is None:
+        return make(*args, **kwargs)
+    with torch.cuda.stream(stream):
+        return make(*args, **kwargs)
+
+
 def _paged_call(op, name, index, known, stream, fields):
     """exattn_paged_run on the device ``index``; ``fields``: the call's from the workspace's
     size on, before and behind the stream."""
@@ -540,9 +548,9 @@ def append_paged(k, v, k_pages, v_pages, page_table, seq_lens, q_starts=None, q=
             raise ValueError(f"inv_freq must be contiguous float32 [pairs] on {lead.device}")
         known = _remember(key, shape)
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _on(stream, torch.empty, q.shape, dtype=q.dtype, device=q.device)
     if ws is None:
-        ws = workspace(256, k.device)
+        ws = _on(stream, workspace, 256, k.device)
     pairs = 0 if inv_freq is None else inv_freq.numel()
     _paged_call(0, "attn_append_paged", k.get_device(), known, stream, (
         (0 if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), k_pages.data_ptr(),
@@ -573,12 +581,13 @@ def _attend_paged(op, name, q, k_pages, v_pages, prefix_table, prefix_len, page_
         raise ValueError(f"prefix_table holds {prefix_table.numel()} pages of {k_pages.shape[2]}, "
                          f"the prefix has {prefix_len} keys")
     if y is None:
-        y = torch.empty(q.shape[:2] + v_pages.shape[3:], dtype=q.dtype, device=q.device)
+        y = _on(stream, torch.empty, q.shape[:2] + v_pages.shape[3:], dtype=q.dtype, device=q.device)
     if L is None:
-        L = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        L = _on(stream, torch.empty, q.shape[:2], dtype=torch.float32, device=q.device)
     if ws is None:
         shape = PagedShape(*known)
-        ws = workspace(prefix_workspace_size(shape) if op == 2 else paged_workspace_size(shape), q.device)
+        size = prefix_workspace_size(shape) if op == 2 else paged_workspace_size(shape)
+        ws = _on(stream, workspace, size, q.device)
     _paged_call(op, name, q.get_device(), known, stream, (
         (q.data_ptr(), 0, 0, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
          seq_lens.data_ptr(), 0 if q_starts is None else q_starts.data_ptr(),

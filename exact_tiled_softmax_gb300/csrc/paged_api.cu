@@ -19,6 +19,7 @@ constexpr int kMaxWidth = 256;
 constexpr int kMaxTokens = 1 << 20;
 constexpr int kMaxKeys = 1 << 30;
 constexpr int kMaxPageSize = 1024;
+constexpr long long kMaxRows = (1ll << 31) - 1024;  // a row and a tile more still count in an int
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -48,7 +49,7 @@ int check_paged(const exattn_paged_shape* s) {
     return EXATTN_MISALIGNED;
   if (s->page_size > kMaxPageSize || (s->page_size & (s->page_size - 1)) != 0) return EXATTN_UNSUPPORTED;
   if (s->batch > kPagedMaxBatch || s->tokens > kMaxTokens || s->heads > 65535 ||
-      (long long)s->tokens * s->heads > INT32_MAX ||
+      (long long)s->tokens * s->heads > kMaxRows ||
       (long long)s->max_pages * s->page_size > kMaxKeys)
     return EXATTN_UNSUPPORTED;
   return EXATTN_OK;

@@ -359,8 +359,9 @@ int attn_step_host(const exattn_shape* shape, const void* Q, const void* K, cons
  * seq_lens[b] - nq + i.  heads is a multiple of kv_heads; query head h reads key
  * head h / (heads / kv_heads).
  *
- * Limits: batch <= 1024, tokens <= 2^20, max_pages * page_size <= 2^30, d, v <=
- * 256 and rows of whole 16-byte pieces.  Masks: NONE, CAUSAL (keys up to the
+ * Limits: batch <= 1024, tokens <= 2^20, heads <= 65535, tokens * heads <= 2^31 -
+ * 1024, max_pages * page_size <= 2^30, prefix_len <= 2^30 - 1024, d, v <= 256 and rows
+ * of whole 16-byte pieces.  Masks: NONE, CAUSAL (keys up to the
  * token's position) and WINDOW (the `window` keys that end there); a bitmask is
  * EXATTN_UNSUPPORTED.
  *
@@ -369,6 +370,11 @@ int attn_step_host(const exattn_shape* shape, const void* Q, const void* K, cons
  * outside [0, max_pages * page_size] (both are clamped), or an entry that was
  * needed is outside [0, num_pages): its keys are left out, its tokens not
  * written.  Nothing outside the caller's arrays is read or written.
+ *
+ * What a page holds where no token of its sequence allows a key (behind the last key,
+ * before every window) meets no result, NaN included, nor do a key's masked scores.  The
+ * values of a key that some tokens of a sequence allow and others do not must be
+ * finite: 0 * NaN may reach the others, as in attn_fwd.
  * Ownership, streams and errors as for attn_fwd.
  * ------------------------------------------------------------------------- */
 typedef struct exattn_paged_shape {

@@ -578,6 +578,28 @@ def test_captured_launch_follows_lengths_and_tables(ex, path):
         check_attention("bf16", y, L, ref, 64, 70)
 
 
+def test_outputs_belong_to_the_call_stream(ex):
+    """What a call allocates is memory of the stream it runs on: a tensor of the current
+    stream that was freed while a write to it was still queued is not handed out again."""
+    b = Batch([300, 80], [1, 1], 4, 2, 64, 64, "bf16", 16, seed=12, prefix=40)
+    q, k, v, table, lens, pt = b.dev("q", "k_pages", "v_pages", "table", "lens", "prefix_table")
+    new, kp, vp = q[:, :2].contiguous(), torch.zeros_like(k), torch.zeros_like(v)
+    side = torch.cuda.Stream()
+    calls = [lambda s: ex.fwd_paged(q, k, v, table, lens, 0.125, "causal", stream=s)[0],
+             lambda s: ex.fwd_prefix(q, k, v, pt, 40, table, lens, 0.125, "causal", stream=s)[0],
+             lambda s: ex.append_paged(new, new, kp, vp, table, lens, q=q, stream=s)]
+    for call in calls:
+        want = call(None)
+        torch.cuda.synchronize()
+        left = torch.empty_like(want)
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+        left.fill_(9.0)
+        del left  # its block is free for the current stream, its write still to come
+        got = call(side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
 def test_two_streams_at_once(ex, path):
     b = Batch([3000, 10, 900], [1, 2, 1], 8, 2, 128, 128, "bf16", 16, seed=51)
     q, k, v, table, lens, starts = b.dev("q", "k_pages", "v_pages", "table", "lens", "starts")

@@ -96,6 +96,7 @@ BAD_SHAPES = [
     (dict(v_stride=64), 1), (dict(d=264), 2), (dict(v=512), 2), (dict(d=68), 2), (dict(dtype=0, v=66), 2),
     (dict(page_size=24), 2), (dict(page_size=2048), 2), (dict(batch=1025, tokens=2050), 2),
     (dict(tokens=1 << 21), 2), (dict(max_pages=1 << 27), 2), (dict(tokens=1 << 20, heads=4096), 2),
+    (dict(tokens=972592, heads=2208), 2), (dict(heads=65536 * 2), 2),
     (dict(q_stride=516), 3), (dict(k_stride=130), 3), (dict(v_stride=129), 3),
 ]
 

@@ -87,10 +87,24 @@ __device__ void append_check(const AppendArgs& a) {
   if (threadIdx.x == 0) *a.status = any ? kStatusBadPage : 0u;
 }
 
+// The pairs (2f, 2f + 1) of a 16-byte piece, which starts at column `col`, turned.
+template <typename T, int W>
+__device__ __forceinline__ void turn_inside(Piece<T, W>& x, const float* cs, const float* sn, int col, int pairs) {
+  const Piece<float, W / 2> c = *reinterpret_cast<const Piece<float, W / 2>*>(cs + col / 2),
+                            s = *reinterpret_cast<const Piece<float, W / 2>*>(sn + col / 2);
+#pragma unroll
+  for (int e = 0; e < W; e += 2) {
+    if ((col + e) >> 1 >= pairs) continue;
+    const float x0 = as_float(x.x[e]), x1 = as_float(x.x[e + 1]);
+    from_float(x.x[e], x0 * c.x[e / 2] - x1 * s.x[e / 2]);
+    from_float(x.x[e + 1], x1 * c.x[e / 2] + x0 * s.x[e / 2]);
+  }
+}
+
 // W: elements of an access.  A row of q or k is cut into units: interleaved, unit u is
 // access u; else units below pairs / W are the accesses u W and pairs + u W of the two
-// halves, those above one access of the columns that pass.
-template <typename T, int W>
+// halves, those above two neighbouring accesses of the columns that pass.
+template <typename T, int W, bool kInterleaved>
 __global__ void __launch_bounds__(kAppendThreads, 6) append_kernel(const __grid_constant__ AppendArgs a) {
   wait_for_previous();
   let_next_start();
@@ -129,53 +143,64 @@ __global__ void __launch_bounds__(kAppendThreads, 6) append_kernel(const __grid_
   __syncwarp();
 
   const int units = a.by_units.d, half = a.pairs / W;
-  const int across = units < 32 ? units : 32, rpp = units < 32 ? div_by(32, a.by_units) : 1;  // rows of a pass
-  const int sub = units < 32 ? div_by(lane, a.by_units) : 0;
   const int rows = (a.q ? a.H : 0) + a.Hk, q_rows = rows - a.Hk;
-  const int step = rpp * a.by_shares.d;
   const T* qsrc = static_cast<const T*>(a.q) + t * a.qs;
   const T* ksrc = static_cast<const T*>(a.k) + t * a.ks;
   T* qdst = static_cast<T*>(a.q_out) + static_cast<size_t>(t) * a.H * a.d;
   T* kdst = static_cast<T*>(a.kp) + slot * a.d;
+  if constexpr (kInterleaved) {
+    // Every lane a piece, whatever the row's width, and two pieces in flight.
+    const int all = (slot < 0 ? q_rows : rows) * units;
 #pragma unroll 1
-  for (int u0 = 0; u0 < units; u0 += 32) {
-    const int u = u0 + lane - sub * across;
-    const bool on = sub < rpp && u < units;
-    const bool turns = a.interleaved || u < half, two = !a.interleaved && u < half;
-    const int col = (turns ? u : u + half) * W;
-    if (!on) continue;
+    for (int i0 = share * 64 + lane; i0 < all; i0 += 64 * a.by_shares.d) {
+      P x[2];
+      T* dst[2];
+      int col[2];
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int i = min(i0 + 32 * z, all - 1), r = div_by(i, a.by_units);
+        col[z] = (i - r * units) * W;
+        x[z] = *reinterpret_cast<const P*>((r < q_rows ? qsrc + r * a.d : ksrc + (r - q_rows) * a.d) + col[z]);
+        dst[z] = (r < q_rows ? qdst + r * a.d : kdst + (static_cast<long long>(r - q_rows) << a.lps) * a.d) + col[z];
+      }
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        turn_inside<T, W>(x[z], cs[warp], sn[warp], col[z], a.pairs);
+        if (z == 0 || i0 + 32 < all) *reinterpret_cast<P*>(dst[z]) = x[z];
+      }
+    }
+  } else {
+    const int across = units < 32 ? units : 32, rpp = units < 32 ? div_by(32, a.by_units) : 1;  // rows of a pass
+    const int sub = units < 32 ? div_by(lane, a.by_units) : 0;
+    const int step = rpp * a.by_shares.d;
 #pragma unroll 1
-    for (int r = share * rpp + sub; r < rows; r += step) {
-      const bool is_q = r < q_rows;
-      const T* src = (is_q ? qsrc + r * a.d : ksrc + (r - q_rows) * a.d) + col;
-      P x = *reinterpret_cast<const P*>(src), y;
-      if (two) y = *reinterpret_cast<const P*>(src + a.pairs);
-      if (!is_q && slot < 0) continue;
-      if (two) {
-        const Piece<float, W> c = *reinterpret_cast<const Piece<float, W>*>(&cs[warp][u * W]),
-                              s = *reinterpret_cast<const Piece<float, W>*>(&sn[warp][u * W]);
+    for (int u0 = 0; u0 < units; u0 += 32) {
+      const int u = u0 + lane - sub * across;
+      const bool two = u < half;
+      const int col = (two ? u : 2 * u) * W, to_second = two ? a.pairs : W;
+      const bool second = col + to_second < a.d;
+      if (sub >= rpp || u >= units) continue;
+#pragma unroll 1
+      for (int r = share * rpp + sub; r < rows; r += step) {
+        const bool is_q = r < q_rows;
+        const T* src = (is_q ? qsrc + r * a.d : ksrc + (r - q_rows) * a.d) + col;
+        P x = *reinterpret_cast<const P*>(src), y;
+        if (second) y = *reinterpret_cast<const P*>(src + to_second);
+        if (!is_q && slot < 0) continue;
+        if (two) {
+          const Piece<float, W> c = *reinterpret_cast<const Piece<float, W>*>(&cs[warp][u * W]),
+                                s = *reinterpret_cast<const Piece<float, W>*>(&sn[warp][u * W]);
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-          const float x0 = as_float(x.x[e]), x1 = as_float(y.x[e]);
-          from_float(x.x[e], x0 * c.x[e] - x1 * s.x[e]);
-          from_float(y.x[e], x1 * c.x[e] + x0 * s.x[e]);
-        }
-      } else if (a.interleaved) {
-        if constexpr (W > 1) {
-          const Piece<float, W / 2> c = *reinterpret_cast<const Piece<float, W / 2>*>(&cs[warp][u * (W / 2)]),
-                                    s = *reinterpret_cast<const Piece<float, W / 2>*>(&sn[warp][u * (W / 2)]);
-#pragma unroll
-          for (int e = 0; e < W; e += 2) {
-            if (((u * W + e) >> 1) >= a.pairs) continue;
-            const float x0 = as_float(x.x[e]), x1 = as_float(x.x[e + 1]);
-            from_float(x.x[e], x0 * c.x[e / 2] - x1 * s.x[e / 2]);
-            from_float(x.x[e + 1], x1 * c.x[e / 2] + x0 * s.x[e / 2]);
+          for (int e = 0; e < W; ++e) {
+            const float x0 = as_float(x.x[e]), x1 = as_float(y.x[e]);
+            from_float(x.x[e], x0 * c.x[e] - x1 * s.x[e]);
+            from_float(y.x[e], x1 * c.x[e] + x0 * s.x[e]);
           }
         }
+        T* dst = (is_q ? qdst + r * a.d : kdst + (static_cast<long long>(r - q_rows) << a.lps) * a.d) + col;
+        *reinterpret_cast<P*>(dst) = x;
+        if (second) *reinterpret_cast<P*>(dst + to_second) = y;
       }
-      T* dst = (is_q ? qdst + r * a.d : kdst + (static_cast<long long>(r - q_rows) << a.lps) * a.d) + col;
-      *reinterpret_cast<P*>(dst) = x;
-      if (two) *reinterpret_cast<P*>(dst + a.pairs) = y;
     }
   }
   if (slot < 0) return;
@@ -189,10 +214,10 @@ __global__ void __launch_bounds__(kAppendThreads, 6) append_kernel(const __grid_
   }
 }
 
-template <typename T, int W>
+template <typename T, int W, bool kInterleaved>
 cudaError_t append_launch(AppendArgs a, cudaStream_t s) {
   a.each = a.T / a.B;
-  a.by_units = fast_div((a.interleaved ? a.d : a.d - a.pairs) / W);
+  a.by_units = fast_div(kInterleaved ? a.d / W : (a.d / W + 1) / 2);
   a.by_vch = fast_div(a.vw * static_cast<int>(sizeof(T)) / 16);
   // A token's rows are shared out while that leaves warps without work: a decode step's
   // few tokens are a matter of latency.
@@ -201,7 +226,7 @@ cudaError_t append_launch(AppendArgs a, cudaStream_t s) {
   a.by_shares = fast_div(shares);
   const unsigned ctas = (static_cast<unsigned>(a.T) * shares + kAppendWarps - 1) / kAppendWarps;
   before_launch(kKernAppend, s);
-  const cudaError_t e = launch_early(append_kernel<T, W>, dim3(ctas + 1), kAppendThreads, 0, s, a);
+  const cudaError_t e = launch_early(append_kernel<T, W, kInterleaved>, dim3(ctas + 1), kAppendThreads, 0, s, a);
   after_launch(kKernAppend, s);
   return e;
 }
@@ -210,9 +235,10 @@ template <typename T>
 cudaError_t append_dispatch(const AppendArgs& a, cudaStream_t s) {
   constexpr int E = 16 / sizeof(T);
   // The widest access that neither half of the rotated columns breaks up.
-  if (a.interleaved || a.pairs % E == 0) return append_launch<T, E>(a, s);
-  if (a.pairs % (E / 2) == 0) return append_launch<T, E / 2>(a, s);
-  return append_launch<T, 1>(a, s);
+  if (a.interleaved) return append_launch<T, E, true>(a, s);
+  if (a.pairs % E == 0) return append_launch<T, E, false>(a, s);
+  if (a.pairs % (E / 2) == 0) return append_launch<T, E / 2, false>(a, s);
+  return append_launch<T, 1, false>(a, s);
 }
 
 }  // namespace

@@ -8,10 +8,11 @@
 // Bound by memory: every element is read once and written once, in 16-byte accesses
 // where the rotated halves allow them.  A warp takes a token (or a share of its rows):
 // it finds the token's place and angles once for all heads.  What hides the latency is
-// warps, not loads of a lane: six CTAs to an SM with one row in flight a lane moved 37
-// thousand tokens of 40 heads of 128 bf16 columns at 5.94 TB/s (88% of the measured
-// copy), two rows at four CTAs 5.41, four rows at two CTAs 4.05.  One CTA more checks that every token has a
-// place and writes the status word.
+// warps, not loads of a lane: six CTAs to an SM with 32 bytes in flight a lane move 40
+// thousand tokens of 48 rows of 128 bf16 columns at 6.20 TB/s (91% of the measured copy);
+// before the angles left double precision it was 5.94, and then two rows at four CTAs 5.41,
+// four rows at two CTAs 4.05, and in fp32 six CTAs 5.74, five 5.01.  One CTA more checks
+// that every token has a place and writes the status word.
 #include "paged.cuh"
 
 namespace exattn {
@@ -43,6 +44,33 @@ __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void from_float(float& x, float f) { x = f; }
 __device__ __forceinline__ void from_float(__nv_bfloat16& x, float f) { x = __float2bfloat16_rn(f); }
+
+// Whole turns that an angle of `freq` radians makes are dropped in fixed point: the turns of
+// one position, freq / (2 pi) modulo 1 in units of 2^-64.  freq is M 2^E, M below 2^24, and
+// 2^64 / (2 pi) an integer to 2^-65, so the result is off by 2^-64 (1 + |freq| / 2) at most,
+// and by p times that after p positions.  (Double precision, 2 operations a clock and SM,
+// took 1 us of a decode step's 4.7 and 6% of a long prompt's time.)
+__device__ __forceinline__ unsigned long long turns_of(float freq) {
+  constexpr unsigned long long kInv2Pi = 0x28be60db9391054aull;  // 2^64 / (2 pi)
+  const unsigned x = __float_as_uint(freq), e = (x >> 23) & 255u;
+  const unsigned long long m = (x & 0x7FFFFFu) | (e ? 0x800000u : 0u);
+  const unsigned long long lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+  const int down = 150 - static_cast<int>(e ? e : 1u);  // -E
+  unsigned long long f;
+  if (down <= 0) f = down > -64 ? lo << -down : 0ull;
+  else if (down < 64) f = (lo >> down) | (hi << (64 - down));
+  else f = down < 128 ? hi >> (down - 64) : 0ull;
+  return x >> 31 ? 0ull - f : f;
+}
+
+// cos and sin of pos * freq.
+__device__ __forceinline__ void angle(long long pos, float freq, float& sn, float& cs) {
+  const unsigned long long t = static_cast<unsigned long long>(pos) * turns_of(freq);
+  // The upper 32 bits, as half turns in [-1, 1): 2^-31 of a half turn is cut off.
+  float half = static_cast<float>(static_cast<int>(t >> 32)) * 0x1p-31f;
+  if (!isfinite(freq)) half = NAN;
+  sincospif(half, &sn, &cs);
+}
 
 // Status: whether every new token has a place.  A thread takes a sequence at a time, a
 // warp the pages of a long one.
@@ -133,13 +161,8 @@ __global__ void __launch_bounds__(kAppendThreads, 6) append_kernel(const __grid_
     if (static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages))
       slot = (static_cast<long long>(page) * a.Hk << a.lps) + (pos & ((1 << a.lps) - 1));
   }
-  for (int f = lane; f < a.pairs; f += 32) {
-    // Whole turns are dropped in 64 bits: far positions keep their angle.
-    constexpr double kInv2Pi = 0.15915494309189533577;
-    const double turns = (static_cast<double>(pos) + a.pos_offset) *
-                         (static_cast<double>(__ldg(a.inv_freq + f)) * kInv2Pi);
-    sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &sn[warp][f], &cs[warp][f]);
-  }
+  const long long at = static_cast<long long>(pos) + a.pos_offset;
+  for (int f = lane; f < a.pairs; f += 32) angle(at, __ldg(a.inv_freq + f), sn[warp][f], cs[warp][f]);
   __syncwarp();
 
   const int units = a.by_units.d, half = a.pairs / W;

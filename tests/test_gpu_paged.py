@@ -435,6 +435,37 @@ def test_append(ex, case):
         assert (out[n:] == 7).all()
 
 
+def test_append_frequencies_of_any_size(ex):
+    """Frequencies that are zero, negative, subnormal, above a turn a token; an infinite or
+    NaN one makes its own pair NaN and no other."""
+    inv = np.array([0.0, -0.5, 1e-12, 3e-39, 7.5, 1000.25, np.inf, 1.0, np.nan, -2.0 ** 100, 2.0 ** 30, 1e-3],
+                   dtype=np.float32)
+    d, n = 2 * len(inv), 1000003
+    q = torch.randn(3, 2, d, generator=torch.Generator().manual_seed(1))
+    pos = np.arange(n - 3, n, dtype=np.float64)
+    table = torch.full((1, -(-n // 1024)), -1, dtype=torch.int32, device="cuda")
+    table[0, -1] = 0
+    pool = torch.zeros(1, 2, 1024, d, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out = ex.append_paged(q.cuda(), q.cuda(), pool, torch.zeros_like(pool), table, lens, q=q.cuda(),
+                          inv_freq=torch.from_numpy(inv).cuda()).double().cpu().numpy()
+    # Angles of 2^30 a token and more lose the low bits of 1 / (2 pi): any angle, but a rotation.
+    exact = np.abs(inv) < 2 ** 20
+    with np.errstate(invalid="ignore", over="ignore"):
+        turn = pos[:, None] * inv.astype(np.float64)
+        c, s = np.cos(turn)[:, None], np.sin(turn)[:, None]
+    x, y = q[..., :len(inv)].double().numpy(), q[..., len(inv):].double().numpy()
+    bad = ~np.isfinite(inv)
+    assert np.isnan(out[..., :len(inv)][..., bad]).all() and np.isnan(out[..., len(inv):][..., bad]).all()
+    # As in test_append; the oracle's own turn of 10^9 radians is off by 2^-24 of one.
+    tol = 2.0 ** -20 * 2 * float(q.abs().max())
+    assert (np.abs(out[..., :len(inv)] - (x * c - y * s))[..., exact] <= tol).all()
+    assert (np.abs(out[..., len(inv):] - (y * c + x * s))[..., exact] <= tol).all()
+    big = ~exact & ~bad
+    size = out[..., :len(inv)] ** 2 + out[..., len(inv):] ** 2
+    assert (np.abs(size - (x * x + y * y))[..., big] <= 2 * tol * np.sqrt(x * x + y * y)[..., big] + tol * tol).all()
+
+
 def test_append_rotates_q_in_place(ex):
     b = Batch([40, 9], [3, 2], 4, 2, 64, 64, "bf16", 16, seed=1)
     q, k, v, table, lens, starts, kn, vn = b.dev("q", "k_pages", "v_pages", "table", "lens", "starts",

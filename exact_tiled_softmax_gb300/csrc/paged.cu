@@ -613,8 +613,8 @@ cudaError_t launch_paged_merge(const PagedArgs& a, int rt, cudaStream_t s) {
   if (rt == kTall)
     e = spread ? launch_early(paged_merge_tall_kernel<2, 8>, dim3((runs + 7) / 8, (n4 + 1) / 2), kTall, 0, s, a)
                : launch_early(paged_merge_tall_kernel<4, 1>, dim3(runs, (n4 + 3) / 4), kTall, 0, s, a);
-  else  // 41: a prime number, so that tiles that start at every so manyth run do not meet in one CTA
-    e = spread ? launch_early(a.v <= 128 ? paged_merge_kernel<true, 1> : paged_merge_kernel<true, 2>, dim3(41, rows),
+  else  // 61: a prime number, so that tiles that start at every so manyth run do not meet in one CTA
+    e = spread ? launch_early(a.v <= 128 ? paged_merge_kernel<true, 1> : paged_merge_kernel<true, 2>, dim3(61, rows),
                               32 * kMergeW, 0, s, a, rt)
                : launch_early(a.v <= 128 ? paged_merge_kernel<false, 1> : paged_merge_kernel<false, 2>,
                               dim3((runs + 1) / 2), 32 * kMergeW, 0, s, a, rt);

@@ -176,7 +176,7 @@ template <typename T, int D, int NT> struct Step;
 // bf16.  o[n][y]: columns 16 y + g (rows x = 0, 1) and 16 y + g + 8.
 template <int D, int NT>
 struct Step<__nv_bfloat16, D, NT> {
-  static constexpr int kW = 4, kStages = D == 128 ? 3 : 6;
+  static constexpr int kW = D == 128 ? 4 : 6, kStages = D == 128 ? 3 : 4;
   uint32_t qb[NT][D / 16][2];
   static __device__ __forceinline__ int kpiece(int r, int c) { return c ^ (r & 7); }
   static __device__ __forceinline__ int vpiece(int r, int c) { return c ^ (r & 7); }
@@ -287,7 +287,7 @@ template <int D, int NT>
 struct Step<float, D, NT> {
   // Width 128: three warps with two stages beat two warps with three (fp32, 8 heads of 80 and
   // 96 columns, windows of 1024 keys: 26.7 -> 22.5 us), whose products are 1700 cycles a tile.
-  static constexpr int kW = D == 128 ? 3 : 4, kStages = D == 128 ? 2 : 3;
+  static constexpr int kW = D == 128 ? 3 : 4, kStages = D == 64 ? 3 : 2;
   float qb[NT][D / 16][4];
   static __device__ __forceinline__ int kpiece(int r, int c) { return c ^ ((r & 1) << 2); }
   static __device__ __forceinline__ int vpiece(int r, int c) { return c ^ ((r & 3) << 1); }
@@ -501,16 +501,25 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
     }
     return page;
   };
-  // A lane's pieces: rows r1, r1 + kStep, ... of a tile, one column each.
-  constexpr int kStep = 32 / CH > 0 ? 32 / CH : 1;
-  const int r1 = lane / CH, pc = lane % CH;
-  uint32_t k_at[kStep < 8 ? 8 / kStep : 1], v_at[kStep < 8 ? 8 / kStep : 1];  // swizzles repeat every 8 rows
-  constexpr int kAts = sizeof(k_at) / 4;
+  // A lane's pieces: numbers lane + 32 x of the tile's kTile * CH.  Every kCols-th is in the
+  // same column, kColRows rows on; every kAts-th also in the same place of a swizzle, which
+  // repeats every 8 rows.
+  constexpr int kCols = 32 % CH == 0 ? 1 : 3, kColRows = kCols * 32 / CH;
+  constexpr int kAts = kCols == 1 && kColRows < 8 ? 8 / kColRows : kCols, kAtRows = kAts * 32 / CH;
+  static_assert(kCols * 32 % CH == 0 && kCopies % kAts == 0 && (kAtRows % 8 == 0 || (sizeof(T) == 4 && kAtRows % 4 == 0)),
+                "pieces of a lane");
+  int rows_at[kCols], pc[kCols];
+#pragma unroll
+  for (int z = 0; z < kCols; ++z) {
+    rows_at[z] = (lane + 32 * z) / CH;
+    pc[z] = (lane + 32 * z) % CH;
+  }
+  uint32_t k_at[kAts], v_at[kAts];
 #pragma unroll
   for (int x = 0; x < kAts; ++x) {
-    const int r = r1 + x * kStep;
-    k_at[x] = kbase + r * Lay::kRowBytes + (St::kpiece(r, pc) << 4);
-    v_at[x] = vbase + r * Lay::kRowBytes + (St::vpiece(r, pc) << 4);
+    const int r = (lane + 32 * x) / CH, c = pc[x % kCols];
+    k_at[x] = kbase + r * Lay::kRowBytes + (St::kpiece(r, c) << 4);
+    v_at[x] = vbase + r * Lay::kRowBytes + (St::vpiece(r, c) << 4);
   }
   int issued = 0;  // tiles copied so far
   // The products' segment.
@@ -591,14 +600,19 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
       if (lpk == 4 && first >= 0 && p_key >= p_j0 && p_key + kTile <= p_j1) {
         // All sixteen keys, one page: rows behind one another.
         const long long row = ((static_cast<long long>(first) * a.Hk + p_h) << a.lps) +
-                              (p_key & ((1 << a.lps) - 1)) + r1;
-        const T* kf = Kp + row * d + pc * E;
-        const T* vf = Vp + row * v + pc * E;
+                              (p_key & ((1 << a.lps) - 1));
+        const T *kf[kCols], *vf[kCols];
+#pragma unroll
+        for (int z = 0; z < kCols; ++z) {
+          kf[z] = Kp + (row + rows_at[z]) * d + pc[z] * E;
+          vf[z] = Vp + (row + rows_at[z]) * v + pc[z] * E;
+        }
 #pragma unroll
         for (int x = 0; x < kCopies; ++x) {
-          const uint32_t up = slot + (x / kAts) * kAts * kStep * Lay::kRowBytes;
-          if (pc < kch) cp16(k_at[x % kAts] + up, kf + x * kStep * d, 16);
-          if (pc < vch) cp16(v_at[x % kAts] + up, vf + x * kStep * v, 16);
+          const uint32_t up = slot + (x / kAts) * kAtRows * Lay::kRowBytes;
+          const int z = x % kCols, on = (x / kCols) * kColRows;
+          if (pc[z] < kch) cp16(k_at[x % kAts] + up, kf[z] + on * d, 16);
+          if (pc[z] < vch) cp16(v_at[x % kAts] + up, vf[z] + on * v, 16);
         }
       } else {
         // Lane r: key r of the tile as a row of the pool, -1 for none.
@@ -611,12 +625,12 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
         have = __ballot_sync(0xFFFFFFFFu, row >= 0) & 0xFFFFu;
 #pragma unroll 1
         for (int x = 0; x < kCopies; ++x) {
-          const int r = r1 + x * kStep;
+          const int r = (lane + 32 * x) / CH, c = (lane + 32 * x) % CH;
           const long long at = __shfl_sync(0xFFFFFFFFu, row, r);
           const long long from = at < 0 ? 0 : at;
           const uint32_t off = slot + r * Lay::kRowBytes;
-          if (pc < kch) cp16(kbase + off + (St::kpiece(r, pc) << 4), Kp + from * d + pc * E, at < 0 ? 0 : 16);
-          if (pc < vch) cp16(vbase + off + (St::vpiece(r, pc) << 4), Vp + from * v + pc * E, at < 0 ? 0 : 16);
+          if (c < kch) cp16(kbase + off + (St::kpiece(r, c) << 4), Kp + from * d + c * E, at < 0 ? 0 : 16);
+          if (c < vch) cp16(vbase + off + (St::vpiece(r, c) << 4), Vp + from * v + c * E, at < 0 ? 0 : 16);
         }
       }
       if (lane == 0) tile_keys[warp][s] = have;
@@ -691,24 +705,36 @@ cudaError_t mma_rows(const PagedArgs& a, int rows, cudaStream_t s) {
   return rows == 8 ? mma_launch<T, D, 1>(a, s) : mma_launch<T, D, 2>(a, s);
 }
 
-bool narrow(int d, int v) { return d <= 64 && v <= 64; }
+// The columns that a kernel is made for.
+int columns_of(int dtype, int d, int v) {
+  const int most = d > v ? d : v;
+  return most <= 64 ? 64 : dtype == kF32 && most <= 96 ? 96 : 128;
+}
 
 }  // namespace
 
 bool paged_mma_shape(int d, int v) { return d <= 128 && v <= 128; }
 PagedKernel paged_mma_kernel_of(int dtype, int d, int v, int rows) {
-  const int warps = dtype == kF32 && !narrow(d, v) ? Step<float, 128, 1>::kW : Step<float, 64, 1>::kW;
+  const int columns = columns_of(dtype, d, v);
+  const int warps = dtype == kF32 ? (columns == 64   ? Step<float, 64, 1>::kW
+                                     : columns == 96 ? Step<float, 96, 1>::kW
+                                                     : Step<float, 128, 1>::kW)
+                                  : (columns == 64 ? Step<__nv_bfloat16, 64, 1>::kW : Step<__nv_bfloat16, 128, 1>::kW);
   // Least units: what a worker streams before it ends a tile, against the workers that join it.
   // One sequence of 1000 keys, 8 key heads of 128 bf16 columns: 12.3 us with 2, 14.3 with 4, 16.4
   // with 8; 16 key heads of 64 columns and 2000 common keys: 17.8, 16.4, 18.4; fp32 windows: 24.6,
   // 22.5.
-  const int least = dtype == kBF16 && !narrow(d, v) ? 2 : 4;
+  const int least = dtype == kBF16 && columns > 64 ? 2 : 4;
   return {rows, kCtas, kCtas * warps, least};
 }
 
 cudaError_t launch_paged_mma(const PagedArgs& a, int rows, cudaStream_t s) {
-  if (a.dtype == kF32) return narrow(a.d, a.v) ? mma_rows<float, 64>(a, rows, s) : mma_rows<float, 128>(a, rows, s);
-  return narrow(a.d, a.v) ? mma_rows<__nv_bfloat16, 64>(a, rows, s) : mma_rows<__nv_bfloat16, 128>(a, rows, s);
+  const int columns = columns_of(a.dtype, a.d, a.v);
+  if (a.dtype == kF32)
+    return columns == 64   ? mma_rows<float, 64>(a, rows, s)
+           : columns == 96 ? mma_rows<float, 96>(a, rows, s)
+                           : mma_rows<float, 128>(a, rows, s);
+  return columns == 64 ? mma_rows<__nv_bfloat16, 64>(a, rows, s) : mma_rows<__nv_bfloat16, 128>(a, rows, s);
 }
 
 }  // namespace exattn

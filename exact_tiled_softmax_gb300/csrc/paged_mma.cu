@@ -176,10 +176,14 @@ template <typename T, int D, int NT> struct Step;
 // bf16.  o[n][y]: columns 16 y + g (rows x = 0, 1) and 16 y + g + 8.
 template <int D, int NT>
 struct Step<__nv_bfloat16, D, NT> {
-  static constexpr int kW = D == 128 ? 4 : 6, kStages = D == 128 ? 3 : 4;
+  // 64 columns: six warps with four stages 26.2 us, four with six 29.5 (12 sequences of 2000
+  // keys, 16 key heads); 96: four with four 86.6, five with three 93.9 (6000 keys, 16 rows; 94.3 on
+  // the kernel of 128).
+  static constexpr int kW = D == 64 ? 6 : 4, kStages = D == 128 ? 3 : 4;
   uint32_t qb[NT][D / 16][2];
-  static __device__ __forceinline__ int kpiece(int r, int c) { return c ^ (r & 7); }
-  static __device__ __forceinline__ int vpiece(int r, int c) { return c ^ (r & 7); }
+  // Eight rows' pieces in eight banks' groups (192-byte rows: every second begins there already).
+  static __device__ __forceinline__ int kpiece(int r, int c) { return D == 96 ? c ^ ((r >> 1) & 3) : c ^ (r & 7); }
+  static __device__ __forceinline__ int vpiece(int r, int c) { return kpiece(r, c); }
   // Row n of the tile's row 8 n + g.
   __device__ __forceinline__ void load_q(int n, const __nv_bfloat16* row, bool on, int t, int d) {
 #pragma unroll
@@ -285,8 +289,9 @@ struct Step<__nv_bfloat16, D, NT> {
 // columns 32 q + 4 g + {0, 1} and {2, 3}.
 template <int D, int NT>
 struct Step<float, D, NT> {
-  // Width 128: three warps with two stages beat two warps with three (fp32, 8 heads of 80 and
-  // 96 columns, windows of 1024 keys: 26.7 -> 22.5 us), whose products are 1700 cycles a tile.
+  // Warps before stages: the products, 1000 to 2000 cycles a tile, are a warp's latency.  96
+  // columns: four warps with two stages 133 us, two with four 158 (12 sequences of 6000 keys, 16
+  // key heads of 80 and 96 columns; 178 on the kernel of 128).
   static constexpr int kW = D == 128 ? 3 : 4, kStages = D == 64 ? 3 : 2;
   float qb[NT][D / 16][4];
   static __device__ __forceinline__ int kpiece(int r, int c) { return c ^ ((r & 1) << 2); }
@@ -706,20 +711,26 @@ cudaError_t mma_rows(const PagedArgs& a, int rows, cudaStream_t s) {
 }
 
 // The columns that a kernel is made for.
-int columns_of(int dtype, int d, int v) {
+int columns_of(int d, int v) {
   const int most = d > v ? d : v;
-  return most <= 64 ? 64 : dtype == kF32 && most <= 96 ? 96 : 128;
+  return most <= 64 ? 64 : most <= 96 ? 96 : 128;
+}
+template <typename T>
+cudaError_t mma_columns(const PagedArgs& a, int columns, int rows, cudaStream_t s) {
+  return columns == 64   ? mma_rows<T, 64>(a, rows, s)
+         : columns == 96 ? mma_rows<T, 96>(a, rows, s)
+                         : mma_rows<T, 128>(a, rows, s);
+}
+template <typename T>
+int warps_of(int columns) {
+  return columns == 64 ? Step<T, 64, 1>::kW : columns == 96 ? Step<T, 96, 1>::kW : Step<T, 128, 1>::kW;
 }
 
 }  // namespace
 
 bool paged_mma_shape(int d, int v) { return d <= 128 && v <= 128; }
 PagedKernel paged_mma_kernel_of(int dtype, int d, int v, int rows) {
-  const int columns = columns_of(dtype, d, v);
-  const int warps = dtype == kF32 ? (columns == 64   ? Step<float, 64, 1>::kW
-                                     : columns == 96 ? Step<float, 96, 1>::kW
-                                                     : Step<float, 128, 1>::kW)
-                                  : (columns == 64 ? Step<__nv_bfloat16, 64, 1>::kW : Step<__nv_bfloat16, 128, 1>::kW);
+  const int columns = columns_of(d, v), warps = dtype == kF32 ? warps_of<float>(columns) : warps_of<__nv_bfloat16>(columns);
   // Least units: what a worker streams before it ends a tile, against the workers that join it.
   // One sequence of 1000 keys, 8 key heads of 128 bf16 columns: 12.3 us with 2, 14.3 with 4, 16.4
   // with 8; 16 key heads of 64 columns and 2000 common keys: 17.8, 16.4, 18.4; fp32 windows: 24.6,
@@ -729,12 +740,8 @@ PagedKernel paged_mma_kernel_of(int dtype, int d, int v, int rows) {
 }
 
 cudaError_t launch_paged_mma(const PagedArgs& a, int rows, cudaStream_t s) {
-  const int columns = columns_of(a.dtype, a.d, a.v);
-  if (a.dtype == kF32)
-    return columns == 64   ? mma_rows<float, 64>(a, rows, s)
-           : columns == 96 ? mma_rows<float, 96>(a, rows, s)
-                           : mma_rows<float, 128>(a, rows, s);
-  return columns == 64 ? mma_rows<__nv_bfloat16, 64>(a, rows, s) : mma_rows<__nv_bfloat16, 128>(a, rows, s);
+  const int columns = columns_of(a.d, a.v);
+  return a.dtype == kF32 ? mma_columns<float>(a, columns, rows, s) : mma_columns<__nv_bfloat16>(a, columns, rows, s);
 }
 
 }  // namespace exattn

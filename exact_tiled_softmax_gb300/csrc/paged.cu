@@ -8,7 +8,12 @@
 // (the running-max recurrence of "txf-modern-flash-attention", Hints, in the
 // exp2 domain).  Groups, then warps, are joined with the star rule.  Keys and
 // values are read straight into registers, so nothing outside a segment's keys
-// is ever read or multiplied: what stale rows of a page hold does not matter.
+// is ever read or multiplied: what stale rows of a page hold does not matter.  Scores are
+// products of exact bf16 or fp32 values summed in fp32.  A CTA is a worker; up to four rows
+// share each read.  Bound by issue: every key costs 2 (d + v) multiply-adds a row and the
+// shuffles of a group.  Heads of 256 columns, 537 MB of keys and values: one row 97 us in bf16
+// (5.5 TB/s), 84 in fp32 (6.4), four rows 246 in bf16.  One row of 128 columns: 333 us for 2.1
+// GB against the tensor cores' 325, which take eight rows in that time.
 #include "paged.cuh"
 
 namespace exattn {
@@ -16,7 +21,10 @@ namespace {
 
 constexpr int kW = 4;
 constexpr int kUnit = 64;  // keys of a unit of work
-constexpr int kCtas = 4 * 152;
+// CTAs of an SM, all at once.  With registers as the compiler likes (2 or 3 CTAs of 4) 151 us for
+// one row of 256 bf16 columns, 272 for four; with three 111 and 246, with four 97 and 252.
+template <int NQ>
+constexpr int kCtas = NQ == 1 ? 4 : 3;
 
 __device__ __forceinline__ float pexp2(float x) {
   float y;
@@ -55,7 +63,7 @@ __device__ __forceinline__ uint4 ldg_once16(const void* p) {
 }
 
 template <typename T, int G, int CPL, int NQ>
-__global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(32 * kW, kCtas<NQ>) paged_simt_kernel(const PagedArgs a) {
   constexpr int E = Row16<T>::E;
   constexpr int KPW = 32 / G;
   constexpr int U = (NQ == 1 ? 8 : 4) / CPL;  // key steps in flight
@@ -265,7 +273,10 @@ __global__ void __launch_bounds__(32 * kW) paged_simt_kernel(const PagedArgs a) 
 // The star merge of the row tiles that one run starts and others end.  Piece 0 of run
 // c's tile is in slot 2c + 1, piece k > 0 in slot 2 (c + k).  Each kernel is
 // launched early and waits for the attention kernel at its start; CTA (0, 0) also joins
-// the status bits of every CTA of the attention launches.
+// the status bits of every CTA of the attention launches.  Bound by latency where few tiles
+// are shared (the launch and three dependent loads, 2 to 3 us behind the attention kernel), by
+// the summaries' traffic in the L2 cache where most are: 14 us for the 40 MB that 152 runs of
+// 256-row tiles leave, 8 for one row tile of 1216 runs in each of 8 heads.
 //
 // A row's state while its pieces come in, four at a time so that their loads overlap.
 template <int N>
@@ -576,14 +587,17 @@ template <typename T, int G, int CPL>
 cudaError_t simt_launch(const PagedArgs& a, bool one_row, cudaStream_t s) {
   auto kern = one_row ? paged_simt_kernel<T, G, CPL, 1> : paged_simt_kernel<T, G, CPL, 4>;
   before_launch(kKernPaged, s);
-  const cudaError_t e = launch_early(kern, dim3(kCtas), 32 * kW, 0, s, a);
+  const cudaError_t e = launch_early(kern, dim3(a.runs), 32 * kW, 0, s, a);
   after_launch(kKernPaged, s);
   return e;
 }
 
 }  // namespace
 
-PagedKernel paged_simt_kernel(bool one_row) { return {one_row ? 1 : 4, kCtas, kCtas, 1}; }
+PagedKernel paged_simt_kernel(bool one_row) {
+  const int ctas = 152 * (one_row ? kCtas<1> : kCtas<4>);
+  return {one_row ? 1 : 4, ctas, ctas, 1};
+}
 
 cudaError_t launch_paged_simt(const PagedArgs& a, bool one_row, cudaStream_t s) {
   const int bytes = (a.d > a.v ? a.d : a.v) * (a.dtype == kF32 ? 4 : 2);

@@ -63,13 +63,21 @@ __device__ __forceinline__ unsigned long long turns_of(float freq) {
   return x >> 31 ? 0ull - f : f;
 }
 
-// cos and sin of pos * freq.
+// cos and sin of pos * freq.  Quarter turns are taken out in fixed point too: what is left is
+// rounded to fp32 at an eighth of a turn at most, off by 2^-28 turns, four times less than whole
+// angles.
 __device__ __forceinline__ void angle(long long pos, float freq, float& sn, float& cs) {
   const unsigned long long t = static_cast<unsigned long long>(pos) * turns_of(freq);
-  // The upper 32 bits, as half turns in [-1, 1): 2^-31 of a half turn is cut off.
-  float half = static_cast<float>(static_cast<int>(t >> 32)) * 0x1p-31f;
-  if (!isfinite(freq)) half = NAN;
-  sincospif(half, &sn, &cs);
+  const unsigned long long quarter = (t + (1ull << 61)) >> 62;
+  const int rest = static_cast<int>((t - (quarter << 62)) >> 32);  // 2^-32 turns are cut off
+  float s, c;
+  sincospif(isfinite(freq) ? static_cast<float>(rest) * 0x1p-31f : NAN, &s, &c);
+  sn = quarter & 1 ? c : s;
+  cs = quarter & 1 ? -s : c;
+  if (quarter & 2) {
+    sn = -sn;
+    cs = -cs;
+  }
 }
 
 // Status: whether every new token has a place.  A thread takes a sequence at a time, a

@@ -26,6 +26,8 @@
 // the product, is left out; lo is cut to tf32, 2^-21 of x).
 // The reference point of the exponentials moves only when a row's maximum passes
 // it by more than 2^8, so p <= 2^8.
+#include <type_traits>
+
 #include "paged.cuh"
 #include "tc_ptx.cuh"
 
@@ -187,6 +189,7 @@ struct Step<__nv_bfloat16, D, NT> {
   // keys, 16 key heads); 96: four with four 86.6, five with three 93.9 (6000 keys, 16 rows; 94.3 on
   // the kernel of 128).
   static constexpr int kW = D == 64 ? 6 : 4, kStages = D == 128 ? 3 : 4;
+  static constexpr bool kSplit = false;  // see fp32
   uint32_t qb[NT][D / 16][2];
   // Eight rows' pieces in eight banks' groups (192-byte rows: every second begins there already).
   static __device__ __forceinline__ int kpiece(int r, int c) { return D == 96 ? c ^ ((r >> 1) & 3) : c ^ (r & 7); }
@@ -201,8 +204,9 @@ struct Step<__nv_bfloat16, D, NT> {
         qb[n][ks][y] = on && c < d ? *reinterpret_cast<const uint32_t*>(row + c) : 0u;
       }
   }
+  template <typename F>
   __device__ __forceinline__ void tile(RowState<D, NT>& st, uint32_t kt, uint32_t vt, unsigned have, int key0,
-                                       const Spans<NT>& sp, float sl2) {
+                                       const Spans<NT>& sp, float sl2, F after_scores) {
     const int lane = threadIdx.x & 31, i = lane >> 3;
     float sc[NT][4], sb[NT][4];  // two chains each
 #pragma unroll
@@ -225,6 +229,7 @@ struct Step<__nv_bfloat16, D, NT> {
       for (int e = 0; e < 4; ++e) sc[n][e] += sb[n][e];
     mask_scores<NT>(sc, sp, have, key0, sl2);
     st.softmax(sc);
+    after_scores();
     uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -296,10 +301,14 @@ struct Step<__nv_bfloat16, D, NT> {
 // columns 32 q + 4 g + {0, 1} and {2, 3}.
 template <int D, int NT>
 struct Step<float, D, NT> {
-  // Warps before stages: the products, 1000 to 2000 cycles a tile, are a warp's latency.  96
-  // columns: four warps with two stages 133 us, two with four 158 (12 sequences of 6000 keys, 16
-  // key heads of 80 and 96 columns; 178 on the kernel of 128).
-  static constexpr int kW = D == 128 ? 3 : 4, kStages = D == 64 ? 3 : 2;
+  // Warps before stages: the products, 1000 to 2000 cycles a tile, are a warp's latency, and
+  // four of a CTA load the SM's quarters evenly.  96 columns: four warps with two stages 133 us, two
+  // with four 158 (12 sequences of 6000 keys, 16 key heads of 80 and 96 columns; 178 on a kernel of
+  // 128).  128 columns: two whole stages fit three warps only; kSplit, keys and values of the
+  // tiles one after another in a ring of three halves, fits four: 19 sequences of 1600 keys, 16
+  // heads of 112 columns 89 -> 80 us, 34 x 8 rows over 12672 common keys 122 -> 106.
+  static constexpr int kW = 4, kStages = D == 64 ? 3 : 2;
+  static constexpr bool kSplit = D == 128;
   float qb[NT][D / 16][4];
   static __device__ __forceinline__ int kpiece(int r, int c) { return c ^ ((r & 1) << 2); }
   static __device__ __forceinline__ int vpiece(int r, int c) { return c ^ ((r & 3) << 1); }
@@ -314,8 +323,9 @@ struct Step<float, D, NT> {
       qb[n][s][3] = q.w;
     }
   }
+  template <typename F>
   __device__ __forceinline__ void tile(RowState<D, NT>& st, uint32_t kt, uint32_t vt, unsigned have, int key0,
-                                       const Spans<NT>& sp, float sl2) {
+                                       const Spans<NT>& sp, float sl2, F after_scores) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float hh[2][NT][4], hl[NT][4], lh[NT][4];  // four chains
 #pragma unroll
@@ -356,6 +366,7 @@ struct Step<float, D, NT> {
     float(&sc)[NT][4] = hh[0];
     mask_scores<NT>(sc, sp, have, key0, sl2);
     st.softmax(sc);
+    after_scores();
     // p as B operands: row g, keys t and t + 4 of each half of the tile.
     uint32_t ph[NT][4], pl[NT][4];
 #pragma unroll
@@ -443,7 +454,7 @@ struct MmaLayout {
   using St = Step<T, D, NT>;
   static constexpr int kRowBytes = D * static_cast<int>(sizeof(T));
   static constexpr int kTileBytes = kTile * kRowBytes;  // of K or V
-  static constexpr int kWarpBytes = 2 * St::kStages * kTileBytes;
+  static constexpr int kWarpBytes = (St::kSplit ? 3 : 2 * St::kStages) * kTileBytes;
   static constexpr int kBytes = St::kW * kWarpBytes;
 };
 
@@ -468,11 +479,15 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
   const T* Kp = static_cast<const T*>(a.Kp);
   const T* Vp = static_cast<const T*>(a.Vp);
   uint8_t* own = sm + warp * Lay::kWarpBytes;
-  const uint32_t kbase = smem_u32(own), vbase = kbase + S * Lay::kTileBytes;
+  const uint32_t kbase = smem_u32(own), vbase = kbase + (St::kSplit ? 0 : S * Lay::kTileBytes);
+  // Where tile i's keys and values are, from kbase and vbase on.  Split: K and V of the tiles
+  // follow one another in a ring of three.
+  auto k_slot = [&](int i) { return static_cast<uint32_t>(St::kSplit ? 2 * i % 3 : i % S) * Lay::kTileBytes; };
+  auto v_slot = [&](int i) { return static_cast<uint32_t>(St::kSplit ? (2 * i + 1) % 3 : i % S) * Lay::kTileBytes; };
   unsigned bits = 0;
   if (threadIdx.x == 0) joined = 0;
-  // Columns of K that the rows do not have stay zero: no copy writes them.
-  if (kch < CH)
+  // Columns of K that the rows do not have stay zero: no copy writes them (split: each does).
+  if (!St::kSplit && kch < CH)
     for (int x = lane; x < S * Lay::kTileBytes / 16; x += 32)
       *reinterpret_cast<uint4*>(own + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();  // `joined` is zero
@@ -599,6 +614,51 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
       }
     }
     __syncwarp();  // every lane is done with tile i - 1
+    // Copies of tile it, keys, values or both.  All sixteen keys, one page: rows behind one
+    // another from `row` of the pool on.
+    auto copy_whole = [&](long long row, auto with_k, auto with_v) {
+      const uint32_t ks = k_slot(it), vs = v_slot(it);
+      const T *kf[kCols], *vf[kCols];
+#pragma unroll
+      for (int z = 0; z < kCols; ++z) {
+        kf[z] = Kp + (row + rows_at[z]) * d + pc[z] * E;
+        vf[z] = Vp + (row + rows_at[z]) * v + pc[z] * E;
+      }
+#pragma unroll
+      for (int x = 0; x < kCopies; ++x) {
+        const uint32_t up = (x / kAts) * kAtRows * Lay::kRowBytes;
+        const int z = x % kCols, on = (x / kCols) * kColRows;
+        if constexpr (with_k) {
+          if (St::kSplit) cp16(k_at[x % kAts] + ks + up, pc[z] < kch ? kf[z] + on * d : Kp, pc[z] < kch ? 16 : 0);
+          else if (pc[z] < kch) cp16(k_at[x % kAts] + ks + up, kf[z] + on * d, 16);
+        }
+        if constexpr (with_v)
+          if (pc[z] < vch) cp16(v_at[x % kAts] + vs + up, vf[z] + on * v, 16);
+      }
+    };
+    // Else lane r's `row`: key r of the tile as a row of the pool, -1 for none.
+    auto copy_rows = [&](long long row, auto with_k, auto with_v) {
+      const uint32_t ks = k_slot(it), vs = v_slot(it);
+#pragma unroll 1
+      for (int x = 0; x < kCopies; ++x) {
+        const int r = (lane + 32 * x) / CH, c = (lane + 32 * x) % CH;
+        const long long at = __shfl_sync(0xFFFFFFFFu, row, r);
+        const long long from = at < 0 ? 0 : at;
+        const uint32_t off = r * Lay::kRowBytes;
+        if constexpr (with_k) {
+          const bool in = c < kch;
+          if (St::kSplit || in)
+            cp16(kbase + ks + off + (St::kpiece(r, c) << 4), in ? Kp + from * d + c * E : Kp, in && at >= 0 ? 16 : 0);
+        }
+        if constexpr (with_v)
+          if (c < vch) cp16(vbase + vs + off + (St::vpiece(r, c) << 4), Vp + from * v + c * E, at < 0 ? 0 : 16);
+      }
+    };
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    constexpr std::bool_constant<!St::kSplit> at_once{};
+    [[maybe_unused]] int left_over = 0;  // split: V of this tile is to be copied, 1 whole, 2 row by row
+    [[maybe_unused]] long long v_row = -1;
     if (p_left > 0) {
       if (p_key - p_base >= span) {
         p_base += span;
@@ -606,28 +666,14 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
         pages_next = entries(p_base + span);
       }
       const int s = issued++ % S;
-      const uint32_t slot = s * Lay::kTileBytes;
       const int first = __shfl_sync(0xFFFFFFFFu, pages, (p_key - p_base) >> lpk);
       unsigned have = 0xFFFFu;
       if (lpk == 4 && first >= 0 && p_key >= p_j0 && p_key + kTile <= p_j1) {
-        // All sixteen keys, one page: rows behind one another.
-        const long long row = ((static_cast<long long>(first) * a.Hk + p_h) << a.lps) +
-                              (p_key & ((1 << a.lps) - 1));
-        const T *kf[kCols], *vf[kCols];
-#pragma unroll
-        for (int z = 0; z < kCols; ++z) {
-          kf[z] = Kp + (row + rows_at[z]) * d + pc[z] * E;
-          vf[z] = Vp + (row + rows_at[z]) * v + pc[z] * E;
-        }
-#pragma unroll
-        for (int x = 0; x < kCopies; ++x) {
-          const uint32_t up = slot + (x / kAts) * kAtRows * Lay::kRowBytes;
-          const int z = x % kCols, on = (x / kCols) * kColRows;
-          if (pc[z] < kch) cp16(k_at[x % kAts] + up, kf[z] + on * d, 16);
-          if (pc[z] < vch) cp16(v_at[x % kAts] + up, vf[z] + on * v, 16);
-        }
+        const long long row = ((static_cast<long long>(first) * a.Hk + p_h) << a.lps) + (p_key & ((1 << a.lps) - 1));
+        copy_whole(row, yes, at_once);
+        left_over = 1;
+        v_row = row;
       } else {
-        // Lane r: key r of the tile as a row of the pool, -1 for none.
         const int key = p_key + (lane & 15);
         const int page = __shfl_sync(0xFFFFFFFFu, pages, (key - p_base) >> lpk);
         const long long row = page < 0 || key < p_j0 || key >= p_j1
@@ -635,26 +681,35 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
                                   : ((static_cast<long long>(page) * a.Hk + p_h) << a.lps) +
                                         (key & ((1 << a.lps) - 1));
         have = __ballot_sync(0xFFFFFFFFu, row >= 0) & 0xFFFFu;
-#pragma unroll 1
-        for (int x = 0; x < kCopies; ++x) {
-          const int r = (lane + 32 * x) / CH, c = (lane + 32 * x) % CH;
-          const long long at = __shfl_sync(0xFFFFFFFFu, row, r);
-          const long long from = at < 0 ? 0 : at;
-          const uint32_t off = slot + r * Lay::kRowBytes;
-          if (c < kch) cp16(kbase + off + (St::kpiece(r, c) << 4), Kp + from * d + c * E, at < 0 ? 0 : 16);
-          if (c < vch) cp16(vbase + off + (St::vpiece(r, c) << 4), Vp + from * v + c * E, at < 0 ? 0 : 16);
-        }
+        copy_rows(row, yes, at_once);
+        left_over = 2;
+        v_row = row;
       }
       if (lane == 0) tile_keys[warp][s] = have;
       p_key += kTile;
       --p_left;
     }
     cp_commit();
-    if (i < 0 || i >= issued) continue;
-    cp_wait<S - 1>();
-    __syncwarp();  // tile i is in
-    const int s = i % S;
-    step.tile(st, kbase + s * Lay::kTileBytes, vbase + s * Lay::kTileBytes, tile_keys[warp][s], key0, sp, a.sl2);
+    // Split: V(it), into the slot of K(i), which every lane is done with.
+    [[maybe_unused]] auto rest = [&]() {
+      if (left_over == 1) copy_whole(v_row, no, yes);
+      else if (left_over == 2) copy_rows(v_row, no, yes);
+      cp_commit();
+    };
+    if (i < 0 || i >= issued) {
+      if constexpr (St::kSplit) rest();
+      continue;
+    }
+    cp_wait<St::kSplit ? 2 : S - 1>();
+    __syncwarp();  // tile i is in (split: its keys)
+    step.tile(st, kbase + k_slot(i), vbase + v_slot(i), tile_keys[warp][i % S], key0, sp, a.sl2, [&]() {
+      if constexpr (St::kSplit) {
+        __syncwarp();
+        rest();
+        cp_wait<2>();
+        __syncwarp();  // V(i) is in
+      }
+    });
     key0 += kTile;
     if (--left > 0) continue;
 

@@ -199,6 +199,25 @@ def test_narrow_rows_and_small_pages(ex, path, d, v, page, nq, dtype):
     check_attention(dtype, y, L, ref, d, 310, _p_bits(path, dtype, b.T, 2, 2))
 
 
+@pytest.mark.parametrize("nq,page", [(1, 16), (5, 8), (3, 128)])
+@pytest.mark.parametrize("dtype,d,v", [("bf16", 72, 96), ("bf16", 96, 80), ("bf16", 104, 128), ("f32", 68, 96),
+                                       ("f32", 96, 72), ("f32", 100, 128), ("f32", 128, 108), ("f32", 112, 112)])
+def test_widths_between(ex, path, dtype, d, v, nq, page):
+    """Widths below those that the kernels are made for: the columns that are missing stay out of
+    the products, also where one is wider than the other; an infinite value stays in its column."""
+    b = Batch([700, nq, 90], [nq, nq, nq], 4, 2, d, v, dtype, page, seed=d + v + nq)
+    ref = oracle.attend(b.np(b.q), b.np(b.k_pages), b.np(b.v_pages), b.table, b.lens, b.starts, 0.1, "causal")
+    y, L, status = _attend(ex, b, "causal", 0, 0.1)
+    assert status == 0
+    bits = _p_bits(path, dtype, b.T, 3, 2)
+    check_attention(dtype, y, L, ref, d, 700, bits)
+    b.v_pages[int(b.table[0, 0]), :, 0, v - 1] = float("inf")  # the first key of the first sequence
+    y2, L2, status = _attend(ex, b, "causal", 0, 0.1)
+    assert status == 0 and torch.equal(L2, L)
+    assert not torch.isfinite(y2[:nq, :, v - 1]).any()
+    assert torch.equal(y2[nq:], y[nq:]) and torch.equal(y2[..., :v - 1], y[..., :v - 1])
+
+
 @pytest.mark.parametrize("prefix", [0, 37])
 @pytest.mark.parametrize("dtype,nq", [("bf16", 1), ("f32", 2), ("bf16", 30)])
 def test_large_batches(ex, path, dtype, nq, prefix):

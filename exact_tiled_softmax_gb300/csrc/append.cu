@@ -8,7 +8,7 @@
 // Bound by memory: every element is read once and written once, in 16-byte accesses
 // where the rotated halves allow them.  A warp takes a token (or a share of its rows):
 // it finds the token's place and angles once for all heads.  What hides the latency is
-// warps, not loads of a lane: six CTAs to an SM with 32 bytes in flight a lane move 40
+// warps, not loads of a lane: six CTAs to an SM with 32 bytes in flight a lane move 36
 // thousand tokens of 48 rows of 128 bf16 columns at 6.20 TB/s (91% of the measured copy);
 // before the angles left double precision it was 5.94, and then two rows at four CTAs 5.41,
 // four rows at two CTAs 4.05, and in fp32 six CTAs 5.74, five 5.01.  One CTA more checks

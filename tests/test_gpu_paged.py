@@ -345,6 +345,8 @@ PREFIX = [
     (130, [7, 9], [1, 1], 2, 2, 200, 104, "bf16", 16, "causal", 0),
     (2000, [1, 1], [1, 1], 4, 4, 128, 128, "f32", 64, "causal", 0),
     (0, [30, 5], [2, 1], 4, 2, 64, 64, "bf16", 16, "causal", 0),
+    # Long enough for tall tiles in a launch of their own.
+    (4001, [40, 1, 90, 17] * 4, [1, 1, 1, 0] + [1] * 12, 32, 8, 128, 128, "bf16", 64, "causal", 1),
 ]
 
 
@@ -626,6 +628,46 @@ def test_captured_launch_follows_lengths_and_tables(ex, path):
         ref = oracle.attend(b.np(b.q), k.double().cpu().numpy(), v.double().cpu().numpy(),
                             b.table, lens.cpu().numpy(), b.starts, 0.125, "causal")
         check_attention("bf16", y, L, ref, 64, 70)
+
+
+def test_captured_prefix_in_two_launches(ex):
+    """A long prefix under few own keys takes two attention launches, the second of which begins
+    beside the first; captured with an append before it and another call behind it on the same
+    workspace, and replayed as the sequences grow."""
+    P, B = 4001, 16
+    b = Batch([60 + 3 * k for k in range(B)], [1] * B, 32, 8, 128, 128, "bf16", 64, seed=43, prefix=P, spare=B)
+    free = np.setdiff1d(np.arange(b.k_pages.shape[0]),
+                        np.concatenate((b.prefix_table, b.table[b.table < b.k_pages.shape[0]])))
+    for x in range(B):  # the page behind the last
+        b.table[x, -(-int(b.lens[x]) // 64)] = free[x]
+    q, k, v, table, lens, kn, vn, pt = b.dev("q", "k_pages", "v_pages", "table", "lens", "k_new", "v_new",
+                                             "prefix_table")
+    shape = ex.paged_shape(q, k, v, table)
+    ws = ex.workspace(ex.prefix_workspace_size(shape), "cuda")
+    outs = [(torch.empty_like(q), torch.empty(B, 32, device="cuda")) for _ in range(2)]
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+
+    def calls():
+        ex.append_paged(kn, vn, k, v, table, lens, ws=ws)
+        for y, L in outs:
+            ex.fwd_prefix(q, k, v, pt, P, table, lens, 0.1, "causal", y=y, L=L, ws=ws)
+
+    with torch.cuda.stream(s):
+        calls()
+    s.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        calls()
+    for step in range(3):
+        lens.add_(1)
+        kn.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert ex.device_status(ws) == 0
+        assert all(torch.equal(x, y) for x, y in zip(*outs))
+        ref = oracle.attend(b.np(b.q), k.double().cpu().numpy(), v.double().cpu().numpy(), b.table,
+                            lens.cpu().numpy(), b.starts, 0.1, "causal", prefix=(b.prefix_table, P))
+        check_attention("bf16", *outs[0], ref, 128, P + 110, 8)
 
 
 def test_outputs_belong_to_the_call_stream(ex):

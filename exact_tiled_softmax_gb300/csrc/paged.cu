@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(32 * kW, kCtas<NQ>) paged_simt_kernel(const Pa
 // the status bits of every CTA of the attention launches.  Bound by latency where few tiles
 // are shared (the launch and three dependent loads, 2 to 3 us behind the attention kernel), by
 // the summaries' traffic in the L2 cache where most are: 14 us for the 40 MB that 152 runs of
-// 256-row tiles leave, 8 for one row tile of 1216 runs in each of 8 heads.
+// 256-row tiles leave, 8 for 8 tiles of 152 runs each.
 //
 // A row's state while its pieces come in, four at a time so that their loads overlap.
 template <int N>

@@ -14,8 +14,8 @@
 // and 32 heads of 128 columns took 341 us.)
 //
 // Measured in bf16: those 2.1 GB 320 to 334 us, 6.4 to 6.7 TB/s or 95 to 98% of the measured
-// copy; 64 sequences of 2048 to 32768 keys, 64 query heads over 8 key heads 674 to 704 us, 97 to
-// 99%; 16 rows over 262147 keys 174 to 180 us, 88 to 91%, of which 8 are the merge.  fp32 is bound by its
+// copy; 64 sequences of 2048 to 32768 keys, 64 query heads over 8 key heads 674 to 707 us, 96 to
+// 100%; 16 rows over 262147 keys 174 to 180 us, 88 to 91%, of which 8 are the merge.  fp32 is bound by its
 // products: 12 sequences of 6000 keys of 16 heads of 80 and 96 columns 133 us, 6.1 TB/s for 4
 // rows, 5.1 for 16.
 //

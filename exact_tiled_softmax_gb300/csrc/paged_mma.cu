@@ -551,7 +551,9 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
   constexpr int kSwizzle = sizeof(T) == 4 ? 4 : 8;
   constexpr int kCols = 32 % CH == 0 ? 1 : 3, kColRows = kCols * 32 / CH;
   constexpr int kAts = kCols == 1 && kColRows < kSwizzle ? kSwizzle / kColRows : kCols, kAtRows = kAts * 32 / CH;
-  static_assert(kCols * 32 % CH == 0 && kCopies % kAts == 0 && kAtRows % kSwizzle == 0, "pieces of a lane");
+  static_assert(kCols * 32 % CH == 0 && kCopies % kAts == 0 && kAtRows % kSwizzle == 0 && 8 % kColRows == 0 &&
+                    kCopies % (2 * kCols) == 0,
+                "pieces of a lane");
   int rows_at[kCols], pc[kCols];
 #pragma unroll
   for (int z = 0; z < kCols; ++z) {
@@ -631,9 +633,11 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
       }
     }
     __syncwarp();  // every lane is done with tile i - 1
-    // Copies of tile it, keys, values or both.  All sixteen keys, one page: rows behind one
-    // another from `row` of the pool on.
-    auto copy_whole = [&](long long row, auto with_k, auto with_v) {
+    // Copies of tile it, keys, values or both.  All sixteen keys, in pages of eight or more: rows
+    // behind one another, the first eight from `row` of the pool on, the others from `row8` (pages
+    // of eight row by row: 482 us in place of 326, 42 sequences of 3000 keys, 16 heads of 128 fp32
+    // columns).
+    auto copy_whole = [&](long long row, long long row8, auto with_k, auto with_v) {
       const uint32_t ks = k_slot(it), vs = v_slot(it);
       const T *kf[kCols], *vf[kCols];
 #pragma unroll
@@ -644,7 +648,14 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
 #pragma unroll
       for (int x = 0; x < kCopies; ++x) {
         const uint32_t up = (x / kAts) * kAtRows * Lay::kRowBytes;
-        const int z = x % kCols, on = (x / kCols) * kColRows;
+        const int z = x % kCols, on = x % (kCopies / 2) / kCols * kColRows;
+        if (x == kCopies / 2) {
+#pragma unroll
+          for (int y = 0; y < kCols; ++y) {
+            kf[y] += (row8 - row) * d;
+            vf[y] += (row8 - row) * v;
+          }
+        }
         if constexpr (with_k) {
           if (St::kSplit) cp16(k_at[x % kAts] + ks + up, pc[z] < kch ? kf[z] + on * d : Kp, pc[z] < kch ? 16 : 0);
           else if (pc[z] < kch) cp16(k_at[x % kAts] + ks + up, kf[z] + on * d, 16);
@@ -675,7 +686,7 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
     constexpr std::false_type no{};
     constexpr std::bool_constant<!St::kSplit> at_once{};
     [[maybe_unused]] int left_over = 0;  // split: V of this tile is to be copied, 1 whole, 2 row by row
-    [[maybe_unused]] long long v_row = -1;
+    [[maybe_unused]] long long v_row = -1, v_row8 = -1;
     if (p_left > 0) {
       if (p_key - p_base >= span) {
         p_base += span;
@@ -685,11 +696,14 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
       const int s = issued++ % S;
       const int first = __shfl_sync(0xFFFFFFFFu, pages, (p_key - p_base) >> lpk);
       unsigned have = 0xFFFFu;
-      if (lpk == 4 && first >= 0 && p_key >= p_j0 && p_key + kTile <= p_j1) {
+      const int second = lpk == 3 ? __shfl_sync(0xFFFFFFFFu, pages, (p_key + 8 - p_base) >> 3) : first;
+      if (lpk >= 3 && first >= 0 && second >= 0 && p_key >= p_j0 && p_key + kTile <= p_j1) {
         const long long row = ((static_cast<long long>(first) * a.Hk + p_h) << a.lps) + (p_key & ((1 << a.lps) - 1));
-        copy_whole(row, yes, at_once);
+        const long long row8 = lpk == 3 ? (static_cast<long long>(second) * a.Hk + p_h) << 3 : row + 8;
+        copy_whole(row, row8, yes, at_once);
         left_over = 1;
         v_row = row;
+        v_row8 = row8;
       } else {
         const int key = p_key + (lane & 15);
         const int page = __shfl_sync(0xFFFFFFFFu, pages, (key - p_base) >> lpk);
@@ -709,7 +723,7 @@ __global__ void __launch_bounds__(32 * Step<T, D, NT>::kW, 2) paged_mma_kernel(c
     cp_commit();
     // Split: V(it), into the slot of K(i), which every lane is done with.
     [[maybe_unused]] auto rest = [&]() {
-      if (left_over == 1) copy_whole(v_row, no, yes);
+      if (left_over == 1) copy_whole(v_row, v_row8, no, yes);
       else if (left_over == 2) copy_rows(v_row, no, yes);
       cp_commit();
     };

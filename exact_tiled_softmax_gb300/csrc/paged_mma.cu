@@ -826,8 +826,8 @@ PagedKernel paged_mma_kernel_of(int dtype, int d, int v, int rows) {
   const int columns = columns_of(d, v), warps = dtype == kF32 ? warps_of<float>(columns) : warps_of<__nv_bfloat16>(columns);
   // Least units: what a worker streams before it ends a tile, against the workers that join it.
   // One sequence of 1000 keys, 8 key heads of 128 bf16 columns: 12.3 us with 2, 14.3 with 4, 16.4
-  // with 8; 16 key heads of 64 columns and 2000 common keys: 17.8, 16.4, 18.4; fp32 windows: 24.6,
-  // 22.5.
+  // with 8; 16 key heads of 64 columns and 2000 common keys: 13.1, 12.6, 13.1; fp32, 2 key heads of
+  // 112 columns, 25 sequences of 600 keys behind 804: 30.3, 25.9, 37.9.
   const int least = dtype == kBF16 && columns > 64 ? 2 : 4;
   return {rows, kCtas, kCtas * warps, least};
 }

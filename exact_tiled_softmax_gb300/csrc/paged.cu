@@ -239,14 +239,14 @@ __global__ void __launch_bounds__(32 * kW, kCtas<NQ>) paged_simt_kernel(const Pa
       float M = -INFINITY;
 #pragma unroll
       for (int k = 0; k < kW; ++k) M = fmaxf(M, red_m[k][q]);
+      // Also where no maximum was found: sums of NaN scores alone are NaN and stay it.
+      const float ref = M == -INFINITY ? 0.f : M;
       float zc = 0.f, lq = 0.f;
-      if (M != -INFINITY) {
 #pragma unroll
-        for (int k = 0; k < kW; ++k) {
-          const float f = pexp2(red_m[k][q] - M);
-          zc = fmaf(f, red_z[k][q][col], zc);
-          lq = fmaf(f, red_l[k][q], lq);
-        }
+      for (int k = 0; k < kW; ++k) {
+        const float f = pexp2(red_m[k][q] - ref);
+        zc = fmaf(f, red_z[k][q][col], zc);
+        lq = fmaf(f, red_l[k][q], lq);
       }
       const size_t out = paged_out_row(a, w.s.s0, w.h, r0 + q, w.s.prefix);
       if (a.info && col == 0 && place.parts >= 0) a.info[out] = make_int2(blockIdx.x, place.parts);

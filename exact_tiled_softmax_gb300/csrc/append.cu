@@ -158,11 +158,11 @@ __global__ void __launch_bounds__(kAppendThreads, 6) append_kernel(const __grid_
   const int b = owner(a, t);
   if (b < 0) return;  // behind the last sequence
   int s0 = b * a.each, nq = a.each;
-  if (a.starts) {
-    s0 = __ldg(a.starts + b);
-    nq = __ldg(a.starts + b + 1) - s0;
+  if (a.starts) {  // clamped, as the attention does
+    s0 = max(__ldg(a.starts + b), 0);
+    nq = min(__ldg(a.starts + b + 1), a.T) - s0;
   }
-  const int pos = __ldg(a.lens + b) - nq + (t - s0);
+  const int pos = max(__ldg(a.lens + b), 0) - nq + (t - s0);
   long long slot = -1;  // the token's row of the pool (of key head 0); -1: nowhere
   if (pos >= 0 && pos < a.max_pages << a.lps) {
     const int page = __ldg(a.table + static_cast<size_t>(b) * a.max_pages + (pos >> a.lps));

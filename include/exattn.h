@@ -367,9 +367,13 @@ int attn_step_host(const exattn_shape* shape, const void* Q, const void* K, cons
  *
  * Status word.  EXATTN_EMPTY_ROW: some row allows no key (Y = 0, L = -inf).
  * EXATTN_BAD_PAGE: q_starts does not ascend inside [0, tokens], a seq_lens is
- * outside [0, max_pages * page_size] (both are clamped), or an entry that was
- * needed is outside [0, num_pages): its keys are left out, its tokens not
- * written.  Nothing outside the caller's arrays is read or written.
+ * outside [0, max_pages * page_size], or an entry that was needed is outside [0,
+ * num_pages): its keys are left out, its tokens not written.  Entries of q_starts are
+ * clamped to [0, tokens] and negative lengths to 0.  A length above max_pages *
+ * page_size is that for the attention; an append takes it as it stands and leaves
+ * out the tokens whose positions lie behind the table, so that no cached key is
+ * written over.  Where q_starts descends, an append may leave tokens out.  Nothing
+ * outside the caller's arrays is read or written.
  *
  * What a page holds where no token of its sequence allows a key (behind the last key,
  * before every window) meets no result, NaN included, nor do a key's masked scores.  The

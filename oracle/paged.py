@@ -26,14 +26,16 @@ def rotate(x, pos, inv_freq, interleaved):
 def append(k, v, k_pages, v_pages, table, lens, starts, q=None, inv_freq=(), interleaved=False,
            offset=0):
     """(q_out, k_pages, v_pages) in float64; tokens without a place are not written and
-    tokens that no sequence owns give NaN rows of q_out (the caller's rows stay)."""
+    tokens that no sequence owns give NaN rows of q_out (the caller's rows stay).  Ends of
+    `starts` outside the tokens and negative lengths are clamped."""
     kp, vp = k_pages.astype(np.float64), v_pages.astype(np.float64)
     page, num = kp.shape[2], kp.shape[0]
     qo = None if q is None else np.full(q.shape, np.nan)
     for b in range(len(lens)):
-        nq = starts[b + 1] - starts[b]
+        first, end = (min(max(int(x), 0), len(k)) for x in starts[b:b + 2])
+        nq = end - first
         for i in range(nq):
-            t, pos = starts[b] + i, int(lens[b]) - nq + i
+            t, pos = first + i, max(int(lens[b]), 0) - nq + i
             if q is not None:
                 qo[t] = rotate(q[t], pos + offset, inv_freq, interleaved)
             if pos < 0 or pos >= table.shape[1] * page or not 0 <= table[b][pos // page] < num:

@@ -274,8 +274,6 @@ cudaError_t append_dispatch(const AppendArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-int append_max_pairs() { return kMaxPairs; }
-
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
   return a.dtype == kF32 ? append_dispatch<float>(a, s) : append_dispatch<__nv_bfloat16>(a, s);
 }

@@ -8,7 +8,6 @@
 #include "paged.cuh"
 
 namespace exattn {
-int append_max_pairs();
 extern thread_local char g_last_error[256];
 int current_path();
 }  // namespace exattn

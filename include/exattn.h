@@ -378,7 +378,13 @@ int attn_step_host(const exattn_shape* shape, const void* Q, const void* K, cons
  * What a page holds where no token of its sequence allows a key (behind the last key,
  * before every window) meets no result, NaN included, nor do a key's masked scores.  The
  * values of a key that some tokens of a sequence allow and others do not must be
- * finite: 0 * NaN may reach the others, as in attn_fwd.
+ * finite: 0 * NaN may reach the others, as in attn_fwd.  Entries that a token allows
+ * should be finite too: on the tensor cores a probability is two bf16 parts and an fp32
+ * operand two tf32 parts, and a part may be zero or of the other sign, so an infinite
+ * value gives NaN or infinities in its column of the rows that allow it, and an
+ * infinite query or key entry may give NaN where its score's limit has a result (the
+ * SIMT kernels follow the formula).  A row with a NaN score is NaN in Y and L.  Other
+ * rows, columns and sequences are not touched by any of these.
  * Ownership, streams and errors as for attn_fwd.
  * ------------------------------------------------------------------------- */
 typedef struct exattn_paged_shape {

@@ -383,8 +383,19 @@ int attn_step_host(const exattn_shape* shape, const void* Q, const void* K, cons
  * operand two tf32 parts, and a part may be zero or of the other sign, so an infinite
  * value gives NaN or infinities in its column of the rows that allow it, and an
  * infinite query or key entry may give NaN where its score's limit has a result (the
- * SIMT kernels follow the formula).  A row with a NaN score is NaN in Y and L.  Other
+ * SIMT kernels follow the formula; fp32 entries within 2^-12 of the largest count as
+ * infinite on the tensor cores).  A row with a NaN score is NaN in Y and L.  Other
  * rows, columns and sequences are not touched by any of these.
+ *
+ * Precision.  Scores, statistics and outputs are summed in fp32, and Y is rounded once.
+ * In bf16 with d, v <= 128, pages of 8 keys or more and a positive scale, the
+ * probabilities are rounded to bf16 before they meet V, as in attn_fwd, wherever the
+ * 256-row kernel runs: in calls of more than 16 rows to a key head on average
+ * (ceil(tokens / batch) * heads / kv_heads), and for a prefix in calls of more than 16
+ * rows of all tokens together, unless it is short (16-row tiles would read it again for
+ * less than 40 MB).  All other kernels keep what a probability's rounding leaves out (to
+ * 2^-17 of it; EXATTN_PATH_SIMT and fp32: whole, or to 2^-21).  The last bits of a
+ * sequence's result therefore depend on the batch that it is computed in.
  * Ownership, streams and errors as for attn_fwd.
  * ------------------------------------------------------------------------- */
 typedef struct exattn_paged_shape {

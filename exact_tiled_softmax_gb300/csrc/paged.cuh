@@ -133,8 +133,17 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int b) {
   return s;
 }
 
-// Keys [lo, hi) that row token i allows (an empty range is lo >= hi).
-__device__ __forceinline__ void paged_row_span(const PagedArgs& a, const PagedSeq& s, int i, int& lo,
+// Keys [lo, hi) that row token i allows (an empty range is lo >= hi).  A: PagedArgs,
+// or what of them a row tile's keys depend on (for functions that are called).
+struct PagedRule {
+  FastDiv by_group;
+  int G, mask_kind, window, least;
+};
+__device__ __forceinline__ PagedRule paged_rule(const PagedArgs& a) {
+  return {a.by_group, a.G, a.mask_kind, a.window, a.least};
+}
+template <typename A>
+__device__ __forceinline__ void paged_row_span(const A& a, const PagedSeq& s, int i, int& lo,
                                                int& hi) {
   lo = 0;
   hi = s.len;
@@ -150,8 +159,8 @@ struct PagedTile {
   int lo, hi, kt0, cnt;
 };
 
-template <int RT, int UK>
-__device__ __forceinline__ PagedTile paged_tile(const PagedArgs& a, const PagedSeq& s, int rt) {
+template <int RT, int UK, typename A>
+__device__ __forceinline__ PagedTile paged_tile(const A& a, const PagedSeq& s, int rt) {
   PagedTile t;
   const int r0 = rt * RT, all = s.nq * a.G;
   t.rows = min(RT, all - r0);
@@ -195,12 +204,72 @@ struct PagedWalk {
   int tiles;  // row tiles of (b, h)
 };
 
+// Units of row tile rt, and of the tiles [first, end) of one (b, h).
+template <int RT, int UK, typename A>
+__device__ __forceinline__ int paged_tile_units(const A& a, const PagedSeq& s, int rt) {
+  return static_cast<int>(round_up(paged_tile<RT, UK>(a, s, rt).cnt, a.least));
+}
+template <int RT, int UK, typename A>
+__device__ __forceinline__ long long paged_tiles_units(const A& a, const PagedSeq& s, int first, int end) {
+  long long u = 0;
+#pragma unroll 1
+  for (int rt = first; rt < end; ++rt) u += paged_tile_units<RT, UK>(a, s, rt);
+  return u;
+}
+// Whether all row tiles have the same keys.
+template <typename A>
+__device__ __forceinline__ bool paged_flat(const A& a, const PagedSeq& s) {
+  return s.prefix || a.mask_kind == kMaskNone;
+}
+__device__ __forceinline__ long long sum_over_lanes_upto(long long x) {  // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// Every worker finds the start of its run in the line by itself, before its first copy.  A
+// sequence may have as many row tiles as tokens and more: above kFewTiles a warp's lanes share
+// them out, and where all tiles have the same keys one is enough.  (One lane over all tiles: 65536
+// fp32 tokens of 4 heads over 64 keys each 2.4 ms, now 0.15; 65536 of 8 heads over a window of 128
+// 5.2 ms, now 0.70.)  That part is two functions, out of the way of other launches: inlined, they
+// cost the tall tiles behind a prefix 1.5 of 29 us in instruction fetches.
+constexpr int kFewTiles = 32;
+
+// Units of each lane's sequence of `tiles` row tiles where these are many, by a whole warp.
+template <int RT, int UK>
+__device__ __noinline__ long long paged_many_units(const PagedRule a, int nq, int len, bool prefix, int tiles) {
+  const int lane = threadIdx.x & 31;
+  const PagedSeq s{0, nq, len, prefix, false};
+  const bool flat = paged_flat(a, s);
+  long long u = flat ? static_cast<long long>(tiles) * paged_tile_units<RT, UK>(a, s, 0) : 0;
+#pragma unroll 1
+  for (unsigned todo = __ballot_sync(0xFFFFFFFFu, !flat && tiles > kFewTiles); todo; todo &= todo - 1) {
+    const int who = __ffs(todo) - 1;
+    PagedSeq of{0, 0, 0, false, false};
+    of.nq = __shfl_sync(0xFFFFFFFFu, nq, who);
+    of.len = __shfl_sync(0xFFFFFFFFu, len, who);
+    const int n = __shfl_sync(0xFFFFFFFFu, tiles, who), per = (n + 31) / 32;
+    long long sum = paged_tiles_units<RT, UK>(a, of, min(lane * per, n), min(lane * per + per, n));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane == who) u = sum;
+  }
+  return u;
+}
+// Units of each lane's sequence (nq = 0: none), by a whole warp.
 template <int RT, int UK>
 __device__ __forceinline__ long long paged_units(const PagedArgs& a, const PagedSeq& s) {
   const int tiles = (s.nq * a.G + RT - 1) / RT;
-  long long u = 0;
-#pragma unroll 1
-  for (int rt = 0; rt < tiles; ++rt) u += round_up(paged_tile<RT, UK>(a, s, rt).cnt, a.least);
+  const bool many = tiles > kFewTiles;
+  long long u = paged_tiles_units<RT, UK>(a, s, 0, many ? 0 : tiles);
+  if (__any_sync(0xFFFFFFFFu, many)) {
+    const long long x = paged_many_units<RT, UK>(paged_rule(a), s.nq, s.len, s.prefix, tiles);
+    if (many) u = x;
+  }
   return u * a.Hk;
 }
 
@@ -217,19 +286,15 @@ __device__ __forceinline__ void paged_scan(const PagedArgs& a, long long* pre, l
 #pragma unroll 1
   for (int k = 0; k < per; ++k) {
     const int b = tid * per + k;
-    if (b >= a.B) break;
-    const PagedSeq s = paged_seq(a, b);
+    PagedSeq s{0, 0, 0, false, false};
+    if (b < a.B) s = paged_seq(a, b);
     bad |= s.bad;
-    pre[b + 1] = mine += paged_units<RT, UK>(a, s);
+    mine += paged_units<RT, UK>(a, s);  // by the whole warp
+    if (b < a.B) pre[b + 1] = mine;
   }
   // Exclusive sum of `mine` over the threads.
   const int lane = tid & 31, warp = tid >> 5;
-  long long inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-    if (lane >= o) inc += x;
-  }
+  const long long inc = sum_over_lanes_upto(mine);
   if (lane == 31) scan[warp] = inc;
   const int any_bad = __syncthreads_or(bad);
   if (blockIdx.x == 0) {
@@ -249,7 +314,35 @@ __device__ __forceinline__ void paged_scan(const PagedArgs& a, long long* pre, l
   __syncthreads();
 }
 
-// w at unit `local` of the `units` of its sequence.
+// The row tile that holds unit `rem` of the `left` tiles of one (b, h), and the unit in it, by a
+// whole warp whose lanes agree on them.
+struct PagedTileUnit {
+  int rt;
+  long long rem;
+};
+template <int RT, int UK>
+__device__ __noinline__ PagedTileUnit paged_find(const PagedRule a, int nq, int len, bool prefix, int left,
+                                                 long long rem) {
+  const int lane = threadIdx.x & 31;
+  const PagedSeq s{0, nq, len, prefix, false};
+  const int same = paged_flat(a, s) ? paged_tile_units<RT, UK>(a, s, 0) : 0;
+  int rt = 0;
+#pragma unroll 1
+  while (left > 1) {  // it is in [rt, rt + left): each lane sums a share of them
+    const int per = (left + 31) / 32;
+    const int first = min(lane * per, left), end = min(lane * per + per, left);
+    const long long mine = same ? static_cast<long long>(end - first) * same
+                                : paged_tiles_units<RT, UK>(a, s, rt + first, rt + end);
+    const long long upto = sum_over_lanes_upto(mine);
+    const unsigned behind = __ballot_sync(0xFFFFFFFFu, rem < upto);
+    const int who = min(behind ? __ffs(behind) - 1 : 31, (left - 1) / per);
+    rem -= __shfl_sync(0xFFFFFFFFu, upto - mine, who);
+    rt += who * per;
+    left = min(per, left - who * per);
+  }
+  return {rt, rem};
+}
+// w at unit `local` of the `units` of its sequence, by a whole warp whose lanes agree on them.
 template <int RT, int UK>
 __device__ __forceinline__ void paged_enter(const PagedArgs& a, PagedWalk& w, long long units, long long local) {
   w.tiles = (w.s.nq * a.G + RT - 1) / RT;
@@ -257,8 +350,13 @@ __device__ __forceinline__ void paged_enter(const PagedArgs& a, PagedWalk& w, lo
   w.h = static_cast<int>(paged_div(local, per_head));
   long long rem = local - w.h * per_head;
   w.rt = 0;
-  w.t = paged_tile<RT, UK>(a, w.s, 0);
-  for (long long n; rem >= (n = round_up(w.t.cnt, a.least));) {
+  if (w.tiles > kFewTiles) {
+    const PagedTileUnit at = paged_find<RT, UK>(paged_rule(a), w.s.nq, w.s.len, w.s.prefix, w.tiles, rem);
+    w.rt = at.rt;
+    rem = at.rem;
+  }
+  w.t = paged_tile<RT, UK>(a, w.s, w.rt);
+  for (long long n; rem >= (n = round_up(w.t.cnt, a.least)) && w.rt + 1 < w.tiles;) {
     rem -= n;
     w.t = paged_tile<RT, UK>(a, w.s, ++w.rt);
   }
@@ -293,22 +391,14 @@ __device__ __forceinline__ bool paged_begin_warp(const PagedArgs& a, int r, Page
                                                  unsigned& bits) {
   const int lane = threadIdx.x & 31;
   PagedSeq s{0, 0, 0, false, false};
-  long long units = 0;
-  if (lane < a.B) {
-    s = paged_seq(a, lane);
-    units = paged_units<RT, UK>(a, s);
-  }
+  if (lane < a.B) s = paged_seq(a, lane);
+  long long units = paged_units<RT, UK>(a, s);
   if (blockIdx.x == 0 && threadIdx.x < 32) {
     const bool any_bad = __any_sync(0xFFFFFFFFu, s.bad);
     if (any_bad) bits |= kStatusBadPage;
     if (a.info && lane == 0 && a.prefix_at != 0) *a.sane = !any_bad;
   }
-  long long upto = units;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-    if (lane >= o) upto += x;
-  }
+  const long long upto = sum_over_lanes_upto(units);
   total = __shfl_sync(0xFFFFFFFFu, upto, 31);
   const long long n = run_units(a, total);
   w.u = n * r;

@@ -24,6 +24,8 @@
 // loads, and Y is then rounded once, on its way out.
 // fp32: m16n8k8 on tf32 parts, x = hi + lo, three products for one (lo lo, 2^-22 of
 // the product, is left out; lo is cut to tf32, 2^-21 of x).
+// A part may be zero or of the other sign, so an infinite V, or fp32 K or Q, that a row allows may
+// give NaN (stated in the header).
 // The reference point of the exponentials moves only when a row's maximum passes
 // it by more than 2^8, so p <= 2^8.
 #include <type_traits>

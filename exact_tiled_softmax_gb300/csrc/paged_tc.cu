@@ -14,8 +14,10 @@
 // the tensor time that bounds this kernel.
 //
 // Measured: chunks of 512 tokens of 4 sequences, 32 query heads over 8 key heads of 128
-// columns, 8192 keys, causal: 197 us, 1.36 PFLOP/s or 73% of the measured peak, as the dense
-// forward; the merge of the tiles that two CTAs share adds 14.  A short share costs its start
+// columns, 8192 keys, causal: 197 to 200 us, 1.36 PFLOP/s or 73% of the measured peak, as the dense
+// forward; the merge of the tiles that two CTAs share adds 14, launch and start 1 to 3.  (215 us
+// a call at 2070 MHz; in a loop of seconds the power limit leaves 1807 MHz, and a call takes 226.)
+// Pages of 8 keys, a box each: 347 us a call.  A short share costs its start
 // and end: 6.7 key blocks a CTA (64 sequences' tokens over 16384 common keys) 28 us, 13 of
 // them in the blocks.  Without the ring of segments, rows of Q read lane by lane, 281 us in
 // place of 223 for the chunks and their merge.

@@ -137,6 +137,17 @@ def load_library():
     lib.attn_fwd_prefix.restype = ci
     lib.exattn_paged_run.argtypes = [ci, ctypes.c_char_p]  # a packed exattn_paged_call
     lib.exattn_paged_run.restype = ci
+    lib.attn_append_paged_e4m3.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, vp, vp, vp, vp,
+                                           vp, vp, sz, vp]
+    lib.attn_append_paged_e4m3.restype = ci
+    lib.attn_fwd_paged_e4m3.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp, cf, ci, ci, vp, vp, vp, sz,
+                                        vp]
+    lib.attn_fwd_paged_e4m3.restype = ci
+    lib.attn_fwd_prefix_e4m3.argtypes = [pp, vp, vp, vp, vp, vp, vp, ci, vp, vp, vp, cf, ci, vp, vp, vp,
+                                         sz, vp]
+    lib.attn_fwd_prefix_e4m3.restype = ci
+    lib.exattn_paged_e4m3_run.argtypes = [ci, ctypes.c_char_p]  # a packed exattn_paged_e4m3_call
+    lib.exattn_paged_e4m3_run.restype = ci
     lib.exattn_last_error.argtypes = []
     lib.exattn_last_error.restype = ctypes.c_char_p
     lib.exattn_host_step_workspace_size.argtypes = [sp, ci]
@@ -426,12 +437,26 @@ def prefix_workspace_size(shape: PagedShape) -> int:
     return load_library().exattn_prefix_workspace_size(ctypes.byref(shape))
 
 
-def _check_paged(q, k_pages, v_pages, page_table, seq_lens, q_starts, ws):
+_SCALE_DTYPES = (torch.uint8,) + ((torch.float8_e8m0fnu,) if hasattr(torch, "float8_e8m0fnu") else ())
+
+
+def _check_paged(q, k_pages, v_pages, page_table, seq_lens, q_starts, ws, k_scales, v_scales):
     """The cache and its tables, which the library takes as bare pointers.  Raises
     ValueError before anything reaches the library; returns the PagedShape."""
     shape = paged_shape(q, k_pages, v_pages, page_table)
     dev = q.device
-    _check((k_pages, v_pages), q.dtype, dev)
+    scales = (("k_scales", k_scales), ("v_scales", v_scales))
+    if torch.float8_e4m3fn in (k_pages.dtype, v_pages.dtype) or k_scales is not None or v_scales is not None:
+        _check((k_pages, v_pages), torch.float8_e4m3fn, dev)
+        for name, t in scales:
+            if t is None:
+                raise ValueError(f"pages in 8 bits have k_scales and v_scales: {name} is missing")
+            if (t.dtype not in _SCALE_DTYPES or not t.is_contiguous() or t.device != dev
+                    or t.shape != k_pages.shape[:3]):
+                raise ValueError(f"{name} must be contiguous exponent bytes of shape "
+                                 f"{tuple(k_pages.shape[:3])} on {dev}")
+    else:
+        _check((k_pages, v_pages), q.dtype, dev)
     if k_pages.shape[:3] != v_pages.shape[:3]:
         raise ValueError(f"v_pages has shape {tuple(v_pages.shape)}, k_pages "
                          f"{tuple(k_pages.shape)}: they differ before the width")
@@ -474,6 +499,7 @@ def _check_outputs(q, vw, y, L):
 # the value is the fields of the PagedShape.
 _paged_known = {}
 _PAGED_CALL = struct.Struct("@10i3q15Qf5i")  # exattn_paged_call
+_PAGED_E4M3_CALL = struct.Struct("@10i3q15Qf5i2Q")  # exattn_paged_e4m3_call
 
 
 def _meta(t):
@@ -496,38 +522,50 @@ def _on(stream, make, *args, **kwargs):
         return make(*args, **kwargs)
 
 
-def _paged_call(op, name, index, known, stream, fields):
-    """exattn_paged_run on the device ``index``; ``fields``: the call's from the workspace's
-    size on, before and behind the stream."""
+def _paged_call(op, name, index, known, stream, fields, k_scales, v_scales):
+    """exattn_paged_run, or with scales exattn_paged_e4m3_run, on the device ``index``; ``fields``: the
+    call's from the pointers on, before and behind the stream."""
     if index < 0:
         raise ValueError("tensors must be on a CUDA device")
     s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    call = _PAGED_CALL.pack(*known, *fields[0], s, *fields[1])
+    if k_scales is None:
+        run, call = _lib.exattn_paged_run, _PAGED_CALL.pack(*known, *fields[0], s, *fields[1])
+    else:
+        run, name = _lib.exattn_paged_e4m3_run, name + "_e4m3"
+        call = _PAGED_E4M3_CALL.pack(*known, *fields[0], s, *fields[1], k_scales.data_ptr(), v_scales.data_ptr())
     if index == torch.cuda.current_device():
-        st = _lib.exattn_paged_run(op, call)
+        st = run(op, call)
     else:
         with torch.cuda.device(index):
-            st = _lib.exattn_paged_run(op, call)
+            st = run(op, call)
     if st != 0:
         raise ExattnError(st, name)
 
 
 def append_paged(k, v, k_pages, v_pages, page_table, seq_lens, q_starts=None, q=None, q_out=None,
-                 inv_freq=None, interleaved=False, pos_offset=0, ws=None, stream=None):
+                 inv_freq=None, interleaved=False, pos_offset=0, ws=None, stream=None, k_scales=None,
+                 v_scales=None):
     """attn_append_paged: the new tokens' k [tokens, kv_heads, d] and v [tokens, kv_heads, v] go
     into the pages of their sequences, k rotated by position with ``inv_freq`` (float32
     [pairs]; None: not rotated).  ``q`` [tokens, heads, d] is rotated beside them and
     returned (``q_out`` may be given, and may be ``q``).  seq_lens [batch] counts each sequence's
     tokens with the new ones; q_starts [batch + 1] gives each its range of tokens (None: equally
-    many each).  k, v and q may be columns of one projection's output."""
+    many each).  k, v and q may be columns of one projection's output.
+
+    A cache in 8 bits (attn_append_paged_e4m3) has pages of torch.float8_e4m3fn and an exponent byte for
+    each row in ``k_scales`` and ``v_scales`` [num_pages, kv_heads, page_size] (uint8 or
+    float8_e8m0fnu): a row stands for its numbers times 2 ** (byte - 127), and is quantised, with the
+    smallest exponent at which nothing saturates, as it is written."""
     load_library()
     pos_offset = _int32("pos_offset", pos_offset)
     key = (0, _meta(k), _meta(v), _meta(k_pages), _meta(v_pages), _meta(page_table), _meta(seq_lens),
            _meta(q_starts), _meta(q), _meta(q_out), _meta(inv_freq), _meta(ws))
+    if k_scales is not None or v_scales is not None:
+        key += (_meta(k_scales), _meta(v_scales))
     known = _paged_known.get(key)
     if known is None:
         lead = k if q is None else q
-        shape = _check_paged(lead, k_pages, v_pages, page_table, seq_lens, q_starts, ws)
+        shape = _check_paged(lead, k_pages, v_pages, page_table, seq_lens, q_starts, ws, k_scales, v_scales)
         for name, t in (("k", k), ("v", v), ("q_out", q_out)):
             if t is not None and (t.dtype != lead.dtype or t.device != lead.device):
                 raise ValueError(f"{name} must be {lead.dtype} on {lead.device}")
@@ -557,20 +595,22 @@ def append_paged(k, v, k_pages, v_pages, page_table, seq_lens, q_starts=None, q=
          v_pages.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
          0 if q_starts is None else q_starts.data_ptr(), 0, inv_freq.data_ptr() if pairs else 0,
          0 if q is None else q_out.data_ptr(), 0, ws.data_ptr(), ws.nbytes),
-        (0.0, 0, 0, pos_offset, pairs, 1 if interleaved else 0)))
+        (0.0, 0, 0, pos_offset, pairs, 1 if interleaved else 0)), k_scales, v_scales)
     return q_out
 
 
 def _attend_paged(op, name, q, k_pages, v_pages, prefix_table, prefix_len, page_table, seq_lens, scale,
-                  mask, window, q_starts, y, L, ws, stream):
+                  mask, window, q_starts, y, L, ws, stream, k_scales, v_scales):
     load_library()
     window = _int32("window", window)
     prefix_len = _int32("prefix_len", prefix_len)
     key = (op, _meta(q), _meta(k_pages), _meta(v_pages), _meta(page_table), _meta(seq_lens),
            _meta(q_starts), _meta(prefix_table), _meta(y), _meta(L), _meta(ws))
+    if k_scales is not None or v_scales is not None:
+        key += (_meta(k_scales), _meta(v_scales))
     known = _paged_known.get(key)
     if known is None:
-        shape = _check_paged(q, k_pages, v_pages, page_table, seq_lens, q_starts, ws)
+        shape = _check_paged(q, k_pages, v_pages, page_table, seq_lens, q_starts, ws, k_scales, v_scales)
         shape.q_stride = _token_stride("q", q, shape.heads, shape.d)
         if op == 2 and (prefix_table.dtype != torch.int32 or prefix_table.dim() != 1
                         or not prefix_table.is_contiguous() or prefix_table.device != q.device):
@@ -593,25 +633,27 @@ def _attend_paged(op, name, q, k_pages, v_pages, prefix_table, prefix_len, page_
          seq_lens.data_ptr(), 0 if q_starts is None else q_starts.data_ptr(),
          0 if prefix_table is None else prefix_table.data_ptr(), 0, y.data_ptr(), L.data_ptr(),
          ws.data_ptr(), ws.nbytes),
-        (float(scale), _mask_kind(mask), window, prefix_len, 0, 0)))
+        (float(scale), _mask_kind(mask), window, prefix_len, 0, 0)), k_scales, v_scales)
     return y, L
 
 
 def fwd_paged(q, k_pages, v_pages, page_table, seq_lens, scale, mask="none", window=0, q_starts=None,
-              y=None, L=None, ws=None, stream=None):
+              y=None, L=None, ws=None, stream=None, k_scales=None, v_scales=None):
     """attn_fwd_paged -> (Y [tokens, heads, v], L [tokens, heads]): q [tokens, heads, d] over the
-    cached keys of each token's sequence (see append_paged for the tables)."""
+    cached keys of each token's sequence (see append_paged for the tables, and for pages in 8 bits
+    and their ``k_scales`` and ``v_scales``)."""
     return _attend_paged(1, "attn_fwd_paged", q, k_pages, v_pages, None, 0, page_table, seq_lens, scale,
-                         mask, window, q_starts, y, L, ws, stream)
+                         mask, window, q_starts, y, L, ws, stream, k_scales, v_scales)
 
 
 def fwd_prefix(q, k_pages, v_pages, prefix_table, prefix_len, page_table, seq_lens, scale,
-               mask="none", q_starts=None, y=None, L=None, ws=None, stream=None):
+               mask="none", q_starts=None, y=None, L=None, ws=None, stream=None, k_scales=None,
+               v_scales=None):
     """attn_fwd_prefix -> (Y, L): fwd_paged for sequences that all begin with the
     ``prefix_len`` keys of the pages ``prefix_table`` (int32 [pages]), which are read once for all of
     them; page_table and seq_lens describe each sequence's own keys behind the prefix."""
     return _attend_paged(2, "attn_fwd_prefix", q, k_pages, v_pages, prefix_table, prefix_len, page_table,
-                         seq_lens, scale, mask, 0, q_starts, y, L, ws, stream)
+                         seq_lens, scale, mask, 0, q_starts, y, L, ws, stream, k_scales, v_scales)
 
 
 def bwd_noalloc(q, k, v, y, dy, L, scale, mask="none", window=0, bitmask=None, dq=None,

@@ -272,7 +272,284 @@ cudaError_t append_dispatch(const AppendArgs& a, cudaStream_t s) {
   return append_launch<T, 1, false>(a, s);
 }
 
+// ------------------------------------------------------------------ pages in 8 bits
+//
+// A row y of w columns (rotated or not) becomes an exponent byte b, the smallest from 1 on with
+// max |y| <= 448 * 2^(b - 127), and RN_e4m3(y * 2^(127 - b)): the scaling is exact.  kLanes lanes
+// hold a row, 16 columns each, so that its maximum is three or four shuffles away and nothing is
+// read twice.
+//
+// A rotated entry's fp32 value is off by some 2^-22 of the pair's length (sine and cosine by 2^-23.5,
+// products and sum by 2^-24 each), so its rounding to 4 bits is settled unless a border lies that
+// near: once in 2^16 entries.  Such entries are computed again in 64 bits (FP64 does two operations
+// a clock and SM: a pair costs a warp half a microsecond), and so are all of a row whose
+// maximum lies that near to 448 times a power of two.  The codes are those of 64-bit arithmetic.
+constexpr float kTurnError = 4e-7f;  // > 2^-22 sqrt(2), of |y0| + |y1|
+
+// Where the pairs of a row are: halves that 8-column accesses reach, neighbours, or anywhere.
+enum PairForm { kHalves, kInside, kAnywhere };
+
+// Entry c of a row, rotated in 64 bits.
+template <typename T>
+__device__ __noinline__ double turned64(const T* row, int c, int pairs, bool inside, long long pos,
+                                        const float* inv_freq) {
+  if (c >= 2 * pairs) return as_float(row[c]);
+  const int f = inside ? c >> 1 : c < pairs ? c : c - pairs;
+  const bool first = inside ? !(c & 1) : c < pairs;
+  const int other = inside ? c ^ 1 : first ? c + pairs : f;
+  double s, k;
+  sincos(static_cast<double>(pos) * static_cast<double>(__ldg(inv_freq + f)), &s, &k);
+  const double x = as_float(row[c]), y = as_float(row[other]);
+  return first ? x * k - y * s : x * k + y * s;
+}
+
+// (a, b) rounded to e4m3, a in the low byte; magnitudes up to 448, NaN stays.
+__device__ __forceinline__ uint32_t e4m3_of(float a, float b) {
+  uint16_t y;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(b), "f"(a));
+  return y;
+}
+__device__ __forceinline__ uint32_t e4m3_of(double z) {
+  float f = __double2float_rz(z);  // to odd, so that the second rounding is the only one
+  if (static_cast<double>(f) != z) f = __uint_as_float(__float_as_uint(f) | 1u);
+  return e4m3_of(f, 0.f) & 0xFFu;
+}
+
+// The exponent byte of a row whose largest magnitude has these fp32 bits.  448 is 1.75 * 2^8.
+__device__ __forceinline__ int exponent_of(unsigned top) {
+  return top == 0u ? 0 : max(1, static_cast<int>((top + 0x1FFFFFu) >> 23) - 8);
+}
+__device__ __forceinline__ int exponent_of(unsigned long long top) {
+  return top == 0ull ? 0 : max(1, static_cast<int>((top + 0x3FFFFFFFFFFFFull) >> 52) - 1023 + 127 - 8);
+}
+
+__device__ __forceinline__ void load8(const float* p, float* x) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float* x) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
+  Piece<__nv_bfloat16, 8> y;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) from_float(y.x[e], x[e]);
+  *reinterpret_cast<Piece<__nv_bfloat16, 8>*>(p) = y;
+}
+
+template <typename T, int kLanes, PairForm kForm>
+__global__ void __launch_bounds__(kAppendThreads, 4) append_e4m3_kernel(const __grid_constant__ AppendArgs a) {
+  wait_for_previous();
+  let_next_start();
+  if (blockIdx.x == gridDim.x - 1) {
+    append_check(a);
+    return;
+  }
+  __shared__ __align__(32) float cs[kAppendWarps][kMaxPairs];
+  __shared__ __align__(32) float sn[kAppendWarps][kMaxPairs];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int job = blockIdx.x * kAppendWarps + warp;
+  const int t = div_by(job, a.by_shares), share = job - t * a.by_shares.d;
+  if (t >= a.T) return;
+  const int b = owner(a, t);
+  if (b < 0) return;  // behind the last sequence
+  int s0 = b * a.each, nq = a.each;
+  if (a.starts) {  // clamped, as the attention does
+    s0 = max(__ldg(a.starts + b), 0);
+    nq = min(__ldg(a.starts + b + 1), a.T) - s0;
+  }
+  const int pos = max(__ldg(a.lens + b), 0) - nq + (t - s0);
+  long long slot = -1;  // the token's row of the pool (of key head 0); -1: nowhere
+  if (pos >= 0 && pos < a.max_pages << a.lps) {
+    const int page = __ldg(a.table + static_cast<size_t>(b) * a.max_pages + (pos >> a.lps));
+    if (static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages))
+      slot = (static_cast<long long>(page) * a.Hk << a.lps) + (pos & ((1 << a.lps) - 1));
+  }
+  const long long at = static_cast<long long>(pos) + a.pos_offset;
+  for (int f = lane; f < a.pairs; f += 32) angle(at, __ldg(a.inv_freq + f), sn[warp][f], cs[warp][f]);
+  __syncwarp();
+
+  constexpr int kPass = 32 / kLanes;  // rows of a pass
+  const int sub = lane / kLanes, u = lane % kLanes, pairs = a.pairs;
+  const int q_rows = a.q ? a.H : 0, rows = q_rows + (slot < 0 ? 0 : 2 * a.Hk);
+  const T* qsrc = static_cast<const T*>(a.q) + t * a.qs;
+  const T* ksrc = static_cast<const T*>(a.k) + t * a.ks;
+  const T* vsrc = static_cast<const T*>(a.v) + t * a.vs;
+  T* qdst = static_cast<T*>(a.q_out) + static_cast<size_t>(t) * a.H * a.d;
+#pragma unroll 1
+  for (int r0 = share * kPass; r0 < rows; r0 += kPass * a.by_shares.d) {
+    const int r = min(r0 + sub, rows - 1);
+    const bool is_q = r < q_rows, is_v = r >= q_rows + a.Hk;
+    const int h = is_q ? r : is_v ? r - q_rows - a.Hk : r - q_rows, w = is_v ? a.vw : a.d;
+    const bool on = r0 + sub < rows && 16 * u < w;
+    const T* src = is_q ? qsrc + h * a.d : is_v ? vsrc + h * a.vw : ksrc + h * a.d;
+    // The lane's columns: eight from c0 on, eight from c1 on.
+    int c0 = 16 * u, c1 = c0 + 8;
+    if (kForm == kHalves && !is_v && pairs > 0) {
+      const int half = pairs >> 3;
+      c0 = u < half ? 8 * u : 2 * pairs + 16 * (u - half);
+      c1 = u < half ? pairs + 8 * u : c0 + 8;
+    }
+    float y[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) y[e] = 0.f;
+    if (on) {
+      load8(src + c0, y);
+      load8(src + c1, y + 8);
+    }
+    float reach[kForm == kAnywhere ? 16 : 8];  // of the entries' errors
+#pragma unroll
+    for (int e = 0; e < (kForm == kAnywhere ? 16 : 8); ++e) reach[e] = 0.f;
+    const bool turned = on && !is_v && (kForm == kHalves ? 8 * u < pairs : kForm == kInside ? 8 * u < pairs : c0 < 2 * pairs);
+    if (turned) {
+      if constexpr (kForm == kAnywhere) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int c = c0 + e;
+          if (c >= 2 * pairs) continue;
+          const bool first = c < pairs;
+          const int f = first ? c : c - pairs;
+          const float other = as_float(src[first ? c + pairs : f]), k = cs[warp][f], s = sn[warp][f];
+          reach[e] = fabsf(y[e]) + fabsf(other);
+          y[e] = first ? y[e] * k - other * s : y[e] * k + other * s;
+        }
+      } else {
+        float k[8], s[8];
+        load8(&cs[warp][8 * u], k);
+        load8(&sn[warp][8 * u], s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (kForm == kInside && 8 * u + e >= pairs) continue;
+          float& p = y[kForm == kInside ? 2 * e : e];
+          float& n = y[kForm == kInside ? 2 * e + 1 : 8 + e];
+          const float x0 = p, x1 = n;
+          p = x0 * k[e] - x1 * s[e];
+          n = x1 * k[e] + x0 * s[e];
+          reach[e] = fabsf(p) + fabsf(n);
+        }
+      }
+    }
+    if (is_q && on) {
+      T* dst = qdst + h * a.d;
+      store8(dst + c0, y);
+      store8(dst + c1, y + 8);
+    }
+    // Every lane of a row's, also those without columns.
+    unsigned top = 0u;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const unsigned m = __float_as_uint(y[e]) & 0x7FFFFFFFu;
+      top = max(top, m < 0x7F800000u ? m : 0u);
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    int ex = exponent_of(top);
+    uint32_t again = 0u;  // entries to be computed again
+    if (__any_sync(0xFFFFFFFFu, !is_q && !is_v && pairs > 0 && top > 8u && exponent_of(top - 8u) != exponent_of(top + 8u))) {
+      unsigned long long most = 0ull;
+      const bool mine = !is_q && !is_v && pairs > 0 && top > 8u && exponent_of(top - 8u) != exponent_of(top + 8u);
+      if (mine && on)
+#pragma unroll 1
+        for (int e = 0; e < 16; ++e) {
+          const double z = turned64(src, (e < 8 ? c0 : c1 - 8) + e, pairs, kForm == kInside, at, a.inv_freq);
+          const unsigned long long m = static_cast<unsigned long long>(__double_as_longlong(fabs(z)));
+          if (m < 0x7FF0000000000000ull) most = max(most, m);
+        }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+      if (mine) {
+        ex = exponent_of(most);
+        again = turned ? 0xFFFFu : 0u;
+      }
+    }
+    if (is_q || !on) continue;
+    const float inv = __uint_as_float(static_cast<unsigned>(254 - max(ex, 1)) << 23);
+    uint32_t code[4];
+    auto pack = [&](int i, float d0, float d1) {  // entries 2 i and 2 i + 1, moved by d0, d1
+      float z[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) z[k] = fmaf(y[2 * i + k], inv, y[2 * i + k] * 0.f + (k ? d1 : d0));  // infinity: NaN
+      return e4m3_of(z[0], z[1]);
+    };
+    if (turned) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e0 = kForm == kAnywhere ? 2 * i : kForm == kInside ? i : 2 * i & 7;
+        const int e1 = kForm == kAnywhere ? 2 * i + 1 : kForm == kInside ? i : (2 * i + 1) & 7;
+        // 2^-22: of subnormal numbers' own spacing
+        const float d0 = reach[e0] > 0.f ? fmaf(reach[e0] * inv, kTurnError, 0x1p-22f) : 0.f;
+        const float d1 = reach[e1] > 0.f ? fmaf(reach[e1] * inv, kTurnError, 0x1p-22f) : 0.f;
+        const uint32_t up = pack(i, d0, d1), diff = up ^ pack(i, -d0, -d1);
+        if (diff & 0xFFu) again |= 1u << 2 * i;
+        if (diff & 0xFF00u) again |= 2u << 2 * i;
+        if (i & 1) code[i >> 1] |= up << 16;
+        else code[i >> 1] = up;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) code[i] = pack(2 * i, 0.f, 0.f) | pack(2 * i + 1, 0.f, 0.f) << 16;
+    }
+#pragma unroll 1
+    for (; again; again &= again - 1) {
+      const int e = __ffs(again) - 1;
+      const double z = turned64(src, (e < 8 ? c0 : c1 - 8) + e, pairs, kForm == kInside, at, a.inv_freq);
+      const uint32_t x = e4m3_of(z * static_cast<double>(inv)) << 8 * (e & 3), keep = ~(0xFFu << 8 * (e & 3));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e >> 2 == i) code[i] = (code[i] & keep) | x;
+    }
+    const long long row = slot + (static_cast<long long>(h) << a.lps);
+    uint8_t* dst = static_cast<uint8_t*>(is_v ? a.vp : a.kp) + row * w;
+    if (c1 == c0 + 8) {
+      *reinterpret_cast<uint4*>(dst + c0) = make_uint4(code[0], code[1], code[2], code[3]);
+    } else {
+      *reinterpret_cast<uint2*>(dst + c0) = make_uint2(code[0], code[1]);
+      *reinterpret_cast<uint2*>(dst + c1) = make_uint2(code[2], code[3]);
+    }
+    if (u == 0) (is_v ? a.v_scales : a.k_scales)[row] = static_cast<uint8_t>(ex);
+  }
+}
+
+template <typename T, int kLanes, PairForm kForm>
+cudaError_t append_e4m3_launch(AppendArgs a, cudaStream_t s) {
+  a.each = a.T / a.B;
+  int shares = 1;
+  while (shares < kAppendWarps && (long long)a.T * shares * 2 <= 152 * 16 && shares < 2 * a.Hk) shares *= 2;
+  a.by_shares = fast_div(shares);
+  const unsigned ctas = (static_cast<unsigned>(a.T) * shares + kAppendWarps - 1) / kAppendWarps;
+  before_launch(kKernAppend, s);
+  const cudaError_t e = launch_early(append_e4m3_kernel<T, kLanes, kForm>, dim3(ctas + 1), kAppendThreads, 0, s, a);
+  after_launch(kKernAppend, s);
+  return e;
+}
+
+template <typename T, int kLanes>
+cudaError_t append_e4m3_form(const AppendArgs& a, cudaStream_t s) {
+  if (a.interleaved) return append_e4m3_launch<T, kLanes, kInside>(a, s);
+  if (a.pairs % 8 == 0) return append_e4m3_launch<T, kLanes, kHalves>(a, s);
+  return append_e4m3_launch<T, kLanes, kAnywhere>(a, s);
+}
+
+template <typename T>
+cudaError_t append_e4m3_dispatch(const AppendArgs& a, cudaStream_t s) {
+  return a.d <= 128 && a.vw <= 128 ? append_e4m3_form<T, 8>(a, s) : append_e4m3_form<T, 16>(a, s);
+}
+
 }  // namespace
+
+cudaError_t launch_append_e4m3(const AppendArgs& a, cudaStream_t s) {
+  return a.dtype == kF32 ? append_e4m3_dispatch<float>(a, s) : append_e4m3_dispatch<__nv_bfloat16>(a, s);
+}
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
   return a.dtype == kF32 ? append_dispatch<float>(a, s) : append_dispatch<__nv_bfloat16>(a, s);

@@ -14,6 +14,10 @@
 // shuffles of a group.  Heads of 256 columns, 537 MB of keys and values: one row 97 us in bf16
 // (5.5 TB/s), 84 in fp32 (6.4), four rows 246 in bf16.  One row of 128 columns: 333 us for 2.1
 // GB against the tensor cores' 325, which take eight rows in that time.
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace exattn {
@@ -54,6 +58,23 @@ template <> struct Row16<__nv_bfloat16> {
   }
 };
 
+template <> struct Row16<E4m3> {
+  static constexpr int E = 16;
+  __device__ static void unpack(const uint4& r, float (&f)[16]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t h[2] = {e4m3_pair(w[i]), e4m3_pair_high(w[i])};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+        f[4 * i + 2 * k] = x.x;
+        f[4 * i + 2 * k + 1] = x.y;
+      }
+    }
+  }
+};
+
 __device__ __forceinline__ uint4 ldg_once16(const void* p) {
   uint4 r;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -62,9 +83,11 @@ __device__ __forceinline__ uint4 ldg_once16(const void* p) {
   return r;
 }
 
-template <typename T, int G, int CPL, int NQ>
+// T: queries and outputs, C: pages.  e4m3: a row's exponent multiplies its score and its probability.
+template <typename T, typename C, int G, int CPL, int NQ>
 __global__ void __launch_bounds__(32 * kW, kCtas<NQ>) paged_simt_kernel(const PagedArgs a) {
-  constexpr int E = Row16<T>::E;
+  constexpr int E = Row16<C>::E, EQ = Row16<T>::E;
+  constexpr bool kScaled = std::is_same<C, E4m3>::value;
   constexpr int KPW = 32 / G;
   constexpr int U = (NQ == 1 ? 8 : 4) / CPL;  // key steps in flight
   constexpr int STEP = KPW * U;
@@ -78,8 +101,8 @@ __global__ void __launch_bounds__(32 * kW, kCtas<NQ>) paged_simt_kernel(const Pa
   const int d = a.d, v = a.v;
   const int kch = d / E, vch = v / E;
   const T* Q = static_cast<const T*>(a.Q);
-  const T* Kp = static_cast<const T*>(a.Kp);
-  const T* Vp = static_cast<const T*>(a.Vp);
+  const C* Kp = static_cast<const C*>(a.Kp);
+  const C* Vp = static_cast<const C*>(a.Vp);
   unsigned bits = 0;
   __shared__ unsigned joined;
   if (!a.second) wait_for_previous();
@@ -111,7 +134,13 @@ __global__ void __launch_bounds__(32 * kW, kCtas<NQ>) paged_simt_kernel(const Pa
         const int pc = gl + c * G;
         float f[E];
         if (pc < kch) {
-          Row16<T>::unpack(*reinterpret_cast<const uint4*>(qr + pc * E), f);
+#pragma unroll
+          for (int y = 0; y < E; y += EQ) {
+            float part[EQ];
+            Row16<T>::unpack(*reinterpret_cast<const uint4*>(qr + pc * E + y), part);
+#pragma unroll
+            for (int e = 0; e < EQ; ++e) f[y + e] = part[e];
+          }
         } else {
 #pragma unroll
           for (int e = 0; e < E; ++e) f[e] = 0.f;
@@ -131,6 +160,7 @@ __global__ void __launch_bounds__(32 * kW, kCtas<NQ>) paged_simt_kernel(const Pa
 
     for (int jb = j0 + warp * STEP; jb < j1; jb += kW * STEP) {
       uint4 kr[U][CPL], vr[U][CPL];
+      [[maybe_unused]] float ks[U], vs[U];
       bool have[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -141,6 +171,10 @@ __global__ void __launch_bounds__(32 * kW, kCtas<NQ>) paged_simt_kernel(const Pa
           if (row < 0) bits |= kStatusBadPage;
         }
         have[u] = row >= 0;
+        if constexpr (kScaled) {
+          ks[u] = have[u] ? e4m3_scale(__ldg(a.Ks + row)) : 0.f;
+          vs[u] = have[u] ? e4m3_scale(__ldg(a.Vs + row)) : 0.f;
+        }
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
           const int pc = gl + c * G;
@@ -159,7 +193,7 @@ __global__ void __launch_bounds__(32 * kW, kCtas<NQ>) paged_simt_kernel(const Pa
 #pragma unroll
           for (int c = 0; c < CPL; ++c) {
             float f[E];
-            Row16<T>::unpack(kr[u][c], f);
+            Row16<C>::unpack(kr[u][c], f);
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
               acc0 = fmaf(qf[q][c * E + e], f[e], acc0);
@@ -169,6 +203,7 @@ __global__ void __launch_bounds__(32 * kW, kCtas<NQ>) paged_simt_kernel(const Pa
           float part = acc0 + acc1;
 #pragma unroll
           for (int o = G / 2; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
+          if constexpr (kScaled) part *= ks[u];
           const int key = jb + u * KPW + g;
           ok[u] = have[u] && key >= lo[q] && key < hi[q];
           s[u] = ok[u] ? part : -INFINITY;
@@ -186,12 +221,14 @@ __global__ void __launch_bounds__(32 * kW, kCtas<NQ>) paged_simt_kernel(const Pa
           const float p = pexp2(s[u] - ref);
           psum += p;
           if (ok[u]) {  // a key that this row does not allow leaves no trace, whatever its value
+            float pv = p;
+            if constexpr (kScaled) pv *= vs[u];
 #pragma unroll
             for (int c = 0; c < CPL; ++c) {
               float f[E];
-              Row16<T>::unpack(vr[u][c], f);
+              Row16<C>::unpack(vr[u][c], f);
 #pragma unroll
-              for (int e = 0; e < E; ++e) z[q][c * E + e] = fmaf(p, f[e], z[q][c * E + e]);
+              for (int e = 0; e < E; ++e) z[q][c * E + e] = fmaf(pv, f[e], z[q][c * E + e]);
             }
           }
         }
@@ -583,9 +620,9 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 32 * kJoinRows)
   }
 }
 
-template <typename T, int G, int CPL>
+template <typename T, int G, int CPL, typename C = T>
 cudaError_t simt_launch(const PagedArgs& a, bool one_row, cudaStream_t s) {
-  auto kern = one_row ? paged_simt_kernel<T, G, CPL, 1> : paged_simt_kernel<T, G, CPL, 4>;
+  auto kern = one_row ? paged_simt_kernel<T, C, G, CPL, 1> : paged_simt_kernel<T, C, G, CPL, 4>;
   before_launch(kKernPaged, s);
   const cudaError_t e = launch_early(kern, dim3(a.runs), 32 * kW, 0, s, a);
   after_launch(kKernPaged, s);
@@ -600,6 +637,13 @@ PagedKernel paged_simt_kernel(bool one_row) {
 }
 
 cudaError_t launch_paged_simt(const PagedArgs& a, bool one_row, cudaStream_t s) {
+  if (a.Ks) {
+    const bool narrow = a.d <= 128 && a.v <= 128;
+    if (a.dtype == kF32)
+      return narrow ? simt_launch<float, 8, 1, E4m3>(a, one_row, s) : simt_launch<float, 16, 1, E4m3>(a, one_row, s);
+    return narrow ? simt_launch<__nv_bfloat16, 8, 1, E4m3>(a, one_row, s)
+                  : simt_launch<__nv_bfloat16, 16, 1, E4m3>(a, one_row, s);
+  }
   const int bytes = (a.d > a.v ? a.d : a.v) * (a.dtype == kF32 ? 4 : 2);
   if (a.dtype == kF32) {
     if (bytes <= 128) return simt_launch<float, 8, 1>(a, one_row, s);

@@ -99,7 +99,27 @@ struct PagedArgs {
   int runs;   // and workers
   int least;  // units that a row tile's (and a short run's) are a multiple of (a power of 2)
   bool second;  // launched early behind another attention launch, independent of it
+  // Pages in 8 bits: the exponent byte of each row of the pools (null: pages hold dtype).
+  const uint8_t* Ks;
+  const uint8_t* Vs;
 };
+
+// e4m3 numbers and their rows' exponent bytes.  Byte b stands for 2^(b - 127); 0 for 0.
+struct E4m3 {
+  uint8_t bits;
+};
+__device__ __forceinline__ float e4m3_scale(uint32_t b) { return __uint_as_float(b << 23); }
+// The two low bytes of x as fp16, exactly.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t x) {
+  uint32_t y;
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l; }" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t e4m3_pair_high(uint32_t x) {
+  uint32_t y;
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(y) : "r"(x));
+  return y;
+}
 
 struct PagedSeq {
   int s0, nq, len;
@@ -593,11 +613,14 @@ struct AppendArgs {
   void* kp;
   void* vp;
   unsigned* status;
+  uint8_t* k_scales;  // pages in 8 bits: the rows' exponent bytes (null: pages hold dtype)
+  uint8_t* v_scales;
   // Set by the launcher: units of a row of q or k, accesses of a row of v, warps that
   // share a token; T / B.
   FastDiv by_units, by_vch, by_shares;
   int each;
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_append_e4m3(const AppendArgs& a, cudaStream_t s);
 
 }  // namespace exattn

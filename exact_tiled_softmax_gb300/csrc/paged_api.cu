@@ -56,6 +56,27 @@ int check_paged(const exattn_paged_shape* s) {
   return EXATTN_OK;
 }
 
+// Pages in 8 bits: rows of whole 16-byte pieces too.
+int check_paged_e4m3(const exattn_paged_shape* s) {
+  const int st = check_paged(s);
+  return st == EXATTN_OK && (s->d % 16 != 0 || s->v % 16 != 0) ? EXATTN_UNSUPPORTED : st;
+}
+
+// The pages of a call, and their rows' exponent bytes where they are in 8 bits.
+struct Pages {
+  const void* k;
+  const void* v;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  bool e4m3;
+};
+int check_shape(const exattn_paged_shape* s, const Pages& p) { return p.e4m3 ? check_paged_e4m3(s) : check_paged(s); }
+int check_scales(const Pages& p) {
+  if (!p.e4m3) return EXATTN_OK;
+  if (!p.k_scales || !p.v_scales) return EXATTN_INVALID_ARG;
+  return aligned(p.k_scales, 16) && aligned(p.v_scales, 16) ? EXATTN_OK : EXATTN_MISALIGNED;
+}
+
 // The kernel of a call.
 enum Kind { kSimtOne, kSimt, kMma8, kMma16, kTc };
 
@@ -82,7 +103,7 @@ constexpr int kTcRows = 16;
 
 Choice choose(const PagedArgs& a) {
   Choice c;
-  if (current_path() != EXATTN_PATH_SIMT && paged_mma_shape(a.d, a.v))
+  if (current_path() != EXATTN_PATH_SIMT && paged_mma_shape(a.d, a.v) && !a.Ks)
     c.kind = rows_of(a) > kTcRows && paged_tc_supported(a) ? kTc : rows_of(a) > 8 ? kMma16 : kMma8;
   else c.kind = !a.starts && a.T == a.B && a.G == 1 ? kSimtOne : kSimt;
   c.k = kernel_of(c.kind, a.dtype, a.d, a.v);
@@ -147,13 +168,16 @@ void place_pass(PagedArgs& a, const PagedKernel& k, char* at) {
   a.pz = reinterpret_cast<float*>(at);
 }
 
-PagedArgs make_args(const exattn_paged_shape* s, const void* Q, const void* Kp, const void* Vp,
-                    const int* table, const int* lens, const int* starts, float scale, int mask_kind,
-                    int window, void* Y, float* L) {
+PagedArgs make_args(const exattn_paged_shape* s, const void* Q, const Pages& pages, const int* table,
+                    const int* lens, const int* starts, float scale, int mask_kind, int window, void* Y, float* L) {
   PagedArgs a{};
   a.Q = Q;
-  a.Kp = Kp;
-  a.Vp = Vp;
+  a.Kp = pages.k;
+  a.Vp = pages.v;
+  if (pages.e4m3) {
+    a.Ks = pages.k_scales;
+    a.Vs = pages.v_scales;
+  }
   a.table = table;
   a.lens = lens;
   a.starts = starts;
@@ -206,27 +230,12 @@ int check_call(const exattn_paged_shape* shape, const void* Q, const void* Kp, c
   return EXATTN_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t exattn_paged_workspace_size(const exattn_paged_shape* shape) {
-  if (check_paged(shape) != EXATTN_OK) return 0;
-  return kStatusBytes + kFlagBytes + most_bytes(shape);
-}
-
-size_t exattn_prefix_workspace_size(const exattn_paged_shape* shape) {
-  if (check_paged(shape) != EXATTN_OK) return 0;
-  const size_t rows = (size_t)shape->tokens * shape->heads;
-  return kStatusBytes + kFlagBytes + 2 * most_bytes(shape) + join_bytes(rows, shape->v);
-}
-
-int attn_append_paged(const exattn_paged_shape* shape, const void* q, const void* k, const void* v,
-                      const int* page_table, const int* seq_lens, const int* q_starts,
-                      const float* inv_freq, int rot_pairs, int interleaved, int pos_offset,
-                      void* q_out, void* k_pages, void* v_pages, void* workspace,
-                      size_t workspace_bytes, void* cuda_stream) {
-  const int st = check_paged(shape);
+int append(const exattn_paged_shape* shape, const void* q, const void* k, const void* v, const int* page_table,
+           const int* seq_lens, const int* q_starts, const float* inv_freq, int rot_pairs, int interleaved,
+           int pos_offset, void* q_out, void* k_pages, void* v_pages, uint8_t* k_scales, uint8_t* v_scales, bool e4m3,
+           void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  const Pages pages{k_pages, v_pages, k_scales, v_scales, e4m3};
+  int st = check_shape(shape, pages);
   if (st != EXATTN_OK) return st;
   if (!k || !v || !page_table || !seq_lens || !k_pages || !v_pages || !workspace || (q && !q_out) ||
       (rot_pairs > 0 && !inv_freq) || rot_pairs < 0 || 2 * (long long)rot_pairs > shape->d ||
@@ -237,6 +246,8 @@ int attn_append_paged(const exattn_paged_shape* shape, const void* q, const void
       !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(page_table, 4) ||
       !aligned(seq_lens, 4) || !aligned(q_starts, 4) || !aligned(inv_freq, 4) || !aligned(workspace, 256))
     return EXATTN_MISALIGNED;
+  st = check_scales(pages);
+  if (st != EXATTN_OK) return st;
   if (workspace_bytes < kStatusBytes) return EXATTN_WORKSPACE_TOO_SMALL;
   g_last_error[0] = 0;
   AppendArgs a{};
@@ -267,23 +278,26 @@ int attn_append_paged(const exattn_paged_shape* shape, const void* q, const void
   a.kp = k_pages;
   a.vp = v_pages;
   a.status = static_cast<unsigned*>(workspace);
-  return cuda_result(launch_append(a, static_cast<cudaStream_t>(cuda_stream)),
-                     "attn_append_paged: launch");
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  return e4m3 ? cuda_result(launch_append_e4m3(a, s), "attn_append_paged_e4m3: launch")
+              : cuda_result(launch_append(a, s), "attn_append_paged: launch");
 }
 
-int attn_fwd_paged(const exattn_paged_shape* shape, const void* Q, const void* k_pages,
-                   const void* v_pages, const int* page_table, const int* seq_lens,
-                   const int* q_starts, float scale, int mask_kind, int window, void* Y, float* L,
-                   void* workspace, size_t workspace_bytes, void* cuda_stream) {
-  int st = check_paged(shape);
+int fwd_paged(const exattn_paged_shape* shape, const void* Q, const Pages& pages, const int* page_table,
+              const int* seq_lens, const int* q_starts, float scale, int mask_kind, int window, void* Y, float* L,
+              void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  int st = check_shape(shape, pages);
   if (st != EXATTN_OK) return st;
-  st = check_call(shape, Q, k_pages, v_pages, page_table, seq_lens, q_starts, mask_kind, window, Y, L,
+  st = check_call(shape, Q, pages.k, pages.v, page_table, seq_lens, q_starts, mask_kind, window, Y, L,
                   workspace);
+  if (st == EXATTN_OK) st = check_scales(pages);
   if (st != EXATTN_OK) return st;
   if (workspace_bytes < exattn_paged_workspace_size(shape)) return EXATTN_WORKSPACE_TOO_SMALL;
   g_last_error[0] = 0;
   char* ws = static_cast<char*>(workspace);
-  PagedArgs a = make_args(shape, Q, k_pages, v_pages, page_table, seq_lens, q_starts, scale, mask_kind,
+  PagedArgs a = make_args(shape, Q, pages, page_table, seq_lens, q_starts, scale, mask_kind,
                           window, Y, L);
   const Choice c = choose(a);
   a.status = static_cast<unsigned*>(workspace);
@@ -297,31 +311,30 @@ int attn_fwd_paged(const exattn_paged_shape* shape, const void* Q, const void* k
   return cuda_result(e, "attn_fwd_paged: launch");
 }
 
-int attn_fwd_prefix(const exattn_paged_shape* shape, const void* Q, const void* k_pages,
-                    const void* v_pages, const int* prefix_table, int prefix_len,
-                    const int* page_table, const int* seq_lens, const int* q_starts, float scale,
-                    int mask_kind, void* Y, float* L, void* workspace, size_t workspace_bytes,
-                    void* cuda_stream) {
-  int st = check_paged(shape);
+int fwd_prefix(const exattn_paged_shape* shape, const void* Q, const Pages& pages, const int* prefix_table,
+               int prefix_len, const int* page_table, const int* seq_lens, const int* q_starts, float scale,
+               int mask_kind, void* Y, float* L, void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  int st = check_shape(shape, pages);
   if (st != EXATTN_OK) return st;
   if (mask_kind == EXATTN_MASK_WINDOW) return EXATTN_UNSUPPORTED;
-  st = check_call(shape, Q, k_pages, v_pages, page_table, seq_lens, q_starts, mask_kind, 0, Y, L,
+  st = check_call(shape, Q, pages.k, pages.v, page_table, seq_lens, q_starts, mask_kind, 0, Y, L,
                   workspace);
+  if (st == EXATTN_OK) st = check_scales(pages);
   if (st != EXATTN_OK) return st;
   if (prefix_len < 0 || (prefix_len > 0 && !prefix_table)) return EXATTN_INVALID_ARG;
   if (prefix_len > kMaxKeys - kMaxPageSize) return EXATTN_UNSUPPORTED;
   if (!aligned(prefix_table, 4)) return EXATTN_MISALIGNED;
   if (workspace_bytes < exattn_prefix_workspace_size(shape)) return EXATTN_WORKSPACE_TOO_SMALL;
   if (prefix_len == 0)
-    return attn_fwd_paged(shape, Q, k_pages, v_pages, page_table, seq_lens, q_starts, scale, mask_kind,
-                          0, Y, L, workspace, workspace_bytes, cuda_stream);
+    return fwd_paged(shape, Q, pages, page_table, seq_lens, q_starts, scale, mask_kind, 0, Y, L, workspace,
+                     workspace_bytes, cuda_stream);
   g_last_error[0] = 0;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   char* ws = static_cast<char*>(workspace);
   const size_t rows = (size_t)shape->tokens * shape->heads;
   char* area = ws + kStatusBytes + kFlagBytes;
   char* sets = area + 2 * most_bytes(shape);
-  PagedArgs a = make_args(shape, Q, k_pages, v_pages, page_table, seq_lens, q_starts, scale, mask_kind, 0, Y, L);
+  PagedArgs a = make_args(shape, Q, pages, page_table, seq_lens, q_starts, scale, mask_kind, 0, Y, L);
   a.Yf = reinterpret_cast<float*>(sets);
   a.L = reinterpret_cast<float*>(sets + align256(sizeof(float) * 2 * rows * a.v));
   a.info = reinterpret_cast<int2*>(reinterpret_cast<char*>(a.L) + align256(sizeof(float) * 2 * rows));
@@ -375,6 +388,99 @@ int attn_fwd_prefix(const exattn_paged_shape* shape, const void* Q, const void* 
   a.status = static_cast<unsigned*>(workspace);
   a.n_flags = launches_ctas;
   return cuda_result(launch_paged_join(a, own.k.rt, p, of.k.rt, s), "attn_fwd_prefix: join launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t exattn_paged_workspace_size(const exattn_paged_shape* shape) {
+  if (check_paged(shape) != EXATTN_OK) return 0;
+  return kStatusBytes + kFlagBytes + most_bytes(shape);
+}
+
+size_t exattn_prefix_workspace_size(const exattn_paged_shape* shape) {
+  if (check_paged(shape) != EXATTN_OK) return 0;
+  const size_t rows = (size_t)shape->tokens * shape->heads;
+  return kStatusBytes + kFlagBytes + 2 * most_bytes(shape) + join_bytes(rows, shape->v);
+}
+
+int attn_append_paged(const exattn_paged_shape* shape, const void* q, const void* k, const void* v,
+                      const int* page_table, const int* seq_lens, const int* q_starts,
+                      const float* inv_freq, int rot_pairs, int interleaved, int pos_offset,
+                      void* q_out, void* k_pages, void* v_pages, void* workspace,
+                      size_t workspace_bytes, void* cuda_stream) {
+  return append(shape, q, k, v, page_table, seq_lens, q_starts, inv_freq, rot_pairs, interleaved, pos_offset,
+                q_out, k_pages, v_pages, nullptr, nullptr, false, workspace, workspace_bytes, cuda_stream);
+}
+
+int attn_fwd_paged(const exattn_paged_shape* shape, const void* Q, const void* k_pages,
+                   const void* v_pages, const int* page_table, const int* seq_lens,
+                   const int* q_starts, float scale, int mask_kind, int window, void* Y, float* L,
+                   void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  return fwd_paged(shape, Q, Pages{k_pages, v_pages, nullptr, nullptr, false}, page_table, seq_lens, q_starts,
+                   scale, mask_kind, window, Y, L, workspace, workspace_bytes, cuda_stream);
+}
+
+int attn_fwd_prefix(const exattn_paged_shape* shape, const void* Q, const void* k_pages,
+                    const void* v_pages, const int* prefix_table, int prefix_len,
+                    const int* page_table, const int* seq_lens, const int* q_starts, float scale,
+                    int mask_kind, void* Y, float* L, void* workspace, size_t workspace_bytes,
+                    void* cuda_stream) {
+  return fwd_prefix(shape, Q, Pages{k_pages, v_pages, nullptr, nullptr, false}, prefix_table, prefix_len,
+                    page_table, seq_lens, q_starts, scale, mask_kind, Y, L, workspace, workspace_bytes,
+                    cuda_stream);
+}
+
+int attn_append_paged_e4m3(const exattn_paged_shape* shape, const void* q, const void* k, const void* v,
+                           const int* page_table, const int* seq_lens, const int* q_starts,
+                           const float* inv_freq, int rot_pairs, int interleaved, int pos_offset,
+                           void* q_out, void* k_pages, void* v_pages, uint8_t* k_scales,
+                           uint8_t* v_scales, void* workspace, size_t workspace_bytes,
+                           void* cuda_stream) {
+  return append(shape, q, k, v, page_table, seq_lens, q_starts, inv_freq, rot_pairs, interleaved, pos_offset,
+                q_out, k_pages, v_pages, k_scales, v_scales, true, workspace, workspace_bytes, cuda_stream);
+}
+
+int attn_fwd_paged_e4m3(const exattn_paged_shape* shape, const void* Q, const void* k_pages,
+                        const void* v_pages, const uint8_t* k_scales, const uint8_t* v_scales,
+                        const int* page_table, const int* seq_lens, const int* q_starts, float scale,
+                        int mask_kind, int window, void* Y, float* L, void* workspace,
+                        size_t workspace_bytes, void* cuda_stream) {
+  return fwd_paged(shape, Q, Pages{k_pages, v_pages, k_scales, v_scales, true}, page_table, seq_lens, q_starts,
+                   scale, mask_kind, window, Y, L, workspace, workspace_bytes, cuda_stream);
+}
+
+int attn_fwd_prefix_e4m3(const exattn_paged_shape* shape, const void* Q, const void* k_pages,
+                         const void* v_pages, const uint8_t* k_scales, const uint8_t* v_scales,
+                         const int* prefix_table, int prefix_len, const int* page_table,
+                         const int* seq_lens, const int* q_starts, float scale, int mask_kind, void* Y,
+                         float* L, void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  return fwd_prefix(shape, Q, Pages{k_pages, v_pages, k_scales, v_scales, true}, prefix_table, prefix_len,
+                    page_table, seq_lens, q_starts, scale, mask_kind, Y, L, workspace, workspace_bytes,
+                    cuda_stream);
+}
+
+int exattn_paged_e4m3_run(int op, const exattn_paged_e4m3_call* call) {
+  if (!call) return EXATTN_INVALID_ARG;
+  const exattn_paged_call* c = &call->call;
+  switch (op) {
+    case EXATTN_PAGED_APPEND:
+      return attn_append_paged_e4m3(&c->shape, c->q, c->k, c->v, c->page_table, c->seq_lens, c->q_starts,
+                                    c->inv_freq, c->rot_pairs, c->interleaved, c->prefix_len, c->y, c->k_pages,
+                                    c->v_pages, call->k_scales, call->v_scales, c->workspace, c->workspace_bytes,
+                                    c->cuda_stream);
+    case EXATTN_PAGED_FWD:
+      return attn_fwd_paged_e4m3(&c->shape, c->q, c->k_pages, c->v_pages, call->k_scales, call->v_scales,
+                                 c->page_table, c->seq_lens, c->q_starts, c->scale, c->mask_kind, c->window, c->y,
+                                 c->L, c->workspace, c->workspace_bytes, c->cuda_stream);
+    case EXATTN_PAGED_PREFIX:
+      return attn_fwd_prefix_e4m3(&c->shape, c->q, c->k_pages, c->v_pages, call->k_scales, call->v_scales,
+                                  c->prefix_table, c->prefix_len, c->page_table, c->seq_lens, c->q_starts,
+                                  c->scale, c->mask_kind, c->y, c->L, c->workspace, c->workspace_bytes,
+                                  c->cuda_stream);
+    default: return EXATTN_INVALID_ARG;
+  }
 }
 
 int exattn_paged_run(int op, const exattn_paged_call* c) {

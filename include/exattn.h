@@ -487,6 +487,60 @@ typedef struct exattn_paged_call {
 enum exattn_paged_op { EXATTN_PAGED_APPEND = 0, EXATTN_PAGED_FWD = 1, EXATTN_PAGED_PREFIX = 2 };
 int exattn_paged_run(int op, const exattn_paged_call* call);
 
+/* ---------------------------------------------------------------------------
+ * The paged cache in 8 bits: the three operators over pages of e4m3 numbers, half
+ * the bytes of a bf16 cache.  Shapes, tables, packing, masks, limits, status word,
+ * workspaces (the same queries) and streams are those above, and `dtype` is that of
+ * q, k, v, Y; what differs:
+ *
+ * Pages.  k_pages [num_pages][kv_heads][page_size][d] and v_pages hold bytes: e4m3
+ * numbers (sign, 4 bits of exponent with bias 7, 3 of significand; 0x7F and 0xFF are NaN,
+ * no infinities, largest 448).  k_scales and v_scales [num_pages][kv_heads][page_size]
+ * hold an exponent byte for each row of the pages: a row with byte b stands for its
+ * numbers times 2^(b - 127), 1 <= b <= 254; b = 0 stands for a row of zeros.  255 is not
+ * a scale: rows that allow such a key are undefined.  The scale arrays are 16-byte
+ * aligned.  d and v are multiples of 16.
+ *
+ * Append.  b is the smallest from 1 on for which the row's largest finite magnitude is at
+ * most 448 * 2^(b - 127), so that nothing saturates and scaling is exact; 0 for a row
+ * without a nonzero finite entry.  Each entry is rounded once, to nearest, ties to even: off
+ * by 2^-4 of itself at most, or by 2^(b - 137) where that is more.  Infinities and NaN become
+ * NaN.  A rotated key is rounded, and its byte chosen, as if its rotation had been computed in
+ * 64 bits; q_out is rotated in fp32 as above.
+ *
+ * Attention.  Scores, statistics and outputs are summed in fp32.  Few rows to a key head (up
+ * to 16), or fp32 queries, with d, v <= 128, pages of 8 keys or more: operands are fp16 parts,
+ * each row of Q scaled by a power of two; bf16 queries are exact where they are no smaller than 2^-30 of their
+ * row's largest, fp32 queries are held to 2^-22 of themselves or 2^-38 of their row's largest,
+ * weights p 2^(b - 127) to 2^-11 (bf16) or 2^-22 (fp32) of themselves or 2^-32 of their row's
+ * largest.  More rows of bf16 queries: probabilities are rounded to bf16, as above.
+ * All other calls follow the formula in fp32.  Non-finite entries act as above.
+ * ------------------------------------------------------------------------- */
+int attn_append_paged_e4m3(const exattn_paged_shape* shape, const void* q, const void* k, const void* v,
+                           const int* page_table, const int* seq_lens, const int* q_starts,
+                           const float* inv_freq, int rot_pairs, int interleaved, int pos_offset,
+                           void* q_out, void* k_pages, void* v_pages, uint8_t* k_scales,
+                           uint8_t* v_scales, void* workspace, size_t workspace_bytes,
+                           void* cuda_stream);
+int attn_fwd_paged_e4m3(const exattn_paged_shape* shape, const void* Q, const void* k_pages,
+                        const void* v_pages, const uint8_t* k_scales, const uint8_t* v_scales,
+                        const int* page_table, const int* seq_lens, const int* q_starts, float scale,
+                        int mask_kind, int window, void* Y, float* L, void* workspace,
+                        size_t workspace_bytes, void* cuda_stream);
+int attn_fwd_prefix_e4m3(const exattn_paged_shape* shape, const void* Q, const void* k_pages,
+                         const void* v_pages, const uint8_t* k_scales, const uint8_t* v_scales,
+                         const int* prefix_table, int prefix_len, const int* page_table,
+                         const int* seq_lens, const int* q_starts, float scale, int mask_kind, void* Y,
+                         float* L, void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* The three with their arguments in one structure (`op` as for exattn_paged_run). */
+typedef struct exattn_paged_e4m3_call {
+  exattn_paged_call call;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+} exattn_paged_e4m3_call;
+int exattn_paged_e4m3_run(int op, const exattn_paged_e4m3_call* call);
+
 /* Waits for `cuda_stream`, then reads the status word of `workspace` (the
  * workspace of the last call queued on it).  Returns EXATTN_OK,
  * EXATTN_EMPTY_ROW, EXATTN_TIMEOUT, EXATTN_BAD_PAGE or EXATTN_CUDA_ERROR. */

@@ -80,14 +80,16 @@ int check_scales(const Pages& p) {
 // The kernel of a call.
 enum Kind { kSimtOne, kSimt, kMma8, kMma16, kTc };
 
-PagedKernel kernel_of(Kind k, int dtype, int d, int v) {
+PagedKernel kernel_of(Kind k, int dtype, int d, int v, bool e4m3) {
+  const int rows = k == kMma8 ? 8 : 16;
   switch (k) {
     case kTc: return paged_tc_kernel_of();
-    case kMma8: return paged_mma_kernel_of(dtype, d, v, 8);
-    case kMma16: return paged_mma_kernel_of(dtype, d, v, 16);
+    case kMma8:
+    case kMma16: return e4m3 ? paged_e4m3_kernel_of(dtype, d, v, rows) : paged_mma_kernel_of(dtype, d, v, rows);
     default: return paged_simt_kernel(k == kSimtOne);
   }
 }
+PagedKernel kernel_of(Kind k, const PagedArgs& a) { return kernel_of(k, a.dtype, a.d, a.v, a.Ks != nullptr); }
 
 struct Choice {
   Kind kind;
@@ -103,10 +105,10 @@ constexpr int kTcRows = 16;
 
 Choice choose(const PagedArgs& a) {
   Choice c;
-  if (current_path() != EXATTN_PATH_SIMT && paged_mma_shape(a.d, a.v) && !a.Ks)
+  if (current_path() != EXATTN_PATH_SIMT && (a.Ks ? paged_e4m3_shape(a.d, a.v, a.lps) : paged_mma_shape(a.d, a.v)))
     c.kind = rows_of(a) > kTcRows && paged_tc_supported(a) ? kTc : rows_of(a) > 8 ? kMma16 : kMma8;
   else c.kind = !a.starts && a.T == a.B && a.G == 1 ? kSimtOne : kSimt;
-  c.k = kernel_of(c.kind, a.dtype, a.d, a.v);
+  c.k = kernel_of(c.kind, a);
   return c;
 }
 
@@ -127,8 +129,10 @@ size_t most_bytes(const exattn_paged_shape* s) {
     if (k >= kMma8 && !paged_mma_shape(s->d, s->v)) continue;
     // A prefix's pass takes all tokens as one sequence's.
     if (k == kTc && (s->dtype != EXATTN_BF16 || (long long)s->tokens * (s->heads / s->kv_heads) <= kTcRows)) continue;
-    const size_t x = pass_bytes(kernel_of(k, s->dtype, s->d, s->v), s->v);
-    most = x > most ? x : most;
+    for (const bool e4m3 : {false, true}) {
+      const size_t x = pass_bytes(kernel_of(k, s->dtype, s->d, s->v, e4m3), s->v);
+      most = x > most ? x : most;
+    }
   }
   return most;
 }
@@ -211,9 +215,9 @@ int cuda_result(cudaError_t e, const char* where) {
 }
 
 cudaError_t run_kernel(const PagedArgs& a, const Choice& c, cudaStream_t s) {
-  return c.kind == kTc     ? launch_paged_tc(a, s)
-         : c.kind >= kMma8 ? launch_paged_mma(a, c.k.rt, s)
-                           : launch_paged_simt(a, c.kind == kSimtOne, s);
+  if (c.kind == kTc) return launch_paged_tc(a, s);
+  if (c.kind < kMma8) return launch_paged_simt(a, c.kind == kSimtOne, s);
+  return a.Ks ? launch_paged_e4m3(a, c.k.rt, s) : launch_paged_mma(a, c.k.rt, s);
 }
 
 int check_call(const exattn_paged_shape* shape, const void* Q, const void* Kp, const void* Vp,
@@ -358,7 +362,7 @@ int fwd_prefix(const exattn_paged_shape* shape, const void* Q, const Pages& page
     const double bytes = (double)prefix_len * a.Hk * (a.d + a.v) * 2, again = (double)((rows_of(p) + 15) / 16 - 1);
     if (again * bytes < 40e6) {
       of.kind = kMma16;
-      of.k = kernel_of(of.kind, a.dtype, a.d, a.v);
+      of.k = kernel_of(of.kind, a);
     }
   }
   const bool together = own.kind == of.kind || own.kind <= kSimt || (own.kind == kMma8 && of.kind == kMma16);

@@ -670,7 +670,7 @@ cudaError_t tc_launch(const PagedArgs& a, cudaStream_t s) {
 // Pages of at least 8 rows (a swizzle atom), pool rows within TMA's 32-bit
 // coordinates, a scale whose sign keeps the maximum a maximum.
 bool paged_tc_supported(const PagedArgs& a) {
-  return a.dtype == kBF16 && paged_mma_shape(a.d, a.v) && a.lps >= 3 && a.sl2 > 0.f &&
+  return a.dtype == kBF16 && !a.Ks && paged_mma_shape(a.d, a.v) && a.lps >= 3 && a.sl2 > 0.f &&
          ((static_cast<long long>(a.num_pages) * a.Hk) << a.lps) < (1ll << 31) && tmap_encoder() != nullptr;
 }
 PagedKernel paged_tc_kernel_of() { return {kRows, kCtas, kCtas, 1}; }

@@ -31,6 +31,7 @@
 //
 // Every wait is bounded; on a timeout the CTA records EXATTN_TIMEOUT, drains its
 // own copies and products, frees TMEM and returns.
+#include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
 #include "paged.cuh"
@@ -48,17 +49,21 @@ constexpr int kHalf = 128;
 constexpr int kRows = 2 * kHalf;
 constexpr int kUnit = 128;
 constexpr int kCtas = 152;
-constexpr int kThreads = 384;
-constexpr int kSoftmaxRegs = 208;
-constexpr int kProducerRegs = 88;
-constexpr int kWarpTMA = 8, kWarpMMA = 9, kWarpQ = 10;
-constexpr int kTakers = 11;  // warps that read a segment from the ring
+constexpr int kWarpTMA = 8, kWarpMMA = 9, kWarpQ = 10, kWarpConvert = 12;
+// kBytes: pages in 8 bits, with four warps more, which convert them.
+template <bool kBytes>
+struct Warps {
+  static constexpr int kThreads = kBytes ? 512 : 384;
+  static constexpr int kSoftmaxRegs = kBytes ? 184 : 208;
+  static constexpr int kProducerRegs = kBytes ? 72 : 88;
+  static constexpr int kTakers = kBytes ? 15 : 11;  // warps that read a segment from the ring
+};
 constexpr int kQThreads = 64;
 constexpr float kRescale = 8.f;
 constexpr uint32_t kTmemCols = 512;
 
 struct TcParams {
-  CUtensorMap tk, tv;  // the pools as [num_pages * Hk * page_size][width], boxes 64 x box_rows
+  CUtensorMap tk, tv;  // the pools as [num_pages * Hk * page_size][width], boxes 64 (bytes: D) x box_rows
   PagedArgs a;
   int box_rows;
 };
@@ -68,20 +73,29 @@ struct TcSegment {
   int n, kb0, j0, j1, rows, r0, h, b, slot, parts, s0, nq, len;  // parts: see PagedPlace
 };
 
-template <int D>
+template <int D, bool kBytes>
 struct TcLayout {
   static constexpr int CHUNKS = D / 64;
   static constexpr int QTILE = kHalf * D * 2;
   static constexpr int SLOT = kUnit * D * 2;
-  static constexpr int NSLOT = D == 128 ? 4 : 8;  // K and V of a block take one each
+  // K and V of a block take one each.  Pages in 8 bits: and one each of the tiles as they are loaded.
+  static constexpr int NSLOT = kBytes ? (D == 128 ? 3 : 6) : D == 128 ? 4 : 8;
+  static constexpr int NRAW = kBytes ? (D == 128 ? 3 : 6) : 0;
+  static constexpr int RAW = kUnit * D;
+  // Blocks whose masks are kept: K of block t + 4 is converted when K of t + 1 (NSLOT 6) or V of t + 2 (3) is
+  // done with, and the softmax with block t before that.
+  static constexpr int kKeepBlocks = 4;
   static constexpr int Q_OFF = 0;
   static constexpr int SLOT_OFF = 2 * QTILE;
-  static constexpr int BAR_OFF = SLOT_OFF + NSLOT * SLOT;
+  static constexpr int RAW_OFF = SLOT_OFF + NSLOT * SLOT;
+  static constexpr int BAR_OFF = RAW_OFF + NRAW * RAW;
   static constexpr int B_Q = 0, B_QFREE = 1, B_KVF = 2, B_KVE = B_KVF + NSLOT, B_S = B_KVE + NSLOT,
                        B_P = B_S + 2, B_O = B_P + 2, B_OREAD = B_O + 2, B_SEGF = B_OREAD + 2, B_SEGE = B_SEGF + 2, B_DRAIN = B_SEGE + 2,
-                       NBAR = B_DRAIN + 1;
-  static constexpr int KEEP_OFF = BAR_OFF + (NBAR * 8 + 15) / 16 * 16;  // 4 words a slot
-  static constexpr int MISC_OFF = KEEP_OFF + NSLOT * 16;                // TMEM base, abort flag, status bits
+                       B_RF = B_DRAIN + 1, B_RE = B_RF + NRAW, NBAR = B_RE + NRAW;
+  static constexpr int KEEP_OFF = BAR_OFF + (NBAR * 8 + 15) / 16 * 16;  // 4 words a slot (bytes: a block)
+  static constexpr int RKEEP_OFF = KEEP_OFF + (kBytes ? kKeepBlocks : NSLOT) * 16;  // the same of the raw tiles
+  static constexpr int EXP_OFF = RKEEP_OFF + NRAW * 16;                 // and their keys' exponent bytes
+  static constexpr int MISC_OFF = EXP_OFF + NRAW * kUnit;               // TMEM base, abort flag, status bits
   static constexpr int SEG_OFF = MISC_OFF + 16;
   static constexpr int TOTAL = SEG_OFF + 2 * 64;
   static constexpr int ALLOC = TOTAL + 1024;
@@ -110,10 +124,25 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_constant__ TcParams p) {
-  using Lay = TcLayout<D>;
-  constexpr int NS = Lay::NSLOT;
+// Sixteen e4m3 numbers of a row with factor f, as bf16: exact.
+__device__ __forceinline__ void bytes_to_bf16(const uint4& raw, float f, uint32_t (&y)[8]) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t h = i & 1 ? e4m3_pair_high(w[i >> 1]) : e4m3_pair(w[i >> 1]);
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    float x0, x1;
+    fmul2(x0, x1, x.x, x.y, f, f);
+    y[i] = pack_bf16x2(x0, x1);
+  }
+}
+
+template <int D, bool kBytes>
+__global__ void __launch_bounds__(Warps<kBytes>::kThreads, 1)
+    paged_tc_kernel(const __grid_constant__ TcParams p) {
+  using Lay = TcLayout<D, kBytes>;
+  constexpr int NS = Lay::NSLOT, NR = kBytes ? Lay::NRAW : 1;
+  constexpr int kThreads = Warps<kBytes>::kThreads;
   extern __shared__ uint8_t smem_raw[];
   __shared__ long long pre[kPagedSums], scan[kThreads / 32];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -131,8 +160,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     mbar_init(bar(Lay::B_Q), kQThreads);
     mbar_init(bar(Lay::B_QFREE), 1);
     for (int s = 0; s < NS; ++s) {
-      mbar_init(bar(Lay::B_KVF + s), 1);
+      mbar_init(bar(Lay::B_KVF + s), kBytes ? 128 : 1);
       mbar_init(bar(Lay::B_KVE + s), 1);
+    }
+    for (int s = 0; s < Lay::NRAW; ++s) {
+      mbar_init(bar(Lay::B_RF + s), 1);
+      mbar_init(bar(Lay::B_RE + s), 4);
     }
     for (int X = 0; X < 2; ++X) {
       mbar_init(bar(Lay::B_S + X), 1);
@@ -140,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       mbar_init(bar(Lay::B_O + X), 1);
       mbar_init(bar(Lay::B_OREAD + X), kHalf);
       mbar_init(bar(Lay::B_SEGF + X), 1);
-      mbar_init(bar(Lay::B_SEGE + X), kTakers);
+      mbar_init(bar(Lay::B_SEGE + X), Warps<kBytes>::kTakers);
     }
     mbar_init(bar(Lay::B_DRAIN), 1);
     misc[1] = misc[2] = 0;
@@ -185,8 +218,60 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
   // ring of tiles, V fill 2 blk + 1.
 
   if (warp >= 8) {
-    regs_dec<kProducerRegs>();
+    regs_dec<Warps<kBytes>::kProducerRegs>();
     const bool leader = elect_one();
+    if constexpr (kBytes) {
+      if (warp >= kWarpConvert) {
+        // A raw tile to bf16 in the products' 128-byte swizzled layout, its rows' powers of two in: warp
+        // by warp 32 rows.  A lane takes 16 columns: quads have four pieces of a row, and neighbouring rows
+        // the two halves of one, so that neither the loads nor the stores of eight lanes meet in a bank.
+        const int wr = (warp - kWarpConvert) * 32, q = lane & 3, odd = (lane >> 2) & 1;
+        volatile uint32_t* rkeep = reinterpret_cast<volatile uint32_t*>(smem + Lay::RKEEP_OFF);
+        bool ok = true;
+        int fill = 0;
+        TcSegment t;
+        for (int seg = 0; take(seg, t, ok) && ok; ++seg) {
+          for (int u = 0; u < 2 * t.n && ok; ++u, ++fill) {
+            const int rs = fill % NR, ks = fill % NS;
+            if (!(ok = wait_all(bar(Lay::B_RF + rs), (fill / NR) & 1, abort_flag))) break;
+            if (!(ok = wait_all(bar(Lay::B_KVE + ks), ((fill / NS) & 1) ^ 1, abort_flag))) break;
+            // V: rows without a key are zero, whatever their page holds (K's scores do not count).
+            uint32_t mine = rkeep[rs * 4 + (wr >> 5)];
+            if (!(u & 1)) {
+              if (lane == 0) keep[(fill / 2 % Lay::kKeepBlocks) * 4 + (wr >> 5)] = mine;
+              mine = 0xFFFFFFFFu;
+            }
+            const uint8_t* ex = smem + Lay::EXP_OFF + rs * kUnit + wr;
+            const uint32_t raw = sbase + Lay::RAW_OFF + rs * Lay::RAW + wr * D;
+            const uint32_t to = sbase + Lay::SLOT_OFF + ks * Lay::SLOT + wr * 128;
+#pragma unroll 2
+            for (int y = 0; y < D / 16; ++y) {
+              const int r = (D == 128 ? y >> 1 : y) * 8 + 2 * (lane >> 3) + odd;  // of the warp's rows
+              const int piece = q + (D == 128 ? 4 * (odd ^ (y & 1)) : 0);
+              uint4 x = ld_shared_v4(raw + r * D + piece * 16);
+              float f = e4m3_scale(ex[r]);
+              if (!((mine >> r) & 1u)) {
+                x = make_uint4(0u, 0u, 0u, 0u);
+                f = 0.f;
+              }
+              uint32_t z[8];
+              bytes_to_bf16(x, f, z);
+              const uint32_t row = to + (piece >> 2) * (kUnit * 128) + r * 128;
+              st_shared_v4(row + (((2 * q) ^ (r & 7)) << 4), z[0], z[1], z[2], z[3]);
+              st_shared_v4(row + (((2 * q + 1) ^ (r & 7)) << 4), z[4], z[5], z[6], z[7]);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(bar(Lay::B_KVF + ks));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(Lay::B_RE + rs));
+          }
+        }
+        if (!ok) {
+          bits |= kStatusTimeout;
+          *abort_flag = 1;
+        }
+      }
+    }
     if (warp == kWarpTMA) {
       if (leader) {
         prefetch_tmap(&p.tk);
@@ -209,34 +294,61 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
           }
           return row;
         };
+        // Bytes: the exponents of keys 4 lane to 4 lane + 3 of the block whose boxes are at `rows`.
+        auto exponents = [&](int rows) {
+          uint2 e = make_uint2(0u, 0u);
+          if constexpr (kBytes) {
+            const int at = __shfl_sync(0xFFFFFFFFu, rows, 4 * lane / br);
+            if (at >= 0) {
+              const size_t from = static_cast<size_t>(at) + 4 * lane % br;
+              e.x = __ldg(reinterpret_cast<const unsigned*>(a.Ks + from));
+              e.y = __ldg(reinterpret_cast<const unsigned*>(a.Vs + from));
+            }
+          }
+          return e;
+        };
         int row = find(0);
+        uint2 ex = exponents(row);
         for (int u = 0; u < t.n && ok; ++u) {
           const int next = find(u + 1);
+          const uint2 ex_next = exponents(next);
           const int kb = t.kb0 + u * kUnit;
           const unsigned boxes = __ballot_sync(0xFFFFFFFFu, row >= 0);
-          const uint32_t bytes = __popc(boxes) * br * 128 * Lay::CHUNKS;
+          const uint32_t bytes = __popc(boxes) * br * (kBytes ? D : 128 * Lay::CHUNKS);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            const int slot = fill % NS, phase = (fill / NS) & 1;
-            if (!(ok = wait_all(bar(Lay::B_KVE + slot), phase ^ 1, abort_flag))) break;
+            // The ring that is loaded into.
+            constexpr int N = kBytes ? NR : NS, kFull = kBytes ? Lay::B_RF : Lay::B_KVF,
+                          kEmpty = kBytes ? Lay::B_RE : Lay::B_KVE, kKeep = kBytes ? Lay::RKEEP_OFF : Lay::KEEP_OFF;
+            const int slot = fill % N, phase = (fill / N) & 1;
+            if (!(ok = wait_all(bar(kEmpty + slot), phase ^ 1, abort_flag))) break;
             ++fill;
-            if (kv == 1 && lane < 4) {
+            if constexpr (kBytes)
+              reinterpret_cast<volatile uint32_t*>(smem + Lay::EXP_OFF)[slot * (kUnit / 4) + lane] = kv ? ex.y : ex.x;
+            if ((kBytes || kv == 1) && lane < 4) {
               uint32_t word = range_bits(t.j0 - kb - 32 * lane, t.j1 - 1 - kb - 32 * lane);
               for (int b = 0; b < nb; ++b)
                 if (!((boxes >> b) & 1u)) word &= ~range_bits(b * br - 32 * lane, b * br + br - 1 - 32 * lane);
-              keep[slot * 4 + lane] = word;
+              reinterpret_cast<volatile uint32_t*>(smem + kKeep)[slot * 4 + lane] = word;
             }
             __syncwarp();
-            if (leader) mbar_arrive_expect_tx(bar(Lay::B_KVF + slot), bytes);
+            if (leader) mbar_arrive_expect_tx(bar(kFull + slot), bytes);
             __syncwarp();
-            const uint32_t dst = sbase + Lay::SLOT_OFF + slot * Lay::SLOT + lane * br * 128;
-            if (row >= 0)
+            if constexpr (kBytes) {
+              if (row >= 0)
+                tma_load_2d(sbase + Lay::RAW_OFF + slot * Lay::RAW + lane * br * D, kv ? &p.tv : &p.tk,
+                            bar(kFull + slot), 0, row);
+            } else {
+              const uint32_t dst = sbase + Lay::SLOT_OFF + slot * Lay::SLOT + lane * br * 128;
+              if (row >= 0)
 #pragma unroll
-              for (int c = 0; c < Lay::CHUNKS; ++c)
-                tma_load_2d(dst + c * (kUnit * 128), kv ? &p.tv : &p.tk, bar(Lay::B_KVF + slot), 64 * c, row);
+                for (int c = 0; c < Lay::CHUNKS; ++c)
+                  tma_load_2d(dst + c * (kUnit * 128), kv ? &p.tv : &p.tk, bar(kFull + slot), 64 * c, row);
+            }
             __syncwarp();
           }
           row = next;
+          ex = ex_next;
         }
         if (!ok) break;
       }
@@ -245,9 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         if (leader) *abort_flag = 1;
       }
       // Never leave with copies in flight: the last fill of every slot has landed.
-      for (int u = 0; u < NS && u < fill; ++u) {
+      constexpr int N = kBytes ? NR : NS, kFull = kBytes ? Lay::B_RF : Lay::B_KVF;
+      for (int u = 0; u < N && u < fill; ++u) {
         const int i = fill - 1 - u;
-        mbar_wait_inflight(bar(Lay::B_KVF + i % NS), (i / NS) & 1);
+        mbar_wait_inflight(bar(kFull + i % N), (i / N) & 1);
       }
     } else if (warp == kWarpMMA) {
       constexpr uint32_t kIdescS = idesc_bf16(kHalf, kUnit, false, false);
@@ -308,10 +421,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
           if (u == n - 1) commit(Lay::B_QFREE);
           commit(Lay::B_KVE + ks);
           if (!(ok = wait_all(bar(Lay::B_KVF + vs), vphase, abort_flag))) break;
-          // Rows without a key are zeroed in V.
+          // Rows without a key are zeroed in V (bytes: they are already).
           uint32_t kw[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) kw[q] = keep[vs * 4 + q];
+          for (int q = 0; q < 4; ++q) kw[q] = kBytes ? 0xFFFFFFFFu : keep[vs * 4 + q];
           if ((kw[0] & kw[1] & kw[2] & kw[3]) != 0xFFFFFFFFu) {
             const uint32_t vt = sbase + Lay::SLOT_OFF + vs * Lay::SLOT;
 #pragma unroll 1
@@ -354,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       __syncwarp();
       commit(Lay::B_DRAIN);
       mbar_wait_inflight(bar(Lay::B_DRAIN), 0);
-    } else {
+    } else if (warp < kWarpConvert) {
       // The rows of Q, in the 128-byte swizzled layout of the products' operand: warp
       // 10 the even groups of 32 rows, warp 11 the odd ones.  A lane finds one row, the
       // warp copies them together.
@@ -445,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       }
     }
   } else {
-    regs_inc<kSoftmaxRegs>();
+    regs_inc<Warps<kBytes>::kSoftmaxRegs>();
     const int X = warp >> 2;
     const int wl = warp & 3;
     const int rl = X * kHalf + wl * 32 + lane;  // row of the tile
@@ -472,13 +585,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
       float m_ref = -INFINITY, l = 0.f;
       for (int u = 0; u < n && on; ++u) {
         const int vf = 2 * (blk + u) + 1, vs = vf % NS;
-        if (!(ok = wait_all(bar(Lay::B_KVF + vs), (vf / NS) & 1, abort_flag))) break;
         uint32_t mw[4];
+        if constexpr (!kBytes) {
+          if (!(ok = wait_all(bar(Lay::B_KVF + vs), (vf / NS) & 1, abort_flag))) break;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) mw[q] = keep[vs * 4 + q];
+          for (int q = 0; q < 4; ++q) mw[q] = keep[vs * 4 + q];
+        }
         const int kb = kb0 + u * kUnit;
-        const bool whole = (mw[0] & mw[1] & mw[2] & mw[3]) == 0xFFFFFFFFu && kb >= all_lo && kb + kUnit <= all_hi;
         if (!(ok = wait_all(bar(Lay::B_S + X), cnt & 1, abort_flag))) break;
+        if constexpr (kBytes) {  // written before K was there for the product
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mw[q] = keep[((blk + u) % Lay::kKeepBlocks) * 4 + q];
+        }
+        const bool whole = (mw[0] & mw[1] & mw[2] & mw[3]) == 0xFFFFFFFFu && kb >= all_lo && kb + kUnit <= all_hi;
         tc_fence_after();
         ++cnt;
         uint32_t s[128];
@@ -634,35 +753,44 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
   }
 }
 
-bool pool_map(CUtensorMap* m, const void* base, const PagedArgs& a, int width, int box_rows) {
+// width: of the pool's rows; box: of a box, in elements.
+bool pool_map(CUtensorMap* m, const void* base, const PagedArgs& a, int width, int box, int box_rows) {
   auto enc = tmap_encoder();
   if (!enc) return false;
+  const bool bytes = a.Ks != nullptr;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(width),
                         (static_cast<cuuint64_t>(a.num_pages) * a.Hk) << a.lps};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(width) * 2};
-  cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(width) * (bytes ? 1 : 2)};
+  cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box), static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[2] = {1, 1};
-  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-                         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const CUresult r = enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                         const_cast<void*>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) record_error("cuTensorMapEncodeTiled", static_cast<int>(r), "");
   return r == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool kBytes>
 cudaError_t tc_launch(const PagedArgs& a, cudaStream_t s) {
   TcParams p;
   p.a = a;
   p.box_rows = min(1 << a.lps, kUnit);
-  if (!pool_map(&p.tk, a.Kp, a, a.d, p.box_rows) || !pool_map(&p.tv, a.Vp, a, a.v, p.box_rows))
+  const int box = kBytes ? D : 64;
+  if (!pool_map(&p.tk, a.Kp, a, a.d, box, p.box_rows) || !pool_map(&p.tv, a.Vp, a, a.v, box, p.box_rows))
     return cudaErrorInvalidValue;
-  auto kern = paged_tc_kernel<D>;
-  const cudaError_t e = allow_smem<paged_tc_kernel<D>>(TcLayout<D>::ALLOC);
+  constexpr int bytes = TcLayout<D, kBytes>::ALLOC;
+  const cudaError_t e = allow_smem<paged_tc_kernel<D, kBytes>>(bytes);
   if (e != cudaSuccess) return e;
   before_launch(kKernPaged, s);
-  const cudaError_t le = launch_early(kern, dim3(kCtas), kThreads, TcLayout<D>::ALLOC, s, p);
+  const cudaError_t le =
+      launch_early(paged_tc_kernel<D, kBytes>, dim3(kCtas), Warps<kBytes>::kThreads, bytes, s, p);
   after_launch(kKernPaged, s);
   return le;
+}
+template <int D>
+cudaError_t tc_pages(const PagedArgs& a, cudaStream_t s) {
+  return a.Ks ? tc_launch<D, true>(a, s) : tc_launch<D, false>(a, s);
 }
 
 }  // namespace
@@ -670,13 +798,13 @@ cudaError_t tc_launch(const PagedArgs& a, cudaStream_t s) {
 // Pages of at least 8 rows (a swizzle atom), pool rows within TMA's 32-bit
 // coordinates, a scale whose sign keeps the maximum a maximum.
 bool paged_tc_supported(const PagedArgs& a) {
-  return a.dtype == kBF16 && !a.Ks && paged_mma_shape(a.d, a.v) && a.lps >= 3 && a.sl2 > 0.f &&
+  return a.dtype == kBF16 && paged_mma_shape(a.d, a.v) && a.lps >= 3 && a.sl2 > 0.f &&
          ((static_cast<long long>(a.num_pages) * a.Hk) << a.lps) < (1ll << 31) && tmap_encoder() != nullptr;
 }
 PagedKernel paged_tc_kernel_of() { return {kRows, kCtas, kCtas, 1}; }
 
 cudaError_t launch_paged_tc(const PagedArgs& a, cudaStream_t s) {
-  return a.d <= 64 && a.v <= 64 ? tc_launch<64>(a, s) : tc_launch<128>(a, s);
+  return a.d <= 64 && a.v <= 64 ? tc_pages<64>(a, s) : tc_pages<128>(a, s);
 }
 
 }  // namespace exattn

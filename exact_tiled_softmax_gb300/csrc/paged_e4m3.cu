@@ -7,25 +7,31 @@
 // the ends of segments) and holds maximum, sum and output of its rows in registers.  An 8-bit tile
 // of 32 keys is the bytes of a 16-bit one of 16.
 //
-// Operands are fp16 (m16n8k16): an e4m3 number is one exactly, and two come out of each conversion.
-// No row's power of two enters them.  A key's comes out of its score.  A value's goes into its
+// K meets Q as it is (m16n8k32 of e4m3, whose products are summed in fp32 as fp16's are, to 2^-24 of
+// their magnitudes): a row of Q, scaled by the power of two that brings its largest entry to [128, 256),
+// is the sum of two e4m3 parts, the second times 2^-4.  A part leaves 2^-5 of what it is given, so that
+// two hold a bf16 entry exactly, down to a floor of 2^-21 of the row's largest.  (K as fp16, two
+// conversions and a shift for four numbers: 8 sequences of 16384 keys 215 us in place of 185.)  fp32
+// queries would be five parts; they are two fp16 parts, 2^-22 of themselves, their row's largest in
+// [2^14, 2^15), and K is fp16 for them (18 us in place of 28, 12 x 2 rows of 80 columns over 3001 keys).
+// V is fp16 (m16n8k16): an e4m3 number is one exactly.  No row's power of two enters an operand.
+// A key's comes out of its score.  A value's goes into its
 // weight: with s in the exp2 domain and e the exponent of V's row, w = s + e, and the operand is
 // 2^(w - M + 7) with M a reference point of its own (the sum l keeps s's), so that unequal rows of V
 // lose nothing; 2^7 puts the largest weight in the middle of fp16's range above its subnormals, and a
-// weight is held to 2^-11 of itself or 2^-32 of the row's largest.  A row of Q is scaled by the power of
-// two that brings its largest entry to [2^14, 2^15).  fp32 queries and their weights are two fp16 parts,
-// 2^-22 of themselves; the two products cost less than the loads.
+// weight is held to 2^-11 of itself or 2^-32 of the row's largest; for fp32 queries two parts, 2^-22.
 // The reference points move only when a row's maximum passes them by more than 2^8, which a vote
 // tells without the maximum.
 //
 // A lane reads 16 columns of a key at once: the products' inner index is permuted so that lane t of
-// a quad has columns 16 t .. 16 t + 15 (64 on, the next eight steps' half), four a step, of the queries
+// a quad has columns 16 t .. 16 t + 15 (and those 64 on), eight a step, of the queries
 // too.  Key 4 g + j of the tile is row g of the quarter j, so that a lane's four keys' exponents are one
 // word and its masks one nibble.  V comes transposed in 16-bit units (ldmatrix): two columns of
-// one key, which two conversions and two byte permutations turn into two keys of one column.
+// one key, which two byte permutations and two conversions turn into two keys of one column.
 #include <cuda_fp16.h>
 
 #include <type_traits>
+#include <utility>
 
 #include "paged.cuh"
 #include "tc_ptx.cuh"
@@ -34,6 +40,9 @@ namespace exattn {
 namespace {
 
 using tc::ex2;
+using tc::fadd2;
+using tc::ffma2;
+using tc::fmul2;
 using tc::ld_shared_v4;
 using tc::pack_bf16x2;
 using tc::smem_u32;
@@ -41,9 +50,14 @@ using tc::smem_u32;
 constexpr int kTile = 32;  // keys of a tile, a unit of work
 constexpr float kRescale = 8.f;
 constexpr float kLift = 7.f;  // weights are held times 2^7
+constexpr float kNoKey = -3.402823466e38f;  // a reference point below every score
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+template <int kTo, int kFrom>
+__device__ __forceinline__ void cp16_at(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(kTo), "n"(kFrom) : "memory");
 }
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -70,6 +84,24 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Two numbers as e4m3, a in the low byte; x becomes what the rounding left out, times 16.
+__device__ __forceinline__ uint32_t take_e4m3(float& a, float& b) {
+  uint16_t y;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(b), "f"(a));
+  const uint32_t h = e4m3_pair(y);
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  a = (a - x.x) * 16.f;
+  b = (b - x.y) * 16.f;
+  return y;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t y;
@@ -111,14 +143,16 @@ struct Place {
   static __device__ __forceinline__ uint32_t v_at(int r, int c) { return at(r, c, (r >> 2) & 7); }
 };
 
-template <typename T, int D>
+template <typename T, int D, int NT>
 struct Config {
-  static constexpr int kW = 4, kStages = 3, kCtas = 2 * 152;
+  static constexpr bool kMany = std::is_same<T, __nv_bfloat16>::value && NT == 1;
+  static constexpr int kW = 4, kStages = kMany ? 2 : 3, kCtas = (kMany ? 3 : 2) * 152;
 };
 
-template <typename T> struct Parts;  // fp16 parts of a query's entry and of a weight
+template <typename T> struct Parts;  // of a query's entry and of a weight
 template <> struct Parts<__nv_bfloat16> {
   static constexpr int N = 1;
+  static constexpr bool kE4m3 = true;  // the query's, two; else N fp16 parts
   // Sixteen columns.
   static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* x) {
 #pragma unroll
@@ -135,6 +169,7 @@ template <> struct Parts<__nv_bfloat16> {
 };
 template <> struct Parts<float> {
   static constexpr int N = 2;
+  static constexpr bool kE4m3 = false;
   static __device__ __forceinline__ void load(const float* p, float* x) {
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
@@ -156,7 +191,9 @@ struct Spans {
 template <typename T, int D, int NT>
 struct Rows {
   static constexpr int P = Parts<T>::N, K = D / 16;
-  uint32_t qb[NT][P][K][2];
+  static constexpr bool kE4m3 = Parts<T>::kE4m3;
+  static constexpr int kSteps = kE4m3 ? D / 32 : K;
+  uint32_t qb[NT][2][kSteps][2];
   float f[NT][2], m[NT][2], M[NT][2], l[NT][2], o[NT][K][4];
 
   // Row n of the tile's row 8 n + g.
@@ -179,24 +216,38 @@ struct Rows {
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
     const unsigned e = max(top >> 23, 15u);  // the largest is below 2^(e - 126)
-    const float up = __uint_as_float((268u - e) << 23), down = __uint_as_float((e - 14u) << 23) * sl2;
+    constexpr unsigned kUp = kE4m3 ? 261u : 268u;  // 254 and 8 bits, or 15
+    const float up = __uint_as_float((kUp - e) << 23), down = __uint_as_float((e - (kUp - 254u)) << 23) * sl2;
 #pragma unroll
     for (int h = 0; h < D / 64; ++h)
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
+      for (int w = 0; w < 4; ++w) {
+        float(&z)[16] = x[h];
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const float a = x[h][4 * w + 2 * y] * up, b = x[h][4 * w + 2 * y + 1] * up;
-          qb[n][0][4 * h + w][y] = pack_f16x2(a, b);
-          if (P == 2) qb[n][P - 1][4 * h + w][y] = rest_f16x2(a, b, qb[n][0][4 * h + w][y]);
+        for (int c = 4 * w; c < 4 * w + 4; ++c) z[c] = fmaf(z[c], up, z[c] * 0.f);  // an infinity: NaN
+        if constexpr (kE4m3) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const uint32_t lo = take_e4m3(z[4 * w], z[4 * w + 1]), hi = take_e4m3(z[4 * w + 2], z[4 * w + 3]);
+            qb[n][p][2 * h + (w >> 1)][w & 1] = lo | hi << 16;
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float a = z[4 * w + 2 * y], b = z[4 * w + 2 * y + 1];
+            const uint32_t hi = pack_f16x2(a, b);
+            qb[n][0][4 * h + w][y] = hi;
+            qb[n][1][4 * h + w][y] = rest_f16x2(a, b, hi);
+          }
         }
+      }
 #pragma unroll
     for (int x2 = 0; x2 < 2; ++x2) f[n][x2] = __shfl_sync(0xFFFFFFFFu, down, 4 * (2 * t + x2));
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      m[n][0] = m[n][1] = M[n][0] = M[n][1] = -INFINITY;
+      m[n][0] = m[n][1] = M[n][0] = M[n][1] = kNoKey;
       l[n][0] = l[n][1] = 0.f;
 #pragma unroll
       for (int y = 0; y < K; ++y) o[n][y][0] = o[n][y][1] = o[n][y][2] = o[n][y][3] = 0.f;
@@ -206,15 +257,18 @@ struct Rows {
   // The tile at kt, vt, its exponents at et (32 of keys, 32 of values).
   __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, uint32_t et, unsigned have, int key0,
                                        const Spans<NT>& sp, int v) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int lane = threadIdx.x & 31, g = lane >> 2;
     const uint32_t ke = lds32(et + 4 * g), ve = lds32(et + 32 + 4 * g);
-    float sc[NT][2][4];  // [row tile][pair of quarters j = 2 q, 2 q + 1][2 (j & 1) + row]
+    // [row tile][pair of quarters j = 2 q, 2 q + 1][2 (j & 1) + row]; the second e4m3 part's.
+    float sc[NT][2][4], low[NT][2][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int q = 0; q < 2; ++q) sc[n][q][0] = sc[n][q][1] = sc[n][q][2] = sc[n][q][3] = 0.f;
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[n][q][e] = low[n][q][e] = 0.f;
     {
-      const uint32_t at = kt + Place<D>::k_at(4 * g, t);
+      const uint32_t at = kt + Place<D>::k_at(4 * g, lane & 3);
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
         uint4 k[4];
@@ -225,40 +279,54 @@ struct Rows {
         for (int w = 0; w < 4; ++w)
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            auto word = [&](const uint4& x) { return w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w; };
-            const uint32_t x0 = word(k[2 * q]), x1 = word(k[2 * q + 1]);
-            const uint32_t a[4] = {e4m3_pair(x0), e4m3_pair(x1), e4m3_pair_high(x0), e4m3_pair_high(x1)};
+            auto word = [&](const uint4& x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; };
+            if constexpr (kE4m3) {
+              if (w & 1) continue;  // two words a step
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+              for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int p = 0; p < P; ++p) mma16(sc[n][q], a, qb[n][p][4 * h + w][0], qb[n][p][4 * h + w][1]);
+                for (int p = 0; p < 2; ++p)
+                  mma32(p ? low[n][q] : sc[n][q], word(k[2 * q], w), word(k[2 * q + 1], w), word(k[2 * q], w + 1),
+                        word(k[2 * q + 1], w + 1), qb[n][p][2 * h + (w >> 1)][0], qb[n][p][2 * h + (w >> 1)][1]);
+            } else {
+              const uint32_t x0 = word(k[2 * q], w), x1 = word(k[2 * q + 1], w);
+              const uint32_t a[4] = {e4m3_pair(x0), e4m3_pair(x1), e4m3_pair_high(x0), e4m3_pair_high(x1)};
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                  mma16(sc[n][q], a, qb[n][p][4 * h + w][0], qb[n][p][4 * h + w][1]);
+            }
           }
       }
     }
     // Scores into the exp2 domain, those that do not count to -inf; w beside them.
     const bool whole = have == 0xFFFFFFFFu && key0 >= sp.all_lo && key0 + kTile <= sp.all_hi;
-    float wt[NT][2][4], over = -INFINITY;
+    float wt[NT][2][4], over = kNoKey;
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const int j = 2 * q + z;
-        const float kf = e4m3_scale((ke >> (8 * j)) & 255u);
-        const float vx = __uint_as_float(0x4B000000u | ((ve >> (8 * j)) & 255u)) - 8388735.f;  // byte - 127
+      for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int z = 0; z < 2; ++z) {
+          const int j = 2 * q + z;
+          const float kf = e4m3_scale((ke >> (8 * j)) & 255u);
+          const float vx = __uint_as_float(0x4B000000u | ((ve >> (8 * j)) & 255u)) - 8388735.f;  // byte - 127
+          float &s0 = sc[n][q][2 * z], &s1 = sc[n][q][2 * z + 1], f0, f1;
+          if (kE4m3) ffma2(s0, s1, low[n][q][2 * z], low[n][q][2 * z + 1], 0x1p-4f, 0x1p-4f, s0, s1);
+          fmul2(f0, f1, f[n][0], f[n][1], kf, kf);
+          fmul2(s0, s1, s0, s1, f0, f1);
+          if (!whole) {
+            const int key = 4 * g + j;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float& s = sc[n][q][2 * z + x];
-            s *= f[n][x] * kf;
-            if (!whole) {
-              const int key = 4 * g + j;
-              if (!((have >> key) & 1u) || key0 + key < sp.lo[n][x] || key0 + key >= sp.hi[n][x]) s = -INFINITY;
-            }
-            wt[n][q][2 * z + x] = s + vx;
-            over = fmaxf(over, fmaxf(s - m[n][x], wt[n][q][2 * z + x] - M[n][x]));
+            for (int x = 0; x < 2; ++x)
+              if (!((have >> key) & 1u) || key0 + key < sp.lo[n][x] || key0 + key >= sp.hi[n][x])
+                sc[n][q][2 * z + x] = -INFINITY;
           }
-      }
+          float &w0 = wt[n][q][2 * z], &w1 = wt[n][q][2 * z + 1];
+          fadd2(w0, w1, s0, s1, vx, vx);
+          over = fmaxf(over, fmaxf(fmaxf(s0 - m[n][0], s1 - m[n][1]), fmaxf(w0 - M[n][0], w1 - M[n][1])));
+        }
     if (__any_sync(0xFFFFFFFFu, over > kRescale)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -267,11 +335,11 @@ struct Rows {
           // Each row by itself: what the others hold does not change its bits.
           const float to = max_over_keys(max4(sc[n], x)), To = max_over_keys(max4(wt[n], x));
           if (to > m[n][x] + kRescale) {
-            l[n][x] *= m[n][x] == -INFINITY ? 0.f : ex2(m[n][x] - to);
+            l[n][x] *= ex2(m[n][x] - to);
             m[n][x] = to;
           }
           if (!(To > M[n][x] + kRescale)) continue;
-          const float F = M[n][x] == -INFINITY ? 0.f : ex2(M[n][x] - To);
+          const float F = ex2(M[n][x] - To);
           M[n][x] = To;
 #pragma unroll
           for (int y = 0; y < K; ++y) {
@@ -283,40 +351,34 @@ struct Rows {
     uint32_t pb[NT][P][2][2];  // [pair of quarters][quarter]
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float ref[2], Ref[2];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        ref[x] = m[n][x] == -INFINITY ? 0.f : m[n][x];
-        Ref[x] = M[n][x] == -INFINITY ? 0.f : M[n][x] - kLift;
-      }
+      const float R0 = kLift - M[n][0], R1 = kLift - M[n][1];
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          float p[2];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            l[n][x] += ex2(sc[n][q][2 * z + x] - ref[x]);
-            p[x] = ex2(wt[n][q][2 * z + x] - Ref[x]);
-          }
-          const uint32_t hi = pack_f16x2(p[0], p[1]);
+          float s0, s1, w0, w1;
+          fadd2(s0, s1, sc[n][q][2 * z], sc[n][q][2 * z + 1], -m[n][0], -m[n][1]);
+          fadd2(w0, w1, wt[n][q][2 * z], wt[n][q][2 * z + 1], R0, R1);
+          fadd2(l[n][0], l[n][1], l[n][0], l[n][1], ex2(s0), ex2(s1));
+          const float p0 = ex2(w0), p1 = ex2(w1);
+          const uint32_t hi = pack_f16x2(p0, p1);
           pb[n][0][q][z] = transpose8(hi);
-          if (P == 2) pb[n][P - 1][q][z] = transpose8(rest_f16x2(p[0], p[1], hi));
+          if (P == 2) pb[n][P - 1][q][z] = transpose8(rest_f16x2(p0, p1, hi));
         }
     }
     {
       const uint32_t at = vt + Place<D>::v_at(4 * (lane & 7) + (lane >> 3), 0);
 #pragma unroll
       for (int y = 0; y < K; ++y) {
-        if (16 * y >= v) break;
+        // (A branch for every y keeps the steps apart: 16 rows over 262147 keys 141 us in place of 129.)
+        if (y == 4 && v <= 64) break;
         uint32_t r[4];  // quarter j: columns 2 g and 2 g + 1 of keys 2 t and 2 t + 1 of it
         ldm4t(r, at ^ (y << 4));
         uint32_t a[2][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t lo = e4m3_pair(r[j]), hi = e4m3_pair_high(r[j]);
-          a[j >> 1][2 * (j & 1)] = __byte_perm(lo, hi, 0x5410);
-          a[j >> 1][2 * (j & 1) + 1] = __byte_perm(lo, hi, 0x7632);
+          a[j >> 1][2 * (j & 1)] = e4m3_pair(__byte_perm(r[j], 0u, 0x4420));
+          a[j >> 1][2 * (j & 1) + 1] = e4m3_pair(__byte_perm(r[j], 0u, 0x4431));
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -340,16 +402,24 @@ struct Rows {
   }
 };
 
-template <typename T, int D>
-constexpr int smem_bytes() {
-  return Config<T, D>::kW * Config<T, D>::kStages * (2 * Place<D>::kTileBytes + 64);
+// A whole tile of rows of D bytes behind one another; x: see the general copy.
+template <int CH, int... X>
+__device__ __forceinline__ void copy_dense(uint32_t k, uint32_t v, uint32_t up, const uint8_t* kf, const uint8_t* vf,
+                                           std::integer_sequence<int, X...>) {
+  (cp16_at<512 * X, 512 * X>((k ^ (CH == 8 ? (X & 1) << 6 : 0)) + up, kf), ...);
+  (cp16_at<512 * X, 512 * X>((v ^ (CH == 8 ? X << 4 : X << 5)) + up, vf), ...);
 }
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(32 * Config<T, D>::kW, Config<T, D>::kCtas / 152)
+constexpr int smem_bytes() {
+  return Config<T, D, NT>::kW * Config<T, D, NT>::kStages * (2 * Place<D>::kTileBytes + 64);
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(32 * Config<T, D, NT>::kW, Config<T, D, NT>::kCtas / 152)
     paged_e4m3_kernel(const PagedArgs a) {
   using At = Place<D>;
-  constexpr int S = Config<T, D>::kStages, kW = Config<T, D>::kW, kRows = 8 * NT, CH = At::CH;
+  constexpr int S = Config<T, D, NT>::kStages, kW = Config<T, D, NT>::kW, kRows = 8 * NT, CH = At::CH;
   constexpr int kStage = 2 * At::kTileBytes;
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ long long pre[kPagedSums], scan[kW];
@@ -414,6 +484,7 @@ __global__ void __launch_bounds__(32 * Config<T, D>::kW, Config<T, D>::kCtas / 1
   const uint8_t* Kp = static_cast<const uint8_t*>(a.Kp) + static_cast<size_t>(pr) * d + 16 * pc;
   const uint8_t* Vp = static_cast<const uint8_t*>(a.Vp) + static_cast<size_t>(pr) * v + 16 * pc;
   const uint8_t* Ep = lane < 8 ? a.Ks : a.Vs;  // lanes 0 to 7 copy keys' exponents, 8 to 15 values'
+  const bool dense = d == D && v == D && lpk == 5;
   int issued = 0;  // tiles copied so far
   // The products' segment.
   int left = 0, key0 = 0;
@@ -486,8 +557,16 @@ __global__ void __launch_bounds__(32 * Config<T, D>::kW, Config<T, D>::kCtas / 1
       }
       const int s = issued++ % S;
       const uint32_t up = s * kStage;
-      // Eight keys at a time are one page's rows behind one another; pool rows of the four eights.
       unsigned have = 0u;
+      const int page0 = __shfl_sync(0xFFFFFFFFu, pages, (p_key - p_base) >> lpk);
+      if (dense && page0 >= 0 && p_key >= p_j0 && p_key + kTile <= p_j1) {
+        // All keys, of one page, in rows of D bytes: one stretch of memory.
+        const long long row = ((static_cast<long long>(page0) * a.Hk + p_h) << a.lps) + (p_key & ((1 << a.lps) - 1));
+        copy_dense<CH>(k_to, v_to, up, Kp + row * D, Vp + row * D, std::make_integer_sequence<int, CH>{});
+        if (lane < 16) cp4(scales + s * 64 + 4 * lane, Ep + row + 4 * (lane & 7), 4);
+        have = 0xFFFFFFFFu;
+      } else {
+      // Eight keys at a time are one page's rows behind one another; pool rows of the four eights.
       long long row[4];
 #pragma unroll
       for (int z = 0; z < 4; ++z) {
@@ -514,6 +593,7 @@ __global__ void __launch_bounds__(32 * Config<T, D>::kW, Config<T, D>::kCtas / 1
         const int z = (lane >> 1) & 3;
         const long long from = z == 0 ? row[0] : z == 1 ? row[1] : z == 2 ? row[2] : row[3];
         cp4(scales + s * 64 + 4 * lane, Ep + from + 4 * (lane & 1), (have >> 8 * z) & 0xFFu ? 4 : 0);
+      }
       }
       if (lane == 0) tile_keys[warp][s] = have;
       p_key += kTile;
@@ -547,13 +627,14 @@ __global__ void __launch_bounds__(32 * Config<T, D>::kW, Config<T, D>::kCtas / 1
         if (a.info && place.parts >= 0 && g == 0) a.info[out] = make_int2(worker, place.parts);
         // From the weights' reference point to the scores', in two factors: 2^(M - m) may be
         // subnormal where what it multiplies is not.
-        const float half = st.m[y][x] == -INFINITY ? 0.f : ex2(0.5f * (st.M[y][x] - kLift - st.m[y][x]));
+        const bool none = l == 0.f;  // no key
+        const float half = none ? 0.f : ex2(0.5f * (st.M[y][x] - kLift - st.m[y][x])), m = none ? -INFINITY : st.m[y][x];
         PagedScale f{1.f, 0.f};
         if (place.slot < 0) {
-          f = paged_finish(st.m[y][x], l);
+          f = paged_finish(m, l);
           if (g == 0) a.L[out] = f.L;
         } else if (g == 0) {
-          a.pm[static_cast<size_t>(place.slot) * kRows + q] = st.m[y][x];
+          a.pm[static_cast<size_t>(place.slot) * kRows + q] = m;
           a.pl[static_cast<size_t>(place.slot) * kRows + q] = l;
         }
         const float rest = half * f.fz;
@@ -577,11 +658,11 @@ __global__ void __launch_bounds__(32 * Config<T, D>::kW, Config<T, D>::kCtas / 1
 
 template <typename T, int D, int NT>
 cudaError_t e4m3_launch(const PagedArgs& a, cudaStream_t s) {
-  constexpr int bytes = smem_bytes<T, D>();
+  constexpr int bytes = smem_bytes<T, D, NT>();
   const cudaError_t e = allow_smem<paged_e4m3_kernel<T, D, NT>>(bytes);
   if (e != cudaSuccess) return e;
   before_launch(kKernPaged, s);
-  const cudaError_t le = launch_early(paged_e4m3_kernel<T, D, NT>, dim3(Config<T, D>::kCtas), 32 * Config<T, D>::kW, bytes, s, a);
+  const cudaError_t le = launch_early(paged_e4m3_kernel<T, D, NT>, dim3(Config<T, D, NT>::kCtas), 32 * Config<T, D, NT>::kW, bytes, s, a);
   after_launch(kKernPaged, s);
   return le;
 }
@@ -591,10 +672,14 @@ cudaError_t e4m3_columns(const PagedArgs& a, int rows, cudaStream_t s) {
   if (a.d <= 64 && a.v <= 64) return rows == 8 ? e4m3_launch<T, 64, 1>(a, s) : e4m3_launch<T, 64, 2>(a, s);
   return rows == 8 ? e4m3_launch<T, 128, 1>(a, s) : e4m3_launch<T, 128, 2>(a, s);
 }
+template <typename T, int D, int NT>
+constexpr PagedKernel e4m3_kernel() {
+  return {8 * NT, Config<T, D, NT>::kCtas, Config<T, D, NT>::kCtas * Config<T, D, NT>::kW, 2};
+}
 template <typename T>
 PagedKernel e4m3_kernel(bool narrow, int rows) {
-  const int ctas = narrow ? Config<T, 64>::kCtas : Config<T, 128>::kCtas;
-  return {rows, ctas, ctas * (narrow ? Config<T, 64>::kW : Config<T, 128>::kW), 2};
+  if (narrow) return rows == 8 ? e4m3_kernel<T, 64, 1>() : e4m3_kernel<T, 64, 2>();
+  return rows == 8 ? e4m3_kernel<T, 128, 1>() : e4m3_kernel<T, 128, 2>();
 }
 
 }  // namespace

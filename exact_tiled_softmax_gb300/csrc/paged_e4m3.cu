@@ -7,27 +7,23 @@
 // the ends of segments) and holds maximum, sum and output of its rows in registers.  An 8-bit tile
 // of 32 keys is the bytes of a 16-bit one of 16.
 //
-// K meets Q as it is (m16n8k32 of e4m3, whose products are summed in fp32 as fp16's are, to 2^-24 of
-// their magnitudes): a row of Q, scaled by the power of two that brings its largest entry to [128, 256),
-// is the sum of two e4m3 parts, the second times 2^-4.  A part leaves 2^-5 of what it is given, so that
-// two hold a bf16 entry exactly, down to a floor of 2^-21 of the row's largest.  (K as fp16, two
-// conversions and a shift for four numbers: 8 sequences of 16384 keys 215 us in place of 185.)  fp32
-// queries would be five parts; they are two fp16 parts, 2^-22 of themselves, their row's largest in
-// [2^14, 2^15), and K is fp16 for them (18 us in place of 28, 12 x 2 rows of 80 columns over 3001 keys).
-// V is fp16 (m16n8k16): an e4m3 number is one exactly.  No row's power of two enters an operand.
+// Operands are fp16 (m16n8k16): an e4m3 number is one exactly, and two come out of each conversion.
+// (mma.sync of e4m3 operands is two of fp16 here, with its conversions once more for each.)  No row's
+// power of two enters them.
 // A key's comes out of its score.  A value's goes into its
 // weight: with s in the exp2 domain and e the exponent of V's row, w = s + e, and the operand is
 // 2^(w - M + 7) with M a reference point of its own (the sum l keeps s's), so that unequal rows of V
 // lose nothing; 2^7 puts the largest weight in the middle of fp16's range above its subnormals, and a
-// weight is held to 2^-11 of itself or 2^-32 of the row's largest; for fp32 queries two parts, 2^-22.
+// weight is held to 2^-11 of itself or 2^-32 of the row's largest.  A row of Q is scaled by the power of
+// two that brings its largest entry to [2^14, 2^15).  fp32 queries and their weights are two fp16 parts,
+// 2^-22 of themselves.
 // The reference points move only when a row's maximum passes them by more than 2^8, which a vote
 // tells without the maximum.
 //
-// A lane reads 16 columns of a key at once: the products' inner index is permuted so that lane t of
-// a quad has columns 16 t .. 16 t + 15 (and those 64 on), eight a step, of the queries
-// too.  Key 4 g + j of the tile is row g of the quarter j, so that a lane's four keys' exponents are one
-// word and its masks one nibble.  V comes transposed in 16-bit units (ldmatrix): two columns of
-// one key, which two byte permutations and two conversions turn into two keys of one column.
+// The products' inner index is permuted freely, as long as both operands agree: a lane of a quad has four
+// columns of 16 of a key or a query, which is what a 16-bit matrix load gives it of the bytes.  V comes
+// transposed byte by byte (four keys of one column), and two conversions make two pairs of keys of
+// it; the rows of the scores follow: row g of the half z of sixteen keys is key 4 (g / 2) + g % 2 + 2 z.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -41,8 +37,6 @@ namespace {
 
 using tc::ex2;
 using tc::fadd2;
-using tc::ffma2;
-using tc::fmul2;
 using tc::ld_shared_v4;
 using tc::pack_bf16x2;
 using tc::smem_u32;
@@ -72,8 +66,15 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
   return x;
 }
-__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// Two 16 x 16 matrices of bytes, transposed: lane (g, t) has row t .. t + 3 of columns g and g + 8 of each.
+__device__ __forceinline__ void ldm2t8(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
@@ -85,23 +86,13 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                      uint32_t b1) {
+// The same from zero.
+__device__ __forceinline__ void mma16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// Two numbers as e4m3, a in the low byte; x becomes what the rounding left out, times 16.
-__device__ __forceinline__ uint32_t take_e4m3(float& a, float& b) {
-  uint16_t y;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(b), "f"(a));
-  const uint32_t h = e4m3_pair(y);
-  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  a = (a - x.x) * 16.f;
-  b = (b - x.y) * 16.f;
-  return y;
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t y;
@@ -129,8 +120,7 @@ __device__ __forceinline__ float max4(const float (&x)[2][4], int at) {
 }
 
 // A tile in shared memory: rows of D bytes in lines of 128, their 16-byte pieces swizzled so that
-// the eight lanes of a phase meet eight banks' groups: keys 4 g + j of neighbouring g for K (bit 2 of
-// the row), of eight g for V.
+// the eight rows of a matrix load meet eight banks' groups: keys 4 i + {0, 1} or {2, 3} for K, eight in a row for V.
 template <int D>
 struct Place {
   static constexpr int CH = D / 16;        // pieces of a row
@@ -139,8 +129,13 @@ struct Place {
   static __device__ __forceinline__ uint32_t at(int r, int c, int swizzle) {
     return D == 128 ? r * 128 + ((c ^ swizzle) << 4) : (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ swizzle) << 4);
   }
-  static __device__ __forceinline__ uint32_t k_at(int r, int c) { return at(r, c, r & 4); }
-  static __device__ __forceinline__ uint32_t v_at(int r, int c) { return at(r, c, (r >> 2) & 7); }
+  static __device__ __forceinline__ uint32_t k_at(int r, int c) {
+    return at(r, c, D == 128 ? ((r >> 1) & 6) | (r & 1) : (r >> 2) & 3);
+  }
+  static __device__ __forceinline__ uint32_t v_at(int r, int c) { return at(r, c, D == 128 ? r & 7 : (r >> 1) & 3); }
+  // What kRows x rows further on the swizzle of a piece's address turns over.
+  static constexpr uint32_t k_turn(int x) { return D == 128 ? (x & 3) << 5 : (x & 1) << 5; }
+  static constexpr uint32_t v_turn(int x) { return D == 128 ? (x & 1) << 6 : 0; }
 };
 
 template <typename T, int D, int NT>
@@ -149,33 +144,21 @@ struct Config {
   static constexpr int kW = 4, kStages = kMany ? 2 : 3, kCtas = (kMany ? 3 : 2) * 152;
 };
 
-template <typename T> struct Parts;  // of a query's entry and of a weight
+template <typename T> struct Parts;  // N: of a query's entry and of a weight
 template <> struct Parts<__nv_bfloat16> {
   static constexpr int N = 1;
-  static constexpr bool kE4m3 = true;  // the query's, two; else N fp16 parts
-  // Sixteen columns.
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* x) {
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const uint4 raw = *reinterpret_cast<const uint4*>(p + 8 * y);
-      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[8 * y + 2 * i] = __uint_as_float(w[i] << 16);
-        x[8 * y + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    }
+  // Four columns.
+  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&x)[4]) {
+    const uint2 raw = *reinterpret_cast<const uint2*>(p);
+    x[0] = __uint_as_float(raw.x << 16), x[1] = __uint_as_float(raw.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(raw.y << 16), x[3] = __uint_as_float(raw.y & 0xFFFF0000u);
   }
 };
 template <> struct Parts<float> {
   static constexpr int N = 2;
-  static constexpr bool kE4m3 = false;
-  static __device__ __forceinline__ void load(const float* p, float* x) {
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const float4 q = *reinterpret_cast<const float4*>(p + 4 * y);
-      x[4 * y] = q.x, x[4 * y + 1] = q.y, x[4 * y + 2] = q.z, x[4 * y + 3] = q.w;
-    }
+  static __device__ __forceinline__ void load(const float* p, float (&x)[4]) {
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    x[0] = q.x, x[1] = q.y, x[2] = q.z, x[3] = q.w;
   }
 };
 
@@ -187,60 +170,42 @@ struct Spans {
 
 // A worker's rows over a segment.  Thread (g, t) = (lane / 4, lane % 4) holds the operands of rows
 // 8 n + g, and of rows 8 n + 2 t + x the factor of their scores, the reference points m and M, the sum
-// over its own keys l, and of the output o[n][y] columns 16 y + 2 g (x = 0, 1) and 16 y + 2 g + 1.
+// over its own keys l, and of the output o[n][y] columns 16 y + g (x = 0, 1) and 16 y + g + 8.
 template <typename T, int D, int NT>
 struct Rows {
   static constexpr int P = Parts<T>::N, K = D / 16;
-  static constexpr bool kE4m3 = Parts<T>::kE4m3;
-  static constexpr int kSteps = kE4m3 ? D / 32 : K;
-  uint32_t qb[NT][2][kSteps][2];
+  uint32_t qb[NT][P][K][2];
   float f[NT][2], m[NT][2], M[NT][2], l[NT][2], o[NT][K][4];
 
   // Row n of the tile's row 8 n + g.
   __device__ __forceinline__ void load_q(int n, const T* row, bool on, int d, float sl2) {
     const int lane = threadIdx.x & 31, t = lane & 3;
-    float x[D / 64][16];
+    float x[K][4];
     unsigned top = 0u;
 #pragma unroll
-    for (int h = 0; h < D / 64; ++h) {
-      const int c = 64 * h + 16 * t;
-      if (on && c < d) {
-        Parts<T>::load(row + c, x[h]);
+    for (int c = 0; c < K; ++c) {
+      if (on && 16 * c < d) {
+        Parts<T>::load(row + 16 * c + 4 * t, x[c]);
       } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[h][e] = 0.f;
+        x[c][0] = x[c][1] = x[c][2] = x[c][3] = 0.f;
       }
 #pragma unroll
-      for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[h][e]) & 0x7FFFFFFFu);
+      for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[c][e]) & 0x7FFFFFFFu);
     }
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
     const unsigned e = max(top >> 23, 15u);  // the largest is below 2^(e - 126)
-    constexpr unsigned kUp = kE4m3 ? 261u : 268u;  // 254 and 8 bits, or 15
-    const float up = __uint_as_float((kUp - e) << 23), down = __uint_as_float((e - (kUp - 254u)) << 23) * sl2;
+    const float up = __uint_as_float((268u - e) << 23), down = __uint_as_float((e - 14u) << 23) * sl2;
 #pragma unroll
-    for (int h = 0; h < D / 64; ++h)
+    for (int c = 0; c < K; ++c) {
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        float(&z)[16] = x[h];
-#pragma unroll
-        for (int c = 4 * w; c < 4 * w + 4; ++c) z[c] = fmaf(z[c], up, z[c] * 0.f);  // an infinity: NaN
-        if constexpr (kE4m3) {
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const uint32_t lo = take_e4m3(z[4 * w], z[4 * w + 1]), hi = take_e4m3(z[4 * w + 2], z[4 * w + 3]);
-            qb[n][p][2 * h + (w >> 1)][w & 1] = lo | hi << 16;
-          }
-        } else {
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float a = z[4 * w + 2 * y], b = z[4 * w + 2 * y + 1];
-            const uint32_t hi = pack_f16x2(a, b);
-            qb[n][0][4 * h + w][y] = hi;
-            qb[n][1][4 * h + w][y] = rest_f16x2(a, b, hi);
-          }
-        }
+      for (int y = 0; y < 2; ++y) {
+        const float p = x[c][2 * y] * up, q = x[c][2 * y + 1] * up;
+        const uint32_t hi = pack_f16x2(p, q);
+        qb[n][0][c][y] = hi;
+        if (P == 2) qb[n][P - 1][c][y] = rest_f16x2(p, q, hi);
       }
+    }
 #pragma unroll
     for (int x2 = 0; x2 < 2; ++x2) f[n][x2] = __shfl_sync(0xFFFFFFFFu, down, 4 * (2 * t + x2));
   }
@@ -258,75 +223,77 @@ struct Rows {
   __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, uint32_t et, unsigned have, int key0,
                                        const Spans<NT>& sp, int v) {
     const int lane = threadIdx.x & 31, g = lane >> 2;
-    const uint32_t ke = lds32(et + 4 * g), ve = lds32(et + 32 + 4 * g);
-    // [row tile][pair of quarters j = 2 q, 2 q + 1][2 (j & 1) + row]; the second e4m3 part's.
-    float sc[NT][2][4], low[NT][2][4];
+    // Of the sixteen keys q, half z (key `first` + 16 q + 2 z): bytes 2 z of the words.
+    const int first = 4 * (g >> 1) + (g & 1);
+    uint32_t ke[2], ve[2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[n][q][e] = low[n][q][e] = 0.f;
+    for (int q = 0; q < 2; ++q) {
+      ke[q] = lds32(et + 16 * q + 4 * (g >> 1)) >> 8 * (g & 1);
+      ve[q] = lds32(et + 32 + 16 * q + 4 * (g >> 1)) >> 8 * (g & 1);
+    }
+    float sc[NT][2][4];  // [row tile][sixteen keys][2 z + row]
     {
-      const uint32_t at = kt + Place<D>::k_at(4 * g, lane & 3);
+      const int i = lane & 7, b = lane >> 3;  // matrices: half b % 2, piece b / 2 of two
+      const uint32_t at = kt + Place<D>::k_at(4 * (i >> 1) + (i & 1) + 2 * (b & 1), b >> 1);
 #pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
-        uint4 k[4];
+      for (int s = 0; s < D / 32; ++s)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          k[j] = ld_shared_v4(D == 128 ? (at ^ (h << 6)) + j * 128 : (at ^ ((j & 1) << 6)) + (j >> 1) * 128);
+        for (int q = 0; q < 2; ++q) {
+          uint32_t k[4];
+          ldm4(k, (at ^ (s << 5)) + q * (16 * D));
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t a[4] = {e4m3_pair(k[2 * c]), e4m3_pair(k[2 * c + 1]), e4m3_pair_high(k[2 * c]),
+                                   e4m3_pair_high(k[2 * c + 1])};
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            auto word = [&](const uint4& x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; };
-            if constexpr (kE4m3) {
-              if (w & 1) continue;  // two words a step
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-                  mma32(p ? low[n][q] : sc[n][q], word(k[2 * q], w), word(k[2 * q + 1], w), word(k[2 * q], w + 1),
-                        word(k[2 * q + 1], w + 1), qb[n][p][2 * h + (w >> 1)][0], qb[n][p][2 * h + (w >> 1)][1]);
-            } else {
-              const uint32_t x0 = word(k[2 * q], w), x1 = word(k[2 * q + 1], w);
-              const uint32_t a[4] = {e4m3_pair(x0), e4m3_pair(x1), e4m3_pair_high(x0), e4m3_pair_high(x1)};
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-                  mma16(sc[n][q], a, qb[n][p][4 * h + w][0], qb[n][p][4 * h + w][1]);
-            }
+              for (int p = 0; p < P; ++p) {
+                const uint32_t(&b)[2] = qb[n][p][2 * s + c];
+                if (s == 0 && c == 0 && p == 0) mma16_first(sc[n][q], a, b[0], b[1]);
+                else mma16(sc[n][q], a, b[0], b[1]);
+              }
           }
-      }
+        }
     }
     // Scores into the exp2 domain, those that do not count to -inf; w beside them.
-    const bool whole = have == 0xFFFFFFFFu && key0 >= sp.all_lo && key0 + kTile <= sp.all_hi;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const float kf = e4m3_scale((ke[q] >> (16 * z)) & 255u);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float &s0 = sc[n][q][2 * z], &s1 = sc[n][q][2 * z + 1];
+          s0 *= f[n][0] * kf;
+          s1 *= f[n][1] * kf;
+        }
+      }
+    if (have != 0xFFFFFFFFu || key0 < sp.all_lo || key0 + kTile > sp.all_hi) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = first + 16 * q + 2 * (e >> 1), x = e & 1;
+            if (!((have >> key) & 1u) || key0 + key < sp.lo[n][x] || key0 + key >= sp.hi[n][x]) sc[n][q][e] = -INFINITY;
+          }
+    }
     float wt[NT][2][4], over = kNoKey;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int z = 0; z < 2; ++z) {
+        const float vx = __uint_as_float(0x4B000000u | ((ve[q] >> (16 * z)) & 255u)) - 8388735.f;  // byte - 127
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          const int j = 2 * q + z;
-          const float kf = e4m3_scale((ke >> (8 * j)) & 255u);
-          const float vx = __uint_as_float(0x4B000000u | ((ve >> (8 * j)) & 255u)) - 8388735.f;  // byte - 127
-          float &s0 = sc[n][q][2 * z], &s1 = sc[n][q][2 * z + 1], f0, f1;
-          if (kE4m3) ffma2(s0, s1, low[n][q][2 * z], low[n][q][2 * z + 1], 0x1p-4f, 0x1p-4f, s0, s1);
-          fmul2(f0, f1, f[n][0], f[n][1], kf, kf);
-          fmul2(s0, s1, s0, s1, f0, f1);
-          if (!whole) {
-            const int key = 4 * g + j;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-              if (!((have >> key) & 1u) || key0 + key < sp.lo[n][x] || key0 + key >= sp.hi[n][x])
-                sc[n][q][2 * z + x] = -INFINITY;
+          for (int x = 0; x < 2; ++x) {
+            const float s = sc[n][q][2 * z + x], w = wt[n][q][2 * z + x] = s + vx;
+            over = tc::fmax3(over, s - m[n][x], w - M[n][x]);
           }
-          float &w0 = wt[n][q][2 * z], &w1 = wt[n][q][2 * z + 1];
-          fadd2(w0, w1, s0, s1, vx, vx);
-          over = fmaxf(over, fmaxf(fmaxf(s0 - m[n][0], s1 - m[n][1]), fmaxf(w0 - M[n][0], w1 - M[n][1])));
-        }
+      }
     if (__any_sync(0xFFFFFFFFu, over > kRescale)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -367,19 +334,21 @@ struct Rows {
         }
     }
     {
-      const uint32_t at = vt + Place<D>::v_at(4 * (lane & 7) + (lane >> 3), 0);
+      const uint32_t at = vt + Place<D>::v_at(lane, 0);
 #pragma unroll
       for (int y = 0; y < K; ++y) {
         // (A branch for every y keeps the steps apart: 16 rows over 262147 keys 141 us in place of 129.)
         if (y == 4 && v <= 64) break;
-        uint32_t r[4];  // quarter j: columns 2 g and 2 g + 1 of keys 2 t and 2 t + 1 of it
-        ldm4t(r, at ^ (y << 4));
+        uint32_t r[4];  // of sixteen keys q: keys 4 t to 4 t + 3 of columns 16 y + g and 16 y + g + 8
+        ldm2t8(r, at ^ (y << 4));
         uint32_t a[2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          a[j >> 1][2 * (j & 1)] = e4m3_pair(__byte_perm(r[j], 0u, 0x4420));
-          a[j >> 1][2 * (j & 1) + 1] = e4m3_pair(__byte_perm(r[j], 0u, 0x4431));
-        }
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            a[q][h] = e4m3_pair(r[2 * q + h]);
+            a[q][2 + h] = e4m3_pair_high(r[2 * q + h]);
+          }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           if constexpr (P == 1) {
@@ -388,11 +357,14 @@ struct Rows {
           } else {
             // A tile's products are summed by the tensor cores, which cut their sums instead of
             // rounding them, and added to the output in rounded fp32.
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            float sum[4];
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
-              for (int p = P - 1; p >= 0; --p) mma16(sum, a[q], pb[n][p][q][0], pb[n][p][q][1]);
+              for (int p = P - 1; p >= 0; --p) {
+                if (q == 0 && p == P - 1) mma16_first(sum, a[q], pb[n][p][q][0], pb[n][p][q][1]);
+                else mma16(sum, a[q], pb[n][p][q][0], pb[n][p][q][1]);
+              }
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][y][e] += sum[e];
           }
@@ -406,8 +378,8 @@ struct Rows {
 template <int CH, int... X>
 __device__ __forceinline__ void copy_dense(uint32_t k, uint32_t v, uint32_t up, const uint8_t* kf, const uint8_t* vf,
                                            std::integer_sequence<int, X...>) {
-  (cp16_at<512 * X, 512 * X>((k ^ (CH == 8 ? (X & 1) << 6 : 0)) + up, kf), ...);
-  (cp16_at<512 * X, 512 * X>((v ^ (CH == 8 ? X << 4 : X << 5)) + up, vf), ...);
+  (cp16_at<512 * X, 512 * X>((k ^ Place<16 * CH>::k_turn(X)) + up, kf), ...);
+  (cp16_at<512 * X, 512 * X>((v ^ Place<16 * CH>::v_turn(X)) + up, vf), ...);
 }
 
 template <typename T, int D, int NT>
@@ -498,7 +470,7 @@ __global__ void __launch_bounds__(32 * Config<T, D, NT>::kW, Config<T, D, NT>::k
   for (int it = 0, i = 1 - S; more || p_left > 0 || i < issued; ++it, ++i) {
     // Segments that start here: who = 0 the copies', 1 the products'.
 #pragma unroll 1
-    for (int who = 0; who < 2; ++who) {
+    for (int who = (p_left == 0 && more) || (left == 0 && i >= 0 && i < issued) ? 0 : 2; who < 2; ++who) {
       const bool starts = who == 0 ? p_left == 0 && more : left == 0 && i >= 0 && i < issued;
       if (!starts) continue;
       PagedWalk w = walks[warp][who];
@@ -581,10 +553,8 @@ __global__ void __launch_bounds__(32 * Config<T, D, NT>::kW, Config<T, D, NT>::k
         for (int x = 0; x < CH; ++x) {
           const int z = CH == 8 ? x >> 1 : x, on = CH == 8 ? 4 * (x & 1) : 0;
           const int bytes = whole ? 16 : ((have >> (pr + At::kRows * x)) & 1u) << 4;
-          // Rows kRows x further: 512 bytes, and the swizzle's bits of x.
-          const uint32_t k_x = CH == 8 ? (x & 1) << 6 : 0, v_x = CH == 8 ? x << 4 : x << 5;
-          if (k_on) cp16((k_to ^ k_x) + up + 512 * x, Kp + (row[z] + on) * d, bytes);
-          if (v_on) cp16((v_to ^ v_x) + up + 512 * x, Vp + (row[z] + on) * v, bytes);
+          if (k_on) cp16((k_to ^ At::k_turn(x)) + up + 512 * x, Kp + (row[z] + on) * d, bytes);
+          if (v_on) cp16((v_to ^ At::v_turn(x)) + up + 512 * x, Vp + (row[z] + on) * v, bytes);
         }
       };
       if (have == 0xFFFFFFFFu) copy(std::true_type{});
@@ -614,42 +584,58 @@ __global__ void __launch_bounds__(32 * Config<T, D, NT>::kW, Config<T, D, NT>::k
     const int n = paged_segment<kTile>(w, j0, j1);
     const PagedPlace place = paged_place<kRows>(a, total, w, n, worker, lane == 0);
 #pragma unroll
-    for (int y = 0; y < NT; ++y)
+    for (int y = 0; y < NT; ++y) {
+      size_t to[2];
+      bool on[2];
+      float f0[2], f1[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int q = 8 * y + 2 * t + x;
-        const bool on = q < w.t.rows;
+        on[x] = q < w.t.rows;
         float l = st.l[y][x];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-        if (!on) continue;
-        const size_t out = paged_out_row(a, w.s.s0, w.h, w.rt * kRows + q, w.s.prefix);
-        if (a.info && place.parts >= 0 && g == 0) a.info[out] = make_int2(worker, place.parts);
+        const size_t out = paged_out_row(a, w.s.s0, w.h, w.rt * kRows + (on[x] ? q : 0), w.s.prefix);
+        const bool none = l == 0.f;  // no key
+        const float m = none ? -INFINITY : st.m[y][x];
+        PagedScale f{1.f, 0.f};
+        if (place.slot < 0) f = paged_finish(m, l);
+        to[x] = place.slot < 0 ? out : static_cast<size_t>(place.slot) * kRows + q;
+        if (on[x] && g == 0) {
+          if (a.info && place.parts >= 0) a.info[out] = make_int2(worker, place.parts);
+          if (place.slot < 0) {
+            a.L[out] = f.L;
+          } else {
+            a.pm[to[x]] = m;
+            a.pl[to[x]] = l;
+          }
+        }
         // From the weights' reference point to the scores', in two factors: 2^(M - m) may be
         // subnormal where what it multiplies is not.
-        const bool none = l == 0.f;  // no key
-        const float half = none ? 0.f : ex2(0.5f * (st.M[y][x] - kLift - st.m[y][x])), m = none ? -INFINITY : st.m[y][x];
-        PagedScale f{1.f, 0.f};
-        if (place.slot < 0) {
-          f = paged_finish(m, l);
-          if (g == 0) a.L[out] = f.L;
-        } else if (g == 0) {
-          a.pm[static_cast<size_t>(place.slot) * kRows + q] = m;
-          a.pl[static_cast<size_t>(place.slot) * kRows + q] = l;
-        }
-        const float rest = half * f.fz;
-        float* z = place.slot < 0 ? a.Yf : a.pz;
-        const size_t to = (place.slot < 0 ? out : static_cast<size_t>(place.slot) * kRows + q) * v;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const int col = 16 * c + 2 * g;
-          if (16 * c >= v) break;
-          const float z0 = st.o[y][c][x] * half * rest, z1 = st.o[y][c][2 + x] * half * rest;
-          if (z) *reinterpret_cast<float2*>(z + to + col) = make_float2(z0, z1);
-          else if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(static_cast<float*>(a.Y) + to + col) = make_float2(z0, z1);
-          else *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.Y) + to + col) = pack_bf16x2(z0, z1);
-        }
+        f0[x] = none ? 0.f : ex2(0.5f * (st.M[y][x] - kLift - st.m[y][x]));
+        f1[x] = f0[x] * f.fz;
       }
+      float* z = place.slot < 0 ? a.Yf : a.pz;
+      if (sizeof(T) == 4 && !z) z = static_cast<float*>(a.Y);
+      if (z) {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (on[x] && 8 * c < v) z[to[x] * v + 8 * c + g] = st.o[y][c >> 1][2 * (c & 1) + x] * f0[x] * f1[x];
+        continue;
+      }
+      // Lane (g, t) stores row g of the tile, two columns at a time, after a transposition.
+      const size_t r0 = __shfl_sync(0xFFFFFFFFu, to[0], g >> 1), r1 = __shfl_sync(0xFFFFFFFFu, to[1], g >> 1);
+      __nv_bfloat16* mine = static_cast<__nv_bfloat16*>(a.Y) + (g & 1 ? r1 : r0) * v + 2 * t;
+      const bool mine_on = 8 * y + g < w.t.rows;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const float* o = &st.o[y][c >> 1][2 * (c & 1)];
+        const uint32_t pair = transpose8(pack_bf16x2(o[0] * f0[0] * f1[0], o[1] * f0[1] * f1[1]));
+        if (mine_on && 8 * c < v) *reinterpret_cast<uint32_t*>(mine + 8 * c) = pair;
+      }
+    }
   }
   cp_wait<0>();
   if (a.second) wait_for_previous();  // the next launch waits for this one alone

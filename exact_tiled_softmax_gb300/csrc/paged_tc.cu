@@ -50,12 +50,12 @@ constexpr int kRows = 2 * kHalf;
 constexpr int kUnit = 128;
 constexpr int kCtas = 152;
 constexpr int kWarpTMA = 8, kWarpMMA = 9, kWarpQ = 10, kWarpConvert = 12;
-// kBytes: pages in 8 bits, with four warps more, which convert them.
+constexpr int kSoftmaxRegs = 208;
+constexpr int kProducerRegs = 88;
+// kBytes: pages in 8 bits, with four warps more, which convert them, and 128 registers for every thread.
 template <bool kBytes>
 struct Warps {
   static constexpr int kThreads = kBytes ? 512 : 384;
-  static constexpr int kSoftmaxRegs = kBytes ? 184 : 208;
-  static constexpr int kProducerRegs = kBytes ? 72 : 88;
   static constexpr int kTakers = kBytes ? 15 : 11;  // warps that read a segment from the ring
 };
 constexpr int kQThreads = 64;
@@ -135,6 +135,79 @@ __device__ __forceinline__ void bytes_to_bf16(const uint4& raw, float f, uint32_
     fmul2(x0, x1, x.x, x.y, f, f);
     y[i] = pack_bf16x2(x0, x1);
   }
+}
+
+// A block's softmax for sixteen warps, which leave a thread 128 registers: the row's scores are read
+// twice, 64 at a time, once for the maximum.  Keys lo to hi of the block where `mw` has them.
+template <int D>
+__device__ __forceinline__ void softmax_by_halves(uint32_t t_s, uint32_t t_o, bool whole, const uint32_t (&mw)[4],
+                                                  int lo, int hi, float sl2, float& m_ref, float& l) {
+  auto load = [&](int half, uint32_t (&s)[64]) {
+    tmem_ld32(t_s + 64 * half, *reinterpret_cast<uint32_t(*)[32]>(s));
+    tmem_ld32(t_s + 64 * half + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+    tmem_ld_wait();
+    reg_fence(s);
+    if (!whole) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t w = mw[2 * half + q] & range_bits(lo - 32 * (2 * half + q), hi - 32 * (2 * half + q));
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (!((w >> c) & 1u)) s[32 * q + c] = __float_as_uint(-INFINITY);
+      }
+    }
+  };
+  float mx = -INFINITY;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t s[64];
+    load(half, s);
+    float mx4[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mx4[k] = __uint_as_float(s[k]);
+#pragma unroll
+    for (int c = 4; c + 8 <= 64; c += 8)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mx4[k] = fmax3(mx4[k], __uint_as_float(s[c + k]), __uint_as_float(s[c + 4 + k]));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mx = fmax3(mx, mx4[k], __uint_as_float(s[60 + k]));
+  }
+  const float m_new = fmaxf(m_ref, mx * sl2);  // sl2 > 0
+  const bool need = m_ref != -INFINITY && m_new > m_ref + kRescale;
+  if (m_ref == -INFINITY) m_ref = m_new;
+  if (__any_sync(0xFFFFFFFFu, need)) {
+    const float alpha = need ? ex2(m_ref - m_new) : 1.f;
+    if (need) m_ref = m_new;
+    l *= alpha;
+#pragma unroll
+    for (int ch = 0; ch < D / 32; ++ch) {
+      uint32_t o[32];
+      tmem_ld32(t_o + ch * 32, o);
+      tmem_ld_wait();
+      reg_fence(o);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+      tmem_st32(t_o + ch * 32, o);
+    }
+  }
+  const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+  float sum2[4][2] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t s[64], pk[32];
+    load(half, s);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      float x0, x1;
+      ffma2(x0, x1, __uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]), sl2, sl2, neg, neg);
+      const float p0 = ex2(x0), p1 = ex2(x1);
+      fadd2(sum2[e & 3][0], sum2[e & 3][1], sum2[e & 3][0], sum2[e & 3][1], p0, p1);
+      pk[e] = pack_bf16x2(p0, p1);
+    }
+    tmem_st32(t_s + 32 * half, pk);
+  }
+  l += ((sum2[0][0] + sum2[0][1]) + (sum2[1][0] + sum2[1][1])) + ((sum2[2][0] + sum2[2][1]) + (sum2[3][0] + sum2[3][1]));
+  tmem_st_wait();
 }
 
 template <int D, bool kBytes>
@@ -218,7 +291,7 @@ __global__ void __launch_bounds__(Warps<kBytes>::kThreads, 1)
   // ring of tiles, V fill 2 blk + 1.
 
   if (warp >= 8) {
-    regs_dec<Warps<kBytes>::kProducerRegs>();
+    if constexpr (!kBytes) regs_dec<kProducerRegs>();
     const bool leader = elect_one();
     if constexpr (kBytes) {
       if (warp >= kWarpConvert) {
@@ -558,7 +631,7 @@ __global__ void __launch_bounds__(Warps<kBytes>::kThreads, 1)
       }
     }
   } else {
-    regs_inc<Warps<kBytes>::kSoftmaxRegs>();
+    if constexpr (!kBytes) regs_inc<kSoftmaxRegs>();
     const int X = warp >> 2;
     const int wl = warp & 3;
     const int rl = X * kHalf + wl * 32 + lane;  // row of the tile
@@ -600,6 +673,12 @@ __global__ void __launch_bounds__(Warps<kBytes>::kThreads, 1)
         const bool whole = (mw[0] & mw[1] & mw[2] & mw[3]) == 0xFFFFFFFFu && kb >= all_lo && kb + kUnit <= all_hi;
         tc_fence_after();
         ++cnt;
+        if constexpr (kBytes) {
+          softmax_by_halves<D>(t_s, t_o, whole, mw, lo - kb, hi - 1 - kb, sl2, m_ref, l);
+          tc_fence_before();
+          mbar_arrive(bar(Lay::B_P + X));
+          continue;
+        }
         uint32_t s[128];
         tmem_ld32(t_s + 0, *reinterpret_cast<uint32_t(*)[32]>(s + 0));
         tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));

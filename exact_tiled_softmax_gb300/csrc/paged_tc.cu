@@ -50,13 +50,16 @@ constexpr int kRows = 2 * kHalf;
 constexpr int kUnit = 128;
 constexpr int kCtas = 152;
 constexpr int kWarpTMA = 8, kWarpMMA = 9, kWarpQ = 10, kWarpConvert = 12;
-constexpr int kSoftmaxRegs = 208;
-constexpr int kProducerRegs = 88;
-// kBytes: pages in 8 bits, with four warps more, which convert them, and 128 registers for every thread.
+// kBytes: pages in 8 bits, with four warps more, which convert them: half of its time, one warp's latency
+// after another (221 us in place of 277 without the conversion), but eight warps leave the softmax too few
+// registers (268 us, and 254 without the conversion).
+constexpr int kConverters = 4;
 template <bool kBytes>
 struct Warps {
-  static constexpr int kThreads = kBytes ? 512 : 384;
-  static constexpr int kTakers = kBytes ? 15 : 11;  // warps that read a segment from the ring
+  static constexpr int kSoftmaxRegs = kBytes ? 168 : 208;
+  static constexpr int kProducerRegs = 88;
+  static constexpr int kThreads = 384 + (kBytes ? 32 * kConverters : 0);
+  static constexpr int kTakers = 11 + (kBytes ? kConverters : 0);  // warps that read a segment from the ring
 };
 constexpr int kQThreads = 64;
 constexpr float kRescale = 8.f;
@@ -137,7 +140,7 @@ __device__ __forceinline__ void bytes_to_bf16(const uint4& raw, float f, uint32_
   }
 }
 
-// A block's softmax for sixteen warps, which leave a thread 128 registers: the row's scores are read
+// A block's softmax for sixteen warps, which leave these 168 registers: the row's scores are read
 // twice, 64 at a time, once for the maximum.  Keys lo to hi of the block where `mw` has them.
 template <int D>
 __device__ __forceinline__ void softmax_by_halves(uint32_t t_s, uint32_t t_o, bool whole, const uint32_t (&mw)[4],
@@ -233,12 +236,12 @@ __global__ void __launch_bounds__(Warps<kBytes>::kThreads, 1)
     mbar_init(bar(Lay::B_Q), kQThreads);
     mbar_init(bar(Lay::B_QFREE), 1);
     for (int s = 0; s < NS; ++s) {
-      mbar_init(bar(Lay::B_KVF + s), kBytes ? 128 : 1);
+      mbar_init(bar(Lay::B_KVF + s), kBytes ? 32 * kConverters : 1);
       mbar_init(bar(Lay::B_KVE + s), 1);
     }
     for (int s = 0; s < Lay::NRAW; ++s) {
       mbar_init(bar(Lay::B_RF + s), 1);
-      mbar_init(bar(Lay::B_RE + s), 4);
+      mbar_init(bar(Lay::B_RE + s), kConverters);
     }
     for (int X = 0; X < 2; ++X) {
       mbar_init(bar(Lay::B_S + X), 1);
@@ -291,14 +294,15 @@ __global__ void __launch_bounds__(Warps<kBytes>::kThreads, 1)
   // ring of tiles, V fill 2 blk + 1.
 
   if (warp >= 8) {
-    if constexpr (!kBytes) regs_dec<kProducerRegs>();
+    regs_dec<Warps<kBytes>::kProducerRegs>();
     const bool leader = elect_one();
     if constexpr (kBytes) {
       if (warp >= kWarpConvert) {
         // A raw tile to bf16 in the products' 128-byte swizzled layout, its rows' powers of two in: warp
-        // by warp 32 rows.  A lane takes 16 columns: quads have four pieces of a row, and neighbouring rows
+        // by warp.  A lane takes 16 columns: quads have four pieces of a row, and neighbouring rows
         // the two halves of one, so that neither the loads nor the stores of eight lanes meet in a bank.
-        const int wr = (warp - kWarpConvert) * 32, q = lane & 3, odd = (lane >> 2) & 1;
+        constexpr int kRowsOf = kUnit / kConverters;
+        const int wr = (warp - kWarpConvert) * kRowsOf, q = lane & 3, odd = (lane >> 2) & 1;
         volatile uint32_t* rkeep = reinterpret_cast<volatile uint32_t*>(smem + Lay::RKEEP_OFF);
         bool ok = true;
         int fill = 0;
@@ -311,14 +315,15 @@ __global__ void __launch_bounds__(Warps<kBytes>::kThreads, 1)
             // V: rows without a key are zero, whatever their page holds (K's scores do not count).
             uint32_t mine = rkeep[rs * 4 + (wr >> 5)];
             if (!(u & 1)) {
-              if (lane == 0) keep[(fill / 2 % Lay::kKeepBlocks) * 4 + (wr >> 5)] = mine;
+              if (lane == 0 && (wr & 31) == 0) keep[(fill / 2 % Lay::kKeepBlocks) * 4 + (wr >> 5)] = mine;
               mine = 0xFFFFFFFFu;
             }
+            mine >>= wr & 31;
             const uint8_t* ex = smem + Lay::EXP_OFF + rs * kUnit + wr;
             const uint32_t raw = sbase + Lay::RAW_OFF + rs * Lay::RAW + wr * D;
             const uint32_t to = sbase + Lay::SLOT_OFF + ks * Lay::SLOT + wr * 128;
-#pragma unroll 2
-            for (int y = 0; y < D / 16; ++y) {
+#pragma unroll 4
+            for (int y = 0; y < D / 16 * kRowsOf / 32; ++y) {
               const int r = (D == 128 ? y >> 1 : y) * 8 + 2 * (lane >> 3) + odd;  // of the warp's rows
               const int piece = q + (D == 128 ? 4 * (odd ^ (y & 1)) : 0);
               uint4 x = ld_shared_v4(raw + r * D + piece * 16);
@@ -631,7 +636,7 @@ __global__ void __launch_bounds__(Warps<kBytes>::kThreads, 1)
       }
     }
   } else {
-    if constexpr (!kBytes) regs_inc<kSoftmaxRegs>();
+    regs_inc<Warps<kBytes>::kSoftmaxRegs>();
     const int X = warp >> 2;
     const int wl = warp & 3;
     const int rl = X * kHalf + wl * 32 + lane;  // row of the tile

@@ -14,6 +14,7 @@
 // four rows at two CTAs 4.05, and in fp32 six CTAs 5.74, five 5.01.  One CTA more checks
 // that every token has a place and writes the status word.
 #include "paged.cuh"
+#include "tc_ptx.cuh"
 
 namespace exattn {
 namespace {
@@ -21,6 +22,9 @@ namespace {
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
 constexpr int kMaxPairs = 128;
+// CTAs of an SM: four 157 us for 37 thousand tokens of 32 + 8 + 8 rows of 128 bf16 columns (5.2 TB/s, 77% of the
+// measured copy), three 158, five 195 (which spill); two rows ahead 165.
+constexpr int kAppendCtas8 = 4;
 
 // The sequence that owns token t, or -1.
 __device__ __forceinline__ int owner(const AppendArgs& a, int t) {
@@ -284,7 +288,7 @@ cudaError_t append_dispatch(const AppendArgs& a, cudaStream_t s) {
 // near: once in 2^16 entries.  Such entries are computed again in 64 bits (FP64 does two operations
 // a clock and SM: a pair costs a warp half a microsecond), and so are all of a row whose
 // maximum lies that near to 448 times a power of two.  The codes are those of 64-bit arithmetic.
-constexpr float kTurnError = 4e-7f;  // > 2^-22 sqrt(2), of |y0| + |y1|
+constexpr float kTurnError = 4e-7f;  // > 2^-22 sqrt(2), of the sum of the pair's magnitudes, before or after
 
 // Where the pairs of a row are: halves that 8-column accesses reach, neighbours, or anywhere.
 enum PairForm { kHalves, kInside, kAnywhere };
@@ -323,19 +327,36 @@ __device__ __forceinline__ int exponent_of(unsigned long long top) {
   return top == 0ull ? 0 : max(1, static_cast<int>((top + 0x3FFFFFFFFFFFFull) >> 52) - 1023 + 127 - 8);
 }
 
-__device__ __forceinline__ void load8(const float* p, float* x) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+// Eight columns from each of two places of a row, as they are loaded.
+template <typename T> struct Raw16;
+template <> struct Raw16<__nv_bfloat16> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, const __nv_bfloat16* q) {
+    a = *reinterpret_cast<const uint4*>(p);
+    b = *reinterpret_cast<const uint4*>(q);
   }
-}
+  __device__ __forceinline__ void to(float (&x)[16]) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
+template <> struct Raw16<float> {
+  float4 v[4];
+  __device__ __forceinline__ void load(const float* p, const float* q) {
+    v[0] = *reinterpret_cast<const float4*>(p);
+    v[1] = *reinterpret_cast<const float4*>(p + 4);
+    v[2] = *reinterpret_cast<const float4*>(q);
+    v[3] = *reinterpret_cast<const float4*>(q + 4);
+  }
+  __device__ __forceinline__ void to(float (&x)[16]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[4 * i] = v[i].x, x[4 * i + 1] = v[i].y, x[4 * i + 2] = v[i].z, x[4 * i + 3] = v[i].w;
+  }
+};
 __device__ __forceinline__ void store8(float* p, const float* x) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
@@ -346,21 +367,246 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
   for (int e = 0; e < 8; ++e) from_float(y.x[e], x[e]);
   *reinterpret_cast<Piece<__nv_bfloat16, 8>*>(p) = y;
 }
+// Where pair f's cosine stands: the fours of a lane's eight apart, so that lanes read next to one another.
+__device__ __forceinline__ int pair_at(int f) { return ((f & 4) << 4) + ((f >> 3) << 2) + (f & 3); }
+__device__ __forceinline__ void load_pairs(const float* c, int u, float (&x)[8]) {
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const float4 v = *reinterpret_cast<const float4*>(c + 64 * y + 4 * u);
+    x[4 * y] = v.x, x[4 * y + 1] = v.y, x[4 * y + 2] = v.z, x[4 * y + 3] = v.w;
+  }
+}
+
+enum RowKind { kQuery, kKey, kValue };
+// What the rows of a token share.
+struct TokenRows {
+  long long slot, at;  // row of the pool of key head 0, position with its offset
+  const float* cs;
+  const float* sn;
+};
+// A lane's columns of a row: eight from c0 on, eight from c1 on.
+struct Columns {
+  int c0, c1, w;
+  bool has;
+};
+template <PairForm kForm, RowKind kKind>
+__device__ __forceinline__ Columns columns_of(const AppendArgs& a, int u) {
+  Columns c;
+  c.w = kKind == kValue ? a.vw : a.d;
+  c.c0 = 16 * u;
+  c.c1 = c.c0 + 8;
+  c.has = 16 * u < c.w;
+  if (kKind != kValue && kForm == kHalves && a.pairs > 0) {
+    const int half = a.pairs >> 3;
+    c.c0 = u < half ? 8 * u : 2 * a.pairs + 16 * (u - half);
+    c.c1 = u < half ? a.pairs + 8 * u : c.c0 + 8;
+  }
+  return c;
+}
+
+// One pass over rows of one kind: row r of `rows` for each kLanes lanes, its columns `raw`; rotated, and into q_out
+// or quantised into their page.
+template <typename T, int kLanes, PairForm kForm, RowKind kKind>
+__device__ __forceinline__ void append_pass(const AppendArgs& a, const TokenRows& t, const T* rows, T* q_out, int r, int n,
+                                            const Raw16<T>& raw) {
+  constexpr bool kTurns = kKind != kValue;
+  const int u = threadIdx.x % kLanes, pairs = a.pairs;
+  const Columns col = columns_of<kForm, kKind>(a, u);
+  const int c0 = col.c0, c1 = col.c1, w = col.w;
+  const bool on = col.has && r < n;
+  const bool turned = kTurns && col.has && (kForm == kAnywhere ? c0 < 2 * pairs : 8 * u < pairs);
+  {
+    float y[16];
+    if (on) {
+      raw.to(y);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) y[e] = 0.f;
+    }
+    [[maybe_unused]] float x0[16], x1[16];  // the pairs, where a lane does not have both of each
+    if (turned && on) {
+      if constexpr (kForm == kAnywhere) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int c = c0 + e;
+          x0[e] = x1[e] = 0.f;
+          if (c >= 2 * pairs) continue;
+          const bool first = c < pairs;
+          const int f = first ? c : c - pairs;
+          const float other = as_float(rows[r * w + (first ? c + pairs : f)]), k = t.cs[pair_at(f)], s = t.sn[pair_at(f)];
+          x0[e] = y[e];
+          x1[e] = other;
+          y[e] = first ? y[e] * k - other * s : y[e] * k + other * s;
+        }
+      } else {
+        float k[8], s[8];
+        load_pairs(t.cs, u, k);
+        load_pairs(t.sn, u, s);
+        if constexpr (kForm == kHalves) {  // two pairs at once
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            float p0, p1, q0, q1;
+            tc::fmul2(p0, p1, y[8 + e], y[9 + e], -s[e], -s[e + 1]);
+            tc::fmul2(q0, q1, y[e], y[e + 1], s[e], s[e + 1]);
+            tc::ffma2(p0, p1, y[e], y[e + 1], k[e], k[e + 1], p0, p1);
+            tc::ffma2(y[8 + e], y[9 + e], y[8 + e], y[9 + e], k[e], k[e + 1], q0, q1);
+            y[e] = p0;
+            y[e + 1] = p1;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (8 * u + e >= pairs) continue;
+            float &p = y[2 * e], &q = y[2 * e + 1];
+            const float u0 = p, u1 = q;
+            p = u0 * k[e] - u1 * s[e];
+            q = u1 * k[e] + u0 * s[e];
+          }
+        }
+      }
+    }
+    if constexpr (kKind == kQuery) {
+      if (kForm == kAnywhere) __syncwarp();  // q_out may be q: every lane has read the pairs' others
+      if (on) {
+        store8(q_out + r * w + c0, y);
+        store8(q_out + r * w + c1, y + 8);
+      }
+      return;
+    }
+    // Every lane of a row's, also those without columns.  An infinity is found by the maximum.
+    float most = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) most = tc::fmax3(most, fabsf(y[e]), fabsf(y[e + 1]));
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+    unsigned top = __float_as_uint(most);
+    if (__any_sync(0xFFFFFFFFu, top == 0x7F800000u)) {  // the largest finite one
+      top = 0u;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const unsigned m = __float_as_uint(y[e]) & 0x7FFFFFFFu;
+        top = max(top, m < 0x7F800000u ? m : 0u);
+        if (m == 0x7F800000u) y[e] = NAN;
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    }
+    int ex = exponent_of(top);
+    uint32_t again = 0u;  // entries to be computed again
+    const T* row = rows + r * w;
+    if constexpr (kTurns) {
+      // (8 units of the last place are more than the error of a pair that is no longer than twice its row's largest.)
+      const bool near = pairs > 0 && top > 8u && exponent_of(top - 8u) != exponent_of(top + 8u);
+      if (__any_sync(0xFFFFFFFFu, near)) {
+        unsigned long long largest = 0ull;
+        if (near && on)
+#pragma unroll 1
+          for (int e = 0; e < 16; ++e) {
+            const double z = turned64(row, (e < 8 ? c0 : c1 - 8) + e, pairs, kForm == kInside, t.at, a.inv_freq);
+            const unsigned long long m = static_cast<unsigned long long>(__double_as_longlong(fabs(z)));
+            if (m < 0x7FF0000000000000ull) largest = max(largest, m);
+          }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) largest = max(largest, __shfl_xor_sync(0xFFFFFFFFu, largest, o));
+        if (near) {
+          ex = exponent_of(largest);
+          again = turned ? 0xFFFFu : 0u;
+        }
+      }
+    }
+    if (!on) return;
+    const float inv = __uint_as_float(static_cast<unsigned>(254 - max(ex, 1)) << 23);
+    uint32_t code[4];
+    if (turned) {
+      // Rounded from either end of what an entry may be.  Zeros of either sign are the same.
+      const float err = inv * kTurnError;
+      float d[kForm == kAnywhere ? 16 : 8];  // of an entry or a pair; 2^-22: of subnormal numbers' own spacing
+#pragma unroll
+      for (int e = 0; e < (kForm == kAnywhere ? 16 : 8); ++e) {
+        const float u0 = kForm == kAnywhere ? x0[e] : kForm == kInside ? y[2 * e] : y[e];
+        const float u1 = kForm == kAnywhere ? x1[e] : kForm == kInside ? y[2 * e + 1] : y[8 + e];
+        d[e] = fmaf(fabsf(u0), err, fmaf(fabsf(u1), err, 0x1p-22f));
+      }
+      uint32_t down[4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e0 = kForm == kAnywhere ? 2 * i : kForm == kInside ? i : 2 * i & 7;
+        const int e1 = kForm == kAnywhere ? 2 * i + 1 : kForm == kInside ? i : (2 * i + 1) & 7;
+        float z0, z1, h0, h1, l0, l1;
+        tc::fmul2(z0, z1, y[2 * i], y[2 * i + 1], inv, inv);
+        tc::fadd2(h0, h1, z0, z1, d[e0], d[e1]);
+        tc::fadd2(l0, l1, z0, z1, -d[e0], -d[e1]);
+        const uint32_t p = e4m3_of(h0, h1), q = e4m3_of(l0, l1);
+        code[i >> 1] = i & 1 ? code[i >> 1] | p << 16 : p;
+        down[i >> 1] = i & 1 ? down[i >> 1] | q << 16 : q;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t diff = (code[i] ^ down[i]) & 0x7F7F7F7Fu;
+        if (diff)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if ((diff >> 8 * k) & 0xFFu) again |= 1u << (4 * i + k);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        code[i] = e4m3_of(y[4 * i] * inv, y[4 * i + 1] * inv) | e4m3_of(y[4 * i + 2] * inv, y[4 * i + 3] * inv) << 16;
+    }
+#pragma unroll 1
+    for (; again; again &= again - 1) {
+      const int e = __ffs(again) - 1;
+      const double z = turned64(row, (e < 8 ? c0 : c1 - 8) + e, pairs, kForm == kInside, t.at, a.inv_freq);
+      const uint32_t x = e4m3_of(z * static_cast<double>(inv)) << 8 * (e & 3), keep = ~(0xFFu << 8 * (e & 3));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e >> 2 == i) code[i] = (code[i] & keep) | x;
+    }
+    const long long to = t.slot + (static_cast<long long>(r) << a.lps);
+    uint8_t* dst = static_cast<uint8_t*>(kKind == kValue ? a.vp : a.kp) + to * w;
+    if (c1 == c0 + 8) {
+      *reinterpret_cast<uint4*>(dst + c0) = make_uint4(code[0], code[1], code[2], code[3]);
+    } else {
+      *reinterpret_cast<uint2*>(dst + c0) = make_uint2(code[0], code[1]);
+      *reinterpret_cast<uint2*>(dst + c1) = make_uint2(code[2], code[3]);
+    }
+    if (u == 0) (kKind == kValue ? a.v_scales : a.k_scales)[to] = static_cast<uint8_t>(ex);
+  }
+}
 
 template <typename T, int kLanes, PairForm kForm>
-__global__ void __launch_bounds__(kAppendThreads, 4) append_e4m3_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas8) append_e4m3_kernel(const __grid_constant__ AppendArgs a) {
   wait_for_previous();
   let_next_start();
   if (blockIdx.x == gridDim.x - 1) {
     append_check(a);
     return;
   }
-  __shared__ __align__(32) float cs[kAppendWarps][kMaxPairs];
-  __shared__ __align__(32) float sn[kAppendWarps][kMaxPairs];
+  __shared__ __align__(16) float cs[kAppendWarps][kMaxPairs];
+  __shared__ __align__(16) float sn[kAppendWarps][kMaxPairs];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int job = blockIdx.x * kAppendWarps + warp;
   const int t = div_by(job, a.by_shares), share = job - t * a.by_shares.d;
   if (t >= a.T) return;
+  // Passes over the token's rows, kPass of one kind each, dealt out to the warps that share it.  A pass's
+  // loads are in flight during the one before, the first one's while the token's place is looked up.
+  constexpr int kPass = 32 / kLanes;
+  const int sub = lane / kLanes;
+  const T* q = static_cast<const T*>(a.q) + t * a.qs;
+  const T* k = static_cast<const T*>(a.k) + t * a.ks;
+  const T* v = static_cast<const T*>(a.v) + t * a.vs;
+  const int q_passes = a.q ? (a.H + kPass - 1) / kPass : 0, k_passes = (a.Hk + kPass - 1) / kPass;
+  const int passes = q_passes + 2 * k_passes;
+  auto fetch = [&](int p, Raw16<T>& to) {
+    const bool is_q = p < q_passes, is_v = p >= q_passes + k_passes;
+    const Columns c = is_v ? columns_of<kForm, kValue>(a, lane % kLanes) : columns_of<kForm, kKey>(a, lane % kLanes);
+    const int r = (p - (is_q ? 0 : is_v ? q_passes + k_passes : q_passes)) * kPass + sub;
+    const T* row = (is_q ? q : is_v ? v : k) + r * c.w;
+    if (c.has && r < (is_q ? a.H : a.Hk) && p < passes) to.load(row + c.c0, row + c.c1);
+  };
+  int pass = share;
+  Raw16<T> next;
+  fetch(pass, next);
   const int b = owner(a, t);
   if (b < 0) return;  // behind the last sequence
   int s0 = b * a.each, nq = a.each;
@@ -376,147 +622,23 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_e4m3_kernel(const __
       slot = (static_cast<long long>(page) * a.Hk << a.lps) + (pos & ((1 << a.lps) - 1));
   }
   const long long at = static_cast<long long>(pos) + a.pos_offset;
-  for (int f = lane; f < a.pairs; f += 32) angle(at, __ldg(a.inv_freq + f), sn[warp][f], cs[warp][f]);
+  for (int f = lane; f < a.pairs; f += 32) angle(at, __ldg(a.inv_freq + f), sn[warp][pair_at(f)], cs[warp][pair_at(f)]);
   __syncwarp();
-
-  constexpr int kPass = 32 / kLanes;  // rows of a pass
-  const int sub = lane / kLanes, u = lane % kLanes, pairs = a.pairs;
-  const int q_rows = a.q ? a.H : 0, rows = q_rows + (slot < 0 ? 0 : 2 * a.Hk);
-  const T* qsrc = static_cast<const T*>(a.q) + t * a.qs;
-  const T* ksrc = static_cast<const T*>(a.k) + t * a.ks;
-  const T* vsrc = static_cast<const T*>(a.v) + t * a.vs;
-  T* qdst = static_cast<T*>(a.q_out) + static_cast<size_t>(t) * a.H * a.d;
+  const TokenRows x{slot, at, cs[warp], sn[warp]};
 #pragma unroll 1
-  for (int r0 = share * kPass; r0 < rows; r0 += kPass * a.by_shares.d) {
-    const int r = min(r0 + sub, rows - 1);
-    const bool is_q = r < q_rows, is_v = r >= q_rows + a.Hk;
-    const int h = is_q ? r : is_v ? r - q_rows - a.Hk : r - q_rows, w = is_v ? a.vw : a.d;
-    const bool on = r0 + sub < rows && 16 * u < w;
-    const T* src = is_q ? qsrc + h * a.d : is_v ? vsrc + h * a.vw : ksrc + h * a.d;
-    // The lane's columns: eight from c0 on, eight from c1 on.
-    int c0 = 16 * u, c1 = c0 + 8;
-    if (kForm == kHalves && !is_v && pairs > 0) {
-      const int half = pairs >> 3;
-      c0 = u < half ? 8 * u : 2 * pairs + 16 * (u - half);
-      c1 = u < half ? pairs + 8 * u : c0 + 8;
-    }
-    float y[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) y[e] = 0.f;
-    if (on) {
-      load8(src + c0, y);
-      load8(src + c1, y + 8);
-    }
-    float reach[kForm == kAnywhere ? 16 : 8];  // of the entries' errors
-#pragma unroll
-    for (int e = 0; e < (kForm == kAnywhere ? 16 : 8); ++e) reach[e] = 0.f;
-    const bool turned = on && !is_v && (kForm == kHalves ? 8 * u < pairs : kForm == kInside ? 8 * u < pairs : c0 < 2 * pairs);
-    if (turned) {
-      if constexpr (kForm == kAnywhere) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int c = c0 + e;
-          if (c >= 2 * pairs) continue;
-          const bool first = c < pairs;
-          const int f = first ? c : c - pairs;
-          const float other = as_float(src[first ? c + pairs : f]), k = cs[warp][f], s = sn[warp][f];
-          reach[e] = fabsf(y[e]) + fabsf(other);
-          y[e] = first ? y[e] * k - other * s : y[e] * k + other * s;
-        }
-      } else {
-        float k[8], s[8];
-        load8(&cs[warp][8 * u], k);
-        load8(&sn[warp][8 * u], s);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (kForm == kInside && 8 * u + e >= pairs) continue;
-          float& p = y[kForm == kInside ? 2 * e : e];
-          float& n = y[kForm == kInside ? 2 * e + 1 : 8 + e];
-          const float x0 = p, x1 = n;
-          p = x0 * k[e] - x1 * s[e];
-          n = x1 * k[e] + x0 * s[e];
-          reach[e] = fabsf(p) + fabsf(n);
-        }
-      }
-    }
-    if (is_q && on) {
-      T* dst = qdst + h * a.d;
-      store8(dst + c0, y);
-      store8(dst + c1, y + 8);
-    }
-    // Every lane of a row's, also those without columns.
-    unsigned top = 0u;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const unsigned m = __float_as_uint(y[e]) & 0x7FFFFFFFu;
-      top = max(top, m < 0x7F800000u ? m : 0u);
-    }
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    int ex = exponent_of(top);
-    uint32_t again = 0u;  // entries to be computed again
-    if (__any_sync(0xFFFFFFFFu, !is_q && !is_v && pairs > 0 && top > 8u && exponent_of(top - 8u) != exponent_of(top + 8u))) {
-      unsigned long long most = 0ull;
-      const bool mine = !is_q && !is_v && pairs > 0 && top > 8u && exponent_of(top - 8u) != exponent_of(top + 8u);
-      if (mine && on)
-#pragma unroll 1
-        for (int e = 0; e < 16; ++e) {
-          const double z = turned64(src, (e < 8 ? c0 : c1 - 8) + e, pairs, kForm == kInside, at, a.inv_freq);
-          const unsigned long long m = static_cast<unsigned long long>(__double_as_longlong(fabs(z)));
-          if (m < 0x7FF0000000000000ull) most = max(most, m);
-        }
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-      if (mine) {
-        ex = exponent_of(most);
-        again = turned ? 0xFFFFu : 0u;
-      }
-    }
-    if (is_q || !on) continue;
-    const float inv = __uint_as_float(static_cast<unsigned>(254 - max(ex, 1)) << 23);
-    uint32_t code[4];
-    auto pack = [&](int i, float d0, float d1) {  // entries 2 i and 2 i + 1, moved by d0, d1
-      float z[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) z[k] = fmaf(y[2 * i + k], inv, y[2 * i + k] * 0.f + (k ? d1 : d0));  // infinity: NaN
-      return e4m3_of(z[0], z[1]);
-    };
-    if (turned) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e0 = kForm == kAnywhere ? 2 * i : kForm == kInside ? i : 2 * i & 7;
-        const int e1 = kForm == kAnywhere ? 2 * i + 1 : kForm == kInside ? i : (2 * i + 1) & 7;
-        // 2^-22: of subnormal numbers' own spacing
-        const float d0 = reach[e0] > 0.f ? fmaf(reach[e0] * inv, kTurnError, 0x1p-22f) : 0.f;
-        const float d1 = reach[e1] > 0.f ? fmaf(reach[e1] * inv, kTurnError, 0x1p-22f) : 0.f;
-        const uint32_t up = pack(i, d0, d1), diff = up ^ pack(i, -d0, -d1);
-        if (diff & 0xFFu) again |= 1u << 2 * i;
-        if (diff & 0xFF00u) again |= 2u << 2 * i;
-        if (i & 1) code[i >> 1] |= up << 16;
-        else code[i >> 1] = up;
-      }
+  for (; pass < passes; pass += a.by_shares.d) {
+    const Raw16<T> raw = next;
+    fetch(pass + a.by_shares.d, next);
+    if (pass < q_passes) {
+      append_pass<T, kLanes, kForm, kQuery>(a, x, q, static_cast<T*>(a.q_out) + static_cast<size_t>(t) * a.H * a.d,
+                                            pass * kPass + sub, a.H, raw);
+    } else if (slot < 0) {
+      break;
+    } else if (pass < q_passes + k_passes) {
+      append_pass<T, kLanes, kForm, kKey>(a, x, k, nullptr, (pass - q_passes) * kPass + sub, a.Hk, raw);
     } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) code[i] = pack(2 * i, 0.f, 0.f) | pack(2 * i + 1, 0.f, 0.f) << 16;
+      append_pass<T, kLanes, kForm, kValue>(a, x, v, nullptr, (pass - q_passes - k_passes) * kPass + sub, a.Hk, raw);
     }
-#pragma unroll 1
-    for (; again; again &= again - 1) {
-      const int e = __ffs(again) - 1;
-      const double z = turned64(src, (e < 8 ? c0 : c1 - 8) + e, pairs, kForm == kInside, at, a.inv_freq);
-      const uint32_t x = e4m3_of(z * static_cast<double>(inv)) << 8 * (e & 3), keep = ~(0xFFu << 8 * (e & 3));
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (e >> 2 == i) code[i] = (code[i] & keep) | x;
-    }
-    const long long row = slot + (static_cast<long long>(h) << a.lps);
-    uint8_t* dst = static_cast<uint8_t*>(is_v ? a.vp : a.kp) + row * w;
-    if (c1 == c0 + 8) {
-      *reinterpret_cast<uint4*>(dst + c0) = make_uint4(code[0], code[1], code[2], code[3]);
-    } else {
-      *reinterpret_cast<uint2*>(dst + c0) = make_uint2(code[0], code[1]);
-      *reinterpret_cast<uint2*>(dst + c1) = make_uint2(code[2], code[3]);
-    }
-    if (u == 0) (is_v ? a.v_scales : a.k_scales)[row] = static_cast<uint8_t>(ex);
   }
 }
 

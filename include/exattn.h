@@ -504,8 +504,8 @@ int exattn_paged_run(int op, const exattn_paged_call* call);
  * Append.  b is the smallest from 1 on for which the row's largest finite magnitude is at
  * most 448 * 2^(b - 127), so that nothing saturates and scaling is exact; 0 for a row
  * without a nonzero finite entry.  Each entry is rounded once, to nearest, ties to even: off
- * by 2^-4 of itself at most, or by 2^(b - 137) where that is more.  Infinities and NaN become
- * NaN.  A rotated key is rounded, and its byte chosen, as if its rotation had been computed in
+ * by 2^-4 of itself at most, or by 2^(b - 137) where that is more.  Infinities, NaN and rotated
+ * entries beyond fp32 become NaN, and so does the other entry of their pair.  A rotated key is rounded, and its byte chosen, as if its rotation had been computed in
  * 64 bits; q_out is rotated in fp32 as above.
  *
  * Attention.  Scores, statistics and outputs are summed in fp32.  Few rows to a key head (up

@@ -50,14 +50,13 @@ constexpr int kRows = 2 * kHalf;
 constexpr int kUnit = 128;
 constexpr int kCtas = 152;
 constexpr int kWarpTMA = 8, kWarpMMA = 9, kWarpQ = 10, kWarpConvert = 12;
-// kBytes: pages in 8 bits, with four warps more, which convert them: half of its time, one warp's latency
-// after another (221 us in place of 277 without the conversion), but eight warps leave the softmax too few
-// registers (268 us, and 254 without the conversion).
+// kBytes: pages in 8 bits, with four warps more, which convert them.  (Eight leave the softmax too few
+// registers: 268 us in place of 257 for the chunks below.)
 constexpr int kConverters = 4;
 template <bool kBytes>
 struct Warps {
-  static constexpr int kSoftmaxRegs = kBytes ? 168 : 208;
-  static constexpr int kProducerRegs = 88;
+  static constexpr int kSoftmaxRegs = kBytes ? 160 : 208;
+  static constexpr int kProducerRegs = kBytes ? 96 : 88;
   static constexpr int kThreads = 384 + (kBytes ? 32 * kConverters : 0);
   static constexpr int kTakers = 11 + (kBytes ? kConverters : 0);  // warps that read a segment from the ring
 };
@@ -140,7 +139,7 @@ __device__ __forceinline__ void bytes_to_bf16(const uint4& raw, float f, uint32_
   }
 }
 
-// A block's softmax for sixteen warps, which leave these 168 registers: the row's scores are read
+// A block's softmax for sixteen warps, which leave these 160 registers: the row's scores are read
 // twice, 64 at a time, once for the maximum.  Keys lo to hi of the block where `mw` has them.
 template <int D>
 __device__ __forceinline__ void softmax_by_halves(uint32_t t_s, uint32_t t_o, bool whole, const uint32_t (&mw)[4],
@@ -302,6 +301,7 @@ __global__ void __launch_bounds__(Warps<kBytes>::kThreads, 1)
         // by warp.  A lane takes 16 columns: quads have four pieces of a row, and neighbouring rows
         // the two halves of one, so that neither the loads nor the stores of eight lanes meet in a bank.
         constexpr int kRowsOf = kUnit / kConverters;
+        static_assert(kRowsOf == 32, "a word of the mask each");
         const int wr = (warp - kWarpConvert) * kRowsOf, q = lane & 3, odd = (lane >> 2) & 1;
         volatile uint32_t* rkeep = reinterpret_cast<volatile uint32_t*>(smem + Lay::RKEEP_OFF);
         bool ok = true;
@@ -315,33 +315,43 @@ __global__ void __launch_bounds__(Warps<kBytes>::kThreads, 1)
             // V: rows without a key are zero, whatever their page holds (K's scores do not count).
             uint32_t mine = rkeep[rs * 4 + (wr >> 5)];
             if (!(u & 1)) {
-              if (lane == 0 && (wr & 31) == 0) keep[(fill / 2 % Lay::kKeepBlocks) * 4 + (wr >> 5)] = mine;
+              if (lane == 0) keep[(fill / 2 % Lay::kKeepBlocks) * 4 + (wr >> 5)] = mine;
               mine = 0xFFFFFFFFu;
             }
-            mine >>= wr & 31;
             const uint8_t* ex = smem + Lay::EXP_OFF + rs * kUnit + wr;
             const uint32_t raw = sbase + Lay::RAW_OFF + rs * Lay::RAW + wr * D;
             const uint32_t to = sbase + Lay::SLOT_OFF + ks * Lay::SLOT + wr * 128;
-#pragma unroll 4
-            for (int y = 0; y < D / 16 * kRowsOf / 32; ++y) {
-              const int r = (D == 128 ? y >> 1 : y) * 8 + 2 * (lane >> 3) + odd;  // of the warp's rows
-              const int piece = q + (D == 128 ? 4 * (odd ^ (y & 1)) : 0);
-              uint4 x = ld_shared_v4(raw + r * D + piece * 16);
-              float f = e4m3_scale(ex[r]);
-              if (!((mine >> r) & 1u)) {
-                x = make_uint4(0u, 0u, 0u, 0u);
-                f = 0.f;
-              }
+            // All loads before the first use: beside the products' own reads a shared load takes long.
+            constexpr int kPieces = D / 16 * kRowsOf / 32;
+            uint4 x[kPieces];
+            float f[kPieces];
+            auto row_of = [&](int y) { return (D == 128 ? y >> 1 : y) * 8 + 2 * (lane >> 3) + odd; };  // of the warp's
+            auto piece_of = [&](int y) { return q + (D == 128 ? 4 * (odd ^ (y & 1)) : 0); };
+#pragma unroll
+            for (int y = 0; y < kPieces; ++y) x[y] = ld_shared_v4(raw + row_of(y) * D + piece_of(y) * 16);
+#pragma unroll
+            for (int y = 0; y < kPieces; ++y) f[y] = e4m3_scale(ex[row_of(y)]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(Lay::B_RE + rs));
+            if (mine != 0xFFFFFFFFu) {  // the same for the whole warp
+#pragma unroll
+              for (int y = 0; y < kPieces; ++y)
+                if (!((mine >> row_of(y)) & 1u)) {
+                  x[y] = make_uint4(0u, 0u, 0u, 0u);
+                  f[y] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < kPieces; ++y) {
+              const int r = row_of(y);
               uint32_t z[8];
-              bytes_to_bf16(x, f, z);
-              const uint32_t row = to + (piece >> 2) * (kUnit * 128) + r * 128;
+              bytes_to_bf16(x[y], f[y], z);
+              const uint32_t row = to + (piece_of(y) >> 2) * (kUnit * 128) + r * 128;
               st_shared_v4(row + (((2 * q) ^ (r & 7)) << 4), z[0], z[1], z[2], z[3]);
               st_shared_v4(row + (((2 * q + 1) ^ (r & 7)) << 4), z[4], z[5], z[6], z[7]);
             }
             fence_proxy_async_smem();
             mbar_arrive(bar(Lay::B_KVF + ks));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(Lay::B_RE + rs));
           }
         }
         if (!ok) {

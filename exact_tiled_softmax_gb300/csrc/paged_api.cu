@@ -102,11 +102,24 @@ long long rows_of(const PagedArgs& a) { return (long long)(a.T + a.B - 1) / a.B 
 // once.  32 sequences of 8192 keys, 8 key heads of 128 columns: 16 rows 183 us (186 on the
 // tall tiles), 24 rows 331 (190), 64 rows 644 (194); 4 of 4000: 16 rows 31 (31), 32 rows 42 (27).
 constexpr int kTcRows = 16;
+// Pages in 8 bits: the tall tiles are bound by their conversion, and a second 16-row tile pays where there are
+// keys enough (of all key heads, as many as the tables can hold).  24 and 32 rows, 32 sequences of 8192 keys of 8
+// heads: 184 and 186 us (225 on the tall tiles, 48 rows 266 and 227); 4 of 4000: 26.8 and 29.3 (29.0, 29.1); 16 of
+// 1000 of 2 heads: 20.2 and 22.4 (16.9, 17.0).
+constexpr int kTcRows8 = 32;
+constexpr long long kManyKeys = 1 << 17;
+int tc_rows(const PagedArgs& a) {
+  if (!a.Ks) return kTcRows;
+  long long own = static_cast<long long>(a.max_pages) << a.lps;
+  if (a.mask_kind == EXATTN_MASK_WINDOW) own = std::min(own, static_cast<long long>(a.window));
+  const long long keys = a.prefix_at == 0 ? a.prefix_len : own * a.B;
+  return keys * a.Hk >= kManyKeys ? kTcRows8 : kTcRows;
+}
 
 Choice choose(const PagedArgs& a) {
   Choice c;
   if (current_path() != EXATTN_PATH_SIMT && (a.Ks ? paged_e4m3_shape(a.d, a.v, a.lps) : paged_mma_shape(a.d, a.v)))
-    c.kind = rows_of(a) > kTcRows && paged_tc_supported(a) ? kTc : rows_of(a) > 8 ? kMma16 : kMma8;
+    c.kind = rows_of(a) > tc_rows(a) && paged_tc_supported(a) ? kTc : rows_of(a) > 8 ? kMma16 : kMma8;
   else c.kind = !a.starts && a.T == a.B && a.G == 1 ? kSimtOne : kSimt;
   c.k = kernel_of(c.kind, a);
   return c;
@@ -359,7 +372,7 @@ int fwd_prefix(const exattn_paged_shape* shape, const void* Q, const Pages& page
   if (own.kind != of.kind && of.kind == kTc && own.kind >= kMma8) {
     // Tall tiles for the prefix alone mean a launch of their own, 6 us; 16-row tiles read the
     // prefix again for each, at some 6.5 TB/s (of the L2 cache).
-    const double bytes = (double)prefix_len * a.Hk * (a.d + a.v) * 2, again = (double)((rows_of(p) + 15) / 16 - 1);
+    const double bytes = (double)prefix_len * a.Hk * (a.d + a.v) * (a.Ks ? 1 : 2), again = (double)((rows_of(p) + 15) / 16 - 1);
     if (again * bytes < 40e6) {
       of.kind = kMma16;
       of.k = kernel_of(of.kind, a);

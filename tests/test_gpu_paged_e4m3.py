@@ -182,6 +182,19 @@ def test_append_of_entries_that_are_not_finite(ex, dtype, pairs):
             assert ve == 0 if (t, h) == (3, 0) else ve > 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pairs,inter", [(32, False), (32, True), (20, False), (13, False)])
+def test_append_rotates_q_in_place(ex, dtype, pairs, inter):
+    b = Batch8([400, 9], [300, 2], 6, 2, 64, 64, dtype, 16, seed=1)
+    k, v, table, lens, starts, ks, vs = b.cache()
+    q, kn, vn = b.dev("q", "k_new", "v_new")
+    inv = torch.pow(10000.0, -torch.arange(pairs, device="cuda") / pairs).float()
+    kw = dict(q_starts=starts, inv_freq=inv, interleaved=inter, k_scales=ks, v_scales=vs)
+    want = ex.append_paged(kn, vn, k, v, table, lens, q=q, **kw)
+    got = ex.append_paged(kn, vn, k, v, table, lens, q=q, q_out=q, **kw)
+    assert got is q and torch.equal(got, want)
+
+
 def test_append_without_a_place(ex):
     """Tokens before position 0, behind the table, or on a page outside the pool: nothing of
     theirs is written, the others' are, and the status word says so."""
@@ -274,6 +287,34 @@ def test_many_rows(ex, nqs, G, page, d, v, mask, window):
     y, L, status = _attend(ex, b, mask, window, 0.03)
     assert status == 0
     _check("auto", b, y, L, 0.03, mask, window)
+
+
+@pytest.mark.parametrize("nqs", [[3, 4], [4, 1]])
+def test_two_row_tiles_over_many_keys(ex, nqs):
+    """17 to 32 bf16 rows to a key head stay on the 16-row tiles where the tables hold many keys."""
+    b = Batch8([8200, 300], nqs, 64, 8, 64, 64, "bf16", 32, seed=15)
+    y, L, status = _attend(ex, b, "causal", 0, 0.03)
+    assert status == 0
+    _check("auto", b, y, L, 0.03, "causal", rows=16)
+
+
+@pytest.mark.parametrize("case", [([300, 40, 512], [1, 1, 1], 32, 8, "bf16"), ([2000, 9], [2, 3], 8, 1, "bf16"),
+                                  ([700, 90], [60, 2], 8, 2, "bf16"), ([300, 900], [2, 1], 8, 2, "f32")], ids=str)
+def test_calls_repeat_themselves(ex, path, case):
+    """The same bits whatever the workspace held, also behind a prefix."""
+    lens, nqs, H, kv, dtype = case
+    b = Batch8(lens, nqs, H, kv, 128, 128, dtype, 16, seed=16, prefix=2500)
+    k, v, table, ln, starts, ks, vs = b.cache()
+    q, pt = b.dev("q", "prefix_table")
+    kw = dict(q_starts=starts, k_scales=ks, v_scales=vs)
+    size = ex.prefix_workspace_size(ex.paged_shape(q, k, v, table))
+    want = None
+    for fill in (0, 0xFF, 0x7F):
+        ws = torch.full((size,), fill, dtype=torch.uint8, device="cuda")
+        got = ex.fwd_paged(q, k, v, table, ln, 0.05, "causal", ws=ws, **kw)
+        got += ex.fwd_prefix(q, k, v, pt, 2500, table, ln, 0.05, "causal", ws=ws, **kw)
+        want = want or got
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
 @pytest.mark.parametrize("scale", [-0.3, 0.0, 2.0])

@@ -479,7 +479,7 @@ def _check_paged(q, k_pages, v_pages, page_table, seq_lens, q_starts, ws, k_scal
 def _int32(name, x) -> int:
     """x as the int that the library takes (ctypes would drop its high bits)."""
     x = int(x)
-    if not -2 ** 31 <= x < 2 ** 31:
+    if not -0x80000000 <= x < 0x80000000:
         raise ValueError(f"{name} = {x} does not fit 32 bits")
     return x
 
@@ -496,10 +496,11 @@ def _check_outputs(q, vw, y, L):
 
 # A decode step's kernels take a few microseconds, so its checks are made once for each
 # combination of shapes, strides, types and devices: the key holds all that they look at,
-# the value is the fields of the PagedShape.
+# the value is the PagedShape and its bytes.
 _paged_known = {}
 _PAGED_CALL = struct.Struct("@10i3q15Qf5i")  # exattn_paged_call
 _PAGED_E4M3_CALL = struct.Struct("@10i3q15Qf5i2Q")  # exattn_paged_e4m3_call
+_BEHIND_SHAPE, _BEHIND_SHAPE_E4M3 = struct.Struct("@15Qf5i"), struct.Struct("@15Qf5i2Q")
 
 
 def _meta(t):
@@ -509,8 +510,7 @@ def _meta(t):
 def _remember(key, shape):
     if len(_paged_known) >= 4096:
         _paged_known.clear()
-    known = tuple(getattr(shape, name) for name, _ in PagedShape._fields_)
-    _paged_known[key] = known
+    _paged_known[key] = known = (shape, bytes(shape))
     return known
 
 
@@ -522,18 +522,18 @@ def _on(stream, make, *args, **kwargs):
         return make(*args, **kwargs)
 
 
-def _paged_call(op, name, index, known, stream, fields, k_scales, v_scales):
-    """exattn_paged_run, or with scales exattn_paged_e4m3_run, on the device ``index``; ``fields``: the
-    call's from the pointers on, before and behind the stream."""
+def _paged_call(op, name, index, shape, stream, pointers, rest, k_scales, v_scales):
+    """exattn_paged_run, or with scales exattn_paged_e4m3_run, on the device ``index``; ``shape``: its
+    bytes, ``pointers`` and ``rest``: the call's fields before and behind the stream."""
     if index < 0:
         raise ValueError("tensors must be on a CUDA device")
     s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if k_scales is None:
-        run, call = _lib.exattn_paged_run, _PAGED_CALL.pack(*known, *fields[0], s, *fields[1])
+        run, call = _lib.exattn_paged_run, shape + _BEHIND_SHAPE.pack(*pointers, s, *rest)
     else:
         run, name = _lib.exattn_paged_e4m3_run, name + "_e4m3"
-        call = _PAGED_E4M3_CALL.pack(*known, *fields[0], s, *fields[1], k_scales.data_ptr(), v_scales.data_ptr())
-    if index == torch.cuda.current_device():
+        call = shape + _BEHIND_SHAPE_E4M3.pack(*pointers, s, *rest, k_scales.data_ptr(), v_scales.data_ptr())
+    if index == torch._C._cuda_getDevice():
         st = run(op, call)
     else:
         with torch.cuda.device(index):
@@ -556,12 +556,16 @@ def append_paged(k, v, k_pages, v_pages, page_table, seq_lens, q_starts=None, q=
     each row in ``k_scales`` and ``v_scales`` [num_pages, kv_heads, page_size] (uint8 or
     float8_e8m0fnu): a row stands for its numbers times 2 ** (byte - 127), and is quantised, with the
     smallest exponent at which nothing saturates, as it is written."""
-    load_library()
+    if _lib is None:
+        load_library()
     pos_offset = _int32("pos_offset", pos_offset)
-    key = (0, _meta(k), _meta(v), _meta(k_pages), _meta(v_pages), _meta(page_table), _meta(seq_lens),
-           _meta(q_starts), _meta(q), _meta(q_out), _meta(inv_freq), _meta(ws))
-    if k_scales is not None or v_scales is not None:
-        key += (_meta(k_scales), _meta(v_scales))
+    index = k.get_device()
+    key = (0, index, k.shape, k.stride(), k.dtype, v.shape, v.stride(), v.dtype, v.get_device(),
+           k_pages.shape, k_pages.stride(), k_pages.dtype, k_pages.get_device(),
+           v_pages.shape, v_pages.stride(), v_pages.dtype, v_pages.get_device(),
+           page_table.shape, page_table.stride(), page_table.dtype, page_table.get_device(),
+           seq_lens.shape, seq_lens.stride(), seq_lens.dtype, seq_lens.get_device(),
+           _meta(q_starts), _meta(q), _meta(q_out), _meta(inv_freq), _meta(ws), _meta(k_scales), _meta(v_scales))
     known = _paged_known.get(key)
     if known is None:
         lead = k if q is None else q
@@ -590,24 +594,27 @@ def append_paged(k, v, k_pages, v_pages, page_table, seq_lens, q_starts=None, q=
     if ws is None:
         ws = _on(stream, workspace, 256, k.device)
     pairs = 0 if inv_freq is None else inv_freq.numel()
-    _paged_call(0, "attn_append_paged", k.get_device(), known, stream, (
+    _paged_call(0, "attn_append_paged", index, known[1], stream,
         (0 if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), k_pages.data_ptr(),
          v_pages.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
          0 if q_starts is None else q_starts.data_ptr(), 0, inv_freq.data_ptr() if pairs else 0,
          0 if q is None else q_out.data_ptr(), 0, ws.data_ptr(), ws.nbytes),
-        (0.0, 0, 0, pos_offset, pairs, 1 if interleaved else 0)), k_scales, v_scales)
+        (0.0, 0, 0, pos_offset, pairs, 1 if interleaved else 0), k_scales, v_scales)
     return q_out
 
 
 def _attend_paged(op, name, q, k_pages, v_pages, prefix_table, prefix_len, page_table, seq_lens, scale,
                   mask, window, q_starts, y, L, ws, stream, k_scales, v_scales):
-    load_library()
+    if _lib is None:
+        load_library()
     window = _int32("window", window)
     prefix_len = _int32("prefix_len", prefix_len)
-    key = (op, _meta(q), _meta(k_pages), _meta(v_pages), _meta(page_table), _meta(seq_lens),
-           _meta(q_starts), _meta(prefix_table), _meta(y), _meta(L), _meta(ws))
-    if k_scales is not None or v_scales is not None:
-        key += (_meta(k_scales), _meta(v_scales))
+    index = q.get_device()
+    key = (op, index, q.shape, q.stride(), q.dtype, k_pages.shape, k_pages.stride(), k_pages.dtype,
+           k_pages.get_device(), v_pages.shape, v_pages.stride(), v_pages.dtype, v_pages.get_device(),
+           page_table.shape, page_table.stride(), page_table.dtype, page_table.get_device(),
+           seq_lens.shape, seq_lens.stride(), seq_lens.dtype, seq_lens.get_device(),
+           _meta(q_starts), _meta(prefix_table), _meta(y), _meta(L), _meta(ws), _meta(k_scales), _meta(v_scales))
     known = _paged_known.get(key)
     if known is None:
         shape = _check_paged(q, k_pages, v_pages, page_table, seq_lens, q_starts, ws, k_scales, v_scales)
@@ -625,15 +632,15 @@ def _attend_paged(op, name, q, k_pages, v_pages, prefix_table, prefix_len, page_
     if L is None:
         L = _on(stream, torch.empty, q.shape[:2], dtype=torch.float32, device=q.device)
     if ws is None:
-        shape = PagedShape(*known)
+        shape = known[0]
         size = prefix_workspace_size(shape) if op == 2 else paged_workspace_size(shape)
         ws = _on(stream, workspace, size, q.device)
-    _paged_call(op, name, q.get_device(), known, stream, (
+    _paged_call(op, name, index, known[1], stream,
         (q.data_ptr(), 0, 0, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
          seq_lens.data_ptr(), 0 if q_starts is None else q_starts.data_ptr(),
          0 if prefix_table is None else prefix_table.data_ptr(), 0, y.data_ptr(), L.data_ptr(),
          ws.data_ptr(), ws.nbytes),
-        (float(scale), _mask_kind(mask), window, prefix_len, 0, 0)), k_scales, v_scales)
+        (float(scale), _mask_kind(mask), window, prefix_len, 0, 0), k_scales, v_scales)
     return y, L
 
 

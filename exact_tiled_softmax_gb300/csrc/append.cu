@@ -22,9 +22,11 @@ namespace {
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
 constexpr int kMaxPairs = 128;
-// CTAs of an SM: four 157 us for 37 thousand tokens of 32 + 8 + 8 rows of 128 bf16 columns (5.2 TB/s, 77% of the
-// measured copy), three 158, five 195 (which spill); two rows ahead 165.
-constexpr int kAppendCtas8 = 4;
+// Pages in 8 bits.  CTAs of an SM: seven of four warps 144 us for 37 thousand tokens of 32 + 8 + 8 rows of 128
+// bf16 columns (5.7 TB/s, 84% of the measured copy), six 148, five 154; three of eight 151, four, which
+// spill, 161.  A second pass's loads ahead: no difference.
+constexpr int kThreads8 = 128, kWarps8 = kThreads8 / 32, kAppendCtas8 = 7;
+constexpr int kMaxPasses = 1 << 17;  // more than a token's rows
 
 // The sequence that owns token t, or -1.
 __device__ __forceinline__ int owner(const AppendArgs& a, int t) {
@@ -90,7 +92,7 @@ __device__ void append_check(const AppendArgs& a) {
   bool bad = false;
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int b0 = (threadIdx.x & ~31); b0 < a.B; b0 += kAppendThreads) {
+  for (int b0 = (threadIdx.x & ~31); b0 < a.B; b0 += blockDim.x) {
     const int b = b0 + lane;
     int first = 0, last = -1;  // pages of the new tokens
     if (b < a.B) {
@@ -404,16 +406,13 @@ __device__ __forceinline__ Columns columns_of(const AppendArgs& a, int u) {
   return c;
 }
 
-// One pass over rows of one kind: row r of `rows` for each kLanes lanes, its columns `raw`; rotated, and into q_out
-// or quantised into their page.
+// One pass over rows of one kind: a row for each kLanes lanes (where it has one: `on`), the lane's columns `raw`;
+// rotated, and into q_row or quantised into the page's row and its exponent byte.
 template <typename T, int kLanes, PairForm kForm, RowKind kKind>
-__device__ __forceinline__ void append_pass(const AppendArgs& a, const TokenRows& t, const T* rows, T* q_out, int r, int n,
-                                            const Raw16<T>& raw) {
+__device__ __forceinline__ void append_pass(const AppendArgs& a, const TokenRows& t, const Columns& col, bool on, const T* row,
+                                            T* q_row, uint8_t* page_row, uint8_t* exponent, const Raw16<T>& raw) {
   constexpr bool kTurns = kKind != kValue;
-  const int u = threadIdx.x % kLanes, pairs = a.pairs;
-  const Columns col = columns_of<kForm, kKind>(a, u);
-  const int c0 = col.c0, c1 = col.c1, w = col.w;
-  const bool on = col.has && r < n;
+  const int u = threadIdx.x % kLanes, pairs = a.pairs, c0 = col.c0, c1 = col.c1;
   const bool turned = kTurns && col.has && (kForm == kAnywhere ? c0 < 2 * pairs : 8 * u < pairs);
   {
     float y[16];
@@ -433,7 +432,7 @@ __device__ __forceinline__ void append_pass(const AppendArgs& a, const TokenRows
           if (c >= 2 * pairs) continue;
           const bool first = c < pairs;
           const int f = first ? c : c - pairs;
-          const float other = as_float(rows[r * w + (first ? c + pairs : f)]), k = t.cs[pair_at(f)], s = t.sn[pair_at(f)];
+          const float other = as_float(row[first ? c + pairs : f]), k = t.cs[pair_at(f)], s = t.sn[pair_at(f)];
           x0[e] = y[e];
           x1[e] = other;
           y[e] = first ? y[e] * k - other * s : y[e] * k + other * s;
@@ -468,8 +467,8 @@ __device__ __forceinline__ void append_pass(const AppendArgs& a, const TokenRows
     if constexpr (kKind == kQuery) {
       if (kForm == kAnywhere) __syncwarp();  // q_out may be q: every lane has read the pairs' others
       if (on) {
-        store8(q_out + r * w + c0, y);
-        store8(q_out + r * w + c1, y + 8);
+        store8(q_row + c0, y);
+        store8(q_row + c1, y + 8);
       }
       return;
     }
@@ -493,7 +492,6 @@ __device__ __forceinline__ void append_pass(const AppendArgs& a, const TokenRows
     }
     int ex = exponent_of(top);
     uint32_t again = 0u;  // entries to be computed again
-    const T* row = rows + r * w;
     if constexpr (kTurns) {
       // (8 units of the last place are more than the error of a pair that is no longer than twice its row's largest.)
       const bool near = pairs > 0 && top > 8u && exponent_of(top - 8u) != exponent_of(top + 8u);
@@ -562,51 +560,65 @@ __device__ __forceinline__ void append_pass(const AppendArgs& a, const TokenRows
       for (int i = 0; i < 4; ++i)
         if (e >> 2 == i) code[i] = (code[i] & keep) | x;
     }
-    const long long to = t.slot + (static_cast<long long>(r) << a.lps);
-    uint8_t* dst = static_cast<uint8_t*>(kKind == kValue ? a.vp : a.kp) + to * w;
     if (c1 == c0 + 8) {
-      *reinterpret_cast<uint4*>(dst + c0) = make_uint4(code[0], code[1], code[2], code[3]);
+      *reinterpret_cast<uint4*>(page_row + c0) = make_uint4(code[0], code[1], code[2], code[3]);
     } else {
-      *reinterpret_cast<uint2*>(dst + c0) = make_uint2(code[0], code[1]);
-      *reinterpret_cast<uint2*>(dst + c1) = make_uint2(code[2], code[3]);
+      *reinterpret_cast<uint2*>(page_row + c0) = make_uint2(code[0], code[1]);
+      *reinterpret_cast<uint2*>(page_row + c1) = make_uint2(code[2], code[3]);
     }
-    if (u == 0) (kKind == kValue ? a.v_scales : a.k_scales)[to] = static_cast<uint8_t>(ex);
+    if (u == 0) *exponent = static_cast<uint8_t>(ex);
+  }
+}
+
+// All passes of a warp over the n rows of one kind, from row r (of the lane) on in steps of `step`.  `next` holds
+// the first one's columns; a pass's loads are in flight during the one before.
+template <typename T, int kLanes, PairForm kForm, RowKind kKind>
+__device__ __forceinline__ void append_rows(const AppendArgs& a, const TokenRows& t, const Columns& col, const T* rows, T* q_out,
+                                            uint8_t* pages, uint8_t* exponents, int n, int r, int step, Raw16<T>& next) {
+  const int sub = (threadIdx.x & 31) / kLanes;
+  const T* row = rows + r * col.w;
+#pragma unroll 1
+  for (int left = n - r; left + sub > 0; left -= step) {
+    const Raw16<T> raw = next;
+    const T* at = row;
+    row += step * col.w;
+    if (col.has && left > step) next.load(row + col.c0, row + col.c1);
+    const long long h = n - left;  // the lane's row
+    append_pass<T, kLanes, kForm, kKind>(
+        a, t, col, col.has && left > 0, at, kKind == kQuery ? q_out + h * col.w : nullptr,
+        kKind == kQuery ? nullptr : pages + (t.slot + (h << a.lps)) * col.w,
+        kKind == kQuery ? nullptr : exponents + t.slot + (h << a.lps), raw);
   }
 }
 
 template <typename T, int kLanes, PairForm kForm>
-__global__ void __launch_bounds__(kAppendThreads, kAppendCtas8) append_e4m3_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kThreads8, kAppendCtas8) append_e4m3_kernel(const __grid_constant__ AppendArgs a) {
   wait_for_previous();
   let_next_start();
   if (blockIdx.x == gridDim.x - 1) {
     append_check(a);
     return;
   }
-  __shared__ __align__(16) float cs[kAppendWarps][kMaxPairs];
-  __shared__ __align__(16) float sn[kAppendWarps][kMaxPairs];
+  __shared__ __align__(16) float cs[kWarps8][kMaxPairs];
+  __shared__ __align__(16) float sn[kWarps8][kMaxPairs];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int job = blockIdx.x * kAppendWarps + warp;
+  const int job = blockIdx.x * kWarps8 + warp;
   const int t = div_by(job, a.by_shares), share = job - t * a.by_shares.d;
   if (t >= a.T) return;
-  // Passes over the token's rows, kPass of one kind each, dealt out to the warps that share it.  A pass's
-  // loads are in flight during the one before, the first one's while the token's place is looked up.
+  // Passes over the token's rows, kPass of one kind each, dealt out to the warps that share it; the first ones'
+  // loads stand before the look-up of the token's place.
   constexpr int kPass = 32 / kLanes;
-  const int sub = lane / kLanes;
+  const int sub = lane / kLanes, shares = a.by_shares.d, step = kPass * shares;
   const T* q = static_cast<const T*>(a.q) + t * a.qs;
   const T* k = static_cast<const T*>(a.k) + t * a.ks;
   const T* v = static_cast<const T*>(a.v) + t * a.vs;
-  const int q_passes = a.q ? (a.H + kPass - 1) / kPass : 0, k_passes = (a.Hk + kPass - 1) / kPass;
-  const int passes = q_passes + 2 * k_passes;
-  auto fetch = [&](int p, Raw16<T>& to) {
-    const bool is_q = p < q_passes, is_v = p >= q_passes + k_passes;
-    const Columns c = is_v ? columns_of<kForm, kValue>(a, lane % kLanes) : columns_of<kForm, kKey>(a, lane % kLanes);
-    const int r = (p - (is_q ? 0 : is_v ? q_passes + k_passes : q_passes)) * kPass + sub;
-    const T* row = (is_q ? q : is_v ? v : k) + r * c.w;
-    if (c.has && r < (is_q ? a.H : a.Hk) && p < passes) to.load(row + c.c0, row + c.c1);
-  };
-  int pass = share;
-  Raw16<T> next;
-  fetch(pass, next);
+  const int H = a.q ? a.H : 0, q_passes = (H + kPass - 1) / kPass, k_passes = (a.Hk + kPass - 1) / kPass;
+  auto first = [&](int base) { return (share + shares * kMaxPasses - base) % shares * kPass + sub; };  // row, of the kind behind `base` passes
+  const int rq = first(0), rk = first(q_passes), rv = first(q_passes + k_passes);
+  const Columns key = columns_of<kForm, kKey>(a, lane % kLanes), val = columns_of<kForm, kValue>(a, lane % kLanes);
+  Raw16<T> next, next_k;
+  if (key.has && rq < H) next.load(q + rq * key.w + key.c0, q + rq * key.w + key.c1);
+  if (key.has && rk < a.Hk) next_k.load(k + rk * key.w + key.c0, k + rk * key.w + key.c1);
   const int b = owner(a, t);
   if (b < 0) return;  // behind the last sequence
   int s0 = b * a.each, nq = a.each;
@@ -625,32 +637,23 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas8) append_e4m3_kern
   for (int f = lane; f < a.pairs; f += 32) angle(at, __ldg(a.inv_freq + f), sn[warp][pair_at(f)], cs[warp][pair_at(f)]);
   __syncwarp();
   const TokenRows x{slot, at, cs[warp], sn[warp]};
-#pragma unroll 1
-  for (; pass < passes; pass += a.by_shares.d) {
-    const Raw16<T> raw = next;
-    fetch(pass + a.by_shares.d, next);
-    if (pass < q_passes) {
-      append_pass<T, kLanes, kForm, kQuery>(a, x, q, static_cast<T*>(a.q_out) + static_cast<size_t>(t) * a.H * a.d,
-                                            pass * kPass + sub, a.H, raw);
-    } else if (slot < 0) {
-      break;
-    } else if (pass < q_passes + k_passes) {
-      append_pass<T, kLanes, kForm, kKey>(a, x, k, nullptr, (pass - q_passes) * kPass + sub, a.Hk, raw);
-    } else {
-      append_pass<T, kLanes, kForm, kValue>(a, x, v, nullptr, (pass - q_passes - k_passes) * kPass + sub, a.Hk, raw);
-    }
-  }
+  append_rows<T, kLanes, kForm, kQuery>(a, x, key, q, static_cast<T*>(a.q_out) + static_cast<size_t>(t) * a.H * a.d, nullptr,
+                                        nullptr, H, rq, step, next);
+  if (slot < 0) return;
+  if (val.has && rv < a.Hk) next.load(v + rv * val.w + val.c0, v + rv * val.w + val.c1);
+  append_rows<T, kLanes, kForm, kKey>(a, x, key, k, nullptr, static_cast<uint8_t*>(a.kp), a.k_scales, a.Hk, rk, step, next_k);
+  append_rows<T, kLanes, kForm, kValue>(a, x, val, v, nullptr, static_cast<uint8_t*>(a.vp), a.v_scales, a.Hk, rv, step, next);
 }
 
 template <typename T, int kLanes, PairForm kForm>
 cudaError_t append_e4m3_launch(AppendArgs a, cudaStream_t s) {
   a.each = a.T / a.B;
   int shares = 1;
-  while (shares < kAppendWarps && (long long)a.T * shares * 2 <= 152 * 16 && shares < 2 * a.Hk) shares *= 2;
+  while (shares < 8 && (long long)a.T * shares * 2 <= 152 * 16 && shares < 2 * a.Hk) shares *= 2;
   a.by_shares = fast_div(shares);
-  const unsigned ctas = (static_cast<unsigned>(a.T) * shares + kAppendWarps - 1) / kAppendWarps;
+  const unsigned ctas = (static_cast<unsigned>(a.T) * shares + kWarps8 - 1) / kWarps8;
   before_launch(kKernAppend, s);
-  const cudaError_t e = launch_early(append_e4m3_kernel<T, kLanes, kForm>, dim3(ctas + 1), kAppendThreads, 0, s, a);
+  const cudaError_t e = launch_early(append_e4m3_kernel<T, kLanes, kForm>, dim3(ctas + 1), kThreads8, 0, s, a);
   after_launch(kKernAppend, s);
   return e;
 }

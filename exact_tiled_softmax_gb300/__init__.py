@@ -503,8 +503,8 @@ _PAGED_E4M3_CALL = struct.Struct("@10i3q15Qf5i2Q")  # exattn_paged_e4m3_call
 _BEHIND_SHAPE, _BEHIND_SHAPE_E4M3 = struct.Struct("@15Qf5i"), struct.Struct("@15Qf5i2Q")
 
 
-def _meta(t):
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+def _meta(t):  # of a tensor that has to be dense
+    return None if t is None else (t.shape, t.is_contiguous(), t.dtype, t.get_device())
 
 
 def _remember(key, shape):
@@ -561,11 +561,11 @@ def append_paged(k, v, k_pages, v_pages, page_table, seq_lens, q_starts=None, q=
     pos_offset = _int32("pos_offset", pos_offset)
     index = k.get_device()
     key = (0, index, k.shape, k.stride(), k.dtype, v.shape, v.stride(), v.dtype, v.get_device(),
-           k_pages.shape, k_pages.stride(), k_pages.dtype, k_pages.get_device(),
-           v_pages.shape, v_pages.stride(), v_pages.dtype, v_pages.get_device(),
-           page_table.shape, page_table.stride(), page_table.dtype, page_table.get_device(),
-           seq_lens.shape, seq_lens.stride(), seq_lens.dtype, seq_lens.get_device(),
-           _meta(q_starts), _meta(q), _meta(q_out), _meta(inv_freq), _meta(ws), _meta(k_scales), _meta(v_scales))
+           k_pages.shape, k_pages.is_contiguous(), k_pages.dtype, k_pages.get_device(),
+           v_pages.shape, v_pages.is_contiguous(), v_pages.dtype, v_pages.get_device(),
+           page_table.shape, page_table.is_contiguous(), page_table.dtype, page_table.get_device(),
+           seq_lens.shape, seq_lens.is_contiguous(), seq_lens.dtype, seq_lens.get_device(),
+           _meta(q_starts), None if q is None else (q.shape, q.stride(), q.dtype, q.get_device()), _meta(q_out), _meta(inv_freq), _meta(ws), _meta(k_scales), _meta(v_scales))
     known = _paged_known.get(key)
     if known is None:
         lead = k if q is None else q
@@ -610,10 +610,10 @@ def _attend_paged(op, name, q, k_pages, v_pages, prefix_table, prefix_len, page_
     window = _int32("window", window)
     prefix_len = _int32("prefix_len", prefix_len)
     index = q.get_device()
-    key = (op, index, q.shape, q.stride(), q.dtype, k_pages.shape, k_pages.stride(), k_pages.dtype,
-           k_pages.get_device(), v_pages.shape, v_pages.stride(), v_pages.dtype, v_pages.get_device(),
-           page_table.shape, page_table.stride(), page_table.dtype, page_table.get_device(),
-           seq_lens.shape, seq_lens.stride(), seq_lens.dtype, seq_lens.get_device(),
+    key = (op, index, q.shape, q.stride(), q.dtype, k_pages.shape, k_pages.is_contiguous(), k_pages.dtype,
+           k_pages.get_device(), v_pages.shape, v_pages.is_contiguous(), v_pages.dtype, v_pages.get_device(),
+           page_table.shape, page_table.is_contiguous(), page_table.dtype, page_table.get_device(),
+           seq_lens.shape, seq_lens.is_contiguous(), seq_lens.dtype, seq_lens.get_device(),
            _meta(q_starts), _meta(prefix_table), _meta(y), _meta(L), _meta(ws), _meta(k_scales), _meta(v_scales))
     known = _paged_known.get(key)
     if known is None:

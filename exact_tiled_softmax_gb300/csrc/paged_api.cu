@@ -156,14 +156,14 @@ size_t join_bytes(size_t rows, int v) {
          align256(sizeof(int2) * 2 * rows) + 256;
 }
 
-// The most units that the tables can hold (paged_mma_kernel's, of 16 keys).
-long long most_units(const PagedArgs& a, int rt) {
+// The most units of `unit` keys that the tables can hold.
+long long most_units(const PagedArgs& a, int rt, int unit) {
   const long long rows = (long long)a.T * a.G, own = a.prefix_at < 0 ? a.B : a.B - 1;
-  long long keys = ((long long)a.max_pages << a.lps) + 16;
-  if (a.mask_kind == EXATTN_MASK_WINDOW) keys = std::min(keys, (long long)a.window + rt + 32);
+  long long keys = ((long long)a.max_pages << a.lps) + unit;
+  if (a.mask_kind == EXATTN_MASK_WINDOW) keys = std::min(keys, (long long)a.window + rt + 2 * unit);
   const long long tiles = a.starts ? rows / rt + own : own * (((long long)a.each * a.G + rt - 1) / rt);
-  long long units = own > 0 ? tiles * (keys / 16) : 0;
-  if (a.prefix_at >= 0) units += (rows + rt - 1) / rt * ((a.prefix_len + 15ll) / 16);
+  long long units = own > 0 ? tiles * (keys / unit) : 0;
+  if (a.prefix_at >= 0) units += (rows + rt - 1) / rt * ((a.prefix_len + unit - 1ll) / unit);
   return units * a.Hk;
 }
 
@@ -174,7 +174,11 @@ void place_pass(PagedArgs& a, const PagedKernel& k, char* at) {
   // 600 keys behind 162, 8 key heads of 80 and 96 fp32 columns 14.4 us in place of 18.2, 5 tokens over
   // 7382 keys of one head of 112 columns 17.0 of 20.9.  (2 for 3 to 5 units a worker: 30.3 in
   // place of 25.9, 17.6 of 15.9.)
-  a.least = k.least > 2 && most_units(a, k.rt) <= 2ll * k.workers ? 2 : k.least;
+  a.least = k.least > 2 && most_units(a, k.rt, 16) <= 2ll * k.workers ? 2 : k.least;
+  // Pages in 8 bits, units of 32 keys: one, where that is all that there can be for a worker.  One sequence of 1000
+  // keys, 8 key heads of 128 bf16 columns: 9.9 us in place of 11.1; fp32 queries 9.9 of 11.1.  (One for 1.5 to 3
+  // units a worker: 21.1 in place of 18.6, 19.6 of 18.0, 15.8 of 14.7.)
+  if (a.Ks && k.least == 2 && most_units(a, k.rt, 32) <= k.workers) a.least = 1;
   const size_t rows = 2 * (size_t)a.runs * k.rt;
   a.desc = reinterpret_cast<int4*>(at);
   at += align256(sizeof(int4) * (size_t)a.runs);

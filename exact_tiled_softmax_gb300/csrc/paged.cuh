@@ -590,8 +590,7 @@ cudaError_t launch_paged_simt(const PagedArgs& a, bool one_row, cudaStream_t s);
 bool paged_mma_shape(int d, int v);
 PagedKernel paged_mma_kernel_of(int dtype, int d, int v, int rows);  // rows: 8 or 16
 cudaError_t launch_paged_mma(const PagedArgs& a, int rows, cudaStream_t s);
-bool paged_e4m3_shape(int d, int v, int lps);
-PagedKernel paged_e4m3_kernel_of(int dtype, int d, int v, int rows);  // rows: 8 or 16
+PagedKernel paged_e4m3_kernel_of(int dtype, int d, int v, int rows);  // rows: 8, or 16 up to 128 columns
 cudaError_t launch_paged_e4m3(const PagedArgs& a, int rows, cudaStream_t s);
 bool paged_tc_supported(const PagedArgs& a);
 PagedKernel paged_tc_kernel_of();

@@ -118,7 +118,9 @@ int tc_rows(const PagedArgs& a) {
 
 Choice choose(const PagedArgs& a) {
   Choice c;
-  if (current_path() != EXATTN_PATH_SIMT && (a.Ks ? paged_e4m3_shape(a.d, a.v, a.lps) : paged_mma_shape(a.d, a.v)))
+  const bool narrow = paged_mma_shape(a.d, a.v);
+  if (current_path() != EXATTN_PATH_SIMT && a.Ks && !narrow) c.kind = kMma8;
+  else if (current_path() != EXATTN_PATH_SIMT && narrow)
     c.kind = rows_of(a) > tc_rows(a) && paged_tc_supported(a) ? kTc : rows_of(a) > 8 ? kMma16 : kMma8;
   else c.kind = !a.starts && a.T == a.B && a.G == 1 ? kSimtOne : kSimt;
   c.k = kernel_of(c.kind, a);
@@ -139,10 +141,10 @@ constexpr size_t kFlagBytes = 8192;  // status bits of the CTAs of two passes (a
 size_t most_bytes(const exattn_paged_shape* s) {
   size_t most = 0;
   for (const Kind k : {kSimtOne, kSimt, kMma8, kMma16, kTc}) {
-    if (k >= kMma8 && !paged_mma_shape(s->d, s->v)) continue;
     // A prefix's pass takes all tokens as one sequence's.
     if (k == kTc && (s->dtype != EXATTN_BF16 || (long long)s->tokens * (s->heads / s->kv_heads) <= kTcRows)) continue;
     for (const bool e4m3 : {false, true}) {
+      if (!paged_mma_shape(s->d, s->v) && (e4m3 ? k >= kMma16 : k >= kMma8)) continue;
       const size_t x = pass_bytes(kernel_of(k, s->dtype, s->d, s->v, e4m3), s->v);
       most = x > most ? x : most;
     }

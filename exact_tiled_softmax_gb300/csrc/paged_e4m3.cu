@@ -1,5 +1,4 @@
-// Paged attention over pages in 8 bits for few rows to a key head, widths up to 128: bound by
-// reading K and V once.
+// Paged attention over pages in 8 bits for few rows to a key head: bound by reading K and V once.
 //
 // The shape of the kernel for 16-bit pages: a row tile is 8 or 16 rows in the N of the products
 // S^T = K Q^T and O^T = V^T P^T, a worker is a warp that streams the 32-key tiles of its units
@@ -126,22 +125,27 @@ struct Place {
   static constexpr int CH = D / 16;        // pieces of a row
   static constexpr int kTileBytes = kTile * D;
   static constexpr int kRows = 32 / CH;    // rows that a warp copies at once, 512 bytes
+  static constexpr __host__ __device__ int k_swizzle(int r) { return D >= 128 ? ((r >> 1) & 6) | (r & 1) : (r >> 2) & 3; }
+  static constexpr __host__ __device__ int v_swizzle(int r) { return D >= 128 ? r & 7 : (r >> 1) & 3; }
   static __device__ __forceinline__ uint32_t at(int r, int c, int swizzle) {
-    return D == 128 ? r * 128 + ((c ^ swizzle) << 4) : (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ swizzle) << 4);
+    return D >= 128 ? r * D + ((c ^ swizzle) << 4) : (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ swizzle) << 4);
   }
-  static __device__ __forceinline__ uint32_t k_at(int r, int c) {
-    return at(r, c, D == 128 ? ((r >> 1) & 6) | (r & 1) : (r >> 2) & 3);
-  }
-  static __device__ __forceinline__ uint32_t v_at(int r, int c) { return at(r, c, D == 128 ? r & 7 : (r >> 1) & 3); }
-  // What kRows x rows further on the swizzle of a piece's address turns over.
-  static constexpr uint32_t k_turn(int x) { return D == 128 ? (x & 3) << 5 : (x & 1) << 5; }
-  static constexpr uint32_t v_turn(int x) { return D == 128 ? (x & 1) << 6 : 0; }
+  static __device__ __forceinline__ uint32_t k_at(int r, int c) { return at(r, c, k_swizzle(r)); }
+  static __device__ __forceinline__ uint32_t v_at(int r, int c) { return at(r, c, v_swizzle(r)); }
+  // What kRows x rows further on the swizzle of a piece's address turns over (a lane's first row is below kRows,
+  // a power of two).
+  static constexpr uint32_t k_turn(int x) { return k_swizzle(kRows * x) << 4; }
+  static constexpr uint32_t v_turn(int x) { return v_swizzle(kRows * x) << 4; }
 };
 
-template <typename T, int D, int NT>
+// C columns (64, 96, 128 or 256) in rows of D bytes.  Up to 128: 12 warps of an SM with two stages (8 sequences of
+// 16384 keys, 32 heads of 128: 169 us; 8 warps with three 177) where 168 registers are enough, else 8 with three.
+template <typename T, int C, int NT>
 struct Config {
-  static constexpr bool kMany = std::is_same<T, __nv_bfloat16>::value && NT == 1;
-  static constexpr int kW = 4, kStages = kMany ? 2 : 3, kCtas = (kMany ? 3 : 2) * 152;
+  static constexpr int D = C <= 64 ? 64 : C <= 128 ? 128 : 256;
+  static constexpr bool kMany = std::is_same<T, __nv_bfloat16>::value && NT == 1 && D <= 128;
+  static constexpr int kW = D == 256 ? 6 : 4, kStages = kMany || D == 256 ? 2 : 3,
+                       kCtas = (D == 256 ? 1 : kMany ? 3 : 2) * 152;
 };
 
 template <typename T> struct Parts;  // N: of a query's entry and of a weight
@@ -171,9 +175,9 @@ struct Spans {
 // A worker's rows over a segment.  Thread (g, t) = (lane / 4, lane % 4) holds the operands of rows
 // 8 n + g, and of rows 8 n + 2 t + x the factor of their scores, the reference points m and M, the sum
 // over its own keys l, and of the output o[n][y] columns 16 y + g (x = 0, 1) and 16 y + g + 8.
-template <typename T, int D, int NT>
+template <typename T, int C, int NT>
 struct Rows {
-  static constexpr int P = Parts<T>::N, K = D / 16;
+  static constexpr int D = Config<T, C, NT>::D, P = Parts<T>::N, K = C / 16;
   uint32_t qb[NT][P][K][2];
   float f[NT][2], m[NT][2], M[NT][2], l[NT][2], o[NT][K][4];
 
@@ -236,7 +240,7 @@ struct Rows {
       const int i = lane & 7, b = lane >> 3;  // matrices: half b % 2, piece b / 2 of two
       const uint32_t at = kt + Place<D>::k_at(4 * (i >> 1) + (i & 1) + 2 * (b & 1), b >> 1);
 #pragma unroll
-      for (int s = 0; s < D / 32; ++s)
+      for (int s = 0; s < C / 32; ++s)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t k[4];
@@ -338,7 +342,7 @@ struct Rows {
 #pragma unroll
       for (int y = 0; y < K; ++y) {
         // (A branch for every y keeps the steps apart: 16 rows over 262147 keys 141 us in place of 129.)
-        if (y == 4 && v <= 64) break;
+        if (y == K / 2 && 16 * y >= v) break;
         uint32_t r[4];  // of sixteen keys q: keys 4 t to 4 t + 3 of columns 16 y + g and 16 y + g + 8
         ldm2t8(r, at ^ (y << 4));
         uint32_t a[2][4];
@@ -382,18 +386,20 @@ __device__ __forceinline__ void copy_dense(uint32_t k, uint32_t v, uint32_t up, 
   (cp16_at<512 * X, 512 * X>((v ^ Place<16 * CH>::v_turn(X)) + up, vf), ...);
 }
 
-template <typename T, int D, int NT>
+template <typename T, int C, int NT>
 constexpr int smem_bytes() {
-  return Config<T, D, NT>::kW * Config<T, D, NT>::kStages * (2 * Place<D>::kTileBytes + 64);
+  return Config<T, C, NT>::kW * Config<T, C, NT>::kStages * (2 * Place<Config<T, C, NT>::D>::kTileBytes + 64) + 256;
 }
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(32 * Config<T, D, NT>::kW, Config<T, D, NT>::kCtas / 152)
+template <typename T, int C, int NT>
+__global__ void __launch_bounds__(32 * Config<T, C, NT>::kW, Config<T, C, NT>::kCtas / 152)
     paged_e4m3_kernel(const PagedArgs a) {
+  constexpr int D = Config<T, C, NT>::D;
   using At = Place<D>;
-  constexpr int S = Config<T, D, NT>::kStages, kW = Config<T, D, NT>::kW, kRows = 8 * NT, CH = At::CH;
+  constexpr int S = Config<T, C, NT>::kStages, kW = Config<T, C, NT>::kW, kRows = 8 * NT, CH = At::CH;
   constexpr int kStage = 2 * At::kTileBytes;
-  extern __shared__ __align__(128) uint8_t sm[];
+  extern __shared__ __align__(128) uint8_t sm_raw[];
+  uint8_t* sm = sm_raw + (0u - smem_u32(sm_raw) & 255u);  // pieces are found by turning bits of an address over
   __shared__ long long pre[kPagedSums], scan[kW];
   __shared__ PagedWalk walks[kW][2];     // the present segment of the copies, of the products
   __shared__ unsigned tile_keys[kW][S];  // bit r: key r of the staged tile exists
@@ -437,6 +443,7 @@ __global__ void __launch_bounds__(32 * Config<T, D, NT>::kW, Config<T, D, NT>::k
   int pages = -1, pages_next = -1;
   const int* p_row = nullptr;
   const int lpk = min(a.lps, 5), span = 32 << lpk;
+  const bool small = a.lps < 3;  // pages of fewer keys than the copies count in
   auto entries = [&](int first) {
     const int key = first + (lane << lpk);
     int page = -1;
@@ -456,12 +463,14 @@ __global__ void __launch_bounds__(32 * Config<T, D, NT>::kW, Config<T, D, NT>::k
   const uint8_t* Kp = static_cast<const uint8_t*>(a.Kp) + static_cast<size_t>(pr) * d + 16 * pc;
   const uint8_t* Vp = static_cast<const uint8_t*>(a.Vp) + static_cast<size_t>(pr) * v + 16 * pc;
   const uint8_t* Ep = lane < 8 ? a.Ks : a.Vs;  // lanes 0 to 7 copy keys' exponents, 8 to 15 values'
-  const bool dense = d == D && v == D && lpk == 5;
+  // Tiles that are copied as one stretch: rows of D bytes, or of any width where the kernel's columns are fewer.
+  // (Both in one kernel cost the first: 8 sequences of 16384 keys 177 us in place of 169.)
+  const bool stretch = lpk == 5 && (C != D || (d == D && v == D));
   int issued = 0;  // tiles copied so far
   // The products' segment.
   int left = 0, key0 = 0;
   Spans<NT> sp;
-  Rows<T, D, NT> st;
+  Rows<T, C, NT> st;
 
   // One loop: step `it` copies tile it in and multiplies tile i = it - (S - 1).  Every
   // part of the code stands in one place, also while the ring fills: code that runs
@@ -531,39 +540,62 @@ __global__ void __launch_bounds__(32 * Config<T, D, NT>::kW, Config<T, D, NT>::k
       const uint32_t up = s * kStage;
       unsigned have = 0u;
       const int page0 = __shfl_sync(0xFFFFFFFFu, pages, (p_key - p_base) >> lpk);
-      if (dense && page0 >= 0 && p_key >= p_j0 && p_key + kTile <= p_j1) {
-        // All keys, of one page, in rows of D bytes: one stretch of memory.
+      if (stretch && page0 >= 0 && p_key >= p_j0 && p_key + kTile <= p_j1) {
+        // All keys, of one page: one stretch of memory.
         const long long row = ((static_cast<long long>(page0) * a.Hk + p_h) << a.lps) + (p_key & ((1 << a.lps) - 1));
-        copy_dense<CH>(k_to, v_to, up, Kp + row * D, Vp + row * D, std::make_integer_sequence<int, CH>{});
+        if constexpr (C == D) {
+          copy_dense<CH>(k_to, v_to, up, Kp + row * D, Vp + row * D, std::make_integer_sequence<int, CH>{});
+        } else {
+          const uint8_t *kf = Kp + row * d, *vf = Vp + row * v;
+#pragma unroll
+          for (int x = 0; x < CH; ++x, kf += At::kRows * d, vf += At::kRows * v) {
+            if (k_on) cp16((k_to ^ At::k_turn(x)) + up + 512 * x, kf, 16);
+            if (v_on) cp16((v_to ^ At::v_turn(x)) + up + 512 * x, vf, 16);
+          }
+        }
         if (lane < 16) cp4(scales + s * 64 + 4 * lane, Ep + row + 4 * (lane & 7), 4);
         have = 0xFFFFFFFFu;
-      } else {
-      // Eight keys at a time are one page's rows behind one another; pool rows of the four eights.
-      long long row[4];
+      } else if (!small) {
+        // Eight keys at a time are one page's rows behind one another; pool rows of the four eights.
+        long long row[4];
 #pragma unroll
-      for (int z = 0; z < 4; ++z) {
-        const int key = p_key + 8 * z, page = __shfl_sync(0xFFFFFFFFu, pages, (key - p_base) >> lpk);
-        if (page >= 0) have |= 0xFFu << 8 * z;
-        row[z] = page < 0 ? 0 : ((static_cast<long long>(page) * a.Hk + p_h) << a.lps) + (key & ((1 << a.lps) - 1));
-      }
-      if (p_j0 > p_key) have &= 0xFFFFFFFFu << min(31, p_j0 - p_key);  // below 32: the segment has keys here
-      if (p_j1 < p_key + kTile) have &= 0xFFFFFFFFu >> min(31, p_key + kTile - p_j1);
-      auto copy = [&](auto whole) {
+        for (int z = 0; z < 4; ++z) {
+          const int key = p_key + 8 * z, page = __shfl_sync(0xFFFFFFFFu, pages, (key - p_base) >> lpk);
+          if (page >= 0) have |= 0xFFu << 8 * z;
+          row[z] = page < 0 ? 0 : ((static_cast<long long>(page) * a.Hk + p_h) << a.lps) + (key & ((1 << a.lps) - 1));
+        }
+        if (p_j0 > p_key) have &= 0xFFFFFFFFu << min(31, p_j0 - p_key);  // below 32: the segment has keys here
+        if (p_j1 < p_key + kTile) have &= 0xFFFFFFFFu >> min(31, p_key + kTile - p_j1);
 #pragma unroll
         for (int x = 0; x < CH; ++x) {
-          const int z = CH == 8 ? x >> 1 : x, on = CH == 8 ? 4 * (x & 1) : 0;
-          const int bytes = whole ? 16 : ((have >> (pr + At::kRows * x)) & 1u) << 4;
+          const int z = At::kRows * x / 8, on = At::kRows * x % 8;
+          const int bytes = ((have >> (pr + At::kRows * x)) & 1u) << 4;
           if (k_on) cp16((k_to ^ At::k_turn(x)) + up + 512 * x, Kp + (row[z] + on) * d, bytes);
           if (v_on) cp16((v_to ^ At::v_turn(x)) + up + 512 * x, Vp + (row[z] + on) * v, bytes);
         }
-      };
-      if (have == 0xFFFFFFFFu) copy(std::true_type{});
-      else copy(std::false_type{});
-      if (lane < 16) {
-        const int z = (lane >> 1) & 3;
-        const long long from = z == 0 ? row[0] : z == 1 ? row[1] : z == 2 ? row[2] : row[3];
-        cp4(scales + s * 64 + 4 * lane, Ep + from + 4 * (lane & 1), (have >> 8 * z) & 0xFFu ? 4 : 0);
-      }
+        if (lane < 16) {
+          const int z = (lane >> 1) & 3;
+          const long long from = z == 0 ? row[0] : z == 1 ? row[1] : z == 2 ? row[2] : row[3];
+          cp4(scales + s * 64 + 4 * lane, Ep + from + 4 * (lane & 1), (have >> 8 * z) & 0xFFu ? 4 : 0);
+        }
+      } else {
+        // Key by key: lane l finds key l.
+        const int key = p_key + lane, page = __shfl_sync(0xFFFFFFFFu, pages, (key - p_base) >> lpk);
+        const bool on = page >= 0 && key >= p_j0 && key < p_j1;
+        const long long mine = on ? ((static_cast<long long>(page) * a.Hk + p_h) << a.lps) + (key & ((1 << a.lps) - 1)) : 0;
+        have = __ballot_sync(0xFFFFFFFFu, on);
+#pragma unroll 1
+        for (int x = 0; x < CH; ++x) {
+          const int r = pr + At::kRows * x, bytes = ((have >> r) & 1u) << 4;
+          const long long row = __shfl_sync(0xFFFFFFFFu, mine, r) - pr;  // Kp and Vp are at row pr
+          const uint8_t* none = static_cast<const uint8_t*>(a.Kp);
+          if (k_on) cp16(base + up + At::k_at(r, pc), bytes ? Kp + row * d : none, bytes);
+          if (v_on) cp16(base + up + At::kTileBytes + At::v_at(r, pc), bytes ? Vp + row * v : none, bytes);
+        }
+        // Exponents byte by byte; the products' loads come after the next barriers of the warp.
+        const unsigned ke = on ? __ldg(a.Ks + mine) : 0u, ve = on ? __ldg(a.Vs + mine) : 0u;
+        asm volatile("st.shared.u8 [%0], %1;" ::"r"(scales + s * 64 + lane), "r"(ke) : "memory");
+        asm volatile("st.shared.u8 [%0], %1;" ::"r"(scales + s * 64 + 32 + lane), "r"(ve) : "memory");
       }
       if (lane == 0) tile_keys[warp][s] = have;
       p_key += kTile;
@@ -619,7 +651,7 @@ __global__ void __launch_bounds__(32 * Config<T, D, NT>::kW, Config<T, D, NT>::k
       if (sizeof(T) == 4 && !z) z = static_cast<float*>(a.Y);
       if (z) {
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c)
+        for (int c = 0; c < C / 8; ++c)
 #pragma unroll
           for (int x = 0; x < 2; ++x)
             if (on[x] && 8 * c < v) z[to[x] * v + 8 * c + g] = st.o[y][c >> 1][2 * (c & 1) + x] * f0[x] * f1[x];
@@ -630,7 +662,7 @@ __global__ void __launch_bounds__(32 * Config<T, D, NT>::kW, Config<T, D, NT>::k
       __nv_bfloat16* mine = static_cast<__nv_bfloat16*>(a.Y) + (g & 1 ? r1 : r0) * v + 2 * t;
       const bool mine_on = 8 * y + g < w.t.rows;
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
+      for (int c = 0; c < C / 8; ++c) {
         const float* o = &st.o[y][c >> 1][2 * (c & 1)];
         const uint32_t pair = transpose8(pack_bf16x2(o[0] * f0[0] * f1[0], o[1] * f0[1] * f1[1]));
         if (mine_on && 8 * c < v) *reinterpret_cast<uint32_t*>(mine + 8 * c) = pair;
@@ -642,42 +674,55 @@ __global__ void __launch_bounds__(32 * Config<T, D, NT>::kW, Config<T, D, NT>::k
   paged_end(a, bits, &joined);
 }
 
-template <typename T, int D, int NT>
+template <typename T, int C, int NT>
 cudaError_t e4m3_launch(const PagedArgs& a, cudaStream_t s) {
-  constexpr int bytes = smem_bytes<T, D, NT>();
-  const cudaError_t e = allow_smem<paged_e4m3_kernel<T, D, NT>>(bytes);
+  constexpr int bytes = smem_bytes<T, C, NT>();
+  const cudaError_t e = allow_smem<paged_e4m3_kernel<T, C, NT>>(bytes);
   if (e != cudaSuccess) return e;
   before_launch(kKernPaged, s);
-  const cudaError_t le = launch_early(paged_e4m3_kernel<T, D, NT>, dim3(Config<T, D, NT>::kCtas), 32 * Config<T, D, NT>::kW, bytes, s, a);
+  const cudaError_t le = launch_early(paged_e4m3_kernel<T, C, NT>, dim3(Config<T, C, NT>::kCtas), 32 * Config<T, C, NT>::kW, bytes, s, a);
   after_launch(kKernPaged, s);
   return le;
 }
 
-template <typename T>
-cudaError_t e4m3_columns(const PagedArgs& a, int rows, cudaStream_t s) {
-  if (a.d <= 64 && a.v <= 64) return rows == 8 ? e4m3_launch<T, 64, 1>(a, s) : e4m3_launch<T, 64, 2>(a, s);
-  return rows == 8 ? e4m3_launch<T, 128, 1>(a, s) : e4m3_launch<T, 128, 2>(a, s);
+// The columns that a kernel is made for; of 256 with 8-row tiles alone, whose registers suffice.
+int columns_of(int d, int v) {
+  const int most = d > v ? d : v;
+  return most <= 64 ? 64 : most <= 96 ? 96 : most <= 128 ? 128 : 256;
 }
-template <typename T, int D, int NT>
+template <typename T>
+cudaError_t e4m3_columns(const PagedArgs& a, int columns, int rows, cudaStream_t s) {
+  switch (columns) {
+    case 64: return rows == 8 ? e4m3_launch<T, 64, 1>(a, s) : e4m3_launch<T, 64, 2>(a, s);
+    case 96: return rows == 8 ? e4m3_launch<T, 96, 1>(a, s) : e4m3_launch<T, 96, 2>(a, s);
+    case 128: return rows == 8 ? e4m3_launch<T, 128, 1>(a, s) : e4m3_launch<T, 128, 2>(a, s);
+    default: return e4m3_launch<T, 256, 1>(a, s);
+  }
+}
+// Least units: see launch_paged_mma's; two, and one where the tables hold no more (place_pass).
+template <typename T, int C, int NT>
 constexpr PagedKernel e4m3_kernel() {
-  return {8 * NT, Config<T, D, NT>::kCtas, Config<T, D, NT>::kCtas * Config<T, D, NT>::kW, 2};
+  return {8 * NT, Config<T, C, NT>::kCtas, Config<T, C, NT>::kCtas * Config<T, C, NT>::kW, 2};
 }
 template <typename T>
-PagedKernel e4m3_kernel(bool narrow, int rows) {
-  if (narrow) return rows == 8 ? e4m3_kernel<T, 64, 1>() : e4m3_kernel<T, 64, 2>();
-  return rows == 8 ? e4m3_kernel<T, 128, 1>() : e4m3_kernel<T, 128, 2>();
+PagedKernel e4m3_kernel(int columns, int rows) {
+  switch (columns) {
+    case 64: return rows == 8 ? e4m3_kernel<T, 64, 1>() : e4m3_kernel<T, 64, 2>();
+    case 96: return rows == 8 ? e4m3_kernel<T, 96, 1>() : e4m3_kernel<T, 96, 2>();
+    case 128: return rows == 8 ? e4m3_kernel<T, 128, 1>() : e4m3_kernel<T, 128, 2>();
+    default: return e4m3_kernel<T, 256, 1>();
+  }
 }
 
 }  // namespace
 
-// Eight rows of a page behind one another are what the copies count in.
-bool paged_e4m3_shape(int d, int v, int lps) { return d <= 128 && v <= 128 && lps >= 3; }
 PagedKernel paged_e4m3_kernel_of(int dtype, int d, int v, int rows) {
-  const bool narrow = d <= 64 && v <= 64;
-  return dtype == kF32 ? e4m3_kernel<float>(narrow, rows) : e4m3_kernel<__nv_bfloat16>(narrow, rows);
+  const int columns = columns_of(d, v);
+  return dtype == kF32 ? e4m3_kernel<float>(columns, rows) : e4m3_kernel<__nv_bfloat16>(columns, rows);
 }
 cudaError_t launch_paged_e4m3(const PagedArgs& a, int rows, cudaStream_t s) {
-  return a.dtype == kF32 ? e4m3_columns<float>(a, rows, s) : e4m3_columns<__nv_bfloat16>(a, rows, s);
+  const int columns = columns_of(a.d, a.v);
+  return a.dtype == kF32 ? e4m3_columns<float>(a, columns, rows, s) : e4m3_columns<__nv_bfloat16>(a, columns, rows, s);
 }
 
 }  // namespace exattn

@@ -508,13 +508,16 @@ int exattn_paged_run(int op, const exattn_paged_call* call);
  * entries beyond fp32 become NaN, and so does the other entry of their pair.  A rotated key is rounded, and its byte chosen, as if its rotation had been computed in
  * 64 bits; q_out is rotated in fp32 as above.
  *
- * Attention.  Scores, statistics and outputs are summed in fp32.  Few rows to a key head (up
- * to 16), or fp32 queries, with d, v <= 128, pages of 8 keys or more: operands are fp16 parts,
- * each row of Q scaled by a power of two; bf16 queries are exact where they are no smaller than 2^-30 of their
- * row's largest, fp32 queries are held to 2^-22 of themselves or 2^-38 of their row's largest,
- * weights p 2^(b - 127) to 2^-11 (bf16) or 2^-22 (fp32) of themselves or 2^-32 of their row's
- * largest.  More rows of bf16 queries: probabilities are rounded to bf16, as above.
- * All other calls follow the formula in fp32.  Non-finite entries act as above.
+ * (Frequencies up to 64 radians a token.)
+ *
+ * Attention.  Scores, statistics and outputs are summed in fp32.  Where the 256-row kernel runs
+ * (bf16 queries, d, v <= 128, pages of 8 keys or more, a positive scale, more than 16 rows to a
+ * key head on average, or more than 32 where the tables or the prefix hold 2^17 keys of all key heads),
+ * probabilities are rounded to bf16 before they meet V, as above.  All other kernels: operands
+ * are fp16 parts, each row of Q scaled by a power of two; bf16 queries are exact where they are no
+ * smaller than 2^-30 of their row's largest entry, fp32 queries are held to 2^-22 of themselves or
+ * 2^-38 of their row's largest, weights p 2^(b - 127) to 2^-11 (bf16) or 2^-22 (fp32) of
+ * themselves or 2^-32 of their row's largest (EXATTN_PATH_SIMT: whole).  Non-finite entries act as above.
  * ------------------------------------------------------------------------- */
 int attn_append_paged_e4m3(const exattn_paged_shape* shape, const void* q, const void* k, const void* v,
                            const int* page_table, const int* seq_lens, const int* q_starts,

@@ -83,11 +83,11 @@ def weight_bits(path, dtype, d, v, page, rows, scale=1.0):
     """Significant bits of a weight in the product with V, by the kernel that `rows` rows to a key
     head take: the tall tiles round probabilities to bf16, the others hold weights in fp16 parts (one
     of bf16 queries, two of fp32 ones); the SIMT kernels hold them in fp32."""
-    if path == "simt" or d > 128 or v > 128 or page < 8:
+    if path == "simt":
         return 22
     if dtype == "f32":
         return 21
-    return 8 if rows > 16 and scale > 0 else 11
+    return 8 if rows > 16 and scale > 0 and d <= 128 and v <= 128 and page >= 8 else 11
 
 
 def small_weights(W, n):

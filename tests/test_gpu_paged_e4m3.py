@@ -445,7 +445,10 @@ def test_entries_that_are_not_numbers_stay_where_they_reach(ex, path, dtype, nq,
 @pytest.mark.parametrize("dtype,d,v,nq,page", [("bf16", 16, 16, 1, 8), ("bf16", 32, 128, 5, 16), ("bf16", 128, 16, 60, 64),
                                                ("bf16", 48, 48, 60, 8), ("f32", 16, 128, 3, 32), ("f32", 112, 112, 9, 8),
                                                ("bf16", 64, 64, 40, 4), ("f32", 64, 32, 3, 2), ("bf16", 144, 32, 2, 16),
-                                               ("f32", 32, 240, 1, 16)])
+                                               ("f32", 32, 240, 1, 16), ("bf16", 96, 96, 2, 64), ("f32", 80, 96, 2, 32),
+                                               ("bf16", 96, 80, 7, 1024), ("bf16", 256, 256, 3, 32), ("f32", 208, 256, 9, 64),
+                                               ("f32", 256, 256, 2, 128), ("bf16", 256, 144, 20, 8), ("bf16", 128, 128, 5, 1),
+                                               ("f32", 96, 64, 1, 2), ("bf16", 256, 256, 2, 2), ("bf16", 64, 64, 1, 4)])
 def test_widths_between(ex, path, dtype, d, v, nq, page):
     b = Batch8([700, nq, 90], [nq, nq, nq], 4, 2, d, v, dtype, page, seed=d + v + nq)
     y, L, status = _attend(ex, b, "causal", 0, 0.03)

@@ -565,7 +565,8 @@ def append_paged(k, v, k_pages, v_pages, page_table, seq_lens, q_starts=None, q=
            v_pages.shape, v_pages.is_contiguous(), v_pages.dtype, v_pages.get_device(),
            page_table.shape, page_table.is_contiguous(), page_table.dtype, page_table.get_device(),
            seq_lens.shape, seq_lens.is_contiguous(), seq_lens.dtype, seq_lens.get_device(),
-           _meta(q_starts), None if q is None else (q.shape, q.stride(), q.dtype, q.get_device()), _meta(q_out), _meta(inv_freq), _meta(ws), _meta(k_scales), _meta(v_scales))
+           _meta(q_starts), None if q is None else (q.shape, q.stride(), q.dtype, q.get_device()),
+           _meta(q_out), _meta(inv_freq), _meta(ws), _meta(k_scales), _meta(v_scales))
     known = _paged_known.get(key)
     if known is None:
         lead = k if q is None else q
@@ -614,7 +615,8 @@ def _attend_paged(op, name, q, k_pages, v_pages, prefix_table, prefix_len, page_
            k_pages.get_device(), v_pages.shape, v_pages.is_contiguous(), v_pages.dtype, v_pages.get_device(),
            page_table.shape, page_table.is_contiguous(), page_table.dtype, page_table.get_device(),
            seq_lens.shape, seq_lens.is_contiguous(), seq_lens.dtype, seq_lens.get_device(),
-           _meta(q_starts), _meta(prefix_table), _meta(y), _meta(L), _meta(ws), _meta(k_scales), _meta(v_scales))
+           _meta(q_starts), _meta(prefix_table), _meta(y), _meta(L), _meta(ws), _meta(k_scales),
+           _meta(v_scales))
     known = _paged_known.get(key)
     if known is None:
         shape = _check_paged(q, k_pages, v_pages, page_table, seq_lens, q_starts, ws, k_scales, v_scales)

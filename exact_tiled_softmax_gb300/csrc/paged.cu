@@ -13,7 +13,8 @@
 // share each read.  Bound by issue: every key costs 2 (d + v) multiply-adds a row and the
 // shuffles of a group.  Heads of 256 columns, 537 MB of keys and values: one row 97 us in bf16
 // (5.5 TB/s), 84 in fp32 (6.4), four rows 246 in bf16.  One row of 128 columns: 333 us for 2.1
-// GB against the tensor cores' 325, which take eight rows in that time.
+// GB against the tensor cores' 325, which take eight rows in that time.  Pages in 8 bits come here only where
+// the path is forced to SIMT: 276 us where the tensor cores take 168.
 #include <cuda_fp16.h>
 
 #include <type_traits>

@@ -19,6 +19,12 @@
 // The reference points move only when a row's maximum passes them by more than 2^8, which a vote
 // tells without the maximum.
 //
+// Measured: one token of 8 sequences over 16384 keys, 32 key heads of 128 columns, 1.08 GB: 168 us, 6.4 TB/s or
+// 95% of the measured copy (16-bit pages: 333); of 96 columns 143 us (5.6 TB/s), 80 136, 64 98; fp32 queries 174.
+// 64 ragged sequences, 8 rows to a key head: 351 us, 98%.  16 rows, 262147 keys of 8 heads: 96 us, 5.6 TB/s, and 9
+// of merge: registers for two row tiles leave two warps to a scheduler.  256 columns, 537 MB: 104 us for one row,
+// 103 for four.  Pages of 8 or 16 keys 184 us in place of 168.
+//
 // The products' inner index is permuted freely, as long as both operands agree: a lane of a quad has four
 // columns of 16 of a key or a query, which is what a 16-bit matrix load gives it of the bytes.  V comes
 // transposed byte by byte (four keys of one column), and two conversions make two pairs of keys of

@@ -3,7 +3,7 @@
 // the tensor cores and the exponentials.
 //
 // A row tile is 256 rows, two 128-row halves A and B that share every key block
-// of 128.  Roles (12 warps): warps 0-3 and 4-7 the softmax of A and B, one thread a
+// of 128.  Roles (12 warps; for 8-bit pages four more): warps 0-3 and 4-7 the softmax of A and B, one thread a
 // row; warp 8 the loads, warp 9 the products, warps 10-11 the rows of Q.  Warp 11
 // also walks the CTA's segments and hands each to the others through a ring of two.  Per
 // key block t the MMA warp issues S_A(t), PV_B(t-1), S_B(t), PV_A(t), so each half's softmax
@@ -28,6 +28,12 @@
 // outside the pool) are not part of any row's mask (`keep`, four words a block,
 // written beside the block's V), and the MMA warp zeroes them in V before P.V, so
 // that what they hold, NaN included, meets no product that counts.
+//
+// Pages in 8 bits.  Their tiles are loaded as they are, and warps 12-15 turn them into the bf16 tiles of the
+// products, a row's power of two folded in: an e4m3 number times it is a bf16 value.  Tensor memory, full of
+// S and O, has no room for the scales of a block-scaled product.  Measured: the chunks above 241 us a launch (258 a
+// call, 1.03 PFLOP/s): converting shares the schedulers and shared memory with the softmax.  Without the
+// conversion's work a call takes 221 us, without the softmax's 241, without both 172.  Pages of 8 keys: 353 us.
 //
 // Every wait is bounded; on a timeout the CTA records EXATTN_TIMEOUT, drains its
 // own copies and products, frees TMEM and returns.

@@ -74,7 +74,7 @@ enum exattn_mask_kind {
 enum exattn_status {
   EXATTN_OK = 0,
   EXATTN_INVALID_ARG = 1,        /* null pointer, non-positive size, bad mask kind/window */
-  EXATTN_UNSUPPORTED = 2,        /* d or v > 256, or bf16 with d or v not a multiple of 8 */
+  EXATTN_UNSUPPORTED = 2,        /* d or v > 256, or bf16 (8-bit pages) with d or v not a multiple of 8 (16) */
   EXATTN_MISALIGNED = 3,         /* a pointer is not 16-byte aligned */
   EXATTN_WORKSPACE_TOO_SMALL = 4,
   EXATTN_EMPTY_ROW = 5,          /* some A_i was empty (status word) */

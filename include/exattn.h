@@ -505,19 +505,19 @@ int exattn_paged_run(int op, const exattn_paged_call* call);
  * most 448 * 2^(b - 127), so that nothing saturates and scaling is exact; 0 for a row
  * without a nonzero finite entry.  Each entry is rounded once, to nearest, ties to even: off
  * by 2^-4 of itself at most, or by 2^(b - 137) where that is more.  Infinities, NaN and rotated
- * entries beyond fp32 become NaN, and so does the other entry of their pair.  A rotated key is rounded, and its byte chosen, as if its rotation had been computed in
- * 64 bits; q_out is rotated in fp32 as above.
- *
- * (Frequencies up to 64 radians a token.)
+ * entries beyond fp32 become NaN, and so does the other entry of their pair.  A rotated key is
+ * rounded, and its byte chosen, as if its rotation had been computed in 64 bits, for frequencies of
+ * up to 64 radians a token; q_out is rotated in fp32 as above.
  *
  * Attention.  Scores, statistics and outputs are summed in fp32.  Where the 256-row kernel runs
  * (bf16 queries, d, v <= 128, pages of 8 keys or more, a positive scale, more than 16 rows to a
- * key head on average, or more than 32 where the tables or the prefix hold 2^17 keys of all key heads),
- * probabilities are rounded to bf16 before they meet V, as above.  All other kernels: operands
+ * key head on average, or more than 32 where the tables, the windows or the prefix can hold 2^17 keys of
+ * all key heads; a short prefix as above), probabilities are rounded to bf16 before they meet V, as above.  All other kernels: operands
  * are fp16 parts, each row of Q scaled by a power of two; bf16 queries are exact where they are no
  * smaller than 2^-30 of their row's largest entry, fp32 queries are held to 2^-22 of themselves or
  * 2^-38 of their row's largest, weights p 2^(b - 127) to 2^-11 (bf16) or 2^-22 (fp32) of
- * themselves or 2^-32 of their row's largest (EXATTN_PATH_SIMT: whole).  Non-finite entries act as above.
+ * themselves or 2^-32 of their row's largest (EXATTN_PATH_SIMT: whole).  Non-finite entries act as above;
+ * so may a score whose scale times the largest entries of its query and key is 2^148 or more.
  * ------------------------------------------------------------------------- */
 int attn_append_paged_e4m3(const exattn_paged_shape* shape, const void* q, const void* k, const void* v,
                            const int* page_table, const int* seq_lens, const int* q_starts,

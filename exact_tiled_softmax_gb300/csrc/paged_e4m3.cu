@@ -21,7 +21,7 @@
 //
 // Measured: one token of 8 sequences over 16384 keys, 32 key heads of 128 columns, 1.08 GB: 168 us, 6.4 TB/s or
 // 95% of the measured copy (16-bit pages: 333); of 96 columns 143 us (5.6 TB/s), 80 136, 64 98; fp32 queries 174.
-// 64 ragged sequences, 8 rows to a key head: 351 us, 98%.  16 rows, 262147 keys of 8 heads: 96 us, 5.6 TB/s, and 9
+// 64 ragged sequences, 8 rows to a key head: 351 us, 98%.  16 rows, 262147 keys of 8 heads: 90 us, 6.0 TB/s, and 9
 // of merge: registers for two row tiles leave two warps to a scheduler.  256 columns, 537 MB: 104 us for one row,
 // 103 for four.  Pages of 8 or 16 keys 184 us in place of 168.
 //
@@ -151,7 +151,7 @@ struct Config {
   static constexpr int D = C <= 64 ? 64 : C <= 128 ? 128 : 256;
   static constexpr bool kMany = std::is_same<T, __nv_bfloat16>::value && NT == 1 && D <= 128;
   // Two row tiles of fp32 queries, whose parts are 64 registers: they stay in shared memory, in place of a stage
-  // (32 sequences of 8192 keys, 8 key heads of 128 columns, 16 rows: 124 us in place of 148, 96 and 64 columns the
+  // (32 sequences of 8192 keys, 8 key heads of 128 columns, 16 rows: 121 us in place of 145, 96 and 64 columns the
   // same; the 32 registers of bf16 ones: 147 in place of 109).
   static constexpr bool kQueries = std::is_same<T, float>::value && NT == 2;
   static constexpr int kW = D == 256 ? 6 : 4, kStages = kMany || D == 256 || kQueries ? 2 : 3,
@@ -162,17 +162,16 @@ struct Config {
 template <typename T> struct Parts;  // N: of a query's entry and of a weight
 template <> struct Parts<__nv_bfloat16> {
   static constexpr int N = 1;
-  // Four columns.
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&x)[4]) {
-    const uint2 raw = *reinterpret_cast<const uint2*>(p);
+  using Raw = uint2;  // four columns
+  static __device__ __forceinline__ void to(const Raw& raw, float (&x)[4]) {
     x[0] = __uint_as_float(raw.x << 16), x[1] = __uint_as_float(raw.x & 0xFFFF0000u);
     x[2] = __uint_as_float(raw.y << 16), x[3] = __uint_as_float(raw.y & 0xFFFF0000u);
   }
 };
 template <> struct Parts<float> {
   static constexpr int N = 2;
-  static __device__ __forceinline__ void load(const float* p, float (&x)[4]) {
-    const float4 q = *reinterpret_cast<const float4*>(p);
+  using Raw = float4;
+  static __device__ __forceinline__ void to(const Raw& q, float (&x)[4]) {
     x[0] = q.x, x[1] = q.y, x[2] = q.z, x[3] = q.w;
   }
 };
@@ -193,18 +192,23 @@ struct Rows {
   uint32_t qb[kQueries ? 1 : NT][P][K][2];  // kQueries: of the row tile that is loaded
   float f[NT][2], m[NT][2], M[NT][2], l[NT][2], o[NT][K][4];
 
-  // The tile's row 8 n + g.  qs: the warp's place for operands in shared memory.
-  __device__ __forceinline__ void load_q(int n, const T* row, bool on, int d, float sl2, uint32_t qs) {
+  using Raw = typename Parts<T>::Raw;
+  // The tile's row 8 n + g.
+  static __device__ __forceinline__ void load_q(Raw (&raw)[K], const T* row, bool on, int d) {
+#pragma unroll
+    for (int c = 0; c < K; ++c) {
+      raw[c] = Raw{};
+      if (on && 16 * c < d) raw[c] = *reinterpret_cast<const Raw*>(row + 16 * c + 4 * (threadIdx.x & 3));
+    }
+  }
+  // Its operands.  qs: the warp's place for them in shared memory.
+  __device__ __forceinline__ void take_q(int n, const Raw (&raw)[K], float sl2, uint32_t qs) {
     const int lane = threadIdx.x & 31, t = lane & 3;
     float x[K][4];
     unsigned top = 0u;
 #pragma unroll
     for (int c = 0; c < K; ++c) {
-      if (on && 16 * c < d) {
-        Parts<T>::load(row + 16 * c + 4 * t, x[c]);
-      } else {
-        x[c][0] = x[c][1] = x[c][2] = x[c][3] = 0.f;
-      }
+      Parts<T>::to(raw[c], x[c]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[c][e]) & 0x7FFFFFFFu);
     }
@@ -507,6 +511,12 @@ __global__ void __launch_bounds__(32 * Config<T, C, NT>::kW, Config<T, C, NT>::k
   // (Both in one kernel cost the first: 8 sequences of 16384 keys 177 us in place of 169.)
   const bool stretch = lpk == 5 && (C != D || (d == D && v == D));
   int issued = 0;  // tiles copied so far
+  // Row q of a segment's row tile (of the first, where the tile has no such).
+  auto query = [&](const PagedWalk& w, int q) {
+    const int r = w.rt * kRows + (q < w.t.rows ? q : 0), tok = div_by(r, a.by_group);
+    return static_cast<const T*>(a.Q) + (w.s.s0 + tok) * a.q_stride + (w.h * a.G + r - tok * a.G) * d;
+  };
+  const int lines = (d * static_cast<int>(sizeof(T)) + 127) / 128;  // of 128 bytes, of a row
   // The products' segment.
   int left = 0, key0 = 0;
   Spans<NT> sp;
@@ -543,18 +553,28 @@ __global__ void __launch_bounds__(32 * Config<T, C, NT>::kW, Config<T, C, NT>::k
         p_j1 = j1;
         p_h = w.h;
         p_row = paged_table(a, w.b);
+        // The segment's rows of Q, on their way before its first product: a miss waits some 4 us behind the streams
+        // (16 fp32 rows over 262147 keys 119 us in place of 121, one bf16 row of 8 x 16384 keys 168.9 of 169.4).
+#pragma unroll 1
+        for (int x = lane; x < w.t.rows * lines; x += 32) {
+          const T* at = query(w, x / lines) + x % lines * (128 / sizeof(T));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+        }
         pages = entries(p_base);
         pages_next = entries(p_base + span);
       } else {
         left = n;
         key0 = key;
         const int r0 = w.rt * kRows;
+        // Row g of the tile for the operand, rows 2 t and 2 t + 1 for the statistics.  All loads first, for the same
+        // reason: one row tile after the other 16 rows over 262147 keys take 105 us in place of 99, 4 x 4000 keys 26.7
+        // of 23.2.
+        typename Parts<T>::Raw raw[NT][C / 16];
+#pragma unroll
+        for (int y = 0; y < NT; ++y) st.load_q(raw[y], query(w, 8 * y + g), 8 * y + g < w.t.rows, d);
 #pragma unroll
         for (int y = 0; y < NT; ++y) {
-          // Row g of the tile for the operand, rows 2 t and 2 t + 1 for the statistics.
-          const int q = 8 * y + g, r = r0 + (q < w.t.rows ? q : 0), tok = div_by(r, a.by_group);
-          st.load_q(y, static_cast<const T*>(a.Q) + (w.s.s0 + tok) * a.q_stride + (w.h * a.G + r - tok * a.G) * d,
-                    q < w.t.rows, d, a.sl2, qs);
+          st.take_q(y, raw[y], a.sl2, qs);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int row = 8 * y + 2 * t + x;

@@ -151,7 +151,7 @@ struct Config {
   static constexpr int D = C <= 64 ? 64 : C <= 128 ? 128 : 256;
   static constexpr bool kMany = std::is_same<T, __nv_bfloat16>::value && NT == 1 && D <= 128;
   // Two row tiles of fp32 queries, whose parts are 64 registers: they stay in shared memory, in place of a stage
-  // (32 sequences of 8192 keys, 8 key heads of 128 columns, 16 rows: 121 us in place of 145, 96 and 64 columns the
+  // (32 sequences of 8192 keys, 8 key heads of 128 columns, 16 rows: 124 us in place of 148, 96 and 64 columns the
   // same; the 32 registers of bf16 ones: 147 in place of 109).
   static constexpr bool kQueries = std::is_same<T, float>::value && NT == 2;
   static constexpr int kW = D == 256 ? 6 : 4, kStages = kMany || D == 256 || kQueries ? 2 : 3,

@@ -138,6 +138,37 @@ def test_append_on_the_borders(ex, dtype, pairs, inter):
     assert np.array_equal(got[2], want[2]) and np.array_equal(got[3], want[3])
 
 
+@pytest.mark.parametrize("offset", [0, 11])
+@pytest.mark.parametrize("pairs,inter", [(32, False), (32, True), (13, False), (21, True)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_append_of_rows_whose_largest_lies_on_the_border(ex, dtype, pairs, inter, offset):
+    """Of columns that pass, of a pair that its rotation brings to 448 times a power of two within a
+    rounding, and of both, at the first position and behind it."""
+    n, d = 48, 128
+    b = Batch8([n], [n], 1, 3, d, d, dtype, 16, seed=23)
+    rng = np.random.default_rng(29)
+    step = 2.0 ** -7 if dtype == "bf16" else 2.0 ** -23
+    inv = (10000.0 ** (-np.arange(pairs) / pairs)).astype(np.float32)
+    x = rng.uniform(-300, 300, (n, 3, d))
+    for i in range(n):
+        for h in range(3):
+            f = int(rng.integers(pairs))
+            turn = float(i + offset) * float(inv[f])
+            at = (2 * f, 2 * f + 1) if inter else (f, f + pairs)
+            if h != 1:  # x cos - y sin = 448
+                x[i, h, at[0]], x[i, h, at[1]] = 448 * math.cos(turn), -448 * math.sin(turn)
+            if h != 0:
+                x[i, h, rng.integers(2 * pairs, d)] = [448, -448 * (1 + step), 448 * (1 - step / 2)][i % 3]
+            x[i, h] *= 2.0 ** int(rng.integers(-20, 20))
+    b.k_new = torch.from_numpy(x).to(DT[dtype])
+    *got, _, status = _append(ex, b, pairs, inter, offset)
+    assert status == 0
+    _, *want = _appended(b, inv, inter, offset)
+    for x, y in zip(got[:2], want[:2]):
+        assert np.array_equal(np.where(x == 0x80, 0, x), np.where(y == 0x80, 0, y))
+    assert np.array_equal(got[2], want[2]) and np.array_equal(got[3], want[3])
+
+
 @pytest.mark.parametrize("form", [(64, False), (64, True), (20, False)])
 def test_append_keeps_its_side_of_every_border(ex, form):
     """Many rotated rows: an entry in some 2^16 lies nearer to a border than fp32 can tell."""

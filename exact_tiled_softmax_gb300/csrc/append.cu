@@ -480,9 +480,31 @@ __device__ __forceinline__ void append_pass(const AppendArgs& a, const TokenRows
     for (int o = kLanes / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
     unsigned top = __float_as_uint(most);
     if (__any_sync(0xFFFFFFFFu, top == 0x7F800000u)) {  // the largest finite one
+      // The other entry of a pair with an infinity is NaN too.  (Where one is NaN the other is not finite: both come
+      // of the same two entries, and finite ones give infinities at most.)
+      [[maybe_unused]] bool other[16];
+      if constexpr (kTurns) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if constexpr (kForm == kAnywhere) {
+            const int c = c0 + e;
+            other[e] = false;
+            if (!turned || !on || c >= 2 * pairs) continue;
+            const bool first = c < pairs;
+            const int f = first ? c : c - pairs;
+            const float k = t.cs[pair_at(f)], s = t.sn[pair_at(f)];
+            other[e] = !isfinite(first ? x1[e] * k + x0[e] * s : x1[e] * k - x0[e] * s);
+          } else {
+            const int o = kForm == kInside ? e ^ 1 : e ^ 8, pair = 8 * u + (kForm == kInside ? e >> 1 : e & 7);
+            other[e] = turned && pair < pairs && !isfinite(y[o]);
+          }
+        }
+      }
       top = 0u;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
+        if constexpr (kTurns)
+          if (other[e]) y[e] = NAN;
         const unsigned m = __float_as_uint(y[e]) & 0x7FFFFFFFu;
         top = max(top, m < 0x7F800000u ? m : 0u);
         if (m == 0x7F800000u) y[e] = NAN;

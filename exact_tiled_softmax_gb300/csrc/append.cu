@@ -295,7 +295,7 @@ constexpr float kTurnError = 4e-7f;  // > 2^-22 sqrt(2), of the sum of the pair'
 // Where the pairs of a row are: halves that 8-column accesses reach, neighbours, or anywhere.
 enum PairForm { kHalves, kInside, kAnywhere };
 
-// Entry c of a row, rotated in 64 bits.
+// Entry c of a row, rotated in 64 bits by the exact angle.
 template <typename T>
 __device__ __noinline__ double turned64(const T* row, int c, int pairs, bool inside, long long pos,
                                         const float* inv_freq) {
@@ -303,8 +303,13 @@ __device__ __noinline__ double turned64(const T* row, int c, int pairs, bool ins
   const int f = inside ? c >> 1 : c < pairs ? c : c - pairs;
   const bool first = inside ? !(c & 1) : c < pairs;
   const int other = inside ? c ^ 1 : first ? c + pairs : f;
-  double s, k;
-  sincos(static_cast<double>(pos) * static_cast<double>(__ldg(inv_freq + f)), &s, &k);
+  // Behind position 2^29 the angle may not fit 53 bits: what its rounding left out, at most 2^-16 radians, is
+  // turned by afterwards (1 - rest^2 / 2 and rest are its cosine and sine to 2^-50).
+  const double at = static_cast<double>(pos), freq = static_cast<double>(__ldg(inv_freq + f));
+  const double angle = at * freq, rest = fma(at, freq, -angle);
+  double s0, k0;
+  sincos(angle, &s0, &k0);
+  const double less = 0.5 * rest * rest, s = fma(k0, rest, fma(-s0, less, s0)), k = fma(-s0, rest, fma(-k0, less, k0));
   const double x = as_float(row[c]), y = as_float(row[other]);
   return first ? x * k - y * s : x * k + y * s;
 }

@@ -506,7 +506,7 @@ int exattn_paged_run(int op, const exattn_paged_call* call);
  * without a nonzero finite entry.  Each entry is rounded once, to nearest, ties to even: off
  * by 2^-4 of itself at most, or by 2^(b - 137) where that is more.  Infinities, NaN and rotated
  * entries beyond fp32 become NaN, and so does the other entry of their pair; neither counts for b.  A rotated key is
- * rounded, and its byte chosen, as if its rotation had been computed in 64 bits, for frequencies of
+ * rounded, and its byte chosen, as if its rotation had been computed in 64 bits by the exact angle, for frequencies of
  * up to 64 radians a token; q_out is rotated in fp32 as above.
  *
  * Attention.  Scores, statistics and outputs are summed in fp32.  Where the 256-row kernel runs

@@ -136,18 +136,16 @@ size_t pass_bytes(const PagedKernel& k, int v) {
 }
 constexpr size_t kFlagBytes = 8192;  // status bits of the CTAs of two passes (at most 2048)
 
-// The most that any kernel of this shape needs (the path may change between the query and
+// The most that any kernel needs of this shape over such pages (the path may change between the query and
 // the call, and q_starts is not part of the shape).
-size_t most_bytes(const exattn_paged_shape* s) {
+size_t most_bytes(const exattn_paged_shape* s, bool e4m3) {
   size_t most = 0;
   for (const Kind k : {kSimtOne, kSimt, kMma8, kMma16, kTc}) {
     // A prefix's pass takes all tokens as one sequence's.
     if (k == kTc && (s->dtype != EXATTN_BF16 || (long long)s->tokens * (s->heads / s->kv_heads) <= kTcRows)) continue;
-    for (const bool e4m3 : {false, true}) {
-      if (!paged_mma_shape(s->d, s->v) && (e4m3 ? k >= kMma16 : k >= kMma8)) continue;
-      const size_t x = pass_bytes(kernel_of(k, s->dtype, s->d, s->v, e4m3), s->v);
-      most = x > most ? x : most;
-    }
+    if (!paged_mma_shape(s->d, s->v) && (e4m3 ? k >= kMma16 : k >= kMma8)) continue;
+    const size_t x = pass_bytes(kernel_of(k, s->dtype, s->d, s->v, e4m3), s->v);
+    most = x > most ? x : most;
   }
   return most;
 }
@@ -156,6 +154,14 @@ size_t most_bytes(const exattn_paged_shape* s) {
 size_t join_bytes(size_t rows, int v) {
   return align256(sizeof(float) * 2 * rows * v) + align256(sizeof(float) * 2 * rows) +
          align256(sizeof(int2) * 2 * rows) + 256;
+}
+
+// What a call over such pages needs.  Heads of 129 to 256 columns need four times as much over pages in 8 bits (the
+// 8-row tiles of a warp each, where pages of the inputs' type have the SIMT kernels alone), and no call is refused
+// for what another type of pages would need.
+size_t paged_bytes(const exattn_paged_shape* s, bool e4m3) { return kStatusBytes + kFlagBytes + most_bytes(s, e4m3); }
+size_t prefix_bytes(const exattn_paged_shape* s, bool e4m3) {
+  return kStatusBytes + kFlagBytes + 2 * most_bytes(s, e4m3) + join_bytes((size_t)s->tokens * s->heads, s->v);
 }
 
 // The most units of `unit` keys that the tables can hold.
@@ -317,7 +323,7 @@ int fwd_paged(const exattn_paged_shape* shape, const void* Q, const Pages& pages
                   workspace);
   if (st == EXATTN_OK) st = check_scales(pages);
   if (st != EXATTN_OK) return st;
-  if (workspace_bytes < exattn_paged_workspace_size(shape)) return EXATTN_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < paged_bytes(shape, pages.e4m3)) return EXATTN_WORKSPACE_TOO_SMALL;
   g_last_error[0] = 0;
   char* ws = static_cast<char*>(workspace);
   PagedArgs a = make_args(shape, Q, pages, page_table, seq_lens, q_starts, scale, mask_kind,
@@ -347,7 +353,7 @@ int fwd_prefix(const exattn_paged_shape* shape, const void* Q, const Pages& page
   if (prefix_len < 0 || (prefix_len > 0 && !prefix_table)) return EXATTN_INVALID_ARG;
   if (prefix_len > kMaxKeys - kMaxPageSize) return EXATTN_UNSUPPORTED;
   if (!aligned(prefix_table, 4)) return EXATTN_MISALIGNED;
-  if (workspace_bytes < exattn_prefix_workspace_size(shape)) return EXATTN_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < prefix_bytes(shape, pages.e4m3)) return EXATTN_WORKSPACE_TOO_SMALL;
   if (prefix_len == 0)
     return fwd_paged(shape, Q, pages, page_table, seq_lens, q_starts, scale, mask_kind, 0, Y, L, workspace,
                      workspace_bytes, cuda_stream);
@@ -356,7 +362,7 @@ int fwd_prefix(const exattn_paged_shape* shape, const void* Q, const Pages& page
   char* ws = static_cast<char*>(workspace);
   const size_t rows = (size_t)shape->tokens * shape->heads;
   char* area = ws + kStatusBytes + kFlagBytes;
-  char* sets = area + 2 * most_bytes(shape);
+  char* sets = area + 2 * most_bytes(shape, pages.e4m3);
   PagedArgs a = make_args(shape, Q, pages, page_table, seq_lens, q_starts, scale, mask_kind, 0, Y, L);
   a.Yf = reinterpret_cast<float*>(sets);
   a.L = reinterpret_cast<float*>(sets + align256(sizeof(float) * 2 * rows * a.v));
@@ -398,7 +404,7 @@ int fwd_prefix(const exattn_paged_shape* shape, const void* Q, const Pages& page
     p = a;
   } else {
     place_pass(p, of.k, area);
-    place_pass(a, own.k, area + most_bytes(shape));
+    place_pass(a, own.k, area + most_bytes(shape, pages.e4m3));
     a.flags = p.flags + of.k.ctas;
     a.second = true;
     launches_ctas = of.k.ctas + own.k.ctas;
@@ -417,15 +423,17 @@ int fwd_prefix(const exattn_paged_shape* shape, const void* Q, const Pages& page
 
 extern "C" {
 
+// The pages' type is not part of the shape: enough for each that its widths allow.
 size_t exattn_paged_workspace_size(const exattn_paged_shape* shape) {
   if (check_paged(shape) != EXATTN_OK) return 0;
-  return kStatusBytes + kFlagBytes + most_bytes(shape);
+  const size_t own = paged_bytes(shape, false);
+  return check_paged_e4m3(shape) == EXATTN_OK ? std::max(own, paged_bytes(shape, true)) : own;
 }
 
 size_t exattn_prefix_workspace_size(const exattn_paged_shape* shape) {
   if (check_paged(shape) != EXATTN_OK) return 0;
-  const size_t rows = (size_t)shape->tokens * shape->heads;
-  return kStatusBytes + kFlagBytes + 2 * most_bytes(shape) + join_bytes(rows, shape->v);
+  const size_t own = prefix_bytes(shape, false);
+  return check_paged_e4m3(shape) == EXATTN_OK ? std::max(own, prefix_bytes(shape, true)) : own;
 }
 
 int attn_append_paged(const exattn_paged_shape* shape, const void* q, const void* k, const void* v,

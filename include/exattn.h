@@ -415,7 +415,9 @@ typedef struct exattn_paged_shape {
 } exattn_paged_shape;
 
 /* Workspace bytes: attn_append_paged and attn_fwd_paged take the first,
- * attn_fwd_prefix the second; 0 if the shape is invalid. */
+ * attn_fwd_prefix the second; 0 if the shape is invalid.  They are enough for any type of pages that the
+ * shape allows; a call asks for what its own pages' kernels need (with d or v above 128 a quarter of that over
+ * pages of `dtype`, where pages in 8 bits are possible). */
 size_t exattn_paged_workspace_size(const exattn_paged_shape* shape);
 size_t exattn_prefix_workspace_size(const exattn_paged_shape* shape);
 

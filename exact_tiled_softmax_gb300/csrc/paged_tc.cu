@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(Warps<kBytes>::kThreads, 1)
         bool ok = true;
         int fill = 0;
         TcSegment t;
-        for (int seg = 0; take(seg, t, ok) && ok; ++seg) {
+        for (int seg = 0; take(seg, t, ok); ++seg) {
           for (int u = 0; u < 2 * t.n && ok; ++u, ++fill) {
             const int rs = fill % NR, ks = fill % NS;
             if (!(ok = wait_all(bar(Lay::B_RF + rs), (fill / NR) & 1, abort_flag))) break;
@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(Warps<kBytes>::kThreads, 1)
             fence_proxy_async_smem();
             mbar_arrive(bar(Lay::B_KVF + ks));
           }
+          if (!ok) break;  // not on to the next segment, whose wait may succeed
         }
         if (!ok) {
           bits |= kStatusTimeout;

@@ -211,10 +211,10 @@ def test_masks_of_fewer_blocks_would_be_written_over(ring):
     assert any(_run([(9, True), (4, False)], seed, NS=ring, NR=ring, keep_blocks=blocks)[1]["masks"] for seed in range(400))
 
 
-@pytest.mark.parametrize("drop", ["KVE0", "RE0", "QFREE", "SEGE0"])
-def test_model_catches_a_missing_wait(drop):
-    assert any(_run([(rnd.randint(1, 4), rnd.random() < 0.5) for _ in range(4)], seed, {drop})[0]
-               for seed, rnd in ((s, random.Random(s)) for s in range(400)))
+@pytest.mark.parametrize("drop,segments", [("KVE0", [(3, True)] * 4), ("RE0", [(3, True)] * 4), ("QFREE", [(3, True)] * 4),
+                                           ("SEGE0", [(1, False)] * 6)])
+def test_model_catches_a_missing_wait(drop, segments):
+    assert any(_run(segments, seed, {drop})[0] for seed in range(400))
 
 
 def test_a_wait_that_gives_up_ends_its_warp():

@@ -13,8 +13,8 @@
 // weight: with s in the exp2 domain and e the exponent of V's row, w = s + e, and the operand is
 // 2^(w - M + 7) with M a reference point of its own (the sum l keeps s's), so that unequal rows of V
 // lose nothing; 2^7 puts the largest weight in the middle of fp16's range above its subnormals, and a
-// weight is held to 2^-11 of itself or 2^-32 of the row's largest.  A row of Q is scaled by the power of
-// two that brings its largest entry to [2^14, 2^15).  fp32 queries and their weights are two fp16 parts,
+// weight is held to 2^-11 of itself or 2^-32 of the row's largest.  A row of Q is scaled by an even power of
+// two that brings its largest entry to [2^13, 2^15).  fp32 queries and their weights are two fp16 parts,
 // 2^-22 of themselves.
 // The reference points move only when a row's maximum passes them by more than 2^8, which a vote
 // tells without the maximum.
@@ -42,6 +42,7 @@ namespace {
 
 using tc::ex2;
 using tc::fadd2;
+using tc::fmul2;
 using tc::ld_shared_v4;
 using tc::pack_bf16x2;
 using tc::smem_u32;
@@ -183,7 +184,7 @@ struct Spans {
 };
 
 // A worker's rows over a segment.  Thread (g, t) = (lane / 4, lane % 4) holds the operands of rows
-// 8 n + g, and of rows 8 n + 2 t + x the factor of their scores, the reference points m and M, the sum
+// 8 n + g, and of rows 8 n + 2 t + x the root f of their power of two, the reference points m and M, the sum
 // over its own keys l, and of the output o[n][y] columns 16 y + g (x = 0, 1) and 16 y + g + 8.
 template <typename T, int C, int NT>
 struct Rows {
@@ -202,7 +203,7 @@ struct Rows {
     }
   }
   // Its operands.  qs: the warp's place for them in shared memory.
-  __device__ __forceinline__ void take_q(int n, const Raw (&raw)[K], float sl2, uint32_t qs) {
+  __device__ __forceinline__ void take_q(int n, const Raw (&raw)[K], uint32_t qs) {
     const int lane = threadIdx.x & 31, t = lane & 3;
     float x[K][4];
     unsigned top = 0u;
@@ -214,8 +215,9 @@ struct Rows {
     }
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    const unsigned e = max(top >> 23, 15u);  // the largest is below 2^(e - 126)
-    const float up = __uint_as_float((268u - e) << 23), down = __uint_as_float((e - 14u) << 23) * sl2;
+    // The largest is below 2^(e - 126), and brought to [2^13, 2^15) by an even power of two, whose root is normal.
+    const unsigned e = max((top >> 23) | 1u, 15u);
+    const float up = __uint_as_float((268u - e) << 23), root = __uint_as_float((e + 113u) >> 1 << 23);
 #pragma unroll
     for (int c = 0; c < K; ++c) {
 #pragma unroll
@@ -235,7 +237,7 @@ struct Rows {
                            qb[0][p][2 * s + 1][0], qb[0][p][2 * s + 1][1]);
     }
 #pragma unroll
-    for (int x2 = 0; x2 < 2; ++x2) f[n][x2] = __shfl_sync(0xFFFFFFFFu, down, 4 * (2 * t + x2));
+    for (int x2 = 0; x2 < 2; ++x2) f[n][x2] = __shfl_sync(0xFFFFFFFFu, root, 4 * (2 * t + x2));
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -249,7 +251,7 @@ struct Rows {
 
   // The tile at kt, vt, its exponents at et (32 of keys, 32 of values).
   __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, uint32_t et, unsigned have, int key0,
-                                       const Spans<NT>& sp, int v, uint32_t qs) {
+                                       const Spans<NT>& sp, int v, float sl2, uint32_t qs) {
     const int lane = threadIdx.x & 31, g = lane >> 2;
     // Of the sixteen keys q, half z (key `first` + 16 q + 2 z): bytes 2 z of the words.
     const int first = 4 * (g >> 1) + (g & 1);
@@ -302,7 +304,11 @@ struct Rows {
         }
       }
     }
-    // Scores into the exp2 domain, those that do not count to -inf; w beside them.
+    // Scores into the exp2 domain, those that do not count to -inf; w beside them.  The power of two of a row of Q comes
+    // as its root, before and after the key's: their product may leave fp32 where the score does not.
+    float fs[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) fs[n][0] = f[n][0] * sl2, fs[n][1] = f[n][1] * sl2;
 #pragma unroll
     for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -311,8 +317,9 @@ struct Rows {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float &s0 = sc[n][q][2 * z], &s1 = sc[n][q][2 * z + 1];
-          s0 *= f[n][0] * kf;
-          s1 *= f[n][1] * kf;
+          fmul2(s0, s1, s0, s1, fs[n][0], fs[n][1]);
+          fmul2(s0, s1, s0, s1, kf, kf);
+          fmul2(s0, s1, s0, s1, f[n][0], f[n][1]);
         }
       }
     if (have != 0xFFFFFFFFu || key0 < sp.all_lo || key0 + kTile > sp.all_hi) {
@@ -574,7 +581,7 @@ __global__ void __launch_bounds__(32 * Config<T, C, NT>::kW, Config<T, C, NT>::k
         for (int y = 0; y < NT; ++y) st.load_q(raw[y], query(w, 8 * y + g), 8 * y + g < w.t.rows, d);
 #pragma unroll
         for (int y = 0; y < NT; ++y) {
-          st.take_q(y, raw[y], a.sl2, qs);
+          st.take_q(y, raw[y], qs);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int row = 8 * y + 2 * t + x;
@@ -666,7 +673,7 @@ __global__ void __launch_bounds__(32 * Config<T, C, NT>::kW, Config<T, C, NT>::k
     cp_wait<S - 1>();
     __syncwarp();  // tile i is in
     const uint32_t at = base + (i % S) * kStage;
-    st.tile(at, at + At::kTileBytes, scales + (i % S) * 64, tile_keys[warp][i % S], key0, sp, v, qs);
+    st.tile(at, at + At::kTileBytes, scales + (i % S) * 64, tile_keys[warp][i % S], key0, sp, v, a.sl2, qs);
     key0 += kTile;
     if (--left > 0) continue;
 

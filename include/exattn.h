@@ -519,7 +519,7 @@ int exattn_paged_run(int op, const exattn_paged_call* call);
  * smaller than 2^-30 of their row's largest entry, fp32 queries are held to 2^-22 of themselves or
  * 2^-38 of their row's largest, weights p 2^(b - 127) to 2^-11 (bf16) or 2^-22 (fp32) of
  * themselves or 2^-32 of their row's largest (EXATTN_PATH_SIMT: whole).  Non-finite entries act as above;
- * so may a score whose scale times the largest entries of its query and key is 2^148 or more.
+ * so may a score whose scale times the largest entries of its query and key is 2^56 or more.
  * ------------------------------------------------------------------------- */
 int attn_append_paged_e4m3(const exattn_paged_shape* shape, const void* q, const void* k, const void* v,
                            const int* page_table, const int* seq_lens, const int* q_starts,

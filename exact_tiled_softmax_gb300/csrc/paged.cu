@@ -14,7 +14,7 @@
 // shuffles of a group.  Heads of 256 columns, 537 MB of keys and values: one row 97 us in bf16
 // (5.5 TB/s), 84 in fp32 (6.4), four rows 246 in bf16.  One row of 128 columns: 333 us for 2.1
 // GB against the tensor cores' 325, which take eight rows in that time.  Pages in 8 bits come here only where
-// the path is forced to SIMT: 276 us where the tensor cores take 168.
+// the path is forced to SIMT: 283 us where the tensor cores take 168.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(32 * kW, kCtas<NQ>) paged_simt_kernel(const Pa
 
     // Rows of Q with scale * log2(e) folded in, and the keys that each allows.
     float qf[NQ][W];
+    [[maybe_unused]] float root[NQ];
     int lo[NQ], hi[NQ];
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
@@ -146,8 +147,27 @@ __global__ void __launch_bounds__(32 * kW, kCtas<NQ>) paged_simt_kernel(const Pa
 #pragma unroll
           for (int e = 0; e < E; ++e) f[e] = 0.f;
         }
+        if constexpr (kScaled) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) qf[q][c * E + e] = f[e] * a.sl2;
+          for (int e = 0; e < E; ++e) qf[q][c * E + e] = f[e];
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e) qf[q][c * E + e] = f[e] * a.sl2;
+        }
+      }
+      if constexpr (kScaled) {
+        // An even power of two out of the row, its root before and after a key's power of two: the products of
+        // codes, which are not the keys themselves, stay inside fp32.
+        unsigned top = 0u;
+#pragma unroll
+        for (int x = 0; x < W; ++x) top = max(top, __float_as_uint(qf[q][x]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        const unsigned e = max((top >> 23) | 1u, 15u);  // the largest is below 2^(e - 126)
+        const float up = __uint_as_float((268u - e) << 23);
+        root[q] = __uint_as_float((e + 113u) >> 1 << 23);
+#pragma unroll
+        for (int x = 0; x < W; ++x) qf[q][x] = qf[q][x] * up * a.sl2;
       }
     }
     float m[NQ], l[NQ], z[NQ][W];
@@ -204,7 +224,7 @@ __global__ void __launch_bounds__(32 * kW, kCtas<NQ>) paged_simt_kernel(const Pa
           float part = acc0 + acc1;
 #pragma unroll
           for (int o = G / 2; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
-          if constexpr (kScaled) part *= ks[u];
+          if constexpr (kScaled) part = part * root[q] * ks[u] * root[q];
           const int key = jb + u * KPW + g;
           ok[u] = have[u] && key >= lo[q] && key < hi[q];
           s[u] = ok[u] ? part : -INFINITY;

@@ -64,7 +64,9 @@ def _coded(rng, shape, size, least, most):
 @pytest.mark.parametrize("k_bytes,k_size,v_bytes,v_size,q_size,gain", [
     ((247, 254), 2.0 ** 121, (247, 254), 2.0 ** 117, 2.0 ** -120, 1),
     ((247, 254), 2.0 ** 126, (1, 2), 2.0 ** -118, 2.0 ** -110, 1),
-    ((252, 254), 2.0 ** 134, (1, 1), 2.0 ** -118, 2.0 ** -123, 1)])  # scale times q below fp32's normal numbers
+    ((252, 254), 2.0 ** 134, (1, 1), 2.0 ** -118, 2.0 ** -123, 1),  # scale times q below fp32's normal numbers
+    ((1, 2), 2.0 ** -118, (1, 254), 2.0 ** -50, 2.0 ** 122, 1),
+    ((1, 1), 2.0 ** -120, (120, 130), 1.0, 2.0 ** 124, 8)])  # scale times q times a code above its largest
 def test_bytes_of_either_end(ex, path, dtype, nq, d, k_bytes, k_size, v_bytes, v_size, q_size, gain):  # noqa: F811
     b = Batch8([150, 35], [nq, nq], 4, 2, d, d, dtype, 16, seed=21 + d, q_gain=q_size)
     rng = np.random.default_rng(33)

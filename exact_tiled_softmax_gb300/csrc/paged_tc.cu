@@ -30,7 +30,8 @@
 // that what they hold, NaN included, meets no product that counts.
 //
 // Pages in 8 bits.  Their tiles are loaded as they are, and warps 12-15 turn them into the bf16 tiles of the
-// products, a row's power of two folded in: an e4m3 number times it is a bf16 value.  Tensor memory, full of
+// products, a row's power of two folded in: an e4m3 number times it is a bf16 value, subnormal ones among them (under
+// bytes 3 to 246; see bytes_to_bf16).  Tensor memory, full of
 // S and O, has no room for the scales of a block-scaled product.  Measured: the chunks above 241 us a launch (258 a
 // call, 1.03 PFLOP/s): converting shares the schedulers and shared memory with the softmax.  Without the
 // conversion's work a call takes 221 us, without the softmax's 241, without both 172.  Pages of 8 keys: 353 us.
@@ -132,7 +133,8 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort));
 }
 
-// Sixteen e4m3 numbers of a row with factor f, as bf16: exact.
+// Sixteen e4m3 numbers of a row with factor f, as bf16: exact from f = 2^-124 to 2^119.  Above, numbers may be 2^128 and
+// infinite, below they may end under bf16's last place, 2^-133.
 __device__ __forceinline__ void bytes_to_bf16(const uint4& raw, float f, uint32_t (&y)[8]) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll

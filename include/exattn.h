@@ -514,7 +514,11 @@ int exattn_paged_run(int op, const exattn_paged_call* call);
  * Attention.  Scores, statistics and outputs are summed in fp32.  Where the 256-row kernel runs
  * (bf16 queries, d, v <= 128, pages of 8 keys or more, a positive scale, more than 16 rows to a
  * key head on average, or more than 32 where the tables, the windows or the prefix can hold 2^17 keys of
- * all key heads; a short prefix as above), probabilities are rounded to bf16 before they meet V, as above.  All other kernels: operands
+ * all key heads; a short prefix as above), probabilities are rounded to bf16 before they meet V, as above, and the
+ * numbers of k_pages and v_pages, times their rows' powers of two, are bf16 operands: exactly under bytes 3 to 246;
+ * under larger bytes those of 2^128 and more are infinite there (an append writes them for entries from 0.968 of the
+ * largest fp32 number on alone), under 1 and 2 those below 2^-133 are rounded to a multiple of it.  Products of queries
+ * and keys have to stay in fp32 there before the scale.  All other kernels take every byte: operands
  * are fp16 parts, each row of Q scaled by a power of two; bf16 queries are exact where they are no
  * smaller than 2^-30 of their row's largest entry, fp32 queries are held to 2^-22 of themselves or
  * 2^-38 of their row's largest, weights p 2^(b - 127) to 2^-11 (bf16) or 2^-22 (fp32) of

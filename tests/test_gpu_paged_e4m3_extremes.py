@@ -80,3 +80,24 @@ def test_bytes_of_either_end(ex, path, dtype, nq, d, k_bytes, k_size, v_bytes, v
     y, L, status = _attend(ex, b, "causal", 0, scale)
     assert status == 0
     _check_at(path, b, y, L, scale, "causal", -round(math.log2(v_size)))
+
+
+# The 256-row kernel's operands are the rows themselves, as bf16 numbers.
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("k_bytes,k_size,v_bytes,v_size,q_size", [
+    ((240, 246), 2.0 ** 118, (240, 246), 2.0 ** 116, 2.0 ** -116),
+    ((3, 6), 2.0 ** -122, (3, 6), 2.0 ** -118, 2.0 ** 118),
+    ((3, 5), 2.0 ** -128, (3, 5), 2.0 ** -122, 2.0 ** 122)])  # keys below 2^-126
+def test_bytes_of_the_tall_tiles(ex, d, page, k_bytes, k_size, v_bytes, v_size, q_size):  # noqa: F811
+    b = Batch8([150, 45], [40, 40], 4, 2, d, d, "bf16", page, seed=27 + d, q_gain=q_size)
+    rng = np.random.default_rng(35)
+    for name, (least, most), size in (("k", k_bytes, k_size), ("v", v_bytes, v_size)):
+        codes, byte = getattr(b, name + "_pages"), getattr(b, name + "_scales")
+        new, new_byte = _coded(rng, codes.shape, size, least, most)
+        used = byte != 255
+        codes[used], byte[used] = new[used], new_byte[used]
+    b.requantised()
+    scale = 1.0 / (k_size * q_size * math.sqrt(d))
+    y, L, status = _attend(ex, b, "causal", 0, scale)
+    assert status == 0
+    _check_at("auto", b, y, L, scale, "causal", -round(math.log2(v_size)))

@@ -430,10 +430,12 @@ def paged_shape(q, k_pages, v_pages, page_table) -> PagedShape:
 
 
 def paged_workspace_size(shape: PagedShape) -> int:
+    """Bytes that are enough for attn_fwd_paged over any type of pages that the widths allow."""
     return load_library().exattn_paged_workspace_size(ctypes.byref(shape))
 
 
 def prefix_workspace_size(shape: PagedShape) -> int:
+    """The same for attn_fwd_prefix."""
     return load_library().exattn_prefix_workspace_size(ctypes.byref(shape))
 
 
@@ -554,8 +556,8 @@ def append_paged(k, v, k_pages, v_pages, page_table, seq_lens, q_starts=None, q=
 
     A cache in 8 bits (attn_append_paged_e4m3) has pages of torch.float8_e4m3fn and an exponent byte for
     each row in ``k_scales`` and ``v_scales`` [num_pages, kv_heads, page_size] (uint8 or
-    float8_e8m0fnu): a row stands for its numbers times 2 ** (byte - 127), and is quantised, with the
-    smallest exponent at which nothing saturates, as it is written."""
+    float8_e8m0fnu): a row stands for its numbers times 2 ** (byte - 127), byte 0 with zeros for a row of
+    zeros, and is quantised, with the smallest exponent at which nothing saturates, as it is written."""
     if _lib is None:
         load_library()
     pos_offset = _int32("pos_offset", pos_offset)

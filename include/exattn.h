@@ -499,7 +499,7 @@ int exattn_paged_run(int op, const exattn_paged_call* call);
  * numbers (sign, 4 bits of exponent with bias 7, 3 of significand; 0x7F and 0xFF are NaN,
  * no infinities, largest 448).  k_scales and v_scales [num_pages][kv_heads][page_size]
  * hold an exponent byte for each row of the pages: a row with byte b stands for its
- * numbers times 2^(b - 127), 1 <= b <= 254; b = 0 stands for a row of zeros.  255 is not
+ * numbers times 2^(b - 127), 1 <= b <= 254; b = 0 is a row of zeros, whose numbers are zeros too.  255 is not
  * a scale: rows that allow such a key are undefined.  The scale arrays are 16-byte
  * aligned.  d and v are multiples of 16.
  *

@@ -292,8 +292,8 @@ cudaError_t append_dispatch(const AppendArgs& a, cudaStream_t s) {
 // maximum lies that near to 448 times a power of two.  The codes are those of 64-bit arithmetic.
 // Behind the first position the bound does not know of pairs that their rotation leaves as they are (frequencies of zero):
 // of their bf16 entries one in 16 lies on a border, and 37 thousand tokens with half of 64 such take 612 us in place of
-// 144.  Columns behind the last pair are computed again where their lane has the last pairs too, whose number is no
-// multiple of 8: 37 thousand tokens of 80 columns with 20 neighbouring pairs 86 us, with 24 75.
+// 144.  Nor does it know of columns behind the last pair in a lane that has pairs, in halves of a number of pairs that is
+// no multiple of 8.
 constexpr float kTurnError = 4e-7f;  // > 2^-22 sqrt(2), of the sum of the pair's magnitudes, before or after
 
 // Where the pairs of a row are: halves that 8-column accesses reach, neighbours, or anywhere.
@@ -563,6 +563,8 @@ __device__ __forceinline__ void append_pass(const AppendArgs& a, const TokenRows
         const float u0 = kForm == kAnywhere ? x0[e] : kForm == kInside ? y[2 * e] : y[e];
         const float u1 = kForm == kAnywhere ? x1[e] : kForm == kInside ? y[2 * e + 1] : y[8 + e];
         d[e] = fmaf(fabsf(u0), err, fmaf(fabsf(u1), err, least));
+        // Columns that pass, of the lane that has the last pairs: no error, whatever stands beside them.
+        if (kForm == kInside && 8 * u + e >= pairs) d[e] = 0.f;
       }
       uint32_t down[4];
 #pragma unroll

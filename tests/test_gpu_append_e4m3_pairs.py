@@ -86,3 +86,30 @@ def test_pairs_that_are_not_finite(d, pairs, inter, dtype):
                 hurt += int((y == 0x7F).sum())
             assert np.array_equal(x, y), (name, t, int((x != y).sum()))
     assert hurt > n * kv  # the pairs were there
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,pairs,inter", [(64, 5, True), (80, 21, True), (256, 90, True), (128, 48, True), (64, 13, False),
+                                           (16, 3, False), (128, 48, False), (64, 0, False)])
+def test_columns_that_pass_do_not_hurt_one_another(d, pairs, inter, dtype):
+    """Behind the last pair each entry is by itself: infinities and NaN there become NaN, their neighbours stay."""
+    import exact_tiled_softmax_gb300 as ex
+    n, kv, pos = 40, 3, 10
+    b = Batch8([pos + 1] * n, [1] * n, 3, kv, d, 16, dtype, 16, seed=d + pairs)
+    rng = np.random.default_rng(d + pairs + inter)
+    inv = rng.uniform(0.0740, 0.0830, pairs).astype(np.float32)
+    x = b.np(b.k_new).copy()
+    for i in range(n):
+        for h in range(kv):
+            x[i, h, rng.integers(2 * pairs, d, 3)] = (np.inf, np.nan, -np.inf)[i % 3]
+    b.k_new = torch.from_numpy(x).to(DT[dtype])
+    k, v, table, lens, starts, ks, vs = b.cache()
+    kn, vn = b.dev("k_new", "v_new")
+    ex.append_paged(kn, vn, k, v, table, lens, q_starts=starts, inv_freq=torch.from_numpy(inv).cuda() if pairs else None,
+                    interleaved=inter, k_scales=ks, v_scales=vs)
+    got, byte = k.view(torch.uint8).cpu().numpy(), ks.cpu().numpy()
+    for t in range(n):
+        at, off = int(b.table[t, pos // 16]), pos % 16
+        codes, want = e4m3.quantise(_rotated(b.np(b.k_new[t]), pos, inv, inter))
+        z, codes = (np.where(y & 0x7F == 0x7F, 0x7F, np.where(y == 0x80, 0, y)) for y in (got[at, :, off], codes))
+        assert np.array_equal(byte[at, :, off], want) and np.array_equal(z, codes), (t, int((z != codes).sum()))
